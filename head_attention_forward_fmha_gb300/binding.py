@@ -55,6 +55,12 @@ SIGNATURES = {
     "fmha_fwd_nvfp4": ([_vp, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _vp],
                        _i32),
     "fmha_quantize_nvfp4": ([_vp, ctypes.c_longlong, _i32, _f32, _vp, _vp, _vp], _i32),
+    "fmha_qk_norm_rope": ([_vp, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp, _f32, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                           _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "fmha_kv4_append": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "fmha_fwd_kv4_plan": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)], _i32),
+    "fmha_fwd_kv4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                      _f32, _i32, _i32, _i32, _i32, _vp, _sz, _vp], _i32),
 }
 # Size of the fixed split-KV scratch fmha_fwd_noalloc uses (FMHA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -412,4 +418,170 @@ def fmha_fwd_noalloc(q, k, v, o, lse, scale=None, window=0, causal=False, stream
                                  b, n_h, n_kv_h, T, s_k, hd, float(scale), int(window), int(bool(causal)),
                                  _stream(stream))
     _check(rc, "fmha_fwd_noalloc")
+    return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Serving operators around the forward: norm and rotation, 4-bit cache
+# ---------------------------------------------------------------------------
+def _ptr(t, name, dtype, shape, device, optional=False):
+    """Data pointer of a contiguous CUDA tensor of this dtype, shape and device (None if optional and absent)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous CUDA %s tensor" % (name, dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    return t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) of the library, with `device` current; stream None is that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    _check(getattr(_lib or load(), fn)(*args, _stream(stream)), fn)
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace of one call from torch's allocator, in the order of the stream that uses it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                      q=None, k=None, v=None, kv_start=None, stream=None):
+    """Rows of a QKV projection to what fmha_fwd takes (fmha_qk_norm_rope in include/fmha.h): RMS norm of every
+    query and key head (weights fp32 [hd]; None: no norm), rotation by position, head-major outputs.
+
+    qkv: bf16 [b, T, (n_h + 2 n_kv_h) * hd], rows contiguous, tokens and sequences at any stride of a multiple of 8
+    elements.  cos_sin: fp32 [max_pos, rot], the cosines and then the sines of each position; positions: int32 [b, T]
+    (a token outside [0, max_pos) is padding, its outputs are left as they are); both None: no rotation.
+    k and v given with more rows than T are written at rows kv_start[b] + t (int32 [b]; None: 0).
+    Returns q [b, n_h, T, hd], k and v [b, n_kv_h, rows, hd]; what is not given is allocated."""
+    if not isinstance(qkv, torch.Tensor) or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
+        raise TypeError("qkv must be a CUDA bf16 tensor")
+    if qkv.dim() != 3 or n_h < 1 or n_kv_h < 1 or qkv.shape[2] % (n_h + 2 * n_kv_h):
+        raise ValueError("qkv [b, T, (n_h + 2 n_kv_h) * hd] expected, got %s" % (tuple(qkv.shape),))
+    b, T, width = qkv.shape
+    hd = width // (n_h + 2 * n_kv_h)
+    sb, st, se = qkv.stride()
+    if se != 1 and width > 1:
+        raise ValueError("the rows of qkv must be contiguous")
+    if T <= 1:
+        st = max(width, (st + 7) // 8 * 8) if T == 0 or st < width or st % 8 else st
+    if b <= 1 and sb % 8:
+        sb = 0
+    dev = qkv.device
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions are given together or not at all")
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape if cos_sin.dim() == 2 else (0, -1)
+    if k is not None and (k.dim() != 4 or v is None):
+        raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
+    rows = T if k is None else k.shape[2]
+    if q is None:
+        q = torch.empty((b, n_h, T, hd), dtype=torch.bfloat16, device=dev)
+    if k is None:
+        if v is not None:
+            raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
+        k = torch.empty((b, n_kv_h, T, hd), dtype=torch.bfloat16, device=dev)
+        v = torch.empty_like(k)
+    kv_shape = (b, n_kv_h, rows, hd)
+    _call("fmha_qk_norm_rope", dev, stream, qkv.data_ptr(), sb, st,
+          _ptr(q_weight, "q_weight", torch.float32, (hd,), dev, True), _ptr(k_weight, "k_weight", torch.float32, (hd,), dev, True),
+          eps, _ptr(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev, True),
+          _ptr(positions, "positions", torch.int32, (b, T), dev, True), max_pos, rot, int(bool(interleaved)),
+          _ptr(q, "q", torch.bfloat16, (b, n_h, T, hd), dev), _ptr(k, "k", torch.bfloat16, kv_shape, dev),
+          _ptr(v, "v", torch.bfloat16, kv_shape, dev), _ptr(kv_start, "kv_start", torch.int32, (b,), dev, True), rows,
+          b, T, n_h, n_kv_h, hd)
+    return q, k, v
+
+
+def fmha_kv4_cache(batch, n_kv_h, cap, hd, device="cuda"):
+    """An empty 4-bit KV cache of `cap` rows (a multiple of 16) per sequence and head: the uint8 tensors
+    (k_codes, k_scales, v_codes, v_scales) that fmha_kv4_append writes and fmha_fwd_kv4 reads."""
+    if hd not in (64, 128, 256, 512) or cap % 16:
+        raise ValueError("hd must be 64, 128, 256 or 512 and cap a multiple of 16 (got hd=%d cap=%d)" % (hd, cap))
+    return tuple(torch.zeros((batch, n_kv_h, cap, hd // w), dtype=torch.uint8, device=device) for w in (2, 16, 2, 16))
+
+
+def _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev):
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes [b, n_kv_h, cap, hd/2] expected, got %s" % (tuple(k_codes.shape),))
+    cap = k_codes.shape[2]
+    cs, ss = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
+    return cap, (_ptr(k_codes, "k_codes", torch.uint8, cs, dev), _ptr(k_scales, "k_scales", torch.uint8, ss, dev),
+                 _ptr(v_codes, "v_codes", torch.uint8, cs, dev), _ptr(v_scales, "v_scales", torch.uint8, ss, dev))
+
+
+def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=1.0, v_global=1.0, k_out=None, v_out=None,
+                    stream=None):
+    """Quantise k, v (bf16 [b, n_kv_h, T, hd]) into a 4-bit cache (fmha_kv4_cache) at rows start[b] + t (int32 [b]; rows
+    outside the cache are left out).  k_out and v_out, bf16 like k, receive the values that the written rows stand for."""
+    if k.dim() != 4:
+        raise ValueError("k [b, n_kv_h, T, hd] expected, got %s" % (tuple(k.shape),))
+    b, n_kv_h, T, hd = k.shape
+    dev = k.device
+    cap, cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev)
+    _call("fmha_kv4_append", dev, stream, _ptr(k, "k", torch.bfloat16, k.shape, dev), _ptr(v, "v", torch.bfloat16, k.shape, dev),
+          *cache, _ptr(start, "start", torch.int32, (b,), dev), k_global, v_global,
+          _ptr(k_out, "k_out", torch.bfloat16, k.shape, dev, True), _ptr(v_out, "v_out", torch.bfloat16, k.shape, dev, True),
+          b, n_kv_h, T, cap, hd)
+
+
+_kv4_plans = {}
+
+
+def fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, window=0, n_first=0, causal=False, kv_chunk=0):
+    """(n_splits, kv_chunk) that fmha_fwd_kv4 uses for sequences of up to s_k keys (kv_chunk 0: its own choice)."""
+    chunk = ctypes.c_int(int(kv_chunk))
+    n = (_lib or load()).fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, int(window), int(n_first), int(bool(causal)),
+                                           ctypes.byref(chunk))
+    _check(n if n < 0 else 0, "fmha_fwd_kv4_plan")
+    return n, chunk.value
+
+
+def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None, lse=None, s_k=None, k_global=1.0,
+                 v_global=1.0, scale=None, window=0, n_first=0, causal=False, sink=None, kv_chunk=0, workspace=None,
+                 stream=None):
+    """O (bf16) and LSE (fp32) of q (bf16 [b, n_h, T, hd]) over a 4-bit cache (fmha_fwd_kv4 in include/fmha.h).
+
+    seq_lens: int32 [b], the keys of each sequence (None: s_k each); s_k: their bound, at most the cache's rows (the
+    default).  With a window, the keys j < n_first stay attended.  workspace: an optional uint8 tensor for the split-KV
+    partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call takes its own from torch."""
+    if q.dim() != 4:
+        raise ValueError("q [b, n_h, T, hd] expected, got %s" % (tuple(q.shape),))
+    b, n_h, T, hd = q.shape
+    dev = q.device
+    n_kv_h = k_codes.shape[1] if k_codes.dim() == 4 else 0
+    cap, cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev)
+    if s_k is None:
+        s_k = cap
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=dev)
+    if scale is None:
+        scale = hd ** -0.5
+    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk)
+    n = _kv4_plans.get(key)
+    if n is None:
+        n = _kv4_plans[key] = fmha_fwd_kv4_plan(*key)[0]
+    if n > 1 and workspace is None:
+        workspace = _scratch(fmha_workspace_bytes(b, n_h, T, hd, n), dev, stream)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _call("fmha_fwd_kv4", dev, stream, _ptr(q, "q", torch.bfloat16, q.shape, dev), *cache,
+          _ptr(seq_lens, "seq_lens", torch.int32, (b,), dev, True), _ptr(o, "o", torch.bfloat16, q.shape, dev),
+          _ptr(lse, "lse", torch.float32, (b, n_h, T), dev), _ptr(sink, "sink", torch.float32, (n_h,), dev, True),
+          k_global, v_global, b, n_h, n_kv_h, T, s_k, cap, hd, scale, int(window), int(n_first), int(bool(causal)), int(kv_chunk),
+          ws, ws_bytes)
     return o, lse

@@ -23,11 +23,11 @@
 
 namespace {
 
-using namespace fmha;
-
 thread_local std::string g_last_error;
 
-int fail(int code, const char* fmt, ...) {
+}  // namespace
+
+int fmha::fail(int code, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -37,9 +37,13 @@ int fail(int code, const char* fmt, ...) {
     return code;
 }
 
-int cuda_fail(cudaError_t e, const char* what) {
+int fmha::cuda_fail(cudaError_t e, const char* what) {
     return fail(FMHA_ERR_LAUNCH, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+namespace {
+
+using namespace fmha;
 
 // ---------------------------------------------------------------- tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -744,7 +748,7 @@ void fmha_release(void) {
     cudaSetDevice(cur);
 }
 
-int fmha_version(void) { return 100; }
+int fmha_version(void) { return 101; }
 
 int fmha_selftest_wait_timeout(unsigned timeout_us, fmha_stream_t stream) {
     if (timeout_us < 1 || timeout_us > 10000000u)
@@ -841,4 +845,247 @@ extern "C" int fmha_fwd_noalloc(const void* q, const void* k, const void* v, voi
     } catch (...) {
         return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_noalloc");
     }
+}
+
+// ---------------------------------------------------------------- norm and rotation, 4-bit cache
+namespace {
+
+bool head_dim_ok(int hd) { return hd == 64 || hd == 128 || hd == 256 || hd == 512; }
+
+// The 4-bit attention's problem after validation: a window that reaches every
+// key of every sequence is none, and first keys matter only with a window.
+int check_kv4(int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, float scale, int window, int n_first,
+              int causal, Kv4Fwd* out) {
+    Problem p;
+    // causal with T > s_k is fine here: a row before its sequence's first key attends nothing
+    const int rc = check_shape(batch, n_h, n_kv_h, T, s_k, hd, scale, window, 0, &p);
+    if (rc) return rc;
+    if (causal != 0 && causal != 1) return fail(FMHA_ERR_SHAPE, "causal must be 0 or 1 (got %d)", causal);
+    if (n_first < 0) return fail(FMHA_ERR_SHAPE, "n_first=%d must be >= 0", n_first);
+    if (cap < s_k || cap % 16 != 0)
+        return fail(FMHA_ERR_SHAPE, "cap=%d must be a multiple of 16 and at least s_k=%d", cap, s_k);
+    if (s_k > INT_MAX - 4096) return fail(FMHA_ERR_SHAPE, "s_k=%d is too long", s_k);
+    Kv4Fwd& f = *out;
+    f = Kv4Fwd{};
+    f.batch = batch;
+    f.n_h = n_h;
+    f.n_kv_h = n_kv_h;
+    f.T = T;
+    f.s_k = s_k;
+    f.cap = cap;
+    f.hd = hd;
+    f.scale = scale;
+    f.window = window >= s_k ? 0 : window;
+    f.n_first = f.window > 0 ? std::min(n_first, s_k) : 0;
+    f.causal = causal;
+    return FMHA_OK;
+}
+
+// Chunks of the virtual key axis (first keys rounded up to tiles, then the
+// window) for sequences of s_k keys: the smallest number of chunks whose
+// estimated time is least.  A block's time is its share of its SM's HBM rate
+// (42 KB/us per SM, spread over the resident blocks) plus ~1.5 us of latency;
+// splitting adds the merge.
+void plan_kv4(Kv4Fwd* f) {
+    const int tile = kv4_kv_tile(f->hd), unit = 4 * tile;
+    const long long R = (long long)f->n_h / f->n_kv_h * f->T;
+    const int rows = kv4_rows_per_cta(f->hd, R), per_sm = kv4_ctas_per_sm(f->hd, rows);
+    // The longest axis that any length up to s_k gives: its body holds at most
+    // window + T - 1 keys and starts up to 15 keys early.
+    long long span = f->s_k;
+    if (f->window > 0)
+        span = (f->n_first + tile - 1) / tile * tile + std::min<long long>(f->s_k, (long long)f->window + f->T - 1 + 15);
+    if (span < 1) span = 1;
+    if (f->kv_chunk <= 0) {
+        const long long units = (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows);
+        const long long slots = (long long)sm_count() * per_sm;
+        const double key_bytes = f->hd * 2 * 0.5625;
+        double best = 0;
+        long long best_n = 1;
+        const long long max_n = std::min<long long>(256, (span + unit - 1) / unit);
+        for (long long n = 1; n <= max_n; ++n) {
+            const long long keys = ((span + n - 1) / n + unit - 1) / unit * unit;
+            const long long waves = (units * n + slots - 1) / slots;
+            double us = (double)waves * (1.5 + (double)keys * key_bytes * per_sm / 42e3);
+            if (n > 1) us += 2.0 + (double)R * f->batch * f->n_kv_h * f->hd * 4.0 * (double)n / 8e6;
+            if (n == 1 || us < best * 0.98) {
+                best = us;
+                best_n = n;
+            }
+        }
+        f->kv_chunk = (int)std::min<long long>(((span + best_n - 1) / best_n + unit - 1) / unit * unit, INT_MAX / 2 / unit * unit);
+    } else {
+        f->kv_chunk = (int)std::min<long long>(((long long)f->kv_chunk + tile - 1) / tile * tile, INT_MAX / 2 / tile * tile);
+    }
+    f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
+}
+
+}  // namespace
+
+extern "C" int fmha_qk_norm_rope(const void* qkv, long long batch_stride, long long token_stride, const float* q_weight,
+                                 const float* k_weight, float eps, const float* cos_sin, const int* positions, int max_pos,
+                                 int rot, int interleaved, void* q, void* k, void* v, const int* kv_start, int kv_rows,
+                                 int batch, int T, int n_h, int n_kv_h, int hd, fmha_stream_t stream) try {
+    if (!head_dim_ok(hd)) return fail(FMHA_ERR_HEADDIM, "hd=%d: supported head dims are 64, 128, 256, 512", hd);
+    if (n_h < 1 || n_kv_h < 1 || n_h % n_kv_h != 0 || n_h > (1 << 20))
+        return fail(FMHA_ERR_HEADS, "n_h=%d n_kv_h=%d: need n_h, n_kv_h >= 1, n_h %% n_kv_h == 0 and n_h <= 2^20", n_h, n_kv_h);
+    if (batch < 0 || T < 0 || kv_rows < 0)
+        return fail(FMHA_ERR_SHAPE, "negative size (batch=%d T=%d kv_rows=%d)", batch, T, kv_rows);
+    if (rot < 0 || rot > hd || rot % 8 != 0) return fail(FMHA_ERR_SHAPE, "rot=%d must be a multiple of 8 in [0, hd]", rot);
+    if (rot > 0 && max_pos < 1) return fail(FMHA_ERR_SHAPE, "max_pos=%d must be >= 1", max_pos);
+    if (interleaved != 0 && interleaved != 1) return fail(FMHA_ERR_SHAPE, "interleaved must be 0 or 1 (got %d)", interleaved);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(FMHA_ERR_SHAPE, "eps must be finite and >= 0");
+    const long long width = ((long long)n_h + 2LL * n_kv_h) * hd;
+    if (token_stride < width || token_stride % 8 != 0 || batch_stride < 0 || batch_stride % 8 != 0)
+        return fail(FMHA_ERR_SHAPE, "strides must be multiples of 8 elements, token_stride at least %lld", width);
+    if ((long long)batch * T > INT_MAX) return fail(FMHA_ERR_SHAPE, "batch * T exceeds 2^31 - 1");
+    if ((long long)batch * T * ((long long)n_h + 2LL * n_kv_h) > (long long)INT_MAX * 4)
+        return fail(FMHA_ERR_SHAPE, "too many head rows");
+    if (batch == 0 || T == 0) return FMHA_OK;
+    if (!qkv || !q || !k || !v || (rot > 0 && (!cos_sin || !positions)))
+        return fail(FMHA_ERR_NULL, "qkv, q, k, v (and cos_sin and positions with rot > 0) must be non-NULL");
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cos_sin, 16) ||
+        !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4) || !aligned(kv_start, 4))
+        return fail(FMHA_ERR_ALIGN, "tensors, weights and cos_sin must be 16-byte, positions and kv_start 4-byte aligned");
+    QkNormRope a = {};
+    a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+    a.batch_stride = batch_stride;
+    a.token_stride = token_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.max_pos = max_pos;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.q = static_cast<__nv_bfloat16*>(q);
+    a.k = static_cast<__nv_bfloat16*>(k);
+    a.v = static_cast<__nv_bfloat16*>(v);
+    a.kv_start = kv_start;
+    a.kv_rows = kv_rows;
+    a.batch = batch;
+    a.T = T;
+    a.n_h = n_h;
+    a.n_kv_h = n_kv_h;
+    a.status = device_status_word();
+    if (!a.status) return fail(FMHA_ERR_LAUNCH, "cannot resolve the device status word");
+    cudaError_t e = launch_qk_norm_rope(a, hd, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm-and-rotation kernel launch");
+    return FMHA_OK;
+} catch (...) {
+    return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_qk_norm_rope");
+}
+
+extern "C" int fmha_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                               const int* start, float k_global, float v_global, void* k_out, void* v_out, int batch,
+                               int n_kv_h, int T, int cap, int hd, fmha_stream_t stream) try {
+    if (!head_dim_ok(hd)) return fail(FMHA_ERR_HEADDIM, "hd=%d: supported head dims are 64, 128, 256, 512", hd);
+    if (n_kv_h < 1) return fail(FMHA_ERR_HEADS, "n_kv_h=%d must be >= 1", n_kv_h);
+    if (batch < 0 || T < 0) return fail(FMHA_ERR_SHAPE, "negative size (batch=%d T=%d)", batch, T);
+    if (cap < 0 || cap % 16 != 0) return fail(FMHA_ERR_SHAPE, "cap=%d must be a multiple of 16", cap);
+    if (!(k_global > 0.f) || !std::isfinite(k_global) || !(v_global > 0.f) || !std::isfinite(v_global))
+        return fail(FMHA_ERR_SHAPE, "k_global and v_global must be finite and > 0");
+    if ((long long)batch * n_kv_h > INT_MAX || (long long)batch * n_kv_h * T > (1LL << 36) / hd)
+        return fail(FMHA_ERR_SHAPE, "too many rows");
+    if (batch == 0 || T == 0 || cap == 0) return FMHA_OK;
+    if (!k || !v || !k_codes || !k_scales || !v_codes || !v_scales || !start)
+        return fail(FMHA_ERR_NULL, "fmha_kv4_append: NULL buffer");
+    if ((k_out == nullptr) != (v_out == nullptr)) return fail(FMHA_ERR_NULL, "k_out and v_out are given together or not at all");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scales, 16) ||
+        !aligned(v_scales, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start, 4))
+        return fail(FMHA_ERR_ALIGN, "rows, codes and scales must be 16-byte, start 4-byte aligned");
+    Kv4Append a = {};
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.k_codes = static_cast<uint8_t*>(k_codes);
+    a.k_scales = static_cast<uint8_t*>(k_scales);
+    a.v_codes = static_cast<uint8_t*>(v_codes);
+    a.v_scales = static_cast<uint8_t*>(v_scales);
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.v_out = static_cast<__nv_bfloat16*>(v_out);
+    a.start = start;
+    a.k_global = k_global;
+    a.v_global = v_global;
+    a.batch = batch;
+    a.n_kv_h = n_kv_h;
+    a.T = T;
+    a.cap = cap;
+    a.status = device_status_word();
+    if (!a.status) return fail(FMHA_ERR_LAUNCH, "cannot resolve the device status word");
+    cudaError_t e = launch_kv4_append(a, hd, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit append kernel launch");
+    return FMHA_OK;
+} catch (...) {
+    return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_kv4_append");
+}
+
+extern "C" int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, int window, int n_first, int causal,
+                                 int* kv_chunk) try {
+    Kv4Fwd f;
+    const int cap = s_k > 0 && s_k < INT_MAX - 16 ? (s_k + 15) / 16 * 16 : s_k;
+    const int rc = check_kv4(batch, n_h, n_kv_h, T, s_k, cap, hd, 1.f, window, n_first, causal, &f);
+    if (rc) return rc;
+    if (kv_chunk && *kv_chunk < 0) return fail(FMHA_ERR_SHAPE, "kv_chunk=%d must be >= 0", *kv_chunk);
+    if (kv_chunk) f.kv_chunk = *kv_chunk;
+    plan_kv4(&f);
+    if (kv_chunk) *kv_chunk = f.kv_chunk;
+    return f.n_splits;
+} catch (...) {
+    return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_kv4_plan");
+}
+
+extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                            const void* v_scales, const int* seq_lens, void* o, float* lse, const float* sink, float k_global,
+                            float v_global, int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, float scale,
+                            int window, int n_first, int causal, int kv_chunk, void* workspace, size_t workspace_bytes,
+                            fmha_stream_t stream) try {
+    Kv4Fwd f;
+    const int rc = check_kv4(batch, n_h, n_kv_h, T, s_k, cap, hd, scale, window, n_first, causal, &f);
+    if (rc) return rc;
+    if (!(k_global > 0.f) || !std::isfinite(k_global) || !(v_global > 0.f) || !std::isfinite(v_global))
+        return fail(FMHA_ERR_SHAPE, "k_global and v_global must be finite and > 0");
+    const long long rows = (long long)batch * n_h * T;
+    if (rows == 0) return FMHA_OK;
+    if (!q || !o || !lse || (s_k > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)))
+        return fail(FMHA_ERR_NULL, "q, the cache, o and lse must be non-NULL");
+    if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(k_scales, 16) || !aligned(v_codes, 16) || !aligned(v_scales, 16) ||
+        !aligned(o, 16) || !aligned(lse, 4) || !aligned(seq_lens, 4) || !aligned(sink, 4))
+        return fail(FMHA_ERR_ALIGN, "q, codes, scales and o must be 16-byte, lse, seq_lens and sink 4-byte aligned");
+    f.q = static_cast<const __nv_bfloat16*>(q);
+    f.k_codes = static_cast<const uint8_t*>(k_codes);
+    f.k_scales = static_cast<const uint8_t*>(k_scales);
+    f.v_codes = static_cast<const uint8_t*>(v_codes);
+    f.v_scales = static_cast<const uint8_t*>(v_scales);
+    f.seq_lens = seq_lens;
+    f.sink = sink;
+    f.o = static_cast<__nv_bfloat16*>(o);
+    f.lse = lse;
+    f.k_global = k_global;
+    f.v_global = v_global;
+    if (kv_chunk < 0) return fail(FMHA_ERR_SHAPE, "kv_chunk=%d must be >= 0", kv_chunk);
+    f.kv_chunk = kv_chunk;
+    plan_kv4(&f);
+    if (f.n_splits > 65535) return fail(FMHA_ERR_SHAPE, "too many KV chunks (%d)", f.n_splits);
+    if (f.n_splits > 1) {
+        const size_t need = partial_bytes(rows, hd, f.n_splits);
+        if (!workspace || workspace_bytes < need)
+            return fail(FMHA_ERR_WORKSPACE, "fmha_fwd_kv4: %zu bytes of workspace needed for %d chunks, %zu given", need,
+                        f.n_splits, workspace ? workspace_bytes : (size_t)0);
+        if (!aligned(workspace, 16)) return fail(FMHA_ERR_ALIGN, "workspace must be 16-byte aligned");
+        const PartialViews pv = partial_views(workspace, rows, hd, f.n_splits, false);
+        f.o_part = static_cast<float*>(pv.o_part);
+        f.lse_part = pv.lse_part;
+    }
+    f.status = device_status_word();
+    if (!f.status) return fail(FMHA_ERR_LAUNCH, "cannot resolve the device status word");
+    cudaError_t e = launch_kv4_fwd(f, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit attention kernel launch");
+    if (f.n_splits > 1) {
+        e = launch_merge(f.o_part, f.lse_part, nullptr, f.n_splits, rows, hd, false, o, lse, stream, sink, T, n_h);
+        if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
+    }
+    return FMHA_OK;
+} catch (...) {
+    return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_kv4");
 }

@@ -2,6 +2,7 @@
 // translation units.  Not part of the public ABI.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -118,6 +119,55 @@ cudaError_t launch_merge_nvfp4(const void* o_parts, const float* lse_parts, cons
 // ---- NVFP4 quantisation of fp32 rows on its own (nvfp4_kernel.cu) ---------
 cudaError_t launch_quantize_nvfp4(const float* x, long long rows, int hd, float g, uint8_t* codes, uint8_t* scales,
                                   cudaStream_t stream);
+
+// ---- norm, rotation and relayout of a QKV projection (qk_norm_rope_kernel.cu)
+struct QkNormRope {
+    const __nv_bfloat16* qkv;  // rows of (n_h + 2 n_kv_h) * hd, q heads, k heads, v heads
+    long long batch_stride, token_stride;  // elements
+    const float *q_weight, *k_weight;      // [hd] or NULL (no norm)
+    const float* cos_sin;                  // [max_pos, rot]
+    const int* positions;                  // [batch, T]
+    __nv_bfloat16 *q, *k, *v;
+    const int* kv_start;  // [batch] first row of k and v, or NULL (0)
+    float eps;
+    int max_pos, rot, interleaved, kv_rows, batch, T, n_h, n_kv_h;
+    unsigned* status;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRope& a, int hd, cudaStream_t stream);
+
+// ---- 4-bit KV cache: append (kv4_append_kernel.cu), attention (kv4_kernel.cu)
+struct Kv4Append {
+    const __nv_bfloat16 *k, *v;  // [batch, n_kv_h, T, hd]
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    __nv_bfloat16 *k_out, *v_out;  // the quantised values, or NULL
+    const int* start;              // [batch] cache row of t = 0
+    float k_global, v_global;
+    int batch, n_kv_h, T, cap;
+    unsigned* status;
+};
+cudaError_t launch_kv4_append(const Kv4Append& a, int hd, cudaStream_t stream);
+
+struct Kv4Fwd {
+    const __nv_bfloat16* q;
+    const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    const int* seq_lens;  // [batch] or NULL (s_k each)
+    const float* sink;    // [n_h] or NULL
+    __nv_bfloat16* o;
+    float* lse;
+    float *o_part, *lse_part;  // n_splits > 1
+    float k_global, v_global, scale;
+    int batch, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, causal;
+    int kv_chunk, n_splits;  // keys per chunk (a multiple of kv4_kv_tile(hd)) and their number
+    unsigned* status;
+};
+int kv4_kv_tile(int hd);                       // keys per tile
+int kv4_rows_per_cta(int hd, long long rows);  // query rows per thread block, given the rows per KV head
+int kv4_ctas_per_sm(int hd, int rows_per_cta);
+cudaError_t launch_kv4_fwd(const Kv4Fwd& a, cudaStream_t stream);
+
+// ---- host-side errors (api.cu): set the calling thread's message, return code
+int fail(int code, const char* fmt, ...);
+int cuda_fail(cudaError_t e, const char* what);
 
 // ---- device status word (status.cu) ---------------------------------------
 // Address of the status word on the current device (nullptr on failure).

@@ -44,7 +44,8 @@ constexpr bool kCheckedBuild = false;
 
 // Site codes: 0x1nn row-tile kernel, 0x2nn hd-512 kernel, 0x3nn decode
 // kernel, 0x4nn merge, 0x5nn shared epilogue / softmax helpers, 0x7nn
-// two-row-tile kernel.
+// two-row-tile kernel, 0x8nn norm-and-rotation, 4-bit cache append, 4-bit
+// cache attention.
 enum CheckSite : unsigned {
     kSiteTcQLoad = 0x101,   // Q box coordinates
     kSiteTcKLoad = 0x102,   // K tile: first key, stage offset
@@ -90,6 +91,12 @@ enum CheckSite : unsigned {
     kSitePairVDesc = 0x705,  // V stage the PV MMAs read
     kSitePairLse = 0x706,    // LSE / partial LSE index
     kSitePairFp4 = 0x707,    // NVFP4 output row
+    kSiteNrCol = 0x801,      // norm-and-rotation kernel: column of a stored vector
+    kSiteKv4Append = 0x802,  // 4-bit append kernel: cache block index
+    kSiteKv4Copy = 0x803,    // 4-bit attention: keys of a bulk copy
+    kSiteKv4Key = 0x804,     // 4-bit attention: shared-memory offset of a key row
+    kSiteKv4Comb = 0x805,    // 4-bit attention: combine buffer index
+    kSiteKv4Out = 0x806,     // 4-bit attention: output / partial row
 };
 
 static __device__ __noinline__ bool bounds_failed(unsigned site, unsigned* status) {
@@ -197,6 +204,17 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const void* tma
         : "memory");
 }
 
+// Untiled bulk copy of `bytes` (a multiple of 16, both addresses 16-byte
+// aligned) into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void bulk_load_hint(uint32_t smem_dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                               uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // TMA store of one box from shared memory (bulk-group completion).  Elements
 // outside the tensor are not written.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int c0, int c1, int c2, const void* smem_src) {
@@ -262,6 +280,45 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with fp16 inputs.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four bytes of E2M1 code pairs -> four fp16 pairs (low nibble in the low half); exact.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+
+// Two E4M3 bytes (low 16 bits) -> an fp16 pair; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+        : "=r"(r)
+        : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // Packed fp32 pairs (sm_100 and later): two lanes of fp32 arithmetic in one

@@ -32,6 +32,12 @@ static_assert(kStatusBitTimeout == kStatusBarrierTimeout && kStatusBitBounds == 
 
 const char* check_site_name(unsigned site) {
     switch (site) {
+        case kSiteNrCol: return "norm-and-rotation kernel: column of a stored vector";
+        case kSiteKv4Append: return "4-bit append kernel: cache block";
+        case kSiteKv4Copy: return "4-bit attention: keys of a bulk copy";
+        case kSiteKv4Key: return "4-bit attention: shared-memory offset of a key row";
+        case kSiteKv4Comb: return "4-bit attention: combine buffer";
+        case kSiteKv4Out: return "4-bit attention: output row";
         case kSiteTcQLoad: return "row-tile kernel: Q box coordinates";
         case kSiteTcKLoad: return "row-tile kernel: K tile key / stage";
         case kSiteTcVLoad: return "row-tile kernel: V tile key / stage";

@@ -374,6 +374,91 @@ int fmha_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float
                      int batch, int n_h, int n_kv_h, int T, int s_k, int hd,
                      float scale, int window, int causal, fmha_stream_t stream);
 
+/*
+ * Serving operators around the forward (no counterpart on the pages the method
+ * comes from).  All of them are stream-ordered, allocate nothing and keep
+ * nothing between calls; a NULL-able argument says so.  Tensors are contiguous
+ * device memory; 16-byte alignment unless said otherwise.
+ */
+
+/*
+ * fmha_qk_norm_rope -- the rows of a QKV projection to what the forward takes.
+ *
+ * qkv: [batch, T] rows of (n_h + 2 n_kv_h) * hd bf16 elements (the query
+ *   heads, the key heads, the value heads), row (b, t) at element
+ *   b * batch_stride + t * token_stride; both strides multiples of 8.
+ * q_weight, k_weight: [hd] fp32.  With a weight each head row x of that kind
+ *   becomes x * rsqrt(mean(x^2) + eps) * weight; NULL leaves it as it is.
+ * cos_sin: [max_pos, rot] fp32, row p the rot / 2 cosines and then the rot / 2
+ *   sines of position p's angles.  Pair i of a query or key row is columns (i,
+ *   rot / 2 + i), or (2 i, 2 i + 1) when interleaved is 1, and becomes
+ *   (lo cos_i - hi sin_i, hi cos_i + lo sin_i); columns from rot on stay.  rot is
+ *   a multiple of 8 up to hd; 0 is no rotation (cos_sin and positions NULL).
+ * positions: [batch, T] int32.  A token whose position is outside
+ *   [0, max_pos) is padding: none of its outputs is written.
+ * q: [batch, n_h, T, hd]; k, v: [batch, n_kv_h, kv_rows, hd], the token's row at
+ *   kv_start[b] + t (kv_start NULL: 0); a row outside [0, kv_rows) is not
+ *   written.  Norm and rotation are computed in fp32 and rounded to bf16 once;
+ *   V is copied bit for bit.  Outputs may not overlap qkv.
+ */
+int fmha_qk_norm_rope(const void* qkv, long long batch_stride, long long token_stride,
+                      const float* q_weight, const float* k_weight, float eps,
+                      const float* cos_sin, const int* positions, int max_pos, int rot, int interleaved,
+                      void* q, void* k, void* v, const int* kv_start, int kv_rows,
+                      int batch, int T, int n_h, int n_kv_h, int hd, fmha_stream_t stream);
+
+/*
+ * A KV cache held in 4 bits, in the NVFP4 format of fmha_fwd_nvfp4:
+ *   codes  [batch, n_kv_h, cap, hd / 2] bytes, scales [batch, n_kv_h, cap, hd / 16]
+ * for K and for V, each with a global scale (k_global, v_global; finite, > 0).
+ * cap, the rows per sequence and head, is a multiple of 16.
+ *
+ * fmha_kv4_append quantises k and v [batch, n_kv_h, T, hd] bf16 as
+ * fmha_quantize_nvfp4 does (on the bf16 values widened to fp32) and writes row
+ * t of sequence b to cache row start[b] + t (start: [batch] int32); a row
+ * outside [0, cap) is left out.  k_out and v_out, both or neither:
+ * [batch, n_kv_h, T, hd] bf16, the values that the written rows stand for
+ * (global * scale * code, rounded to bf16; rows left out of the cache are left
+ * unwritten here too).
+ */
+int fmha_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                    const int* start, float k_global, float v_global, void* k_out, void* v_out,
+                    int batch, int n_kv_h, int T, int cap, int hd, fmha_stream_t stream);
+
+/*
+ * The plan of fmha_fwd_kv4: returns the number of KV chunks for sequences of up
+ * to s_k keys.  *kv_chunk (may be NULL) holds the chunk length asked for, in
+ * keys, 0 for the library's choice, and receives the one used (a multiple of
+ * the kernel's key tile).
+ */
+int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, int window, int n_first, int causal,
+                      int* kv_chunk);
+
+/*
+ * The forward over a 4-bit cache: O (bf16) and LSE (fp32) as fmha_fwd_sink, with
+ * K and V the values that the cache stands for.
+ *
+ * seq_lens: [batch] int32, the keys of each sequence (clamped to [0, s_k]), or
+ *   NULL: s_k each.  s_k <= cap bounds them on the host and shapes the launch.
+ *   Rows of the cache from a sequence's length on are not read into any result.
+ * Query row t of a sequence with len keys sits at position len - T + t; with
+ *   causal, a row at a negative position attends nothing (O = 0, LSE = -inf, or
+ *   the sink's).
+ * n_first: with a window, the keys j < n_first stay attended as well (still
+ *   subject to causal).
+ * sink: [n_h] fp32 logits or NULL.
+ * kv_chunk: keys per split-KV chunk, 0 for the library's choice.
+ * workspace: fmha_workspace_bytes(batch, n_h, T, hd, n_splits) bytes for the
+ *   partials when fmha_fwd_kv4_plan (same arguments, same kv_chunk) returns
+ *   n_splits > 1, else unused; FMHA_ERR_WORKSPACE if it is smaller.  Two calls
+ *   that may run at the same time need two workspaces.
+ */
+int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                 const int* seq_lens, void* o, float* lse, const float* sink, float k_global, float v_global,
+                 int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, float scale,
+                 int window, int n_first, int causal, int kv_chunk, void* workspace, size_t workspace_bytes,
+                 fmha_stream_t stream);
+
 /* ABI version: major * 10000 + minor * 100 + patch. */
 int fmha_version(void);
 

@@ -1,0 +1,82 @@
+"""Refusals of the serving operators, without a GPU: the C entry points' argument
+checks (nothing is launched on an error), the 4-bit plan, and the binding's own checks."""
+import pytest
+import torch
+
+from head_attention_forward_fmha_gb300 import binding, build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.load()
+
+
+P = 4096  # an aligned address that is never read: every call below is refused
+
+NORM = dict(qkv=P, bs=0, ts=1280, qw=None, kw=None, eps=1e-6, cs=P, pos=P, max_pos=64, rot=128, inter=0, q=P, k=P, v=P, start=None,
+            rows=1, b=1, T=1, n_h=8, n_kv=1, hd=128, stream=None)
+APPEND = dict(k=P, v=P, kc=P, ks=P, vc=P, vs=P, start=P, kg=1.0, vg=1.0, ko=None, vo=None, b=1, n_kv=1, T=1, cap=64, hd=128, stream=None)
+KV4 = dict(q=P, kc=P, ks=P, vc=P, vs=P, lens=None, o=P, lse=P, sink=None, kg=1.0, vg=1.0, b=1, n_h=8, n_kv=1, T=1, s_k=64, cap=64,
+           hd=128, scale=0.1, window=0, n_first=0, causal=0, chunk=0, ws=None, wsb=0, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(hd=96), -3), (dict(n_h=3, n_kv=2), -4), (dict(n_kv=0), -4), (dict(b=-1), -5), (dict(T=-1), -5), (dict(rows=-1), -5),
+    (dict(rot=4), -5), (dict(rot=136), -5), (dict(rot=-8), -5), (dict(max_pos=0), -5), (dict(inter=2), -5), (dict(eps=-1.0), -5),
+    (dict(eps=float("nan")), -5), (dict(ts=1272), -5), (dict(ts=1284), -5), (dict(bs=4), -5), (dict(bs=-8), -5), (dict(qkv=None), -1),
+    (dict(cs=None), -1), (dict(pos=None), -1), (dict(q=None), -1), (dict(v=None), -1), (dict(qkv=P + 8), -2), (dict(k=P + 2), -2),
+    (dict(qw=P + 4), -2), (dict(start=P + 1), -2), (dict(b=0), 0), (dict(T=0), 0),
+])
+def test_norm_rope_refusals(lib, change, code):
+    assert lib.fmha_qk_norm_rope(*{**NORM, **change}.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(hd=32), -3), (dict(n_kv=0), -4), (dict(b=-1), -5), (dict(cap=40), -5), (dict(cap=-16), -5), (dict(kg=0.0), -5),
+    (dict(vg=float("inf")), -5), (dict(k=None), -1), (dict(start=None), -1), (dict(ko=P), -1), (dict(vc=P + 8), -2), (dict(k=P + 8), -2),
+    (dict(b=0), 0), (dict(T=0), 0), (dict(cap=0), 0), (dict(b=1 << 20, n_kv=1 << 8, T=1 << 12), -5),
+])
+def test_append_refusals(lib, change, code):
+    assert lib.fmha_kv4_append(*{**APPEND, **change}.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(hd=80), -3), (dict(n_h=6, n_kv=4), -4), (dict(T=-1), -5), (dict(s_k=-1), -5), (dict(s_k=65), -5), (dict(cap=72), -5),
+    (dict(window=-1), -5), (dict(n_first=-1), -5), (dict(causal=2), -5), (dict(scale=float("nan")), -5), (dict(kg=-1.0), -5),
+    (dict(chunk=-1), -5), (dict(b=70000), -5), (dict(q=None), -1), (dict(vs=None), -1), (dict(lse=None), -1), (dict(q=P + 4), -2),
+    (dict(kc=P + 8), -2), (dict(lens=P + 2), -2), (dict(T=0), 0), (dict(b=0), 0),
+    (dict(s_k=1024, cap=1024, chunk=256), -6), (dict(s_k=1024, cap=1024, chunk=256, ws=P, wsb=16), -6),
+    (dict(s_k=1024, cap=1024, chunk=256, ws=P + 8, wsb=1 << 20), -2),
+])
+def test_kv4_refusals(lib, change, code):
+    assert lib.fmha_fwd_kv4(*{**KV4, **change}.values()) == code
+    if code < 0:
+        assert binding.fmha_get_last_error()
+
+
+def test_kv4_plan():
+    n, chunk = binding.fmha_fwd_kv4_plan(1, 64, 8, 1, 8192, 128)
+    assert n > 1 and chunk % 32 == 0 and n * chunk >= 8192
+    assert binding.fmha_fwd_kv4_plan(1, 64, 8, 1, 8192, 128, kv_chunk=1000) == (8, 1024)
+    # a window shorter than the sequence: the first keys' tile and the window's keys
+    assert binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 8192, 128, window=512, n_first=4, kv_chunk=32) == (18, 32)
+    assert binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 0, 128)[0] == 1
+    with pytest.raises(binding.FmhaError):
+        binding.fmha_fwd_kv4_plan(1, 8, 3, 1, 64, 128)
+
+
+def test_binding_refusals():
+    bf = torch.zeros(1, 8, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):  # host tensors
+        binding.fmha_qk_norm_rope(torch.zeros(1, 1, 1280, dtype=torch.bfloat16), None, None, 8, 1)
+    cache = binding.fmha_kv4_cache(1, 1, 64, 128, device="cpu")
+    assert [tuple(t.shape) for t in cache] == [(1, 1, 64, 64), (1, 1, 64, 8)] * 2
+    with pytest.raises(TypeError):
+        binding.fmha_fwd_kv4(bf, *cache, s_k=64)
+    with pytest.raises(TypeError):
+        binding.fmha_kv4_append(bf[:, :1], bf[:, :1], *cache, torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        binding.fmha_fwd_kv4(bf[0], *cache)
+    with pytest.raises(ValueError):
+        binding.fmha_kv4_cache(1, 1, 40, 128, device="cpu")
