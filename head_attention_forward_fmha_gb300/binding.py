@@ -61,6 +61,9 @@ SIGNATURES = {
     "fmha_fwd_kv4_plan": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)], _i32),
     "fmha_fwd_kv4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                       _f32, _i32, _i32, _i32, _i32, _vp, _sz, _vp], _i32),
+    "fmha_fwd_first_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "fmha_fwd_first": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp, _sz,
+                        _vp], _i32),
 }
 # Size of the fixed split-KV scratch fmha_fwd_noalloc uses (FMHA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -403,6 +406,7 @@ def fmha_set_kernel_path(path):
     P V in the SS form (P through shared memory) instead of the TS form, 4 tensor-core kernels,
     one row tile per block (TS form)."""
     _check(load().fmha_set_kernel_path(int(path)), "fmha_set_kernel_path")
+    _first_plans.clear()
 
 
 def fmha_fwd_noalloc(q, k, v, o, lse, scale=None, window=0, causal=False, stream=None):
@@ -584,4 +588,43 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
           _ptr(lse, "lse", torch.float32, (b, n_h, T), dev), _ptr(sink, "sink", torch.float32, (n_h,), dev, True),
           k_global, v_global, b, n_h, n_kv_h, T, s_k, cap, hd, scale, int(window), int(n_first), int(bool(causal)), int(kv_chunk),
           ws, ws_bytes)
+    return o, lse
+
+
+_first_plans = {}  # workspace bytes by shape, for the kernel path that is set
+
+
+def fmha_fwd_first_workspace_bytes(batch, n_h, n_kv_h, T, s_k, hd, window, n_first, causal=False):
+    """Workspace bytes that fmha_fwd_first needs for this shape (0: none)."""
+    return int((_lib or load()).fmha_fwd_first_workspace_bytes(batch, n_h, n_kv_h, T, s_k, hd, int(window), int(n_first),
+                                                               int(bool(causal))))
+
+
+def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, causal=False, sink=None, workspace=None,
+                   stream=None):
+    """fmha_fwd with the keys j < n_first attended outside the window too (fmha_fwd_first in include/fmha.h).
+    workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call takes its own from torch."""
+    b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
+    dev = q.device
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=dev)
+    if scale is None:
+        scale = hd ** -0.5
+    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal)
+    need = _first_plans.get(key)
+    if need is None:
+        need = _first_plans[key] = fmha_fwd_first_workspace_bytes(*key)
+    if need and workspace is None:
+        workspace = _scratch(need, dev, stream)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    bf = torch.bfloat16
+    _call("fmha_fwd_first", dev, stream, _ptr(q, "q", bf, q.shape, dev), _ptr(k, "k", bf, k.shape, dev),
+          _ptr(v, "v", bf, k.shape, dev), _ptr(o, "o", bf, q.shape, dev), _ptr(lse, "lse", torch.float32, (b, n_h, T), dev),
+          _ptr(sink, "sink", torch.float32, (n_h,), dev, True), b, n_h, n_kv_h, T, s_k, hd, scale, int(window), int(n_first),
+          int(bool(causal)), ws, ws_bytes)
     return o, lse

@@ -63,12 +63,13 @@ bool tensor_map_encoder() {
 
 // K or V [slabs, s_k, hd] bf16 viewed as a 3-D tensor (hd fastest); boxes of
 // 64 head-dim columns (128 bytes, 128-byte swizzle) x box_rows keys x 1 slab.
-int make_kv_map(CUtensorMap* m, const void* base, int hd, int s_k, long long slabs, int box_rows) {
+// slab_rows: rows from one slab to the next, when the map covers only the first s_k of them.
+int make_kv_map(CUtensorMap* m, const void* base, int hd, int s_k, long long slabs, int box_rows, int slab_rows = 0) {
     std::memset(m, 0, sizeof *m);
     if (s_k == 0) return FMHA_OK;  // nothing will be loaded
     if (!tensor_map_encoder()) return fail(FMHA_ERR_LAUNCH, "cuTensorMapEncodeTiled is unavailable");
     cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)s_k, (cuuint64_t)slabs};
-    cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)s_k * hd * 2};
+    cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)(slab_rows ? slab_rows : s_k) * hd * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     cuuint32_t elem[3] = {1, 1, 1};
     CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
@@ -258,7 +259,15 @@ TcChoice tc_best_split(const Problem& p, Path path, long long span) {
     return best;
 }
 
-long long kv_span(const Problem& p) {
+// First key of the window part next to first keys: the first key of row 0's
+// window, or the one behind the first keys.
+long long first_begin(const Problem& p) {
+    return std::max<long long>(p.n_first, std::max<long long>(0, (long long)p.s_k - p.T - p.window + 1));
+}
+
+// Keys of the chunks' axis; with first keys for a kernel of `tile` keys per tile.
+long long kv_span(const Problem& p, int tile) {
+    if (p.n_first > 0) return ((long long)p.n_first + tile - 1) / tile * tile + std::max(0LL, p.s_k - first_begin(p));
     const SplitPlan whole = split_layout(p.T, p.s_k, p.window, p.s_k > 0 ? p.s_k : 1);
     return (long long)p.s_k - whole.kv_begin;
 }
@@ -272,7 +281,7 @@ Path choose_path(const Problem& p) {
     const bool pair_ok = tc_pair_supports(p.hd) && p.R > kTcRows;
     if (!pair_ok || ov == 3 || ov == 4) return Path::TensorCore;
     if (ov == 2) return Path::TensorCorePair;
-    const long long span = kv_span(p);
+    const long long span = kv_span(p, tc_pair_kv_tile());  // both kernels have tiles of 128 keys at hd <= 128
     return tc_best_split(p, Path::TensorCorePair, span).us < tc_best_split(p, Path::TensorCore, span).us
                ? Path::TensorCorePair
                : Path::TensorCore;
@@ -290,8 +299,17 @@ SplitPlan choose_split(const Problem& p) {
     const KernelShape ks = kernel_shape(p, path);
     const long long units = (long long)p.batch * p.n_kv_h * ((p.R + ks.rows_per_cta - 1) / ks.rows_per_cta) *
                             ks.blocks_per_row_tile;
-    SplitPlan whole = split_layout(p.T, p.s_k, p.window, p.s_k > 0 ? p.s_k : 1);
-    const long long span = (long long)p.s_k - whole.kv_begin;
+    const long long span = kv_span(p, ks.kv_tile);
+    auto layout = [&](long long chunk) {
+        if (p.n_first == 0) return split_layout(p.T, p.s_k, p.window, (int)chunk);
+        SplitPlan sp;
+        sp.kv_begin = (int)first_begin(p);
+        sp.kv_chunk = (int)chunk;
+        sp.first_span = (p.n_first + ks.kv_tile - 1) / ks.kv_tile * ks.kv_tile;
+        sp.n_splits = (int)((span + chunk - 1) / chunk);
+        return sp;
+    };
+    const SplitPlan whole = layout(p.n_first > 0 ? (span + ks.kv_tile - 1) / ks.kv_tile * ks.kv_tile : p.s_k > 0 ? p.s_k : 1);
     if (units <= 0 || span <= ks.min_chunk) return whole;
     long long n = 1;
     if (path != Path::Decode) {
@@ -306,7 +324,7 @@ SplitPlan choose_split(const Problem& p) {
     if (n <= 1) return whole;
     long long chunk = (span + n - 1) / n;
     chunk = (chunk + ks.kv_tile - 1) / ks.kv_tile * ks.kv_tile;
-    return split_layout(p.T, p.s_k, p.window, (int)chunk);
+    return layout(chunk);
 }
 
 // ---------------------------------------------------------------- workspace
@@ -441,6 +459,10 @@ int run_kernel(const void* q, const void* k, const void* v, const Problem& p, co
         if (rc) return rc;
         rc = make_kv_map(&L.tmap_v, v, p.hd, p.s_k, slabs, ks.kv_tile);
         if (rc) return rc;
+        if (p.n_first > 0) {
+            rc = make_kv_map(&L.tmap_v_first, v, p.hd, p.n_first, slabs, ks.kv_tile, p.s_k);
+            if (rc) return rc;
+        }
         // The two-row-tile kernel has no NVFP4 epilogue (its O is transposed in
         // tensor memory): an NVFP4 output takes the one-row-tile kernel, with
         // the same KV tiles and chunks.
@@ -468,6 +490,10 @@ int run_kernel(const void* q, const void* k, const void* v, const Problem& p, co
     if (rc) return rc;
     rc = make_kv_map(&L.tmap_v, v, p.hd, p.s_k, slabs, ks.kv_tile);
     if (rc) return rc;
+    if (p.n_first > 0) {
+        rc = make_kv_map(&L.tmap_v_first, v, p.hd, p.n_first, slabs, ks.kv_tile, p.s_k);
+        if (rc) return rc;
+    }
     cudaError_t e = launch_decode(L, stream);
     if (e != cudaSuccess) return cuda_fail(e, "decode kernel launch");
     return FMHA_OK;
@@ -1088,4 +1114,65 @@ extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_sc
     return FMHA_OK;
 } catch (...) {
     return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_kv4");
+}
+
+// ---------------------------------------------------------------- window with first keys
+namespace {
+
+int check_first(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, float scale, int window, int n_first, int causal,
+                Problem* p) {
+    const int rc = check_shape(batch, n_h, n_kv_h, T, s_k, hd, scale, window, causal, p);
+    if (rc) return rc;
+    if (n_first < 0) return fail(FMHA_ERR_SHAPE, "n_first=%d must be >= 0", n_first);
+    if (s_k > (1 << 30) || T > (1 << 30)) return fail(FMHA_ERR_SHAPE, "s_k=%d or T=%d is too long", s_k, T);
+    if (window >= s_k) p->window = 0;  // holds every key of every row
+    p->n_first = p->window > 0 ? std::min(n_first, s_k) : 0;
+    return FMHA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t fmha_fwd_first_workspace_bytes(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, int window,
+                                                 int n_first, int causal) try {
+    Problem p;
+    if (check_first(batch, n_h, n_kv_h, T, s_k, hd, 1.f, window, n_first, causal, &p) != FMHA_OK) return 0;
+    const long long rows = (long long)batch * n_h * T;
+    const SplitPlan sp = choose_split(p);
+    return rows == 0 || sp.n_splits == 1 ? 0 : partial_bytes(rows, hd, sp.n_splits, use_f16_partials(p));
+} catch (...) {
+    return 0;
+}
+
+extern "C" int fmha_fwd_first(const void* q, const void* k, const void* v, void* o, float* lse, const float* sink, int batch,
+                              int n_h, int n_kv_h, int T, int s_k, int hd, float scale, int window, int n_first, int causal,
+                              void* ws, size_t workspace_bytes, fmha_stream_t stream) try {
+    Problem p;
+    int rc = check_first(batch, n_h, n_kv_h, T, s_k, hd, scale, window, n_first, causal, &p);
+    if (rc) return rc;
+    rc = check_inputs(q, k, v, s_k);
+    if (rc) return rc;
+    if (!o || !lse) return fail(FMHA_ERR_NULL, "o and lse must be non-NULL");
+    if (!aligned(o, 16) || !aligned(lse, 4)) return fail(FMHA_ERR_ALIGN, "o must be 16-byte, lse 4-byte aligned");
+    if (sink && !aligned(sink, 4)) return fail(FMHA_ERR_ALIGN, "sink must be 4-byte aligned");
+    const long long rows = (long long)batch * n_h * T;
+    if (rows == 0) return FMHA_OK;
+    const SplitPlan sp = choose_split(p);
+    rc = check_chunks(p, sp.n_splits);
+    if (rc) return rc;
+    if (sp.n_splits == 1) return run_kernel(q, k, v, p, sp, o, lse, nullptr, nullptr, false, stream, false, nullptr, sink);
+    const bool f16 = use_f16_partials(p);
+    const size_t need = partial_bytes(rows, hd, sp.n_splits, f16);
+    if (!ws || workspace_bytes < need)
+        return fail(FMHA_ERR_WORKSPACE, "fmha_fwd_first: %zu bytes of workspace needed for %d chunks, %zu given", need,
+                    sp.n_splits, ws ? workspace_bytes : (size_t)0);
+    if (!aligned(ws, 16)) return fail(FMHA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    const PartialViews pv = partial_views(ws, rows, hd, sp.n_splits, f16);
+    rc = run_kernel(q, k, v, p, sp, nullptr, nullptr, pv.o_part, pv.lse_part, true, stream, f16, pv.range_part);
+    if (rc) return rc;
+    const cudaError_t e =
+        launch_merge(pv.o_part, pv.lse_part, pv.range_part, sp.n_splits, rows, hd, f16, o, lse, stream, sink, T, n_h);
+    if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
+    return FMHA_OK;
+} catch (...) {
+    return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_first");
 }

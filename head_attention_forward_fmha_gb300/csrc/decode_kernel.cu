@@ -16,12 +16,16 @@
 // un-normalised; the single divide by the running sum happens in the
 // epilogue, after the warps' partial states are merged through shared memory.
 //
+// With first keys (a window that keeps the first n_first keys visible) a block's
+// tiles are those of first_keys.cuh; everything else is the same.
+//
 // Output: bf16 O and fp32 LSE directly, or fp32 partials (O_i, lse_i) of this
 // chunk for the LSE merge (CURRENT_ISSUE.md, "Next steps" item 4).
 #include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <atomic>
+#include "first_keys.cuh"
 #include "internal.h"
 #include "nvfp4.cuh"
 #include "ptx.cuh"
@@ -52,6 +56,7 @@ struct DCfg {
 };
 
 struct DecodeArgs {
+    static constexpr bool kFirst = false;
     const __nv_bfloat16* q;
     __nv_bfloat16* o;
     float* lse;
@@ -66,6 +71,12 @@ struct DecodeArgs {
     const float* sink;     // [n_h] sink logits (final output only) or NULL
 };
 
+// with first keys (first_keys.cuh)
+struct DecodeArgsFirst : DecodeArgs {
+    static constexpr bool kFirst = true;
+    int n_first, first_span;
+};
+
 __device__ __forceinline__ void attended(int t, const DecodeArgs& a, int& lo, int& hi) {
     const int p = a.s_k - a.T + t;
     lo = 0;
@@ -78,10 +89,10 @@ __device__ __forceinline__ void attended(int t, const DecodeArgs& a, int& lo, in
 // are a parameter of their own: as a DecodeArgs field they changed ptxas's
 // register allocation of the bf16 instantiations (hd 128 with 16 rows went from
 // 147 to 128 registers and ran 11 % slower at s_k 32768).
-template <int HD, int NB, int EPI>
+template <int HD, int NB, int EPI, class Args>
 __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
-    decode_splitkv_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                          const DecodeArgs a, const Fp4Out fp4) {
+    decode_splitkv_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ VMaps<Args::kFirst> tmv,
+                          const Args a, const Fp4Out fp4) {
     using C = DCfg<HD, NB>;
     launch_dependents();  // the merge grid may be scheduled now; it waits for this grid's results
     extern __shared__ uint8_t smem_raw[];
@@ -101,8 +112,8 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
     const int r_end = min(a.R, r_begin + C::RT);
 
     // Keys this CTA visits: its chunk, intersected with the union of its rows' ranges.
-    const int c_lo = a.kv_begin + split * a.kv_chunk;
-    const int c_hi = min(a.s_k, c_lo + a.kv_chunk);
+    const ChunkRange cr = chunk_range(a, split, C::KT);
+    const int c_lo = cr.c_lo, c_hi = cr.c_hi;
     int u_lo = INT_MAX, u_hi = -1;
     for (int r = r_begin; r < r_end; ++r) {
         int lo, hi;
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
         u_hi = max(u_hi, hi);
     }
     const int k_lo = max(c_lo, u_lo), k_hi = min(c_hi, u_hi + 1);
-    const int n_tiles = (k_hi > k_lo) ? (k_hi - k_lo + C::KT - 1) / C::KT : 0;
+    const int n_tiles = cr.f_tiles + ((k_hi > k_lo) ? (k_hi - k_lo + C::KT - 1) / C::KT : 0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -128,24 +139,26 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
     if (warp == C::NCW) {
         if (lane == 0 && n_tiles > 0) {
             tma_prefetch_desc(&tmk);
-            tma_prefetch_desc(&tmv);
+            tma_prefetch_desc(&tmv.m[0]);
             const uint64_t pol = l2_policy_evict_first();
             int issued = 0;
             for (int it = 0; it < n_tiles; ++it) {
                 const int s = it % C::STAGES;
                 if (it >= C::STAGES && !mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1, a.status)) break;
-                const int key = k_lo + it * C::KT;
-                if (!FMHA_IN_BOUNDS(key >= 0 && key < k_hi && k_hi <= a.s_k && s < C::STAGES &&
+                const int key = tile_key(a, cr, k_lo, it, C::KT), k_end = tile_end(a, cr, k_hi, it);
+                if (!FMHA_IN_BOUNDS(key >= 0 && key < k_end && k_end <= a.s_k && s < C::STAGES &&
                                         slab < (int)gridDim.z,
                                     kSiteDecKVLoad, a.status))
                     break;
                 mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
                 uint8_t* kst = stages + s * C::STAGE_BYTES;
                 uint8_t* vst = kst + C::TILE_BYTES;
+                const CUtensorMap* vmap = &tmv.m[0];
+                if constexpr (Args::kFirst) vmap = &tmv.m[it < cr.f_tiles ? 1 : 0];
 #pragma unroll
                 for (int c = 0; c < C::NBOX; ++c) {
                     tma_load_3d_hint(kst + c * C::BOX_BYTES, &tmk, c * 64, key, slab, &full[s], pol);
-                    tma_load_3d_hint(vst + c * C::BOX_BYTES, &tmv, c * 64, key, slab, &full[s], pol);
+                    tma_load_3d_hint(vst + c * C::BOX_BYTES, vmap, c * 64, key, slab, &full[s], pol);
                 }
                 ++issued;
             }
@@ -173,14 +186,17 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
     // Attended key interval of each accumulator row this thread holds
     // (rows nb*8 + 2*(lane%4) + i), clipped to the chunk.
     int jlo[NB][2], jhi[NB][2];
+    int fhi[NB][2];  // last attended first key (kFirst only)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = r_begin + nb * 8 + 2 * (lane & 3) + i;
             int lo = INT_MAX, hi = -1;
+            fhi[nb][i] = -1;
             if (r < r_end) {
                 attended(r % a.T, a, lo, hi);
+                if constexpr (Args::kFirst) fhi[nb][i] = min(hi, a.n_first - 1);
                 lo = max(lo, c_lo);
                 hi = min(hi, c_hi - 1);
             }
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
         }
 
         // scale + mask, online softmax (log2 domain)
-        const int j0 = k_lo + it * C::KT + 16 * kw + (lane >> 2);
+        const int j0 = tile_key(a, cr, k_lo, it, C::KT) + 16 * kw + (lane >> 2);
         const int j1 = j0 + 8;
         uint32_t pb[NB][2];
 #pragma unroll
@@ -256,8 +272,14 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
             float mx[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float x0 = (j0 >= jlo[nb][i] && j0 <= jhi[nb][i]) ? sc[nb][i] * a.scale_log2 : -INFINITY;
-                const float x1 = (j1 >= jlo[nb][i] && j1 <= jhi[nb][i]) ? sc[nb][2 + i] * a.scale_log2 : -INFINITY;
+                int lo = jlo[nb][i], hi = jhi[nb][i];
+                if constexpr (Args::kFirst)
+                    if (it < cr.f_tiles) {
+                        lo = 0;
+                        hi = fhi[nb][i];
+                    }
+                const float x0 = (j0 >= lo && j0 <= hi) ? sc[nb][i] * a.scale_log2 : -INFINITY;
+                const float x1 = (j1 >= lo && j1 <= hi) ? sc[nb][2 + i] * a.scale_log2 : -INFINITY;
                 sc[nb][i] = x0;
                 sc[nb][2 + i] = x1;
                 mx[i] = fmaxf(x0, x1);
@@ -441,10 +463,10 @@ __global__ void __launch_bounds__(DCfg<HD, NB>::THREADS)
     }
 }
 
-template <int HD, int NB, int EPI>
-cudaError_t launch_t(const DecodeLaunch& L, cudaStream_t stream) {
+template <int HD, int NB, int EPI, class Args>
+cudaError_t launch_a(const DecodeLaunch& L, cudaStream_t stream) {
     using C = DCfg<HD, NB>;
-    auto kern = decode_splitkv_kernel<HD, NB, EPI>;
+    auto kern = decode_splitkv_kernel<HD, NB, EPI, Args>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -454,7 +476,14 @@ cudaError_t launch_t(const DecodeLaunch& L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 128) attr_set[dev] = true;
     }
-    DecodeArgs a;
+    Args a;
+    VMaps<Args::kFirst> vm;
+    vm.m[0] = L.tmap_v;
+    if constexpr (Args::kFirst) {
+        vm.m[1] = L.tmap_v_first;
+        a.n_first = L.p.n_first;
+        a.first_span = L.sp.first_span;
+    }
     a.q = static_cast<const __nv_bfloat16*>(L.q);
     a.o = static_cast<__nv_bfloat16*>(L.o);
     a.lse = L.lse;
@@ -485,7 +514,14 @@ cudaError_t launch_t(const DecodeLaunch& L, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, L.tmap_k, L.tmap_v, a, L.fp4);
+    return cudaLaunchKernelEx(&cfg, kern, L.tmap_k, vm, a, L.fp4);
+}
+
+template <int HD, int NB, int EPI>
+cudaError_t launch_t(const DecodeLaunch& L, cudaStream_t stream) {
+    if constexpr (EPI != kEpiNvfp4)
+        if (L.p.n_first > 0) return launch_a<HD, NB, EPI, DecodeArgsFirst>(L, stream);
+    return launch_a<HD, NB, EPI, DecodeArgs>(L, stream);
 }
 
 }  // namespace

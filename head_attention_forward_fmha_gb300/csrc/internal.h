@@ -28,11 +28,23 @@ struct Problem {
     float scale;
     int group;  // n_h / n_kv_h
     int R;      // query rows sharing one KV head: group * T
+    int n_first = 0;  // first keys that stay attended outside the window (0: none)
 };
 
 // Split-KV layout: chunk i covers keys [kv_begin + i*kv_chunk, ... + kv_chunk).
+// With first keys (first_span > 0) the chunks divide a virtual key axis: the
+// first n_first keys, rounded up to first_span (whole tiles), and then the keys
+// from kv_begin on; kv_chunk is then a multiple of the kernel's key tile.
 struct SplitPlan {
     int kv_begin, kv_chunk, n_splits;
+    int first_span = 0;
+};
+
+// V's tensor maps: the whole tensor, and for a kernel with first keys its first
+// n_first rows (rows behind them load as zeros, whatever memory holds there).
+template <bool FIRST>
+struct VMaps {
+    CUtensorMap m[FIRST ? 2 : 1];
 };
 
 // ---- decode / small-row kernel (decode_kernel.cu) -------------------------
@@ -46,6 +58,7 @@ struct DecodeLaunch {
     const float* sink;  // [n_h] attention-sink logits or NULL; applied when !to_partials
     Fp4Out fp4;         // NVFP4 final output when fp4.codes != NULL (no sink, !to_partials)
     CUtensorMap tmap_k, tmap_v;
+    CUtensorMap tmap_v_first;  // first keys only
     Problem p;
     SplitPlan sp;
     unsigned* status;
@@ -67,6 +80,7 @@ struct TcLaunch {
     Fp4Out fp4;         // NVFP4 final output when fp4.codes != NULL (no sink, !to_partials)
     bool ss_pv;         // row-tile kernel: P through shared memory (SS-form PV) instead of TMEM (TS form)
     CUtensorMap tmap_q, tmap_k, tmap_v;
+    CUtensorMap tmap_v_first;  // first keys only
     // bf16 O [slabs, R, hd] (box 64 x 128), fp32 partials [n_splits*slabs, R, hd]
     // (box 32 x 128) or fp16 partials (box 64 x 128)
     CUtensorMap tmap_o;

@@ -33,6 +33,7 @@
 // released with the address tcgen05.alloc returned.
 #include <climits>
 #include <atomic>
+#include "first_keys.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -85,6 +86,7 @@ struct TCfg {
 };
 
 struct TcArgs {
+    static constexpr bool kFirst = false;
     __nv_bfloat16* o;
     float* lse;
     float* o_part;
@@ -99,6 +101,12 @@ struct TcArgs {
     Fp4Out fp4;         // NVFP4 final output (EPI == kEpiNvfp4)
 };
 
+// with first keys (first_keys.cuh)
+struct TcArgsFirst : TcArgs {
+    static constexpr bool kFirst = true;
+    int n_first, first_span;
+};
+
 __device__ __forceinline__ void attended_rows(int t, const TcArgs& a, int& lo, int& hi) {
     const int p = a.s_k - a.T + t;
     lo = 0;
@@ -107,10 +115,11 @@ __device__ __forceinline__ void attended_rows(int t, const TcArgs& a, int& lo, i
     if (a.window > 0) lo = max(lo, p - a.window + 1);
 }
 
-template <int HD, int EPI, bool TS>
+template <int HD, int EPI, bool TS, class Args>
 __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                  const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, const TcArgs a) {
+                  const __grid_constant__ VMaps<Args::kFirst> tmv, const __grid_constant__ CUtensorMap tmo,
+                  const Args a) {
     using C = TCfg<HD, TS>;
     constexpr int BM = C::BM, BN = C::BN, KST = C::KST, VST = C::VST;
     constexpr bool SINK = EPI == kEpiSink;
@@ -144,8 +153,8 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
     const int r_end = min(a.R, r_begin + BM);
 
     // KV range of this CTA: its chunk intersected with what its rows attend.
-    const int c_lo = a.kv_begin + split * a.kv_chunk;
-    const int c_hi = min(a.s_k, c_lo + a.kv_chunk);
+    const ChunkRange cr = chunk_range(a, split, BN);
+    const int c_lo = cr.c_lo, c_hi = cr.c_hi;
     int u_lo, u_hi;
     if (r_end - r_begin >= a.T) {
         int l0, h0, l1, h1;
@@ -170,14 +179,14 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
         }
     }
     const int k_lo = max(c_lo, u_lo), k_hi = min(c_hi, u_hi + 1);
-    const int n_tiles = (k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0;
+    const int n_tiles = cr.f_tiles + ((k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0);
 
     // K tile j into stage j % KST (the caller has made sure the stage is free).
     uint64_t pol_k = 0;
     auto issue_k = [&](int j) -> bool {
         const int s = j % KST;
-        const int key = k_lo + j * BN;
-        if (!FMHA_IN_BOUNDS(key >= 0 && key < k_hi && k_hi <= a.s_k && s < KST, kSiteTcKLoad, a.status)) return false;
+        const int key = tile_key(a, cr, k_lo, j, BN), k_end = tile_end(a, cr, k_hi, j);
+        if (!FMHA_IN_BOUNDS(key >= 0 && key < k_end && k_end <= a.s_k && s < KST, kSiteTcKLoad, a.status)) return false;
         mbar_arrive_expect_tx(&k_full[s], C::KV_TILE);
 #pragma unroll
         for (int c = 0; c < C::NB; ++c)
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
     } else if (warp == 6) {
         // ------------------------------------------------------------ V producer
         if (lane == 0 && n_tiles > 0) {
-            tma_prefetch_desc(&tmv);
+            tma_prefetch_desc(&tmv.m[0]);
             const uint64_t pol = l2_policy_evict_first();
             // V_0 is needed only after S_0 and its softmax: at hd >= 128, where Q
             // and K_0 are large, let them take the SM's load bandwidth first
@@ -267,12 +276,14 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
             for (int j = 0; q_in && j < n_tiles; ++j) {
                 const int s = j % VST;
                 if (j >= VST && !mbar_wait(&v_empty[s], ((j / VST) - 1) & 1, a.status)) break;
-                const int key = k_lo + j * BN;
-                if (!FMHA_IN_BOUNDS(key >= 0 && key < k_hi && k_hi <= a.s_k && s < VST, kSiteTcVLoad, a.status)) break;
+                const int key = tile_key(a, cr, k_lo, j, BN), k_end = tile_end(a, cr, k_hi, j);
+                if (!FMHA_IN_BOUNDS(key >= 0 && key < k_end && k_end <= a.s_k && s < VST, kSiteTcVLoad, a.status)) break;
+                const CUtensorMap* vmap = &tmv.m[0];
+                if constexpr (Args::kFirst) vmap = &tmv.m[j < cr.f_tiles ? 1 : 0];
                 mbar_arrive_expect_tx(&v_full[s], C::KV_TILE);
 #pragma unroll
                 for (int c = 0; c < C::NB; ++c)
-                    tma_load_3d_hint(sv + s * C::KV_TILE + c * BN * 128, &tmv, c * 64, key, slab, &v_full[s], pol);
+                    tma_load_3d_hint(sv + s * C::KV_TILE + c * BN * 128, vmap, c * 64, key, slab, &v_full[s], pol);
                 ++v_issued;
             }
             drain_ring(v_full, VST, v_issued, a.status);
@@ -348,8 +359,10 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
         const int grow = r_begin + row;
         const bool valid = grow < r_end;
         int jlo = INT_MAX, jhi = -1;
+        int fhi = -1;  // last attended first key (kFirst only)
         if (valid) {
             attended_rows(grow % a.T, a, jlo, jhi);
+            if constexpr (Args::kFirst) fhi = min(jhi, a.n_first - 1);
             jlo = max(jlo, c_lo);
             jhi = min(jhi, c_hi - 1);
         }
@@ -377,7 +390,9 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
             // Exponentials and the row sum before waiting on the tensor core.
             float alpha;
             uint32_t pk[BN / 2];
-            softmax_row_tile<BN, !C::ONES>(x, pk, k_lo + j * BN, jlo, jhi, a.scale_log2, m_ref, l, l_o, alpha);
+            const bool first = Args::kFirst && j < cr.f_tiles;
+            softmax_row_tile<BN, !C::ONES>(x, pk, tile_key(a, cr, k_lo, j, BN), first ? 0 : jlo, first ? fhi : jhi,
+                                           a.scale_log2, m_ref, l, l_o, alpha);
             const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
             // SS: P buffer pb was last read by PV_{j-2}.  TS: P_j goes over S_j,
             // whose QK the MMA issuer queued after PV_{j-NSB}, so S_j being ready
@@ -475,10 +490,10 @@ __global__ void __launch_bounds__(TCfg<HD, TS>::THREADS, 1)
     }
 }
 
-template <int HD, int EPI, bool TS>
-cudaError_t launch_t(const TcLaunch& L, cudaStream_t stream) {
+template <int HD, int EPI, bool TS, class Args>
+cudaError_t launch_a(const TcLaunch& L, cudaStream_t stream) {
     using C = TCfg<HD, TS>;
-    auto kern = fwd_tc_kernel<HD, EPI, TS>;
+    auto kern = fwd_tc_kernel<HD, EPI, TS, Args>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -488,7 +503,14 @@ cudaError_t launch_t(const TcLaunch& L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 128) attr_set[dev] = true;
     }
-    TcArgs a;
+    Args a;
+    VMaps<Args::kFirst> vm;
+    vm.m[0] = L.tmap_v;
+    if constexpr (Args::kFirst) {
+        vm.m[1] = L.tmap_v_first;
+        a.n_first = L.p.n_first;
+        a.first_span = L.sp.first_span;
+    }
     a.o = static_cast<__nv_bfloat16*>(L.o);
     a.lse = L.lse;
     a.o_part = static_cast<float*>(L.o_part);
@@ -518,7 +540,15 @@ cudaError_t launch_t(const TcLaunch& L, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, L.tmap_q, L.tmap_k, L.tmap_v, L.tmap_o, a);
+    return cudaLaunchKernelEx(&cfg, kern, L.tmap_q, L.tmap_k, vm, L.tmap_o, a);
+}
+
+// First keys come with the TS form only (the SS form is there to be compared with it).
+template <int HD, int EPI, bool TS>
+cudaError_t launch_t(const TcLaunch& L, cudaStream_t stream) {
+    if constexpr (EPI != kEpiNvfp4 && TS)
+        if (L.p.n_first > 0) return launch_a<HD, EPI, TS, TcArgsFirst>(L, stream);
+    return launch_a<HD, EPI, TS, TcArgs>(L, stream);
 }
 
 }  // namespace
@@ -546,7 +576,7 @@ cudaError_t launch_hd(const TcLaunch& L, cudaStream_t stream) {
 
 template <int EPI>
 cudaError_t launch_form(const TcLaunch& L, cudaStream_t stream) {
-    return L.ss_pv ? launch_hd<EPI, false>(L, stream) : launch_hd<EPI, true>(L, stream);
+    return L.ss_pv && L.p.n_first == 0 ? launch_hd<EPI, false>(L, stream) : launch_hd<EPI, true>(L, stream);
 }
 
 cudaError_t launch_tc(const TcLaunch& L, cudaStream_t stream) {

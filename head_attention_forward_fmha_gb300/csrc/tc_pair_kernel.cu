@@ -45,6 +45,7 @@
 // s_k 32768 in 125.6 us (57 %) against 149.9 us.
 #include <climits>
 #include <atomic>
+#include "first_keys.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -80,6 +81,7 @@ struct PCfg {
 };
 
 struct PairArgs {
+    static constexpr bool kFirst = false;
     __nv_bfloat16* o;
     float* lse;
     float* lse_part;
@@ -90,6 +92,12 @@ struct PairArgs {
     long long rows_total;
     unsigned* status;
     const float* sink;  // [n_h] sink logits (final output only) or NULL
+};
+
+// with first keys (first_keys.cuh)
+struct PairArgsFirst : PairArgs {
+    static constexpr bool kFirst = true;
+    int n_first, first_span;
 };
 
 __device__ __forceinline__ void pair_attended(int t, const PairArgs& a, int& lo, int& hi) {
@@ -130,11 +138,11 @@ __device__ __forceinline__ void write_p_row256(uint8_t* pbuf, int row, const uin
     }
 }
 
-template <int HD, int EPI>
+template <int HD, int EPI, class Args>
 __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
     fwd_tc_pair_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
-                       const PairArgs a) {
+                       const __grid_constant__ VMaps<Args::kFirst> tmv, const __grid_constant__ CUtensorMap tmo,
+                       const Args a) {
     using C = PCfg<HD>;
     constexpr int BM = C::BM, BN = C::BN, NSLOT = C::NSLOT;
     constexpr bool SINK = EPI == kEpiSink;
@@ -166,8 +174,8 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
     const int n_rt = (re - rb > BM) ? 2 : 1;   // row tiles with rows (tile B may lie past the slab's end)
 
     // KV range of this block: its chunk intersected with what its rows attend.
-    const int c_lo = a.kv_begin + split * a.kv_chunk;
-    const int c_hi = min(a.s_k, c_lo + a.kv_chunk);
+    const ChunkRange cr = chunk_range(a, split, BN);
+    const int c_lo = cr.c_lo, c_hi = cr.c_hi;
     int u_lo, u_hi;
     {
         int t0, t1;
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
         u_hi = h1;
     }
     const int k_lo = max(c_lo, u_lo), k_hi = min(c_hi, u_hi + 1);
-    const int n_tiles = (k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0;
+    const int n_tiles = cr.f_tiles + ((k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0);
 
     // Ring items in the order the MMA issuer consumes them: K_0, then per KV
     // tile j: K_{j+1} (if any) and V_j.  Item i -> (is V, KV tile).
@@ -208,14 +216,16 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
             }
         }
         const int s = i % NSLOT;
-        const int key = k_lo + tile * BN;
-        if (!FMHA_IN_BOUNDS(key >= 0 && key < k_hi && k_hi <= a.s_k && s < NSLOT, is_v ? kSitePairVLoad : kSitePairKLoad,
+        const int key = tile_key(a, cr, k_lo, tile, BN), k_end = tile_end(a, cr, k_hi, tile);
+        const CUtensorMap* vmap = &tmv.m[0];
+        if constexpr (Args::kFirst) vmap = &tmv.m[tile < cr.f_tiles ? 1 : 0];
+        if (!FMHA_IN_BOUNDS(key >= 0 && key < k_end && k_end <= a.s_k && s < NSLOT, is_v ? kSitePairVLoad : kSitePairKLoad,
                             a.status))
             return false;
         mbar_arrive_expect_tx(&slot_full[s], C::KV_TILE);
 #pragma unroll
         for (int c = 0; c < C::NB; ++c)
-            tma_load_3d_hint(ring + s * C::KV_TILE + c * BN * 128, is_v ? &tmv : &tmk, c * 64, key, slab, &slot_full[s],
+            tma_load_3d_hint(ring + s * C::KV_TILE + c * BN * 128, is_v ? vmap : &tmk, c * 64, key, slab, &slot_full[s],
                              pol);
         return true;
     };
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
         if (n_tiles > 0) {
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
-            tma_prefetch_desc(&tmv);
+            tma_prefetch_desc(&tmv.m[0]);
             pol = l2_policy_evict_first();
             grid_dependency_wait();  // the preceding kernel's writes (Q, K, V) are visible
             if (FMHA_IN_BOUNDS(rb >= 0 && rb + (n_rt - 1) * BM < a.R && slab < (int)gridDim.z, kSitePairQLoad,
@@ -368,8 +378,10 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
             const int grow = r_tile + row;
             const bool valid = grow < re;
             int jlo = INT_MAX, jhi = -1;
+            int fhi = -1;  // last attended first key (kFirst only)
             if (valid) {
                 pair_attended(grow % a.T, a, jlo, jhi);
+                if constexpr (Args::kFirst) fhi = min(jhi, a.n_first - 1);
                 jlo = max(jlo, c_lo);
                 jhi = min(jhi, c_hi - 1);
             }
@@ -399,7 +411,9 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
                     tmem_wait_ld();
                     tc_fence_before();
                     mbar_arrive(&s_free[t]);  // S_t may now be overwritten by QK_t(j + 1)
-                    softmax_row_tile<BN>(x, pk, k_lo + j * BN, jlo, jhi, a.scale_log2, m_ref, l, l_o, alpha);
+                    const bool first = Args::kFirst && j < cr.f_tiles;
+                    softmax_row_tile<BN>(x, pk, tile_key(a, cr, k_lo, j, BN), first ? 0 : jlo, first ? fhi : jhi,
+                                         a.scale_log2, m_ref, l, l_o, alpha);
                     // PV(j - 1) has read the P buffer and updated O^T (each
                     // o_done barrier has at most one phase outstanding: PV(j)
                     // needs this step's P)
@@ -533,10 +547,10 @@ __global__ void __launch_bounds__(PCfg<HD>::THREADS, 1)
     }
 }
 
-template <int HD, int EPI>
-cudaError_t launch_pair_t(const TcLaunch& L, cudaStream_t stream) {
+template <int HD, int EPI, class Args>
+cudaError_t launch_pair_a(const TcLaunch& L, cudaStream_t stream) {
     using C = PCfg<HD>;
-    auto kern = fwd_tc_pair_kernel<HD, EPI>;
+    auto kern = fwd_tc_pair_kernel<HD, EPI, Args>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -546,7 +560,14 @@ cudaError_t launch_pair_t(const TcLaunch& L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 128) attr_set[dev] = true;
     }
-    PairArgs a;
+    Args a;
+    VMaps<Args::kFirst> vm;
+    vm.m[0] = L.tmap_v;
+    if constexpr (Args::kFirst) {
+        vm.m[1] = L.tmap_v_first;
+        a.n_first = L.p.n_first;
+        a.first_span = L.sp.first_span;
+    }
     a.o = static_cast<__nv_bfloat16*>(L.o);
     a.lse = L.lse;
     a.lse_part = L.lse_part;
@@ -573,7 +594,12 @@ cudaError_t launch_pair_t(const TcLaunch& L, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, L.tmap_q, L.tmap_k, L.tmap_v, L.tmap_o, a);
+    return cudaLaunchKernelEx(&cfg, kern, L.tmap_q, L.tmap_k, vm, L.tmap_o, a);
+}
+
+template <int HD, int EPI>
+cudaError_t launch_pair_t(const TcLaunch& L, cudaStream_t stream) {
+    return L.p.n_first > 0 ? launch_pair_a<HD, EPI, PairArgsFirst>(L, stream) : launch_pair_a<HD, EPI, PairArgs>(L, stream);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <climits>
 #include <atomic>
+#include "first_keys.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -92,6 +93,7 @@ struct WCfgT {
 using WCfg = WCfgT<false>;
 
 struct WideArgs {
+    static constexpr bool kFirst = false;
     __nv_bfloat16* o;
     float* lse;
     float* lse_part;
@@ -107,6 +109,12 @@ struct WideArgs {
     Fp4Out fp4;         // NVFP4 final output (EPI == kEpiNvfp4)
 };
 
+// with first keys (first_keys.cuh)
+struct WideArgsFirst : WideArgs {
+    static constexpr bool kFirst = true;
+    int n_first, first_span;
+};
+
 __device__ __forceinline__ void w_attended(int t, const WideArgs& a, int& lo, int& hi) {
     const int p = a.s_k - a.T + t;
     lo = 0;
@@ -115,11 +123,11 @@ __device__ __forceinline__ void w_attended(int t, const WideArgs& a, int& lo, in
     if (a.window > 0) lo = max(lo, p - a.window + 1);
 }
 
-template <int EPI, bool QRES, int QROWS>
+template <int EPI, bool QRES, int QROWS, class Args>
 __global__ void __launch_bounds__(WCfg::THREADS, 1)
     fwd_tc_wide_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
-                       const WideArgs a) {
+                       const __grid_constant__ VMaps<Args::kFirst> tmv, const __grid_constant__ CUtensorMap tmo,
+                       const Args a) {
     using C = WCfgT<QRES, QROWS>;
     constexpr int BM = C::BM, BN = C::BN;
     constexpr bool SINK = EPI == kEpiSink;
@@ -148,8 +156,8 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
     const int r_begin = rt * BM;
     const int r_end = min(a.R, r_begin + BM);
 
-    const int c_lo = a.kv_begin + split * a.kv_chunk;
-    const int c_hi = min(a.s_k, c_lo + a.kv_chunk);
+    const ChunkRange cr = chunk_range(a, split, BN);
+    const int c_lo = cr.c_lo, c_hi = cr.c_hi;
     int u_lo, u_hi;
     {
         int t0, t1;
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         u_hi = h1;
     }
     const int k_lo = max(c_lo, u_lo), k_hi = min(c_hi, u_hi + 1);
-    const int n_tiles_all = (k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0;
+    const int n_tiles_all = cr.f_tiles + ((k_hi > k_lo) ? (k_hi - k_lo + BN - 1) / BN : 0);
     // without a resident Q a block holds one tile (the host picks the resident
     // Q for longer spans), which its ring item order relies on
     const int n_tiles =
@@ -204,8 +212,10 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         int kind, tile, c;
         item_of(i, kind, tile, c);
         const int s = i % C::NSLOT;
-        const int key = k_lo + tile * BN;
-        const bool key_ok = key >= 0 && key < k_hi && k_hi <= a.s_k;
+        const int key = tile_key(a, cr, k_lo, tile, BN), k_end = tile_end(a, cr, k_hi, tile);
+        const CUtensorMap* vmap = &tmv.m[0];
+        if constexpr (Args::kFirst) vmap = &tmv.m[tile < cr.f_tiles ? 1 : 0];
+        const bool key_ok = key >= 0 && key < k_end && k_end <= a.s_k;
         const bool in_range = kind == 1 ? (key_ok && c >= 0 && c < C::QK_ITEMS && (QRES || (r_begin >= 0 && r_begin < a.R)))
                                         : (key_ok && c >= 0 && c < C::V_ITEMS);
         if (!FMHA_IN_BOUNDS(in_range && s >= 0 && s < C::NSLOT && slab < (int)gridDim.z, kSiteWideItem, a.status))
@@ -213,8 +223,8 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         mbar_arrive_expect_tx(&slot_full[s], C::ITEM_BYTES);
         uint8_t* dst = ring + s * C::ITEM_BYTES;
         if (kind == 2) {
-            tma_load_3d_hint(dst, &tmv, half * C::HALF + 2 * c * 64, key, slab, &slot_full[s], pol_kv);
-            tma_load_3d_hint(dst + C::SLOT_BYTES, &tmv, half * C::HALF + (2 * c + 1) * 64, key, slab, &slot_full[s],
+            tma_load_3d_hint(dst, vmap, half * C::HALF + 2 * c * 64, key, slab, &slot_full[s], pol_kv);
+            tma_load_3d_hint(dst + C::SLOT_BYTES, vmap, half * C::HALF + (2 * c + 1) * 64, key, slab, &slot_full[s],
                              pol_kv);
         } else if (QRES) {
             tma_load_3d_hint(dst, &tmk, 2 * c * 64, key, slab, &slot_full[s], pol_kv);
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         if (n_tiles > 0) {
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
-            tma_prefetch_desc(&tmv);
+            tma_prefetch_desc(&tmv.m[0]);
             pol_kv = l2_policy_evict_first();
             pol_q = l2_policy_evict_last();
             grid_dependency_wait();  // the preceding kernel's writes (Q, K, V) are visible
@@ -382,8 +392,10 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
         const int grow = r_begin + row;
         const bool valid = grow < r_end;
         int jlo = INT_MAX, jhi = -1;
+        int fhi = -1;  // last attended first key (kFirst only)
         if (valid) {
             w_attended(grow % a.T, a, jlo, jhi);
+            if constexpr (Args::kFirst) fhi = min(jhi, a.n_first - 1);
             jlo = max(jlo, c_lo);
             jhi = min(jhi, c_hi - 1);
         }
@@ -408,7 +420,9 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
             tmem_wait_ld();
             float alpha;
             uint32_t pk[BN / 2];
-            softmax_row_tile<BN>(x, pk, k_lo + j * BN, jlo, jhi, a.scale_log2, m_ref, l, l_o, alpha);
+            const bool first = Args::kFirst && j < cr.f_tiles;
+            softmax_row_tile<BN>(x, pk, tile_key(a, cr, k_lo, j, BN), first ? 0 : jlo, first ? fhi : jhi, a.scale_log2,
+                                 m_ref, l, l_o, alpha);
             // P_j goes over S_j, whose QK the MMA issuer queued after PV_{j-2}, so
             // S_j being ready means that PV is done; a rescale of O needs PV_{j-1}.
             const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
@@ -527,28 +541,40 @@ __global__ void __launch_bounds__(WCfg::THREADS, 1)
 
 int tc_wide_kv_tile() { return WCfg::BN; }
 
+// Keys of a block's chunk at most (with first keys: of its virtual axis).
+static int wide_span(const Problem& p, const SplitPlan& sp) {
+    return p.n_first > 0 ? sp.kv_chunk : std::min(sp.kv_chunk, p.s_k);
+}
+
 // Q stays resident when a block may see two or more 128-key tiles, and then
 // only 32 or 64 rows of each chunk are loaded if no KV head has more query rows.
 int tc_wide_q_box_rows(const Problem& p, const SplitPlan& sp) {
-    const int span = std::min(sp.kv_chunk, p.s_k);
+    const int span = wide_span(p, sp);
     if (span <= WCfg::BN) return 128;
     return p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
 }
 
-template <int EPI, bool QRES, int QROWS>
-cudaError_t launch_wide_t(const TcLaunch& L, cudaStream_t stream) {
+template <int EPI, bool QRES, int QROWS, class Args>
+cudaError_t launch_wide_a(const TcLaunch& L, cudaStream_t stream) {
     using C = WCfgT<QRES, QROWS>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 128 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(fwd_tc_wide_kernel<EPI, QRES, QROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(fwd_tc_wide_kernel<EPI, QRES, QROWS, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 128) attr_set[dev] = true;
     }
-    WideArgs a;
+    Args a;
+    VMaps<Args::kFirst> vm;
+    vm.m[0] = L.tmap_v;
+    if constexpr (Args::kFirst) {
+        vm.m[1] = L.tmap_v_first;
+        a.n_first = L.p.n_first;
+        a.first_span = L.sp.first_span;
+    }
     a.o = static_cast<__nv_bfloat16*>(L.o);
     a.lse = L.lse;
     a.lse_part = L.lse_part;
@@ -578,7 +604,14 @@ cudaError_t launch_wide_t(const TcLaunch& L, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fwd_tc_wide_kernel<EPI, QRES, QROWS>, L.tmap_q, L.tmap_k, L.tmap_v, L.tmap_o, a);
+    return cudaLaunchKernelEx(&cfg, fwd_tc_wide_kernel<EPI, QRES, QROWS, Args>, L.tmap_q, L.tmap_k, vm, L.tmap_o, a);
+}
+
+template <int EPI, bool QRES, int QROWS>
+cudaError_t launch_wide_t(const TcLaunch& L, cudaStream_t stream) {
+    if constexpr (EPI != kEpiNvfp4)
+        if (L.p.n_first > 0) return launch_wide_a<EPI, QRES, QROWS, WideArgsFirst>(L, stream);
+    return launch_wide_a<EPI, QRES, QROWS, WideArgs>(L, stream);
 }
 
 template <int EPI>
@@ -586,7 +619,7 @@ cudaError_t launch_wide_q(const TcLaunch& L, cudaStream_t stream) {
     const int rows = tc_wide_q_box_rows(L.p, L.sp);
     if (rows == 32) return launch_wide_t<EPI, true, 32>(L, stream);
     if (rows == 64) return launch_wide_t<EPI, true, 64>(L, stream);
-    const int span = std::min(L.sp.kv_chunk, L.p.s_k);
+    const int span = wide_span(L.p, L.sp);
     return span > WCfg::BN ? launch_wide_t<EPI, true, 128>(L, stream) : launch_wide_t<EPI, false, 128>(L, stream);
 }
 

@@ -459,6 +459,27 @@ int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const
                  int window, int n_first, int causal, int kv_chunk, void* workspace, size_t workspace_bytes,
                  fmha_stream_t stream);
 
+/*
+ * fmha_fwd_first -- fmha_fwd_sink with a few first keys that a sliding window
+ * does not hide: row t at position p = s_k - T + t attends key j iff
+ *     (j <= p with causal)  and  (j > p - window  or  j < n_first).
+ * Without a window (0, or one of at least s_k keys) n_first changes nothing.
+ * Only the first keys' tiles and the window's keys are read.  Keys that no row
+ * of the call attends do not reach any result, whatever memory holds there; V
+ * has to be finite at keys that some row of the sequence attends.
+ * sink: [n_h] fp32 logits or NULL.  Kernels, plan and partial format are those of
+ * fmha_fwd; the partials live in `workspace`, of at least
+ * fmha_fwd_first_workspace_bytes(same shape) bytes (0: none needed; also 0 for an
+ * invalid shape, which the call then refuses), 16-byte aligned.  Two calls that
+ * may run at the same time need two workspaces.
+ */
+size_t fmha_fwd_first_workspace_bytes(int batch, int n_h, int n_kv_h, int T, int s_k, int hd,
+                                      int window, int n_first, int causal);
+int fmha_fwd_first(const void* q, const void* k, const void* v, void* o, float* lse, const float* sink,
+                   int batch, int n_h, int n_kv_h, int T, int s_k, int hd,
+                   float scale, int window, int n_first, int causal,
+                   void* workspace, size_t workspace_bytes, fmha_stream_t stream);
+
 /* ABI version: major * 10000 + minor * 100 + patch. */
 int fmha_version(void);
 

@@ -55,6 +55,31 @@ def test_kv4_refusals(lib, change, code):
         assert binding.fmha_get_last_error()
 
 
+FIRST = dict(q=P, k=P, v=P, o=P, lse=P, sink=None, b=1, n_h=8, n_kv=1, T=1, s_k=64, hd=128, scale=0.1, window=16, n_first=4, causal=0,
+             ws=None, wsb=0, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(hd=80), -3), (dict(n_h=6, n_kv=4), -4), (dict(T=-1), -5), (dict(s_k=-1), -5), (dict(window=-1), -5), (dict(n_first=-1), -5),
+    (dict(causal=2), -5), (dict(causal=1, T=65), -5), (dict(scale=float("inf")), -5), (dict(q=None), -1), (dict(v=None), -1), (dict(o=None), -1),
+    (dict(q=P + 8), -2), (dict(sink=P + 1), -2), (dict(T=0), 0), (dict(b=0), 0), (dict(s_k=1 << 30 | 1), -5),
+    (dict(s_k=65536, window=65000), -6), (dict(s_k=65536, window=65000, ws=P, wsb=100), -6),
+    (dict(s_k=65536, window=65000, ws=P + 4, wsb=1 << 30), -2),
+])
+def test_first_refusals(lib, change, code):
+    assert lib.fmha_fwd_first(*{**FIRST, **change}.values()) == code
+
+
+def test_first_workspace():
+    f = binding.fmha_fwd_first_workspace_bytes
+    assert f(1, 8, 1, 1, 64, 128, 16, 4) == 0          # one chunk
+    assert f(1, 8, 1, 1, 65536, 128, 65000, 4) > 0
+    assert f(1, 8, 3, 1, 65536, 128, 65000, 4) == 0    # refused by the call
+    # a window that holds every key is none: fmha_fwd's plan
+    n, _ = binding.fmha_fwd_plan(1, 8, 1, 1, 4096, 128)
+    assert f(1, 8, 1, 1, 4096, 128, 4096, 4) == binding.fmha_workspace_bytes(1, 8, 1, 128, n)
+
+
 def test_kv4_plan():
     n, chunk = binding.fmha_fwd_kv4_plan(1, 64, 8, 1, 8192, 128)
     assert n > 1 and chunk % 32 == 0 and n * chunk >= 8192

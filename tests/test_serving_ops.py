@@ -293,6 +293,91 @@ def test_kv4_long_cache_past_32_bit_offsets():
     ref.assert_attention((o, lse), want)
 
 
+# ------------------------------------------------------------------ window with first keys
+@pytest.fixture
+def path():
+    yield binding.fmha_set_kernel_path
+    binding.fmha_set_kernel_path(0)
+
+
+def check_first(hd, b, n_h, n_kv, T, s_k, window, n_first, causal, sink=False, seed=0):
+    r = gen(seed + hd)
+    q, k, v = normal(r, b, n_h, T, hd), normal(r, b, n_kv, s_k, hd) * 2, normal(r, b, n_kv, s_k, hd)
+    sg = torch.randn(n_h, generator=r, device=DEV) * 2 if sink else None
+    # keys that no row attends hold NaN and infinities
+    lo = max(0, s_k - T - window + 1)
+    if window < s_k and n_first < lo:
+        k[:, :, n_first:lo] = float("nan")
+        v[:, :, n_first:lo] = float("inf")
+    got = binding.fmha_fwd_first(q, k, v, n_first, window=window, causal=causal, sink=sg)
+    if window < s_k and n_first < lo:
+        k[:, :, n_first:lo] = 0
+        v[:, :, n_first:lo] = 0
+    want = ref.attend(q, k, v, [s_k] * b, hd ** -0.5, window, n_first, causal, sg, p_bits=8)
+    ref.assert_attention(got, want, "first hd %d T %d s_k %d window %d n_first %d" % (hd, T, s_k, window, n_first))
+
+
+@pytest.mark.parametrize("which", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+@pytest.mark.parametrize("n_h,n_kv,T,s_k,window,n_first,causal,sink", [
+    (8, 1, 1, 700, 200, 4, False, False), (6, 2, 1, 333, 64, 70, False, True), (4, 4, 1, 513, 1, 1, True, False),
+    (4, 2, 9, 400, 100, 130, True, False), (2, 2, 33, 300, 280, 17, True, True), (16, 1, 40, 500, 37, 4, True, False),
+    (8, 2, 128, 600, 150, 16, True, False), (3, 1, 100, 450, 30, 300, False, True), (4, 1, 64, 64, 5, 3, True, False),
+    (2, 1, 5, 90, 90, 4, True, False), (2, 1, 5, 90, 1000, 4, False, False), (2, 1, 3, 200, 199, 200, False, False),
+    (1, 1, 1, 1, 1, 4, True, False), (32, 1, 8, 1500, 900, 128, True, True)])
+def test_first_keys(hd, n_h, n_kv, T, s_k, window, n_first, causal, sink, which, path):
+    path(which)
+    check_first(hd, 2, n_h, n_kv, T, s_k, window, n_first, causal, sink)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+@pytest.mark.parametrize("T,n_first", [(1, 4), (16, 200), (128, 64)])
+def test_first_keys_split(hd, T, n_first):
+    """Long windows on few heads: the plan splits the key axis, the first keys among its chunks."""
+    n_h = 2 if T > 1 else 8
+    assert binding.fmha_fwd_first_workspace_bytes(1, n_h, 1, T, 20000, hd, 9000, n_first, True) > 0
+    check_first(hd, 1, n_h, 1, T, 20000, 9000, n_first, True, sink=True)
+
+
+def test_first_keys_without_any_is_the_windowed_forward():
+    r = gen(50)
+    q, k, v = normal(r, 2, 8, 3, 128), normal(r, 2, 2, 500, 128), normal(r, 2, 2, 500, 128)
+    for window in (0, 77, 500):
+        a = binding.fmha_fwd_first(q, k, v, 0, window=window, causal=True)
+        b = binding.fmha_fwd(q, k, v, window=window, causal=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a = binding.fmha_fwd_first(q, k, v, 9, window=0)
+    b = binding.fmha_fwd(q, k, v)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_first_keys_captured_twice_on_one_stream():
+    """Two graphs of split calls captured on one stream and replayed at once keep their workspaces apart."""
+    r = gen(51)
+    sets, graphs, st = [], [], torch.cuda.Stream()
+    for i in range(2):
+        q, k, v = normal(r, 1, 8, 1, 128), normal(r, 1, 1, 9000, 128), normal(r, 1, 1, 9000, 128)
+        o, lse = binding.fmha_fwd_first(q, k, v, 4, window=8000)
+        sets.append((q, k, v, o, lse))
+    torch.cuda.synchronize()
+    for q, k, v, o, lse in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            binding.fmha_fwd_first(q, k, v, 4, window=8000, o=o, lse=lse)
+        graphs.append(graph)
+    for s in sets:
+        s[0].copy_(normal(r, 1, 8, 1, 128))
+    torch.cuda.synchronize()
+    lanes = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for graph, lane in zip(graphs, lanes):
+            with torch.cuda.stream(lane):
+                graph.replay()
+    torch.cuda.synchronize()
+    for q, k, v, o, lse in sets:
+        ref.assert_attention((o, lse), ref.attend(q, k, v, [9000], 128 ** -0.5, 8000, 4, p_bits=8))
+
+
 # ------------------------------------------------------------------ together, streams and graphs
 def step(s, stream=None):
     """One decode step: projection rows -> norm and rotation -> append -> attention."""
