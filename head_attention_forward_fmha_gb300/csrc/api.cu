@@ -965,7 +965,7 @@ extern "C" int fmha_qk_norm_rope(const void* qkv, long long batch_stride, long l
     if (token_stride < width || token_stride % 8 != 0 || batch_stride < 0 || batch_stride % 8 != 0)
         return fail(FMHA_ERR_SHAPE, "strides must be multiples of 8 elements, token_stride at least %lld", width);
     if ((long long)batch * T > INT_MAX) return fail(FMHA_ERR_SHAPE, "batch * T exceeds 2^31 - 1");
-    if ((long long)batch * T * ((long long)n_h + 2LL * n_kv_h) > (long long)INT_MAX * 4)
+    if ((long long)batch * T * ((long long)n_h + 2LL * n_kv_h) > INT_MAX)
         return fail(FMHA_ERR_SHAPE, "too many head rows");
     if (batch == 0 || T == 0) return FMHA_OK;
     if (!qkv || !q || !k || !v || (rot > 0 && (!cos_sin || !positions)))
@@ -1012,7 +1012,7 @@ extern "C" int fmha_kv4_append(const void* k, const void* v, void* k_codes, void
     if (cap < 0 || cap % 16 != 0) return fail(FMHA_ERR_SHAPE, "cap=%d must be a multiple of 16", cap);
     if (!(k_global > 0.f) || !std::isfinite(k_global) || !(v_global > 0.f) || !std::isfinite(v_global))
         return fail(FMHA_ERR_SHAPE, "k_global and v_global must be finite and > 0");
-    if ((long long)batch * n_kv_h > INT_MAX || (long long)batch * n_kv_h * T > (1LL << 36) / hd)
+    if ((long long)batch * n_kv_h > INT_MAX || (long long)batch * n_kv_h * T > INT_MAX)
         return fail(FMHA_ERR_SHAPE, "too many rows");
     if (batch == 0 || T == 0 || cap == 0) return FMHA_OK;
     if (!k || !v || !k_codes || !k_scales || !v_codes || !v_scales || !start)

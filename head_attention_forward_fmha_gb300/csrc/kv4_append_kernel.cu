@@ -6,8 +6,16 @@
 // values that the cache now stands for, g * s * e, come back as bf16 rows (s
 // e has at most 6 significant bits, so only the product with g can round).
 //
-// One thread per block, K and V in one launch: 32 bytes in, 9 out (41 with the
-// values).  Bound by HBM for long prompts, by launch latency for decode steps.
+// Two threads per 16-element block (16 bytes in each, coalesced), each for K and V.
+// 2 bytes in and 0.5625 out per element (2.5625 with the values): bound by HBM
+// for long prompts if the quantiser's arithmetic is cheap, by launch latency
+// for decode steps.  So the codes' divisions x / (g s) are done as
+//   q = x r,  q' = q + (x - q g s) r,  r = 1 / (g s) correctly rounded,
+// which is the correctly rounded quotient (Markstein 1990) as long as nothing
+// overflows or underflows, and the roundings to E4M3 and E2M1 are the
+// hardware's conversions, which go to nearest, ties to even, and saturate, as
+// the format asks.  A block with a NaN, an infinity or a scale g s outside
+// [2^-90, 2^90] takes the quantiser of nvfp4.cuh, and all of them give its codes.
 #include "internal.h"
 #include "nvfp4.cuh"
 #include "ptx.cuh"
@@ -15,69 +23,135 @@
 namespace fmha {
 namespace {
 
-__global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4Append a, int blocks_per_row) {
-    launch_dependents();
-    grid_dependency_wait();
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long rows = (long long)a.batch * a.n_kv_h * a.T;
-    const long long row = i / blocks_per_row;
-    const int blk = (int)(i - row * blocks_per_row);
-    if (row >= rows) return;
-    const bool is_v = blockIdx.y != 0;
-    const long long slab = row / a.T;
-    const long long at = __ldg(a.start + slab / a.n_kv_h) + (row - slab * a.T);
-    if (at < 0 || at >= a.cap) return;  // outside the cache: left out
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + i * 16);
-    const uint4 u0 = __ldcs(src), u1 = __ldcs(src + 1);
-    const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-    float x[16];
+// Eight fp32 values (as pairs) -> eight E2M1 codes, element i in bits 4 i.  The
+// conversion keeps the sign of values that round to zero; the format has none there.
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&y)[4]) {
+    uint32_t w;
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[2 * e] = bf16_lo(w[e]);
-        x[2 * e + 1] = bf16_hi(w[e]);
-    }
-    uint32_t pk[2];
-    const float g = is_v ? a.v_global : a.k_global;
-    const uint32_t sc = nvfp4_block(x, g, pk);
-    const long long dst = (slab * a.cap + at) * blocks_per_row + blk;
-    if (!FMHA_IN_BOUNDS(dst >= 0 && dst < (long long)a.batch * a.n_kv_h * a.cap * blocks_per_row, kSiteKv4Append, a.status))
-        return;
-    *reinterpret_cast<uint2*>((is_v ? a.v_codes : a.k_codes) + dst * 8) = make_uint2(pk[0], pk[1]);
-    (is_v ? a.v_scales : a.k_scales)[dst] = (uint8_t)sc;
-    __nv_bfloat16* out = is_v ? a.v_out : a.k_out;
-    if (out) {
-        const float s = e4m3_value(sc);
-        uint32_t o[8];
+    for (int i = 0; i < 4; ++i) f32x2_split(y[i], v[2 * i], v[2 * i + 1]);
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    const uint32_t some = (w | (w >> 1) | (w >> 2)) & 0x11111111u;  // magnitude not zero
+    return w & (0x77777777u | (some << 3));
+}
+
+// E4M3 code of a >= 0, finite.
+__device__ __forceinline__ uint32_t e4m3_code_cvt(float a) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(a));
+    return c;
+}
+
+// Codes, scale and values of this thread's 8 columns, of which its neighbour has the block's other 8.
+__device__ __forceinline__ void quantise8(const uint4& u, const __nv_bfloat16* block, float g, int half, uint32_t& codes,
+                                          uint32_t& sc) {
+    uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);  // largest magnitude of the block, as bf16 bits
+    sc = e4m3_code_cvt(__fdiv_rn(__uint_as_float(top << 16), __fmul_rn(6.f, g)));
+    const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16(sc) & 0xFFFFu)));
+    const float gs = __fmul_rn(g, s);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    codes = 0u;
+    if (top < 0x7F80u && (s == 0.f || (gs >= 0x1p-90f && gs <= 0x1p90f))) {
+        if (s > 0.f) {
+            const float r = __frcp_rn(gs);
+            const uint64_t r2 = f32x2(r, r), n2 = f32x2(-gs, -gs);
+            uint64_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t x = bf16x2_to_f32x2(w[e]);
+                const uint64_t q = mul_f32x2(x, r2);
+                y[e] = fma_f32x2(fma_f32x2(q, n2, x), r2, q);
+            }
+            codes = e2m1x8(y);
+        }
+    } else {
+        float x[16];
+        const uint4* src = reinterpret_cast<const uint4*>(block);
+        const uint4 u0 = __ldg(src), u1 = __ldg(src + 1);
+        const uint32_t z[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const uint32_t c = (pk[e >> 2] >> (8 * (e & 3) + 4 * f)) & 15u;
-                v[f] = __fmul_rn(__fmul_rn(e2m1_value(c), s), g);
-            }
-            o[e] = pack_bf16x2(v[0], v[1]);
+            x[2 * e] = bf16_lo(z[e]);
+            x[2 * e + 1] = bf16_hi(z[e]);
         }
-        uint4* to = reinterpret_cast<uint4*>(out + i * 16);
-        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        uint32_t pk[2];
+        sc = nvfp4_block(x, g, pk);
+        codes = half ? pk[1] : pk[0];
+    }
+}
+
+// The bf16 values of 8 codes under scale code sc.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sc, float g) {
+    const uint32_t s2 = __byte_perm(e4m3x2_to_f16(sc), 0u, 0x1010);
+    uint32_t f[4], o[4];
+    e2m1x8_to_f16(codes, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[e] = mul_f16x2(f[e], s2);  // exact
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[e]));
+        o[e] = pack_bf16x2(__fmul_rn(v.x, g), __fmul_rn(v.y, g));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One thread: 8 columns of one row of K and of V.  log_tpr: log2 of hd / 8.
+__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Append a, int log_tpr) {
+    launch_dependents();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const unsigned rows = (unsigned)(a.batch * a.n_kv_h) * (unsigned)a.T;  // < 2^31
+    const unsigned row = (unsigned)(i >> log_tpr);
+    const int part = (int)i & ((1 << log_tpr) - 1);
+    const unsigned slab = row / (unsigned)a.T, t = row - slab * (unsigned)a.T;
+    grid_dependency_wait();
+    // The two threads of a block are neighbours in a warp and live or die together.
+    long long at = -1;
+    uint4 uk = make_uint4(0u, 0u, 0u, 0u), uv = uk;
+    if (row < rows) {
+        uk = __ldcs(reinterpret_cast<const uint4*>(a.k + i * 8));
+        uv = __ldcs(reinterpret_cast<const uint4*>(a.v + i * 8));
+        at = __ldg(a.start + slab / (unsigned)a.n_kv_h) + (long long)t;
+    }
+    uint32_t ck, cv, sk, sv;
+    quantise8(uk, a.k + (i & ~1LL) * 8, a.k_global, part & 1, ck, sk);
+    quantise8(uv, a.v + (i & ~1LL) * 8, a.v_global, part & 1, cv, sv);
+    if (at < 0 || at >= a.cap) return;  // outside the cache, or past the rows: left out
+    const long long dst = (((long long)slab * a.cap + at) << log_tpr) + part;
+    if (!FMHA_IN_BOUNDS(dst >= 0 && dst < ((long long)a.batch * a.n_kv_h * a.cap) << log_tpr, kSiteKv4Append, a.status)) return;
+    *reinterpret_cast<uint32_t*>(a.k_codes + dst * 4) = ck;
+    *reinterpret_cast<uint32_t*>(a.v_codes + dst * 4) = cv;
+    if ((part & 1) == 0) {
+        a.k_scales[dst >> 1] = (uint8_t)sk;
+        a.v_scales[dst >> 1] = (uint8_t)sv;
+    }
+    if (a.k_out) {
+        __stcs(reinterpret_cast<uint4*>(a.k_out + i * 8), values8(ck, sk, a.k_global));
+        __stcs(reinterpret_cast<uint4*>(a.v_out + i * 8), values8(cv, sv, a.v_global));
     }
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4Append& a, int hd, cudaStream_t stream) {
-    const int per_row = hd / 16;
-    const long long blocks = (long long)a.batch * a.n_kv_h * a.T * per_row;
-    if ((blocks + 127) / 128 > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int log_tpr = hd == 64 ? 3 : hd == 128 ? 4 : hd == 256 ? 5 : 6;
+    const long long blocks = (((long long)a.batch * a.n_kv_h * a.T << log_tpr) + 255) / 256;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((blocks + 127) / 128), 2);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_append_kernel, a, per_row);
+    return cudaLaunchKernelEx(&cfg, kv4_append_kernel, a, log_tpr);
 }
 
 }  // namespace fmha

@@ -37,6 +37,7 @@
 // down to 2^-20 of the reference.
 #include <climits>
 #include <atomic>
+#include <type_traits>
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -57,7 +58,7 @@ struct K4Cfg {
     static constexpr int OFF_VC = OFF_KS + KT * SB;
     static constexpr int OFF_VS = OFF_VC + KT * CB;
     static constexpr int STAGE = OFF_VS + KT * SB;
-    static constexpr int STAGES = HD == 512 ? 3 : 4;
+    static constexpr int STAGES = HD == 256 ? 4 : 3;
     static constexpr int RING = STAGES * STAGE;        // per warp
     static constexpr int NCH = HD >= 128 ? HD / 128 : 1;  // 128-column chunks
     static constexpr int TW = HD >= 128 ? 32 : 16;     // columns of a chunk per lane in S^T
@@ -79,7 +80,8 @@ struct K4Cfg {
 struct K4Args {
     Kv4Fwd f;
     int group, R;
-    float sl2;  // scale * k_global * log2(e)
+    float sl2;       // |scale| * k_global * log2(e), 1 for a scale of zero
+    float sl2_sign;  // of the scale: -1, 0 or 1
     long long rows_total;
 };
 
@@ -258,7 +260,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             // subnormals, infinities or NaN stay as they are
             const int e = (int)(mx >> 7);
             const int k = (e > 0 && e < 255) ? min(max(14 - (e - 127), -120), 120) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+            // the sign of the scale goes into Q, so that a larger product is a larger score
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2_sign;
             fac_g[nb] = __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
             for (int i = 0; i < C::QSTEPS; ++i) {
@@ -318,19 +321,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
 
     const int row_a = key_of_row(g), row_b = row_a + 8;            // S^T rows of this lane
     const int key_x = key_of_row(2 * t4), key_y = key_of_row(2 * t4 + 1);  // P's keys (and + 8)
-    bool ok = true;
-    for (int i = 0; i < my_tiles; ++i) {
-        const int s = i % C::STAGES;
-        if (!mbar_wait(&full[s], (i / C::STAGES) & 1, f.status)) {
-            ok = false;
-            break;
-        }
-        const uint32_t st = ring + s * C::STAGE;
-        int key0, end;
-        tile_of(i, key0, end);
-        const bool head = warp + i * kWarps < n_head;
-        const bool whole = !head && key0 >= full_lo && key0 + KT - 1 <= full_hi;
-
+    // One tile.  EDGE: some key of it is masked for some row, or holds no data.
+    auto tile_step = [&](auto edge, uint32_t st, int key0, int end, bool head) {
+        constexpr bool EDGE = decltype(edge)::value;
         float sc[GR][NB][4];
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
@@ -376,42 +369,47 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             }
         }
 
-        // scale, mask, running reference
-        bool grow = false;
+        // mask, running reference
+        if constexpr (EDGE) {
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[gr][nb][e] * qs[nb][e & 1];
-                    if (!whole) {
+                    for (int e = 0; e < 4; ++e) {
                         const int key = key0 + gr * 16 + (e < 2 ? row_a : row_b);
-                        const int jl = jlo[nb][e & 1], jh = jhi[nb][e & 1];
-                        bool in = key >= jl && key <= jh;
+                        bool in = key >= jlo[nb][e & 1] && key <= jhi[nb][e & 1];
                         if (head) {
                             const int r = r_begin + nb * 8 + 2 * t4 + (e & 1);
                             in = r < r_end && key < n_first && (!f.causal || key <= len - f.T + r % f.T);
                         }
-                        x = in ? x : -INFINITY;
+                        sc[gr][nb][e] = in ? sc[gr][nb][e] : -INFINITY;
                     }
-                    sc[gr][nb][e] = x;
-                    grow |= x > m_ref[nb][e & 1] + 8.f;
-                }
+        }
+        float mx[NB][2];
+        bool grow = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float m = -INFINITY;
+#pragma unroll
+                for (int gr = 0; gr < GR; ++gr) m = fmaxf(m, fmaxf(sc[gr][nb][q], sc[gr][nb][2 + q]));
+                mx[nb][q] = m * qs[nb][q];
+                grow |= mx[nb][q] > m_ref[nb][q] + 8.f;
+            }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int gr = 0; gr < GR; ++gr) mx = fmaxf(mx, fmaxf(sc[gr][nb][q], sc[gr][nb][2 + q]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    if (mx > m_ref[nb][q] + 8.f) {
-                        const float alpha = ex2_approx(m_ref[nb][q] - mx);  // 0 when the reference was -inf
-                        m_ref[nb][q] = mx;
+                    float m = mx[nb][q];
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m > m_ref[nb][q] + 8.f) {
+                        const float alpha = ex2_approx(m_ref[nb][q] - m);  // 0 when the reference was -inf
+                        m_ref[nb][q] = m;
                         l[nb][q] *= alpha;
 #pragma unroll
                         for (int d = 0; d < C::ODB; ++d) {
@@ -424,12 +422,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         uint32_t pb[GR][NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float mu0 = (m_ref[nb][0] == -INFINITY ? 0.f : m_ref[nb][0]) - kPBias;
-            const float mu1 = (m_ref[nb][1] == -INFINITY ? 0.f : m_ref[nb][1]) - kPBias;
+            const float mu0 = kPBias - (m_ref[nb][0] == -INFINITY ? 0.f : m_ref[nb][0]);
+            const float mu1 = kPBias - (m_ref[nb][1] == -INFINITY ? 0.f : m_ref[nb][1]);
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr) {
-                const float p0 = ex2_approx(sc[gr][nb][0] - mu0), p1 = ex2_approx(sc[gr][nb][1] - mu1);
-                const float p2 = ex2_approx(sc[gr][nb][2] - mu0), p3 = ex2_approx(sc[gr][nb][3] - mu1);
+                const float p0 = ex2_approx(fmaf(sc[gr][nb][0], qs[nb][0], mu0));
+                const float p1 = ex2_approx(fmaf(sc[gr][nb][1], qs[nb][1], mu1));
+                const float p2 = ex2_approx(fmaf(sc[gr][nb][2], qs[nb][0], mu0));
+                const float p3 = ex2_approx(fmaf(sc[gr][nb][3], qs[nb][1], mu1));
                 l[nb][0] += p0 + p2;
                 l[nb][1] += p1 + p3;
                 pb[gr][nb][0] = movmatrix_t(pack_f16x2(p0, p1));
@@ -440,22 +440,27 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         // O^T += V^T P^T
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
-            // Rows outside [.., end) hold stale or no data: their scales count as
+            // Keys outside [from, end) hold stale or no data: their scales count as
             // zero, so that P = 0 meets 0 and never a NaN.
-            const int kx = key0 + gr * 16 + key_x, ky = key0 + gr * 16 + key_y;
-            const int from = head ? 0 : u_lo;
-            const bool zx = !whole && (kx < from || kx >= end), zy = !whole && (ky < from || ky >= end);
-            const bool zx8 = !whole && (kx + 8 < from || kx + 8 >= end), zy8 = !whole && (ky + 8 < from || ky + 8 >= end);
+            bool in_x = true, in_y = true, in_x8 = true, in_y8 = true;
+            if constexpr (EDGE) {
+                const int kx = key0 + gr * 16 + key_x, ky = key0 + gr * 16 + key_y;
+                const int from = head ? 0 : u_lo;
+                in_x = kx >= from && kx < end;
+                in_y = ky >= from && ky < end;
+                in_x8 = kx + 8 >= from && kx + 8 < end;
+                in_y8 = ky + 8 >= from && ky + 8 < end;
+            }
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c) {
                 const uint32_t vs = st + C::OFF_VS + gr * 16 * C::SB + c * 8 + (HD >= 128 ? g : g >> 1);
                 uint32_t s0 = lds8(vs + key_x * C::SB), s1 = lds8(vs + key_y * C::SB);
                 uint32_t s2 = lds8(vs + (key_x + 8) * C::SB), s3 = lds8(vs + (key_y + 8) * C::SB);
-                if (!whole) {
-                    s0 = zx ? 0u : s0;
-                    s1 = zy ? 0u : s1;
-                    s2 = zx8 ? 0u : s2;
-                    s3 = zy8 ? 0u : s3;
+                if constexpr (EDGE) {
+                    s0 = in_x ? s0 : 0u;
+                    s1 = in_y ? s1 : 0u;
+                    s2 = in_x8 ? s2 : 0u;
+                    s3 = in_y8 ? s3 : 0u;
                 }
                 const uint32_t sp = e4m3x2_to_f16(s0 | (s1 << 8)), sq = e4m3x2_to_f16(s2 | (s3 << 8));
                 constexpr int W = HD >= 128 ? 2 : 1;
@@ -488,6 +493,21 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                 }
             }
         }
+    };
+    bool ok = true;
+    for (int i = 0; i < my_tiles; ++i) {
+        const int s = i % C::STAGES;
+        if (!mbar_wait(&full[s], (i / C::STAGES) & 1, f.status)) {
+            ok = false;
+            break;
+        }
+        int key0, end;
+        tile_of(i, key0, end);
+        const bool head = warp + i * kWarps < n_head;
+        if (!head && key0 >= full_lo && key0 + KT - 1 <= full_hi)
+            tile_step(std::false_type{}, ring + s * C::STAGE, key0, end, false);
+        else
+            tile_step(std::true_type{}, ring + s * C::STAGE, key0, end, head);
         __syncwarp();  // every lane is done with the stage
         if (lane == 0 && issued == i + C::STAGES && issued < my_tiles && issue(issued)) ++issued;
     }
@@ -594,7 +614,9 @@ cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
     a.f = f;
     a.group = f.n_h / f.n_kv_h;
     a.R = a.group * f.T;
-    a.sl2 = (float)((double)f.scale * f.k_global * 1.4426950408889634);
+    const double sl2 = (double)f.scale * f.k_global * 1.4426950408889634;
+    a.sl2_sign = sl2 > 0 ? 1.f : sl2 < 0 ? -1.f : 0.f;
+    a.sl2 = sl2 != 0 ? (float)(sl2 < 0 ? -sl2 : sl2) : 1.f;
     a.rows_total = (long long)f.batch * f.n_h * f.T;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.R + C::RT - 1) / C::RT, f.n_splits, f.batch * f.n_kv_h);

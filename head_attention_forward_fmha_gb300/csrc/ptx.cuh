@@ -339,10 +339,21 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+
+// The two bf16 halves of a packed pair as an fp32 pair.
+__device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t pk) {
+    return f32x2(__uint_as_float(pk << 16), __uint_as_float(pk & 0xffff0000u));
 }
 
 // The two bf16 halves of a packed pair, widened exactly to fp32.

@@ -15,9 +15,12 @@
 // each holding two 4-element vectors that contain whole rotation pairs (the
 // lower and the upper half's columns, or 8 neighbouring ones when
 // interleaved), so the rotation needs no exchange between lanes and the sum of
-// squares is one shuffle tree.  A warp takes UNROLL row sets of one token at
-// a time, with all their loads issued before any arithmetic; the cosines and
-// sines of the token stay in registers for all of its heads.
+// squares is one shuffle tree.  A warp takes up to UNROLL row sets of one kind
+// (query, key or value heads) of one token, with all their loads issued before
+// any arithmetic.  Norm weight and rotation are one linear map of a pair of
+// columns, out = x A + x' B with A, B made of the weights, cosines and sines;
+// a warp forms A and B once and applies them to all its heads, two columns per
+// instruction (packed fp32 pairs).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -33,146 +36,168 @@ struct NrCfg {
     static constexpr int UNITS = HD / 8 / LANES;           // pairs of 4-element vectors per lane
 };
 
-// Columns of vector `half` (0 lower, 1 upper) of unit u of a head row.
-template <int HD>
-__device__ __forceinline__ int nr_column(int u, int half, int rot, bool interleaved) {
-    const int c = 8 * u;
-    if (interleaved || c >= rot) return c + 4 * half;
-    return 4 * u + half * (rot >> 1);
-}
-
-__device__ __forceinline__ void nr_unpack(uint2 v, float (&x)[4]) {
-    x[0] = bf16_lo(v.x);
-    x[1] = bf16_hi(v.x);
-    x[2] = bf16_lo(v.y);
-    x[3] = bf16_hi(v.y);
-}
-
 template <int HD, int UNROLL>
-__global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNormRope a) {
+__global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNormRope a, int q_sets, int kv_sets) {
     using C = NrCfg<HD>;
     launch_dependents();
-    grid_dependency_wait();  // every global access below follows the preceding kernel
     const int lane = threadIdx.x & 31;
-    const int heads = a.n_h + 2 * a.n_kv_h;
     constexpr int kSet = C::RPW * UNROLL;  // heads per warp
-    const int sets = (heads + kSet - 1) / kSet;
-    const long long task = (long long)blockIdx.x * kNrWarps + (threadIdx.x >> 5);
-    const long long token = task / sets;
-    if (token >= (long long)a.batch * a.T) return;
-    const int set = (int)(task - token * sets);
-    const int b = (int)(token / a.T), t = (int)(token - (long long)b * a.T);
+    const int sets = q_sets + 2 * kv_sets;
+    const unsigned task = blockIdx.x * kNrWarps + (threadIdx.x >> 5);  // < 2^31 + 4
+    const int token = (int)(task / (unsigned)sets);
+    if (token >= a.batch * a.T) return;
+    int set = (int)(task - (unsigned)token * sets);
+    const int type = set < q_sets ? 0 : set < q_sets + kv_sets ? 1 : 2;  // q, k, v: the same for the warp
+    if (type == 1) set -= q_sets;
+    if (type == 2) set -= q_sets + kv_sets;
+    const int heads = type == 0 ? a.n_h : a.n_kv_h;
+    const int b = token / a.T, t = token - b * a.T;
     const int sub = lane / C::LANES, u0 = lane - sub * C::LANES;
-
-    // Every load is issued before any arithmetic.
-    const __nv_bfloat16* row = a.qkv + b * a.batch_stride + t * a.token_stride;
-    uint2 raw[UNROLL][C::UNITS][2];
-#pragma unroll
-    for (int i = 0; i < UNROLL; ++i) {
-        const int h = set * kSet + i * C::RPW + sub;
-        if (h >= heads) continue;
-#pragma unroll
-        for (int k = 0; k < C::UNITS; ++k)
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                raw[i][k][f] = __ldcs(reinterpret_cast<const uint2*>(
-                    row + (long long)h * HD + nr_column<HD>(u0 + k * C::LANES, f, a.rot, a.interleaved)));
-    }
-    const int pos = a.rot > 0 ? __ldg(a.positions + token) : 0;
-    if (a.rot > 0 && (pos < 0 || pos >= a.max_pos)) return;  // a padding token: nothing of it is written
-    float4 cs[C::UNITS], sn[C::UNITS];
+    const int h0 = set * kSet + sub;  // this lane's heads of the kind: h0, h0 + RPW, ...
+    const bool inter = a.interleaved != 0;
+    const int half = a.rot >> 1;
+    int col[C::UNITS][2];
+    bool turned[C::UNITS];
 #pragma unroll
     for (int k = 0; k < C::UNITS; ++k) {
         const int u = u0 + k * C::LANES;
-        cs[k] = make_float4(1.f, 1.f, 1.f, 1.f);
-        sn[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (8 * u < a.rot) {
-            const float* tab = a.cos_sin + (long long)pos * a.rot + 4 * u;
-            cs[k] = __ldg(reinterpret_cast<const float4*>(tab));
-            sn[k] = __ldg(reinterpret_cast<const float4*>(tab + (a.rot >> 1)));
-        }
+        turned[k] = 8 * u < a.rot;
+        col[k][0] = turned[k] && !inter ? 4 * u : 8 * u;
+        col[k][1] = turned[k] && !inter ? half + 4 * u : 8 * u + 4;
     }
-    const long long kv_row = (a.kv_start ? __ldg(a.kv_start + b) : 0) + (long long)t;
-    const bool kv_ok = kv_row >= 0 && kv_row < a.kv_rows;
+    grid_dependency_wait();  // every global access below follows the preceding kernel
 
+    // Every load is issued before any arithmetic.
+    const __nv_bfloat16* src = a.qkv + b * a.batch_stride + t * a.token_stride +
+                               (long long)(h0 + (type == 0 ? 0 : a.n_h + (type == 2 ? a.n_kv_h : 0))) * HD;
+    uint2 raw[UNROLL][C::UNITS][2];
 #pragma unroll
-    for (int i = 0; i < UNROLL; ++i) {
-        const int h = set * kSet + i * C::RPW + sub;
-        const bool live = h < heads;
-        const int type = h < a.n_h ? 0 : h < a.n_h + a.n_kv_h ? 1 : 2;  // q, k, v
-        float x[C::UNITS][2][4];
-        float ss = 0.f;
+    for (int i = 0; i < UNROLL; ++i)
 #pragma unroll
         for (int k = 0; k < C::UNITS; ++k)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                nr_unpack(live ? raw[i][k][f] : make_uint2(0u, 0u), x[k][f]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ss += x[k][f][e] * x[k][f][e];
+                raw[i][k][f] = make_uint2(0u, 0u);
+                if (h0 + i * C::RPW < heads)
+                    raw[i][k][f] = __ldcs(reinterpret_cast<const uint2*>(src + i * C::RPW * HD + col[k][f]));
             }
-#pragma unroll
-        for (int m = C::LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        if (!live) continue;
-        __nv_bfloat16* dst;
-        if (type == 0) {
-            dst = a.q + (((long long)b * a.n_h + h) * a.T + t) * HD;
-        } else {
-            if (!kv_ok) continue;
-            const int kvh = h - a.n_h - (type == 2 ? a.n_kv_h : 0);
-            dst = (type == 1 ? a.k : a.v) + (((long long)b * a.n_kv_h + kvh) * a.kv_rows + kv_row) * HD;
-        }
+    const int pos = a.rot > 0 ? __ldg(a.positions + token) : 0;
+    if (a.rot > 0 && (pos < 0 || pos >= a.max_pos)) return;  // a padding token: nothing of it is written
+    __nv_bfloat16* dst;
+    long long step;  // elements from one head to the next
+    if (type == 0) {
+        step = (long long)a.T * HD;
+        dst = a.q + ((long long)b * a.n_h * a.T + t) * HD;
+    } else {
+        const long long kv_row = (a.kv_start ? __ldg(a.kv_start + b) : 0) + (long long)t;
+        if (kv_row < 0 || kv_row >= a.kv_rows) return;
+        step = (long long)a.kv_rows * HD;
+        dst = (type == 1 ? a.k : a.v) + ((long long)b * a.n_kv_h * a.kv_rows + kv_row) * HD;
+    }
+    dst += h0 * step;
+    if (!FMHA_IN_BOUNDS(col[0][0] >= 0 && col[C::UNITS - 1][1] + 4 <= HD && col[C::UNITS - 1][0] + 4 <= HD, kSiteNrCol, a.status))
+        return;
+
+    if (type != 2) {
+        // A and B of this lane's columns, as pairs of neighbouring columns
         const float* w = type == 0 ? a.q_weight : a.k_weight;
-        const float inv = rsqrtf(ss * (1.f / HD) + a.eps);
+        uint64_t ca[C::UNITS][2][2], cb[C::UNITS][2][2];
 #pragma unroll
         for (int k = 0; k < C::UNITS; ++k) {
-            const int u = u0 + k * C::LANES;
-            const int col0 = nr_column<HD>(u, 0, a.rot, a.interleaved), col1 = nr_column<HD>(u, 1, a.rot, a.interleaved);
-            uint2 out0 = raw[i][k][0], out1 = raw[i][k][1];
-            if (type != 2) {
-                float(&lo)[4] = x[k][0];
-                float(&hi)[4] = x[k][1];
-                if (w) {
-                    const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + col0));
-                    const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + col1));
-                    lo[0] *= inv * w0.x; lo[1] *= inv * w0.y; lo[2] *= inv * w0.z; lo[3] *= inv * w0.w;
-                    hi[0] *= inv * w1.x; hi[1] *= inv * w1.y; hi[2] *= inv * w1.z; hi[3] *= inv * w1.w;
+            float w4[2][4], c4[4] = {1.f, 1.f, 1.f, 1.f}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const float4 v = w ? __ldg(reinterpret_cast<const float4*>(w + col[k][f])) : make_float4(1.f, 1.f, 1.f, 1.f);
+                w4[f][0] = v.x; w4[f][1] = v.y; w4[f][2] = v.z; w4[f][3] = v.w;
+            }
+            if (turned[k]) {
+                const float* tab = a.cos_sin + (long long)pos * a.rot + 4 * (u0 + k * C::LANES);
+                const float4 c = __ldg(reinterpret_cast<const float4*>(tab));
+                const float4 s = __ldg(reinterpret_cast<const float4*>(tab + half));
+                c4[0] = c.x; c4[1] = c.y; c4[2] = c.z; c4[3] = c.w;
+                s4[0] = s.x; s4[1] = s.y; s4[2] = s.z; s4[3] = s.w;
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * e, j = 2 * e + 1;
+                    if (inter) {  // columns i and j of one vector are a pair, number 2 f + e
+                        const float c = c4[2 * f + e], s = s4[2 * f + e];
+                        ca[k][f][e] = f32x2(w4[f][i] * c, w4[f][j] * c);
+                        cb[k][f][e] = f32x2(-w4[f][j] * s, w4[f][i] * s);
+                    } else {  // column i of the lower vector pairs with column i of the upper one
+                        ca[k][f][e] = f32x2(w4[f][i] * c4[i], w4[f][j] * c4[j]);
+                        const float sign = f == 0 ? -1.f : 1.f;
+                        cb[k][f][e] = f32x2(sign * w4[1 - f][i] * s4[i], sign * w4[1 - f][j] * s4[j]);
+                    }
                 }
-                const float c4[4] = {cs[k].x, cs[k].y, cs[k].z, cs[k].w};
-                const float s4[4] = {sn[k].x, sn[k].y, sn[k].z, sn[k].w};
-                if (8 * u >= a.rot) {
-                    // past the rotated columns
-                } else if (a.interleaved) {  // pairs (0,1) (2,3) of the lower vector, then of the upper one
+        }
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            uint64_t x[C::UNITS][2][2], ss2 = 0ull;
+#pragma unroll
+            for (int k = 0; k < C::UNITS; ++k)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    x[k][f][0] = bf16x2_to_f32x2(raw[i][k][f].x);
+                    x[k][f][1] = bf16x2_to_f32x2(raw[i][k][f].y);
+                    ss2 = fma_f32x2(x[k][f][0], x[k][f][0], ss2);
+                    ss2 = fma_f32x2(x[k][f][1], x[k][f][1], ss2);
+                }
+            float inv = 1.f;
+            if (w) {
+                float s0, s1;
+                f32x2_split(ss2, s0, s1);
+                float ss = s0 + s1;
+#pragma unroll
+                for (int m = C::LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                inv = rsqrtf(ss * (1.f / HD) + a.eps);
+            }
+            const uint64_t inv2 = f32x2(inv, inv);
+#pragma unroll
+            for (int k = 0; k < C::UNITS; ++k)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    uint32_t out[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float l0 = lo[2 * e], l1 = lo[2 * e + 1], h0 = hi[2 * e], h1 = hi[2 * e + 1];
-                        lo[2 * e] = l0 * c4[e] - l1 * s4[e];
-                        lo[2 * e + 1] = l1 * c4[e] + l0 * s4[e];
-                        hi[2 * e] = h0 * c4[2 + e] - h1 * s4[2 + e];
-                        hi[2 * e + 1] = h1 * c4[2 + e] + h0 * s4[2 + e];
+                        const uint64_t y = mul_f32x2(x[k][f][e], inv2);
+                        uint64_t r = mul_f32x2(y, ca[k][f][e]);
+                        if (turned[k]) {
+                            uint64_t z;
+                            if (inter) {
+                                float y0, y1;
+                                f32x2_split(y, y0, y1);
+                                z = f32x2(y1, y0);
+                            } else {
+                                z = mul_f32x2(x[k][1 - f][e], inv2);
+                            }
+                            r = fma_f32x2(z, cb[k][f][e], r);
+                        }
+                        float r0, r1;
+                        f32x2_split(r, r0, r1);
+                        out[e] = pack_bf16x2(r0, r1);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float l0 = lo[e], h0 = hi[e];
-                        lo[e] = l0 * c4[e] - h0 * s4[e];
-                        hi[e] = h0 * c4[e] + l0 * s4[e];
-                    }
+                    raw[i][k][f] = make_uint2(out[0], out[1]);
                 }
-                out0 = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
-                out1 = make_uint2(pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]));
-            }
-            if (!FMHA_IN_BOUNDS(col0 >= 0 && col0 + 4 <= HD && col1 >= 0 && col1 + 4 <= HD, kSiteNrCol, a.status)) continue;
-            *reinterpret_cast<uint2*>(dst + col0) = out0;
-            *reinterpret_cast<uint2*>(dst + col1) = out1;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+        if (h0 + i * C::RPW >= heads) break;
+#pragma unroll
+        for (int k = 0; k < C::UNITS; ++k)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) __stcs(reinterpret_cast<uint2*>(dst + i * C::RPW * step + col[k][f]), raw[i][k][f]);
     }
 }
 
 template <int HD, int UNROLL>
 cudaError_t launch_u(const QkNormRope& a, cudaStream_t stream) {
-    const int heads = a.n_h + 2 * a.n_kv_h;
-    const int sets = (heads + NrCfg<HD>::RPW * UNROLL - 1) / (NrCfg<HD>::RPW * UNROLL);
-    const long long tasks = (long long)a.batch * a.T * sets;
+    constexpr int kSet = NrCfg<HD>::RPW * UNROLL;
+    const int q_sets = (a.n_h + kSet - 1) / kSet, kv_sets = (a.n_kv_h + kSet - 1) / kSet;
+    const long long tasks = (long long)a.batch * a.T * (q_sets + 2 * kv_sets);
     const long long blocks = (tasks + kNrWarps - 1) / kNrWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -182,13 +207,13 @@ cudaError_t launch_u(const QkNormRope& a, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<HD, UNROLL>, a);
+    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<HD, UNROLL>, a, q_sets, kv_sets);
 }
 
 template <int HD>
 cudaError_t launch_hd(const QkNormRope& a, cudaStream_t stream) {
     const long long rows = (long long)a.batch * a.T * (a.n_h + 2 * a.n_kv_h);
-    return rows >= 65536 ? launch_u<HD, 4>(a, stream) : launch_u<HD, 1>(a, stream);
+    return rows >= 16384 ? launch_u<HD, 4>(a, stream) : launch_u<HD, 1>(a, stream);
 }
 
 }  // namespace
