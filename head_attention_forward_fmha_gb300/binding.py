@@ -408,6 +408,7 @@ def fmha_set_kernel_path(path):
     one row tile per block (TS form)."""
     _check(load().fmha_set_kernel_path(int(path)), "fmha_set_kernel_path")
     _first_plans.clear()
+    _kv4_plans.clear()
 
 
 def fmha_fwd_noalloc(q, k, v, o, lse, scale=None, window=0, causal=False, stream=None):

@@ -907,15 +907,26 @@ int check_kv4(int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, f
     return FMHA_OK;
 }
 
+// Kernel and chunks of the 4-bit attention.  The tensor-core kernel takes over
+// where a KV head has so many query rows that the other one, which converts the
+// cache again for every 8 to 32 rows, costs more; fmha_set_kernel_path applies
+// here too (1: never, 2 to 4: always).
+bool kv4_use_tc(int hd, long long R) {
+    const int ov = g_path_override.load();
+    if (ov != 0) return ov >= 2;
+    return R >= (hd <= 128 ? 48 : 24);
+}
+
 // Chunks of the virtual key axis (first keys rounded up to tiles, then the
 // window) for sequences of s_k keys: the smallest number of chunks whose
 // estimated time is least.  A block's time is its share of its SM's HBM rate
-// (42 KB/us per SM, spread over the resident blocks) plus ~1.5 us of latency;
-// splitting adds the merge.
+// (42 KB/us per SM, spread over the resident blocks) plus ~1.5 us of latency,
+// or with the tensor-core kernel ~1.4 us per tile and 4 us; splitting adds the merge.
 void plan_kv4(Kv4Fwd* f) {
-    const int tile = kv4_kv_tile(f->hd), unit = 4 * tile;
     const long long R = (long long)f->n_h / f->n_kv_h * f->T;
-    const int rows = kv4_rows_per_cta(f->hd, R), per_sm = kv4_ctas_per_sm(f->hd, rows);
+    f->tc = kv4_use_tc(f->hd, R);
+    const int tile = f->tc ? kv4_tc_kv_tile(f->hd) : kv4_kv_tile(f->hd), unit = f->tc ? tile : 4 * tile;
+    const int rows = f->tc ? 128 : kv4_rows_per_cta(f->hd, R), per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows);
     // The longest axis that any length up to s_k gives: its body holds at most
     // window + T - 1 keys and starts up to 15 keys early.
     long long span = f->s_k;
@@ -923,7 +934,8 @@ void plan_kv4(Kv4Fwd* f) {
         span = (f->n_first + tile - 1) / tile * tile + std::min<long long>(f->s_k, (long long)f->window + f->T - 1 + 15);
     if (span < 1) span = 1;
     if (f->kv_chunk <= 0) {
-        const long long units = (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows);
+        const long long units =
+            (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
         const long long slots = (long long)sm_count() * per_sm;
         const double key_bytes = f->hd * 2 * 0.5625;
         double best = 0;
@@ -932,7 +944,8 @@ void plan_kv4(Kv4Fwd* f) {
         for (long long n = 1; n <= max_n; ++n) {
             const long long keys = ((span + n - 1) / n + unit - 1) / unit * unit;
             const long long waves = (units * n + slots - 1) / slots;
-            double us = (double)waves * (1.5 + (double)keys * key_bytes * per_sm / 42e3);
+            double us = f->tc ? (double)waves * (4.0 + (double)keys / tile * 1.4)
+                              : (double)waves * (1.5 + (double)keys * key_bytes * per_sm / 42e3);
             if (n > 1) us += 2.0 + (double)R * f->batch * f->n_kv_h * f->hd * 4.0 * (double)n / 8e6;
             if (n == 1 || us < best * 0.98) {
                 best = us;
@@ -1105,7 +1118,7 @@ extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_sc
     }
     f.status = device_status_word();
     if (!f.status) return fail(FMHA_ERR_LAUNCH, "cannot resolve the device status word");
-    cudaError_t e = launch_kv4_fwd(f, stream);
+    cudaError_t e = f.tc ? launch_kv4_tc(f, stream) : launch_kv4_fwd(f, stream);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit attention kernel launch");
     if (f.n_splits > 1) {
         e = launch_merge(f.o_part, f.lse_part, nullptr, f.n_splits, rows, hd, false, o, lse, stream, sink, T, n_h);

@@ -171,13 +171,18 @@ struct Kv4Fwd {
     float *o_part, *lse_part;  // n_splits > 1
     float k_global, v_global, scale;
     int batch, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, causal;
-    int kv_chunk, n_splits;  // keys per chunk (a multiple of kv4_kv_tile(hd)) and their number
+    int kv_chunk, n_splits;  // keys per chunk (a multiple of the kernel's key tile) and their number
+    bool tc;                 // the tensor-core kernel
     unsigned* status;
 };
 int kv4_kv_tile(int hd);                       // keys per tile
 int kv4_rows_per_cta(int hd, long long rows);  // query rows per thread block, given the rows per KV head
 int kv4_ctas_per_sm(int hd, int rows_per_cta);
 cudaError_t launch_kv4_fwd(const Kv4Fwd& a, cudaStream_t stream);
+// 128-row query tiles on the tcgen05 tensor cores (kv4_tc_kernel.cu)
+int kv4_tc_kv_tile(int hd);
+int kv4_tc_blocks_per_row_tile(int hd);
+cudaError_t launch_kv4_tc(const Kv4Fwd& a, cudaStream_t stream);
 
 // ---- host-side errors (api.cu): set the calling thread's message, return code
 int fail(int code, const char* fmt, ...);

@@ -199,7 +199,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
 
     const uint32_t ring = smem_u32(smem) + warp * C::RING;
     uint64_t* full = bars + warp * C::STAGES;
-    const long long slab_row = (long long)slab * f.cap;
+    // this slab's rows
+    const uint8_t* const kc = f.k_codes + (long long)slab * f.cap * C::CB;
+    const uint8_t* const ks = f.k_scales + (long long)slab * f.cap * C::SB;
+    const uint8_t* const vc = f.v_codes + (long long)slab * f.cap * C::CB;
+    const uint8_t* const vs = f.v_scales + (long long)slab * f.cap * C::SB;
     const uint64_t pol = l2_policy_evict_first();
     const int my_tiles = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
 
@@ -214,26 +218,25 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             end = b_hi;
         }
     };
-    auto issue = [&](int i) {  // one lane; the stage is free
+    auto issue = [&](int i, int s) {  // one lane; tile i into stage s = i % STAGES, which is free
         int key, end;
         tile_of(i, key, end);
         const int n = min(KT, ((warp + i * kWarps) < n_head ? head_end16 : body_end16) - key);
         if (!FMHA_IN_BOUNDS(key >= 0 && key % 16 == 0 && n > 0 && n % 16 == 0 && key + n <= f.cap, kSiteKv4Copy, f.status))
             return false;
-        const int s = i % C::STAGES;
         const uint32_t dst = ring + s * C::STAGE;
-        const long long r = slab_row + key;
+        const unsigned long long r = (unsigned)key;
         mbar_arrive_expect_tx(&full[s], n * 2 * (C::CB + C::SB));
-        bulk_load_hint(dst, f.k_codes + r * C::CB, n * C::CB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_KS, f.k_scales + r * C::SB, n * C::SB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_VC, f.v_codes + r * C::CB, n * C::CB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_VS, f.v_scales + r * C::SB, n * C::SB, &full[s], pol);
+        bulk_load_hint(dst, kc + r * C::CB, n * C::CB, &full[s], pol);
+        bulk_load_hint(dst + C::OFF_KS, ks + r * C::SB, n * C::SB, &full[s], pol);
+        bulk_load_hint(dst + C::OFF_VC, vc + r * C::CB, n * C::CB, &full[s], pol);
+        bulk_load_hint(dst + C::OFF_VS, vs + r * C::SB, n * C::SB, &full[s], pol);
         return true;
     };
     __syncthreads();  // barriers initialised
     int issued = 0;   // lane 0: tiles issued
     if (lane == 0)
-        while (issued < min(C::STAGES, my_tiles) && issue(issued)) ++issued;
+        while (issued < min(C::STAGES, my_tiles) && issue(issued, issued)) ++issued;
 
     // Q fragments: for step s of chunk c, row n = g: columns 128 c + TW t + 4 s ..+3.
     uint2 qf[C::QREG ? C::QSTEPS : 1][NB];
@@ -453,9 +456,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             }
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c) {
-                const uint32_t vs = st + C::OFF_VS + gr * 16 * C::SB + c * 8 + (HD >= 128 ? g : g >> 1);
-                uint32_t s0 = lds8(vs + key_x * C::SB), s1 = lds8(vs + key_y * C::SB);
-                uint32_t s2 = lds8(vs + (key_x + 8) * C::SB), s3 = lds8(vs + (key_y + 8) * C::SB);
+                const uint32_t sv = st + C::OFF_VS + gr * 16 * C::SB + c * 8 + (HD >= 128 ? g : g >> 1);
+                uint32_t s0 = lds8(sv + key_x * C::SB), s1 = lds8(sv + key_y * C::SB);
+                uint32_t s2 = lds8(sv + (key_x + 8) * C::SB), s3 = lds8(sv + (key_y + 8) * C::SB);
                 if constexpr (EDGE) {
                     s0 = in_x ? s0 : 0u;
                     s1 = in_y ? s1 : 0u;
@@ -464,20 +467,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                 }
                 const uint32_t sp = e4m3x2_to_f16(s0 | (s1 << 8)), sq = e4m3x2_to_f16(s2 | (s3 << 8));
                 constexpr int W = HD >= 128 ? 2 : 1;
-                const uint32_t vc = st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * W);
+                const uint32_t cv = st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * W);
                 uint32_t x[W], y[W], x8[W], y8[W];
                 if constexpr (W == 2) {
-                    const uint2 u0 = lds64(vc + key_x * C::CB), u1 = lds64(vc + key_y * C::CB);
-                    const uint2 u2 = lds64(vc + (key_x + 8) * C::CB), u3 = lds64(vc + (key_y + 8) * C::CB);
+                    const uint2 u0 = lds64(cv + key_x * C::CB), u1 = lds64(cv + key_y * C::CB);
+                    const uint2 u2 = lds64(cv + (key_x + 8) * C::CB), u3 = lds64(cv + (key_y + 8) * C::CB);
                     x[0] = u0.x; x[1] = u0.y;
                     y[0] = u1.x; y[1] = u1.y;
                     x8[0] = u2.x; x8[1] = u2.y;
                     y8[0] = u3.x; y8[1] = u3.y;
                 } else {
-                    x[0] = lds32(vc + key_x * C::CB);
-                    y[0] = lds32(vc + key_y * C::CB);
-                    x8[0] = lds32(vc + (key_x + 8) * C::CB);
-                    y8[0] = lds32(vc + (key_y + 8) * C::CB);
+                    x[0] = lds32(cv + key_x * C::CB);
+                    y[0] = lds32(cv + key_y * C::CB);
+                    x8[0] = lds32(cv + (key_x + 8) * C::CB);
+                    y8[0] = lds32(cv + (key_y + 8) * C::CB);
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -495,9 +498,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         }
     };
     bool ok = true;
+    int s = 0;
+    unsigned phase = 0;
     for (int i = 0; i < my_tiles; ++i) {
-        const int s = i % C::STAGES;
-        if (!mbar_wait(&full[s], (i / C::STAGES) & 1, f.status)) {
+        if (!mbar_wait(&full[s], phase, f.status)) {
             ok = false;
             break;
         }
@@ -509,7 +513,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         else
             tile_step(std::true_type{}, ring + s * C::STAGE, key0, end, head);
         __syncwarp();  // every lane is done with the stage
-        if (lane == 0 && issued == i + C::STAGES && issued < my_tiles && issue(issued)) ++issued;
+        if (lane == 0 && issued == i + C::STAGES && issued < my_tiles && issue(issued, s)) ++issued;
+        if (++s == C::STAGES) {
+            s = 0;
+            phase ^= 1;
+        }
     }
 
     // ------------------------------------------------------------ epilogue
@@ -661,6 +669,7 @@ int kv4_rows_per_cta(int hd, long long rows) {
 
 int kv4_ctas_per_sm(int hd, int rows_per_cta) {
     if (hd == 512) return 2;
+    if (hd * rows_per_cta <= 128 * 8) return 4;
     return hd * rows_per_cta >= 128 * 32 ? 2 : 3;
 }
 

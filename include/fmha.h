@@ -331,7 +331,8 @@ int fmha_selftest_bounds_check(fmha_stream_t stream);
  * CURRENT_ISSUE.md "Next steps", TS MMA for PV), 4 = always the tensor-core
  * kernels, one row tile per thread block, TS form.  Meant for tests and
  * measurements that compare kernels on one shape; results agree within the
- * documented tolerance.  Returns FMHA_ERR_SHAPE for other values.
+ * documented tolerance.  For fmha_fwd_kv4, 1 selects its mma.sync kernel and 2
+ * to 4 its tensor-core kernel.  Returns FMHA_ERR_SHAPE for other values.
  */
 int fmha_set_kernel_path(int path);
 

@@ -174,6 +174,14 @@ def test_append_leaves_rows_outside_the_cache_out():
 
 
 # ------------------------------------------------------------------ attention over the 4-bit cache
+@pytest.fixture(params=[1, 2], ids=["rows8", "rows128"])
+def kernel(request):
+    """Both kernels of the 4-bit attention."""
+    binding.fmha_set_kernel_path(request.param)
+    yield
+    binding.fmha_set_kernel_path(0)
+
+
 def filled(r, b, n_kv, cap, hd, g=1.0):
     k, v = normal(r, b, n_kv, cap, hd), normal(r, b, n_kv, cap, hd)
     k[..., 3] *= 6
@@ -212,13 +220,13 @@ def check_kv4(hd, n_h, n_kv, T, cap, lens, window=0, n_first=0, causal=False, si
 
 @pytest.mark.parametrize("hd", [64, 128, 256, 512])
 @pytest.mark.parametrize("n_h,n_kv", [(1, 1), (8, 1), (6, 2), (10, 2), (24, 1), (64, 2)])
-def test_kv4_decode_lengths(hd, n_h, n_kv):
+def test_kv4_decode_lengths(hd, n_h, n_kv, kernel):
     check_kv4(hd, n_h, n_kv, 1, 352, [0, 1, 2, 15, 16, 17, 31, 33, 64, 127, 129, 352, 351])
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256, 512])
 @pytest.mark.parametrize("T,causal", [(2, True), (5, True), (5, False), (37, True)])
-def test_kv4_more_rows(hd, T, causal):
+def test_kv4_more_rows(hd, T, causal, kernel):
     """Rows before their sequence's first key attend nothing (causal, T > length)."""
     check_kv4(hd, 6, 2, T, 128, [0, 1, 3, 36, 100, 128], causal=causal)
 
@@ -226,18 +234,18 @@ def test_kv4_more_rows(hd, T, causal):
 @pytest.mark.parametrize("hd", [64, 128, 256, 512])
 @pytest.mark.parametrize("window,n_first", [(1, 0), (1, 1), (17, 4), (64, 33), (100, 64), (300, 16), (1000, 7), (5, 200)])
 @pytest.mark.parametrize("T,causal", [(1, False), (9, True), (3, False)])
-def test_kv4_window_and_first_keys(hd, window, n_first, T, causal):
+def test_kv4_window_and_first_keys(hd, window, n_first, T, causal, kernel):
     check_kv4(hd, 4, 2, T, 400, [0, 4, 40, 111, 256, 400, 399], window=window, n_first=n_first, causal=causal)
 
 
 @pytest.mark.parametrize("kv_chunk", [16, 32, 64, 100, 512])
 @pytest.mark.parametrize("hd,window,n_first,sink", [(128, 0, 0, False), (128, 150, 40, True), (64, 0, 0, True), (256, 70, 5, False), (512, 99, 17, True)])
-def test_kv4_splits(hd, kv_chunk, window, n_first, sink):
+def test_kv4_splits(hd, kv_chunk, window, n_first, sink, kernel):
     check_kv4(hd, 8, 2, 3, 512, [0, 1, 130, 511, 512], window=window, n_first=n_first, causal=True, sink=sink, kv_chunk=kv_chunk)
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256, 512])
-def test_kv4_sink_scales_and_bounds(hd):
+def test_kv4_sink_scales_and_bounds(hd, kernel):
     check_kv4(hd, 8, 2, 1, 256, [0, 7, 256], sink=True, g=0.25)
     check_kv4(hd, 8, 2, 2, 256, [0, 7, 200], g=3.0, s_k=200)
     check_kv4(hd, 8, 2, 1, 256, [0, 7, 256], scale=-0.2)          # a negative scale turns the order round
@@ -246,7 +254,7 @@ def test_kv4_sink_scales_and_bounds(hd):
     check_kv4(hd, 8, 2, 1, 256, [5, 256], q_mult=2.0 ** -70, scale=2.0 ** 67)
 
 
-def test_kv4_lengths_beyond_bounds_are_clamped():
+def test_kv4_lengths_beyond_bounds_are_clamped(kernel):
     r = gen(9)
     cache = filled(r, 4, 1, 128, 64)
     q = normal(r, 4, 2, 1, 64)
@@ -259,7 +267,7 @@ def test_kv4_lengths_beyond_bounds_are_clamped():
     assert (o[0] == 0).all() and torch.isinf(lse[0]).all()
 
 
-def test_kv4_one_dominant_key_and_rising_scores():
+def test_kv4_one_dominant_key_and_rising_scores(kernel):
     """Scores that rise along the keys (the running reference moves often) and one key far above the rest."""
     hd, n = 128, 1024
     r = gen(11)
@@ -276,7 +284,7 @@ def test_kv4_one_dominant_key_and_rising_scores():
         ref.assert_attention(got, want)
 
 
-def test_kv4_long_cache_past_32_bit_offsets():
+def test_kv4_long_cache_past_32_bit_offsets(kernel):
     """The last sequence's rows lie more than 2^32 bytes into the cache."""
     b, n_kv, cap, hd = 5, 8, 1 << 19, 512
     cache = [torch.zeros((b, n_kv, cap, hd // w), dtype=torch.uint8, device=DEV) for w in (2, 16, 2, 16)]
@@ -451,6 +459,14 @@ def test_two_streams_at_once():
         binding.fmha_fwd_kv4(states[0]["q"].transpose(1, 2), *states[0]["cache"])
     with pytest.raises(ValueError):
         binding.fmha_fwd_kv4(states[0]["q"], *states[0]["cache"], states[0]["lens"][:2].contiguous())
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+def test_kv4_many_rows(hd):
+    """Prompt chunks and shared heads: whole and part row tiles, the automatic choice of kernel."""
+    check_kv4(hd, 16, 2, 40, 512, [0, 7, 39, 300, 512], causal=True, window=200, n_first=4)
+    check_kv4(hd, 128, 1, 1, 512, [1, 511, 64], sink=True)
+    check_kv4(hd, 3, 1, 100, 256, [100, 256, 30], causal=True, kv_chunk=64)
 
 
 def test_kv4_same_call_twice_is_bitwise_the_same():
