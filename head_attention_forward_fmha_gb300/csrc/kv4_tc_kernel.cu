@@ -9,14 +9,14 @@
 //   S_j = Q K_j^T   tcgen05.mma M = 128, N = BN, K = hd    (both from shared memory)
 //   O  += P_j V_j   tcgen05.mma M = 128, N = hd, K = BN    (P from tensor memory)
 // At hd 512 two blocks share a row tile: each computes all of S and one 256-column
-// half of O (which fills tensor memory next to S).
+// half of O (which fills tensor memory next to S), and K's single stage is
+// refilled in two column chunks, each as soon as the MMAs have read it.
 //
 // Warp roles (13 warps): 0..3 Q's conversion to fp16 (scaled by a power of two
 // per row), then softmax and epilogue, one query row per thread; 4 tensor memory
-// and MMA issue; 5..8 K's conversion; 9..12 V's conversion.  A conversion thread
-// holds part of one key's row: its loads for the next tile are in flight
-// while it converts this one, and eight lanes store to eight different
-// 16-byte columns of the swizzled tile.
+// and MMA issue; 5..12 the conversion.  A conversion thread
+// holds its share of two or three tiles in registers, so that their loads are in
+// flight while it converts another.
 //
 // Bounded by the tensor cores and the softmax beside the conversion: per 128 keys
 // at hd 128 the MMAs take ~1000 clocks, the exponentials 512 and the
@@ -43,15 +43,18 @@ struct K4TCfg {
     static constexpr int K_TILE = BN * HD * 2;
     static constexpr int V_TILE = BN * HDV * 2;
     static constexpr int THREADS = 13 * 32;
-    static constexpr int TPK = 128 / BN;                  // conversion threads per key
-    static constexpr int KCOLS = HD / TPK, VCOLS = HDV / TPK;  // columns per conversion thread
+    static constexpr int CT = 256;                        // conversion threads
+    static constexpr int NKC = HD == 512 ? 2 : 1;         // column chunks of a K tile, each with barriers of its own
+    static constexpr int KCH = HD / NKC;                  // columns of a chunk
+    static constexpr int KP = BN * KCH / 32 / CT;         // 32-column pieces of a K chunk, of V, per conversion thread
+    static constexpr int VP = BN * HDV / 32 / CT;
     static constexpr int O_COL = NSB * BN;
     static constexpr int P_COL = O_COL + HDV;             // P buffers, BN / 2 columns of fp16 pairs each
     static constexpr int TMEM_COLS = 512;
     static constexpr int OFF_K = Q_BYTES;
     static constexpr int OFF_V = OFF_K + STG * K_TILE;
     static constexpr int OFF_BAR = OFF_V + STG * V_TILE;
-    static constexpr int N_BARS = 1 + 4 * STG + 3 * NSB + 1;
+    static constexpr int N_BARS = 1 + 2 * STG * NKC + 2 * STG + 3 * NSB + 1;
     static constexpr int OFF_QS = OFF_BAR + N_BARS * 8 + 16;   // per-row factor of Q
     static constexpr int NEED = 1024 + OFF_QS + BM * 4;
     static constexpr int SMEM = NEED < 120000 ? 120000 : NEED;  // one block per SM: each takes all of tensor memory
@@ -81,45 +84,65 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Codes and scales of COLS consecutive columns of one key.
-template <int COLS>
-struct RowPart {
-    uint4 codes[COLS / 32];
-    uint32_t scales[COLS / 64];
+// One conversion thread's share of a tile: N pieces of 32 columns (16 bytes of
+// codes, two scales).  The tile's pieces, PPR per key, go round the CT threads in
+// order, so a warp's load covers 512 neighbouring bytes (or whole 128-byte parts of
+// rows).  Piece i of its key starts at column 32 i of the tile; STRIDE pieces lie
+// between two keys in memory.
+template <int N, int PPR, int STRIDE, int CT>
+struct Pieces {
+    uint4 codes[N];
+    uint32_t scales[N];  // packing them would wait for the loads
 
-    __device__ __forceinline__ void load(const uint8_t* c, const uint8_t* s, bool live) {
+    // c, s: piece 0 of the tile's first key; `keys` of them are there.
+    __device__ __forceinline__ void load(int tid, const uint4* c, const unsigned short* s, int keys) {
 #pragma unroll
-        for (int i = 0; i < COLS / 32; ++i)
-            codes[i] = live ? __ldg(reinterpret_cast<const uint4*>(c) + i) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (COLS == 64) {
-            scales[0] = live ? __ldg(reinterpret_cast<const unsigned int*>(s)) : 0u;
-        } else if constexpr (COLS == 128) {
-            const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(s)) : make_uint2(0u, 0u);
-            scales[0] = v.x; scales[1] = v.y;
-        } else {
-            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(s)) : make_uint4(0u, 0u, 0u, 0u);
-            scales[0] = v.x; scales[1] = v.y; scales[2] = v.z; scales[3] = v.w;
+        for (int p = 0; p < N; ++p) {
+            const int idx = p * CT + tid, key = idx / PPR;
+            const int at = STRIDE == PPR ? idx : key * STRIDE + idx % PPR;
+            const bool live = key < keys;
+            codes[p] = live ? __ldg(c + at) : make_uint4(0u, 0u, 0u, 0u);
+            scales[p] = live ? __ldg(s + at) : 0u;
         }
     }
 
-    // As fp16 into row `key` of a tile of 64-column boxes of `rows` 128-byte
-    // rows (16-byte chunk c of row r at chunk c ^ (r % 8)), from column col0 on.
-    __device__ __forceinline__ void store(uint8_t* tile, int rows, int key, int col0) const {
+    // As fp16 into a tile of 64-column boxes of `rows` 128-byte rows (16-byte
+    // chunk c of row r at chunk c ^ (r % 8)).  A piece is four chunks; lanes take
+    // theirs in different orders, c ^ x, so that eight lanes always store to eight
+    // different chunk positions (bank groups).
+    __device__ __forceinline__ void store(int tid, uint8_t* tile, int rows) const {
 #pragma unroll
-        for (int b = 0; b < COLS / 16; ++b) {  // 16-column blocks
-            const uint32_t pair = e4m3x2_to_f16(scales[b / 4] >> (16 * ((b / 2) & 1)));
-            const uint32_t s2 = __byte_perm(pair, pair, b & 1 ? 0x3232 : 0x1010);
-            const uint4 c4 = codes[b / 2];
-            const uint32_t w[2] = {b & 1 ? c4.z : c4.x, b & 1 ? c4.w : c4.y};
+        for (int p = 0; p < N; ++p) {
+            const int idx = p * CT + tid;
+            const int key = idx / PPR, i = idx % PPR;
+            const int x = PPR == 4 ? (i >> 1) * 2 : (i >> 1) & 3;
+            const uint32_t pair = e4m3x2_to_f16(scales[p]);
+            uint32_t s0 = __byte_perm(pair, pair, 0x1010), s1 = __byte_perm(pair, pair, 0x3232);
+            uint32_t w[4] = {codes[p].x, codes[p].y, codes[p].z, codes[p].w};
+            if constexpr (PPR > 4) {
+                const bool swap = x & 1;
+                const uint32_t t0 = swap ? w[1] : w[0], t1 = swap ? w[0] : w[1];
+                const uint32_t t2 = swap ? w[3] : w[2], t3 = swap ? w[2] : w[3];
+                w[0] = t0; w[1] = t1; w[2] = t2; w[3] = t3;
+            }
+            if constexpr (PPR >= 4) {
+                const bool swap = x & 2;
+                const uint32_t t0 = swap ? w[2] : w[0], t1 = swap ? w[3] : w[1];
+                const uint32_t t2 = swap ? w[0] : w[2], t3 = swap ? w[1] : w[3];
+                w[0] = t0; w[1] = t1; w[2] = t2; w[3] = t3;
+                const uint32_t u = swap ? s1 : s0;
+                s1 = swap ? s0 : s1;
+                s0 = u;
+            }
+            uint8_t* row = tile + (i >> 1) * rows * 128 + key * 128;
+            const int pos = ((i & 1) * 4) ^ x ^ (key & 7);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int c = 0; c < 4; ++c) {
                 uint32_t r[4];
-                e2m1x8_to_f16(w[h], r);
+                e2m1x8_to_f16(w[c], r);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = mul_f16x2(r[e], s2);
-                const int col = col0 + b * 16 + h * 8;
-                uint8_t* dst = tile + (col >> 6) * rows * 128 + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4);
-                *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+                for (int e = 0; e < 4; ++e) r[e] = mul_f16x2(r[e], c < 2 ? s0 : s1);
+                *reinterpret_cast<uint4*>(row + ((pos ^ c) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
     }
@@ -139,8 +162,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* q_full = bars;
     uint64_t* k_full = bars + 1;
-    uint64_t* k_empty = k_full + STG;
-    uint64_t* v_full = k_empty + STG;
+    uint64_t* k_empty = k_full + STG * C::NKC;  // by stage and chunk
+    uint64_t* v_full = k_empty + STG * C::NKC;
     uint64_t* v_empty = v_full + STG;
     uint64_t* s_full = v_empty + STG;    // [NSB]
     uint64_t* p_ready = s_full + NSB;    // [NSB]
@@ -158,11 +181,13 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
     const int r_end = min(a.R, r_begin + BM);
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 128);
-        for (int s = 0; s < STG; ++s) {
-            mbar_init(&k_full[s], 128);
+        mbar_init(q_full, 12 * 32);
+        for (int s = 0; s < STG * C::NKC; ++s) {
+            mbar_init(&k_full[s], C::CT);
             mbar_init(&k_empty[s], 1);
-            mbar_init(&v_full[s], 128);
+        }
+        for (int s = 0; s < STG; ++s) {
+            mbar_init(&v_full[s], C::CT);
             mbar_init(&v_empty[s], 1);
         }
         for (int s = 0; s < NSB; ++s) {
@@ -211,38 +236,131 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
     auto tile_key = [&](int j) { return j < n_head ? h_lo + j * BN : u_lo + (j - n_head) * BN; };
     auto tile_end = [&](int j) { return j < n_head ? n_first : b_hi; };
 
+    // Q's rows w, w + 12, ... of the tile (pairs or quads of rows at hd 128 and
+    // 64) as fp16, scaled by a power of two per row and by the sign of the
+    // scale, into 64-column boxes of 128 swizzled rows; all but the MMA warp
+    // take part, w = 0 .. 11.
+    auto load_q = [&](int w) {
+        constexpr int LPR = HD >= 256 ? 32 : HD / 8, RPI = 32 / LPR, VEC = HD >= 256 ? HD / 256 : 1;
+        constexpr int SETS = BM / RPI, BATCH = HD == 512 ? 3 : 6;
+        const int lr = lane / LPR, lc = lane % LPR;
+#pragma unroll 1
+        for (int base = w; base < SETS; base += 12 * BATCH) {
+            uint4 u[BATCH][VEC];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = (base + 12 * i) * RPI + lr;
+                const bool live = row < BM && r_begin + row < r_end;
+                const uint4* src = reinterpret_cast<const uint4*>(f.q + (row0 + r_begin + (live ? row : 0)) * HD);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) u[i][v] = live ? __ldg(src + v * 32 + lc) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = (base + 12 * i) * RPI + lr;
+                uint32_t mx = 0;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[i][v].x & 0x7FFF7FFFu, u[i][v].y & 0x7FFF7FFFu),
+                                               __vmaxu2(u[i][v].z & 0x7FFF7FFFu, u[i][v].w & 0x7FFF7FFFu)));
+                mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+                for (int m = LPR / 2; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+                const int e = (int)(mx >> 7);
+                const int k = (e > 0 && e < 255) ? min(max(14 - (e - 127), -120), 120) : 0;
+                const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2_sign;
+                if (row >= BM) continue;
+                if (lc == 0) row_fac[row] = __uint_as_float((uint32_t)(127 - k) << 23) * a.sl2;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const int col = v * 256 + lc * 8;
+                    const uint32_t x[4] = {u[i][v].x, u[i][v].y, u[i][v].z, u[i][v].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) h[y] = pack_f16x2(bf16_lo(x[y]) * up, bf16_hi(x[y]) * up);
+                    *reinterpret_cast<uint4*>(sq + (col >> 6) * BM * 128 + row * 128 +
+                                              ((((col & 63) >> 3) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+    };
+
     if (warp >= 5) {
         // ------------------------------------------------------------ conversion
-        const bool is_v = warp >= 9;
-        const int tid = threadIdx.x - (is_v ? 9 : 5) * 32;
-        const int key = tid % BN, sub = tid / BN;
-        auto convert = [&](auto part_type, uint8_t* tiles, int tile_bytes, const uint8_t* codes, const uint8_t* scales,
-                           uint64_t* full, uint64_t* empty, int col0, int smem_col0) {
-            using Part = decltype(part_type);
-            Part cur, next;
-            auto fetch = [&](Part& p, int j) {
-                const int k = tile_key(j) + key;
-                const bool live = k < tile_end(j) && FMHA_IN_BOUNDS(k >= 0 && k < f.cap, kSiteKv4Copy, f.status);
-                const long long r = (long long)slab * f.cap + (live ? k : 0);
-                p.load(codes + r * (HD / 2) + col0 / 2, scales + r * (HD / 16) + col0 / 16, live);
-            };
-            if (n_tiles > 0) fetch(cur, 0);
-            for (int j = 0; j < n_tiles; ++j) {
-                const int s = j % STG;
-                if (j + 1 < n_tiles) fetch(next, j + 1);
-                if (j >= STG && !mbar_wait(&empty[s], ((j / STG) - 1) & 1, f.status)) break;
-                cur.store(tiles + s * tile_bytes, BN, key, smem_col0);
-                fence_proxy_async_smem();
-                mbar_arrive(&full[s]);
-                cur = next;
-            }
+        // K_0, K_1, V_0, K_2, V_1, ...: the order the MMA warp takes them in.
+        // NBUF tiles of K and V are held in registers, their loads in flight
+        // while others are converted.
+        const int tid = threadIdx.x - 5 * 32;
+        constexpr int NBUF = HD <= 128 ? 3 : 2;
+        constexpr int KPPR = C::KCH / 32, VPPR = C::HDV / 32, RP = HD / 32;
+        Pieces<C::KP, KPPR, RP, C::CT> kb[NBUF][C::NKC];
+        Pieces<C::VP, VPPR, RP, C::CT> vb[NBUF];
+        const long long base = (long long)slab * f.cap * RP;
+        const uint4* const kc = reinterpret_cast<const uint4*>(f.k_codes) + base;
+        const uint4* const vc = reinterpret_cast<const uint4*>(f.v_codes) + base + part * VPPR;
+        const unsigned short* const ks = reinterpret_cast<const unsigned short*>(f.k_scales) + base;
+        const unsigned short* const vs = reinterpret_cast<const unsigned short*>(f.v_scales) + base + part * VPPR;
+        auto keys_of = [&](int j, long long& at) {
+            const int k0 = tile_key(j), n = min(BN, tile_end(j) - k0);
+            at = (long long)k0 * RP;
+            return FMHA_IN_BOUNDS(k0 >= 0 && k0 + n <= f.cap, kSiteKv4Copy, f.status) ? n : 0;
         };
-        if (is_v)
-            convert(RowPart<C::VCOLS>{}, sv, C::V_TILE, f.v_codes, f.v_scales, v_full, v_empty,
-                    part * C::HDV + sub * C::VCOLS, sub * C::VCOLS);
-        else
-            convert(RowPart<C::KCOLS>{}, sk, C::K_TILE, f.k_codes, f.k_scales, k_full, k_empty, sub * C::KCOLS,
-                    sub * C::KCOLS);
+        auto fetch_k = [&](auto& p, int j) {
+            long long at;
+            const int n = keys_of(j, at);
+#pragma unroll
+            for (int c = 0; c < C::NKC; ++c) p[c].load(tid, kc + at + c * KPPR, ks + at + c * KPPR, n);
+        };
+        auto fetch_v = [&](auto& p, int j) {
+            long long at;
+            const int n = keys_of(j, at);
+            p.load(tid, vc + at, vs + at, n);
+        };
+#pragma unroll
+        for (int i = 0; i < NBUF; ++i)
+            if (i < n_tiles) {
+                fetch_k(kb[i], i);
+                fetch_v(vb[i], i);
+            }
+        if (n_tiles > 0) load_q(warp - 1);
+        bool ok = true;
+        // K_j and then V_{j-1}, for j up to n_tiles (where there is no K_j)
+#pragma unroll 1
+        for (int j0 = 0; ok && j0 <= n_tiles && n_tiles > 0; j0 += NBUF) {
+#pragma unroll
+            for (int i = 0; i < NBUF; ++i) {
+                const int j = j0 + i;
+                if (!ok || j > n_tiles) continue;
+                const int s = STG == 1 ? 0 : j & 1;
+                if (j < n_tiles) {
+#pragma unroll
+                    for (int c = 0; c < C::NKC; ++c) {
+                        const int q = s * C::NKC + c;
+                        ok = ok && (j < STG || mbar_wait(&k_empty[q], ((j / STG) - 1) & 1, f.status));
+                        if (ok) {
+                            kb[i][c].store(tid, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), BN);
+                            fence_proxy_async_smem();
+                            mbar_arrive(&k_full[q]);
+                        }
+                    }
+                    if (j + NBUF < n_tiles) fetch_k(kb[i], j + NBUF);
+                }
+                if (j > 0) {
+                    constexpr int LAST = NBUF - 1;
+                    auto& v = vb[i == 0 ? LAST : i - 1];
+                    const int jv = j - 1, sv_ = STG == 1 ? 0 : jv & 1;
+                    ok = ok && (jv < STG || mbar_wait(&v_empty[sv_], ((jv / STG) - 1) & 1, f.status));
+                    if (ok) {
+                        v.store(tid, sv + sv_ * C::V_TILE, BN);
+                        fence_proxy_async_smem();
+                        mbar_arrive(&v_full[sv_]);
+                        if (jv + NBUF < n_tiles) fetch_v(v, jv + NBUF);
+                    }
+                }
+            }
+        }
     } else if (warp == 4) {
         // ------------------------------------------------------------ MMA issuer
         // Order: QK_0 .. QK_{NSB-1}, then per tile j: PV_j, QK_{j+NSB}.
@@ -252,19 +370,26 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
             bool ok = mbar_wait(q_full, 0, f.status);
             auto issue_qk = [&](int j) -> bool {
-                const int s = j % STG;
-                if (!mbar_wait(&k_full[s], (j / STG) & 1, f.status)) return false;
-                tc_fence_after();
+                const int s = STG == 1 ? 0 : j & 1;
                 const uint32_t d = tmem + (j % NSB) * BN;
+                // A descriptor's low word holds the address in units of 16 bytes: the
+                // operands of a step are a constant distance from the stage's first.
+                const uint64_t a0 = smem_desc_sw128(q_addr, 16, 1024);
+                const uint64_t b0 = smem_desc_sw128(k_addr + s * C::K_TILE, 16, 1024);
+#pragma unroll 1
+                for (int c = 0; c < C::NKC; ++c) {
+                    if (!mbar_wait(&k_full[s * C::NKC + c], (j / STG) & 1, f.status)) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = c * (C::KCH / 64); x < (c + 1) * (C::KCH / 64); ++x) {  // 64-column boxes
+                        const uint64_t ax = a0 + x * (BM * 128 / 16), bx = b0 + x * (BN * 128 / 16);
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk & 3) * 32;  // 16 columns = 32 bytes into the swizzled row
-                    const uint64_t ad = smem_desc_sw128(q_addr + (kk >> 2) * BM * 128 + off, 16, 1024);
-                    const uint64_t bd = smem_desc_sw128(k_addr + s * C::K_TILE + (kk >> 2) * BN * 128 + off, 16, 1024);
-                    tc_mma_f16(d, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
+                            tc_mma_f16(d, ax + kk * 2, bx + kk * 2, idesc_s, (x > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc_commit(&k_empty[s * C::NKC + c]);
                 }
                 tc_commit(&s_full[j % NSB]);
-                tc_commit(&k_empty[s]);
                 return true;
             };
             for (int j = 0; ok && j < NSB && j < n_tiles; ++j) ok = issue_qk(j);
@@ -273,11 +398,11 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 if (!mbar_wait(&v_full[s], (j / STG) & 1, f.status)) break;
                 if (!mbar_wait(&p_ready[pb], (j / NSB) & 1, f.status)) break;
                 tc_fence_after();
+                const uint64_t b0 = smem_desc_sw128(v_addr + s * C::V_TILE, BN * 128, 1024);
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk) {
-                    const uint64_t bd = smem_desc_sw128(v_addr + s * C::V_TILE + kk * 16 * 128, BN * 128, 1024);
-                    tc_mma_f16_ts(tmem + C::O_COL, tmem + C::P_COL + pb * (BN / 2) + kk * 8, bd, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-                }
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    tc_mma_f16_ts(tmem + C::O_COL, tmem + C::P_COL + pb * (BN / 2) + kk * 8, b0 + kk * (16 * 128 / 16),
+                                  idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(&o_done[pb]);
                 tc_commit(&v_empty[s]);
                 if (j + NSB < n_tiles && !issue_qk(j + NSB)) break;
@@ -288,47 +413,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             mbar_wait(mma_drain, 0, f.status);
         }
     } else {
-        // ------------------------------------------------------------ Q
-        // A warp takes its 32 rows; lanes hold 8 columns each (16 lanes or 8 per
-        // row at hd 128 and 64).  The sign of the scale goes into Q.
-        constexpr int LPR = HD >= 256 ? 32 : HD / 8, RPI = 32 / LPR, VEC = HD >= 256 ? HD / 256 : 1;
-        if (n_tiles > 0) {
-            const int lr = lane / LPR, lc = lane % LPR;
-#pragma unroll 4
-            for (int i = 0; i < 32 / RPI; ++i) {
-                const int row = warp * 32 + i * RPI + lr;
-                const bool live = r_begin + row < r_end;
-                const uint4* src = reinterpret_cast<const uint4*>(f.q + (row0 + r_begin + (live ? row : 0)) * HD);
-                uint4 u[VEC];
-                uint32_t mx = 0;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    u[v] = live ? __ldg(src + v * 32 + lc) : make_uint4(0u, 0u, 0u, 0u);
-                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[v].x & 0x7FFF7FFFu, u[v].y & 0x7FFF7FFFu),
-                                               __vmaxu2(u[v].z & 0x7FFF7FFFu, u[v].w & 0x7FFF7FFFu)));
-                }
-                mx = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-                for (int m = LPR / 2; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-                const int e = (int)(mx >> 7);
-                const int k = (e > 0 && e < 255) ? min(max(14 - (e - 127), -120), 120) : 0;
-                const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2_sign;
-                if (lc == 0) row_fac[row] = __uint_as_float((uint32_t)(127 - k) << 23) * a.sl2;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const int col = v * 256 + lc * 8;
-                    const uint32_t w[4] = {u[v].x, u[v].y, u[v].z, u[v].w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(w[x]) * up, bf16_hi(w[x]) * up);
-                    *reinterpret_cast<uint4*>(sq + (col >> 6) * BM * 128 + row * 128 +
-                                              ((((col & 63) >> 3) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
-            __syncwarp();  // row_fac of this warp's rows
-        }
+        if (n_tiles > 0) load_q(warp);
         // ------------------------------------------------------------ softmax
         const int row = threadIdx.x;  // tile row and TMEM lane
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
@@ -346,10 +431,10 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             }
             if (f.window > 0) jlo = max(jlo, p - f.window + 1);
         }
-        const float qs = n_tiles > 0 ? row_fac[row] : 1.f;
         float m_ref = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n_tiles; ++j) {
+        bool ok = n_tiles == 0 || mbar_wait(q_full, 0, f.status);
+        const float qs = n_tiles > 0 && ok ? row_fac[row] : 1.f;
+        for (int j = 0; ok && j < n_tiles; ++j) {
             const int pb = j % NSB;
             if (!mbar_wait(&s_full[pb], (j / NSB) & 1, f.status)) {
                 ok = false;
@@ -361,17 +446,20 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             const int lo = j < n_head ? 0 : jlo, hi = j < n_head ? fhi : jhi;
             const bool full = key0 >= lo && key0 + BN - 1 <= hi;
             const uint32_t p_addr = t_lane + C::P_COL + pb * (BN / 2);
-            float sum = 0.f, mx = -INFINITY;
+            float alpha = 1.f;
             // P of the whole tile against the present reference, its sum, and the
-            // tile's largest score; S stays as it is.  The P buffer is free: S_j's QK
-            // was queued after PV_{j-NSB}, which read it.
-            auto pass = [&](bool exps) {
+            // tile's largest score; S stays as it is.  Usually the reference stands;
+            // where a row of the warp has none yet or exceeds it by more than 8, it
+            // moves to the tile's maximum and the tile is done once more.  The P
+            // buffer is free: S_j's QK was queued after PV_{j-NSB}, which read it.
+            bool exps = !__any_sync(0xffffffffu, m_ref == -INFINITY);
+#pragma unroll 1
+            for (int again = 0;; ++again) {
                 const float mu = kPBias - (m_ref == -INFINITY ? 0.f : m_ref);
-                sum = 0.f;
-                mx = -INFINITY;
+                float mx = -INFINITY;
                 uint64_t s2[2] = {0ull, 0ull};
                 const uint64_t q2 = f32x2(qs, qs), mu2 = f32x2(mu, mu);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
                     float x[32];
                     tmem_ld32(s_addr + c * 32, x);
@@ -399,28 +487,22 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                         tmem_st16u(p_addr + c * 16, pk);
                     }
                 }
-                float a0, a1, b0, b1;
-                f32x2_split(s2[0], a0, a1);
-                f32x2_split(s2[1], b0, b1);
-                sum = (a0 + a1) + (b0 + b1);
-            };
-            // Usually the reference stands; where a row of the warp has none yet or
-            // exceeds it by more than 8, it moves to the tile's maximum first.
-            bool redo = __any_sync(0xffffffffu, m_ref == -INFINITY);
-            pass(!redo);
-            float alpha = 1.f;
-            const float mt = mx * qs;
-            const bool grow_ref = mt > m_ref + 8.f;
-            redo = __any_sync(0xffffffffu, grow_ref) || redo;
-            if (redo) {
-                if (grow_ref) {
+                const float mt = mx * qs;
+                const bool move = again == 0 && mt > m_ref + 8.f;
+                if (again > 0 || (exps && !__any_sync(0xffffffffu, move))) {
+                    float a0, a1, b0, b1;
+                    f32x2_split(s2[0], a0, a1);
+                    f32x2_split(s2[1], b0, b1);
+                    l += (a0 + a1) + (b0 + b1);
+                    break;
+                }
+                if (move) {
                     alpha = ex2_approx(m_ref - mt);  // 0 when the reference was -inf
                     m_ref = mt;
                     l *= alpha;
                 }
-                pass(true);
+                exps = true;
             }
-            l += sum;
             // a rescale of O needs PV_{j-1}
             const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
             if (rescale && !mbar_wait(&o_done[(j - 1) % NSB], ((j - 1) / NSB) & 1, f.status)) {
