@@ -79,6 +79,17 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
         : "memory");
 }
 
+// One lane of the (converged) warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Instruction descriptor, kind::f16 with fp16 A and B, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -364,52 +375,65 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
     } else if (warp == 4) {
         // ------------------------------------------------------------ MMA issuer
         // Order: QK_0 .. QK_{NSB-1}, then per tile j: PV_j, QK_{j+NSB}.
-        if (lane == 0 && n_tiles > 0) {
+        // The whole warp walks the loop and one elected lane issues, so that the
+        // descriptors stay in uniform registers: issued by `lane == 0` alone, each MMA
+        // took ~95 clocks (hd 512: 3000 per tile of 32) however small it was.
+        if (n_tiles > 0) {
             constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, 0);
             constexpr uint32_t idesc_o = idesc_f16_f32(BM, C::HDV, 1);
-            const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
+            // A descriptor's low word holds the address in units of 16 bytes: the
+            // operands of a step are a constant distance from the stage's first.
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(sq), 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(sk), 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(sv), BN * 128, 1024);
             bool ok = mbar_wait(q_full, 0, f.status);
             auto issue_qk = [&](int j) -> bool {
                 const int s = STG == 1 ? 0 : j & 1;
                 const uint32_t d = tmem + (j % NSB) * BN;
-                // A descriptor's low word holds the address in units of 16 bytes: the
-                // operands of a step are a constant distance from the stage's first.
-                const uint64_t a0 = smem_desc_sw128(q_addr, 16, 1024);
-                const uint64_t b0 = smem_desc_sw128(k_addr + s * C::K_TILE, 16, 1024);
+                const uint64_t b0 = k_desc + s * (C::K_TILE / 16);
 #pragma unroll 1
                 for (int c = 0; c < C::NKC; ++c) {
                     if (!mbar_wait(&k_full[s * C::NKC + c], (j / STG) & 1, f.status)) return false;
                     tc_fence_after();
-#pragma unroll 1
-                    for (int x = c * (C::KCH / 64); x < (c + 1) * (C::KCH / 64); ++x) {  // 64-column boxes
-                        const uint64_t ax = a0 + x * (BM * 128 / 16), bx = b0 + x * (BN * 128 / 16);
+                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
-                            tc_mma_f16(d, ax + kk * 2, bx + kk * 2, idesc_s, (x > 0 || kk > 0) ? 1u : 0u);
+                        for (int y = 0; y < C::KCH / 64; ++y) {  // 64-column boxes
+                            const int x = c * (C::KCH / 64) + y;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
+                                tc_mma_f16(d, q_desc + x * (BM * 128 / 16) + kk * 2, b0 + x * (BN * 128 / 16) + kk * 2, idesc_s,
+                                           (c > 0 || y > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        tc_commit(&k_empty[s * C::NKC + c]);
+                        if (c == C::NKC - 1) tc_commit(&s_full[j % NSB]);
                     }
-                    tc_commit(&k_empty[s * C::NKC + c]);
+                    __syncwarp();
                 }
-                tc_commit(&s_full[j % NSB]);
                 return true;
             };
             for (int j = 0; ok && j < NSB && j < n_tiles; ++j) ok = issue_qk(j);
             for (int j = 0; ok && j < n_tiles; ++j) {
-                const int s = j % STG, pb = j % NSB;
+                const int s = STG == 1 ? 0 : j & 1, pb = j % NSB;
                 if (!mbar_wait(&v_full[s], (j / STG) & 1, f.status)) break;
                 if (!mbar_wait(&p_ready[pb], (j / NSB) & 1, f.status)) break;
                 tc_fence_after();
-                const uint64_t b0 = smem_desc_sw128(v_addr + s * C::V_TILE, BN * 128, 1024);
+                const uint64_t b0 = v_desc + s * (C::V_TILE / 16);
+                const uint32_t p_col = tmem + C::P_COL + pb * (BN / 2);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_f16_ts(tmem + C::O_COL, tmem + C::P_COL + pb * (BN / 2) + kk * 8, b0 + kk * (16 * 128 / 16),
-                                  idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(&o_done[pb]);
-                tc_commit(&v_empty[s]);
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        tc_mma_f16_ts(tmem + C::O_COL, p_col + kk * 8, b0 + kk * (16 * 128 / 16), idesc_o,
+                                      (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&o_done[pb]);
+                    tc_commit(&v_empty[s]);
+                }
+                __syncwarp();
                 if (j + NSB < n_tiles && !issue_qk(j + NSB)) break;
             }
             // Exit drain: whatever the loop issued has completed before tensor
             // memory and the operand buffers are released, even if a wait gave up.
-            tc_commit(mma_drain);
+            if (elect_one()) tc_commit(mma_drain);
+            __syncwarp();
             mbar_wait(mma_drain, 0, f.status);
         }
     } else {
