@@ -7,6 +7,7 @@ kernels; there is no CPU fallback, and a missing library raises.
 """
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -379,7 +380,9 @@ def fmha_quantize_nvfp4(x, global_scale=1.0, stream=None):
 
 
 def fmha_release():
+    """Free the library's workspaces and the binding's."""
     load().fmha_release()
+    _workspaces.clear()
 
 
 def fmha_version():
@@ -428,41 +431,66 @@ def fmha_fwd_noalloc(q, k, v, o, lse, scale=None, window=0, causal=False, stream
 
 
 # ---------------------------------------------------------------------------
-# Serving operators around the forward: norm and rotation, 4-bit cache
+# Serving operators around the forward: norm and rotation, 4-bit cache, window
+# with first keys.  Their smallest calls take a few microseconds on the GPU, so
+# the checks here are written for few Python steps per tensor.
 # ---------------------------------------------------------------------------
-def _ptr(t, name, dtype, shape, device, optional=False):
-    """Data pointer of a contiguous CUDA tensor of this dtype, shape and device (None if optional and absent)."""
-    if t is None and optional:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+_BF16, _FP32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """Data pointer of a contiguous tensor of this dtype and shape on CUDA device `dev` (an index)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise TypeError("%s must be a contiguous CUDA %s tensor" % (name, dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    return t.data_ptr()
+    raise ValueError("%s must be on cuda:%d" % (name, dev))
 
 
-def _call(fn, device, stream, *args):
-    """fn(*args, stream) of the library, with `device` current; stream None is that device's current stream."""
-    current = torch.cuda.current_device()
-    if device.index != current:
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
-    handle = torch._C._cuda_getCurrentRawStream(current) if stream is None else _stream(stream)
+def _device(t, name):
+    """CUDA device index of the tensor that decides where a call runs."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) of the library with device `dev` current; stream None is that device's current stream."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     rc = getattr(_lib or load(), fn)(*args, handle)
     if rc:
         _check(rc, fn)
 
 
-def _scratch(nbytes, device, stream):
-    """Workspace of one call from torch's allocator, in the order of the stream that uses it."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+_workspaces = {}  # uint8 tensor by (thread, device, stream)
+
+
+def _workspace(nbytes, dev, stream):
+    """A tensor of at least nbytes for the partials of one call on `stream`.
+
+    Calls of one thread on one stream follow each other, so they share one that is kept (and grown): allocating it anew
+    costs the host more than the rest of a call.  A call that is being captured into a graph gets a new one, which the
+    graph's memory pool holds: graphs captured on one stream may be replayed at the same time."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            return _workspace(nbytes, dev, None)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=_U8, device=dev)
+    key = threading.get_ident(), dev, torch._C._cuda_getCurrentRawStream(dev)
+    t = _workspaces.get(key)
+    if t is None or t.numel() < nbytes:
+        t = _workspaces[key] = torch.empty(nbytes, dtype=_U8, device=dev)
+    return t
 
 
 def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -475,7 +503,8 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     (a token outside [0, max_pos) is padding, its outputs are left as they are); both None: no rotation.
     k and v given with more rows than T are written at rows kv_start[b] + t (int32 [b]; None: 0).
     Returns q [b, n_h, T, hd], k and v [b, n_kv_h, rows, hd]; what is not given is allocated."""
-    if not isinstance(qkv, torch.Tensor) or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
+    dev = _device(qkv, "qkv")
+    if qkv.dtype is not _BF16:
         raise TypeError("qkv must be a CUDA bf16 tensor")
     if qkv.dim() != 3 or n_h < 1 or n_kv_h < 1 or qkv.shape[2] % (n_h + 2 * n_kv_h):
         raise ValueError("qkv [b, T, (n_h + 2 n_kv_h) * hd] expected, got %s" % (tuple(qkv.shape),))
@@ -484,31 +513,35 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     sb, st, se = qkv.stride()
     if se != 1 and width > 1:
         raise ValueError("the rows of qkv must be contiguous")
-    if T <= 1:
-        st = max(width, (st + 7) // 8 * 8) if T == 0 or st < width or st % 8 else st
-    if b <= 1 and sb % 8:
+    if T <= 1:  # strides of dimensions of one element say nothing
+        st = max(width, (st + 7) // 8 * 8)
+    if b <= 1:
         sb = 0
-    dev = qkv.device
     if (cos_sin is None) != (positions is None):
         raise ValueError("cos_sin and positions are given together or not at all")
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape if cos_sin.dim() == 2 else (0, -1)
-    if k is not None and (k.dim() != 4 or v is None):
+    if (k is None) != (v is None) or (k is not None and k.dim() != 4):
         raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
-    rows = T if k is None else k.shape[2]
+    if cos_sin is None:
+        cs_ptr = pos_ptr = None
+        max_pos = rot = 0
+    else:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin [max_pos, rot] expected, got %s" % (tuple(cos_sin.shape),))
+        max_pos, rot = cos_sin.shape
+        cs_ptr = _ptr(cos_sin, "cos_sin", _FP32, (max_pos, rot), dev)
+        pos_ptr = _ptr(positions, "positions", _I32, (b, T), dev)
     if q is None:
-        q = torch.empty((b, n_h, T, hd), dtype=torch.bfloat16, device=dev)
+        q = torch.empty((b, n_h, T, hd), dtype=_BF16, device=dev)
     if k is None:
-        if v is not None:
-            raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
-        k = torch.empty((b, n_kv_h, T, hd), dtype=torch.bfloat16, device=dev)
+        k = torch.empty((b, n_kv_h, T, hd), dtype=_BF16, device=dev)
         v = torch.empty_like(k)
+    rows = k.shape[2]
     kv_shape = (b, n_kv_h, rows, hd)
     _call("fmha_qk_norm_rope", dev, stream, qkv.data_ptr(), sb, st,
-          _ptr(q_weight, "q_weight", torch.float32, (hd,), dev, True), _ptr(k_weight, "k_weight", torch.float32, (hd,), dev, True),
-          eps, _ptr(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev, True),
-          _ptr(positions, "positions", torch.int32, (b, T), dev, True), max_pos, rot, int(bool(interleaved)),
-          _ptr(q, "q", torch.bfloat16, (b, n_h, T, hd), dev), _ptr(k, "k", torch.bfloat16, kv_shape, dev),
-          _ptr(v, "v", torch.bfloat16, kv_shape, dev), _ptr(kv_start, "kv_start", torch.int32, (b,), dev, True), rows,
+          None if q_weight is None else _ptr(q_weight, "q_weight", _FP32, (hd,), dev),
+          None if k_weight is None else _ptr(k_weight, "k_weight", _FP32, (hd,), dev), eps, cs_ptr, pos_ptr, max_pos, rot,
+          bool(interleaved), _ptr(q, "q", _BF16, (b, n_h, T, hd), dev), _ptr(k, "k", _BF16, kv_shape, dev),
+          _ptr(v, "v", _BF16, kv_shape, dev), None if kv_start is None else _ptr(kv_start, "kv_start", _I32, (b,), dev), rows,
           b, T, n_h, n_kv_h, hd)
     return q, k, v
 
@@ -518,34 +551,38 @@ def fmha_kv4_cache(batch, n_kv_h, cap, hd, device="cuda"):
     (k_codes, k_scales, v_codes, v_scales) that fmha_kv4_append writes and fmha_fwd_kv4 reads."""
     if hd not in (64, 128, 256, 512) or cap % 16:
         raise ValueError("hd must be 64, 128, 256 or 512 and cap a multiple of 16 (got hd=%d cap=%d)" % (hd, cap))
-    return tuple(torch.zeros((batch, n_kv_h, cap, hd // w), dtype=torch.uint8, device=device) for w in (2, 16, 2, 16))
+    return tuple(torch.zeros((batch, n_kv_h, cap, hd // w), dtype=_U8, device=device) for w in (2, 16, 2, 16))
 
 
-def _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev):
-    if k_codes.dim() != 4:
-        raise ValueError("k_codes [b, n_kv_h, cap, hd/2] expected, got %s" % (tuple(k_codes.shape),))
-    cap = k_codes.shape[2]
+def _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev):
     cs, ss = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
-    return cap, (_ptr(k_codes, "k_codes", torch.uint8, cs, dev), _ptr(k_scales, "k_scales", torch.uint8, ss, dev),
-                 _ptr(v_codes, "v_codes", torch.uint8, cs, dev), _ptr(v_scales, "v_scales", torch.uint8, ss, dev))
+    return (_ptr(k_codes, "k_codes", _U8, cs, dev), _ptr(k_scales, "k_scales", _U8, ss, dev),
+            _ptr(v_codes, "v_codes", _U8, cs, dev), _ptr(v_scales, "v_scales", _U8, ss, dev))
+
+
+def _kv4_heads_rows(k_codes):
+    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+        raise ValueError("k_codes [b, n_kv_h, cap, hd/2] expected")
+    return k_codes.shape[1:3]
 
 
 def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=1.0, v_global=1.0, k_out=None, v_out=None,
                     stream=None):
     """Quantise k, v (bf16 [b, n_kv_h, T, hd]) into a 4-bit cache (fmha_kv4_cache) at rows start[b] + t (int32 [b]; rows
     outside the cache are left out).  k_out and v_out, bf16 like k, receive the values that the written rows stand for."""
+    dev = _device(k, "k")
     if k.dim() != 4:
         raise ValueError("k [b, n_kv_h, T, hd] expected, got %s" % (tuple(k.shape),))
-    b, n_kv_h, T, hd = k.shape
-    dev = k.device
-    cap, cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev)
-    _call("fmha_kv4_append", dev, stream, _ptr(k, "k", torch.bfloat16, k.shape, dev), _ptr(v, "v", torch.bfloat16, k.shape, dev),
-          *cache, _ptr(start, "start", torch.int32, (b,), dev), k_global, v_global,
-          _ptr(k_out, "k_out", torch.bfloat16, k.shape, dev, True), _ptr(v_out, "v_out", torch.bfloat16, k.shape, dev, True),
-          b, n_kv_h, T, cap, hd)
+    shape = k.shape
+    b, n_kv_h, T, hd = shape
+    cap = _kv4_heads_rows(k_codes)[1]
+    _call("fmha_kv4_append", dev, stream, _ptr(k, "k", _BF16, shape, dev), _ptr(v, "v", _BF16, shape, dev),
+          *_kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev), _ptr(start, "start", _I32, (b,), dev),
+          k_global, v_global, None if k_out is None else _ptr(k_out, "k_out", _BF16, shape, dev),
+          None if v_out is None else _ptr(v_out, "v_out", _BF16, shape, dev), b, n_kv_h, T, cap, hd)
 
 
-_kv4_plans = {}
+_kv4_plans = {}  # (chunk length, workspace bytes) by shape, for the kernel path that is set
 
 
 def fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, window=0, n_first=0, causal=False, kv_chunk=0):
@@ -564,37 +601,39 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
 
     seq_lens: int32 [b], the keys of each sequence (None: s_k each); s_k: their bound, at most the cache's rows (the
     default).  With a window, the keys j < n_first stay attended.  workspace: an optional uint8 tensor for the split-KV
-    partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call takes its own from torch."""
+    partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call uses the
+    binding's own (one per thread and stream; a new one under graph capture)."""
+    dev = _device(q, "q")
     if q.dim() != 4:
         raise ValueError("q [b, n_h, T, hd] expected, got %s" % (tuple(q.shape),))
-    b, n_h, T, hd = q.shape
-    dev = q.device
-    n_kv_h = k_codes.shape[1] if k_codes.dim() == 4 else 0
-    cap, cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, hd, dev)
+    shape = q.shape
+    b, n_h, T, hd = shape
+    n_kv_h, cap = _kv4_heads_rows(k_codes)
     if s_k is None:
         s_k = cap
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=dev)
-    if scale is None:
-        scale = hd ** -0.5
+        lse = torch.empty((b, n_h, T), dtype=_FP32, device=dev)
     key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk)
     plan = _kv4_plans.get(key)
     if plan is None:
-        plan = _kv4_plans[key] = fmha_fwd_kv4_plan(*key)
-    n, kv_chunk = plan
-    if n > 1 and workspace is None:
-        workspace = _scratch(fmha_workspace_bytes(b, n_h, T, hd, n), dev, stream)
-    ws, ws_bytes = None, 0
+        n, chunk = fmha_fwd_kv4_plan(*key)
+        plan = _kv4_plans[key] = chunk, (fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0)
+    kv_chunk, need = plan
+    q_ptr = _ptr(q, "q", _BF16, shape, dev)
+    cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev)
+    ws = None
     if workspace is not None:
-        ws_bytes = workspace.numel()
-        ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    _call("fmha_fwd_kv4", dev, stream, _ptr(q, "q", torch.bfloat16, q.shape, dev), *cache,
-          _ptr(seq_lens, "seq_lens", torch.int32, (b,), dev, True), _ptr(o, "o", torch.bfloat16, q.shape, dev),
-          _ptr(lse, "lse", torch.float32, (b, n_h, T), dev), _ptr(sink, "sink", torch.float32, (n_h,), dev, True),
-          k_global, v_global, b, n_h, n_kv_h, T, s_k, cap, hd, scale, int(window), int(n_first), int(bool(causal)), int(kv_chunk),
-          ws, ws_bytes)
+        ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
+        need = workspace.numel()
+    elif need:
+        workspace = _workspace(need, dev, stream)
+        ws = workspace.data_ptr()
+    _call("fmha_fwd_kv4", dev, stream, q_ptr, *cache, None if seq_lens is None else _ptr(seq_lens, "seq_lens", _I32, (b,), dev),
+          _ptr(o, "o", _BF16, shape, dev), _ptr(lse, "lse", _FP32, (b, n_h, T), dev),
+          None if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), k_global, v_global, b, n_h, n_kv_h, T, s_k, cap, hd,
+          hd ** -0.5 if scale is None else scale, window, n_first, bool(causal), kv_chunk, ws, need)
     return o, lse
 
 
@@ -610,28 +649,28 @@ def fmha_fwd_first_workspace_bytes(batch, n_h, n_kv_h, T, s_k, hd, window, n_fir
 def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, causal=False, sink=None, workspace=None,
                    stream=None):
     """fmha_fwd with the keys j < n_first attended outside the window too (fmha_fwd_first in include/fmha.h).
-    workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call takes its own from torch."""
+    workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call uses the
+    binding's own (one per thread and stream; a new one under graph capture)."""
+    dev = _device(q, "q")
     b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
-    dev = q.device
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=dev)
-    if scale is None:
-        scale = hd ** -0.5
+        lse = torch.empty((b, n_h, T), dtype=_FP32, device=dev)
     key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal)
     need = _first_plans.get(key)
     if need is None:
         need = _first_plans[key] = fmha_fwd_first_workspace_bytes(*key)
-    if need and workspace is None:
-        workspace = _scratch(need, dev, stream)
-    ws, ws_bytes = None, 0
+    q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
+    q_ptr, k_ptr = _ptr(q, "q", _BF16, q_shape, dev), _ptr(k, "k", _BF16, kv_shape, dev)
+    ws = None
     if workspace is not None:
-        ws_bytes = workspace.numel()
-        ws = _ptr(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    bf = torch.bfloat16
-    _call("fmha_fwd_first", dev, stream, _ptr(q, "q", bf, q.shape, dev), _ptr(k, "k", bf, k.shape, dev),
-          _ptr(v, "v", bf, k.shape, dev), _ptr(o, "o", bf, q.shape, dev), _ptr(lse, "lse", torch.float32, (b, n_h, T), dev),
-          _ptr(sink, "sink", torch.float32, (n_h,), dev, True), b, n_h, n_kv_h, T, s_k, hd, scale, int(window), int(n_first),
-          int(bool(causal)), ws, ws_bytes)
+        ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
+        need = workspace.numel()
+    elif need:
+        workspace = _workspace(need, dev, stream)
+        ws = workspace.data_ptr()
+    _call("fmha_fwd_first", dev, stream, q_ptr, k_ptr, _ptr(v, "v", _BF16, kv_shape, dev), _ptr(o, "o", _BF16, q_shape, dev),
+          _ptr(lse, "lse", _FP32, (b, n_h, T), dev), None if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev),
+          b, n_h, n_kv_h, T, s_k, hd, hd ** -0.5 if scale is None else scale, window, n_first, bool(causal), ws, need)
     return o, lse

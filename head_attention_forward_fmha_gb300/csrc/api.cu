@@ -917,45 +917,69 @@ bool kv4_use_tc(int hd, long long R) {
     return R >= (hd <= 128 ? 48 : 24);
 }
 
-// Chunks of the virtual key axis (first keys rounded up to tiles, then the
-// window) for sequences of s_k keys: the smallest number of chunks whose
-// estimated time is least.  A block's time is its share of its SM's HBM rate
-// (42 KB/us per SM, spread over the resident blocks) plus ~1.5 us of latency,
-// or with the tensor-core kernel ~1.4 us per tile and 4 us; splitting adds the merge.
+// How fmha_fwd_kv4 divides its work: the virtual key axis (first keys rounded up
+// to tiles, then the window) of sequences of s_k keys into n chunks, and for the
+// mma.sync kernel the warps per block; the candidate with the least estimated time.
+//
+// mma.sync kernel: a warp needs at least ~0.8 us for a tile of 4096 K and V codes
+// whatever else runs, an SM at least ~0.13 us (35 KB of cache per us), a block
+// ~3 us before and after; the merge kernel ~2.5 us and its partials.
+// Tensor-core kernel: ~1.4 us per tile, ~6 us before and after.
 void plan_kv4(Kv4Fwd* f) {
     const long long R = (long long)f->n_h / f->n_kv_h * f->T;
     f->tc = kv4_use_tc(f->hd, R);
-    const int tile = f->tc ? kv4_tc_kv_tile(f->hd) : kv4_kv_tile(f->hd), unit = f->tc ? tile : 4 * tile;
-    const int rows = f->tc ? 128 : kv4_rows_per_cta(f->hd, R), per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows);
+    const int tile = f->tc ? kv4_tc_kv_tile(f->hd) : kv4_kv_tile(f->hd);
+    const int rows = f->tc ? 128 : kv4_rows_per_cta(f->hd, R);
     // The longest axis that any length up to s_k gives: its body holds at most
     // window + T - 1 keys and starts up to 15 keys early.
     long long span = f->s_k;
     if (f->window > 0)
         span = (f->n_first + tile - 1) / tile * tile + std::min<long long>(f->s_k, (long long)f->window + f->T - 1 + 15);
     if (span < 1) span = 1;
-    if (f->kv_chunk <= 0) {
-        const long long units =
-            (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
-        const long long slots = (long long)sm_count() * per_sm;
-        const double key_bytes = f->hd * 2 * 0.5625;
-        double best = 0;
-        long long best_n = 1;
-        const long long max_n = std::min<long long>(256, (span + unit - 1) / unit);
-        for (long long n = 1; n <= max_n; ++n) {
-            const long long keys = ((span + n - 1) / n + unit - 1) / unit * unit;
-            const long long waves = (units * n + slots - 1) / slots;
-            double us = f->tc ? (double)waves * (4.0 + (double)keys / tile * 1.4)
-                              : (double)waves * (1.5 + (double)keys * key_bytes * per_sm / 42e3);
-            if (n > 1) us += 2.0 + (double)R * f->batch * f->n_kv_h * f->hd * 4.0 * (double)n / 8e6;
-            if (n == 1 || us < best * 0.98) {
-                best = us;
-                best_n = n;
-            }
+    f->warps = 4;
+    const long long most = INT_MAX / 2 / tile * tile;
+    const long long units =
+        (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
+    const long long sms = sm_count(), tiles = (span + tile - 1) / tile;
+    const double parts_us = (double)R * f->batch * f->n_kv_h * f->hd * 4.0 / 8e6;  // one chunk's partials, written and read
+    const double size = tile * f->hd / 4096.0, lat = 0.8 * size * (0.75 + rows / 32.0), thr = 0.13 * size * (0.9 + rows / 80.0);
+    double best = 1e30;
+    long long best_n = 1;
+    auto consider = [&](int warps, long long n) {
+        if (n < 1 || n > 256 || (n > 1 && n > tiles)) return;
+        const int per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps);
+        const long long blocks = units * n, slots = sms * per_sm, waves = (blocks + slots - 1) / slots;
+        const long long mine = (tiles + n - 1) / n;  // tiles of a block
+        double us;
+        if (f->tc) {
+            us = (double)waves * (6.0 + (double)mine * 1.4);
+        } else {
+            const long long resident = std::min<long long>(per_sm, (blocks + sms - 1) / sms);
+            const double busy = (double)std::min<long long>(warps, mine) * (double)resident;
+            us = (double)waves * (3.0 + (double)((mine + warps - 1) / warps) * std::max(lat, busy * thr));
         }
-        f->kv_chunk = (int)std::min<long long>(((span + best_n - 1) / best_n + unit - 1) / unit * unit, INT_MAX / 2 / unit * unit);
-    } else {
-        f->kv_chunk = (int)std::min<long long>(((long long)f->kv_chunk + tile - 1) / tile * tile, INT_MAX / 2 / tile * tile);
+        if (n > 1) us += 2.5 + parts_us * (double)n;
+        if (us < best * 0.98) {
+            best = us;
+            best_n = n;
+            f->warps = warps;
+        }
+    };
+    const int big = f->tc ? 4 : kv4_big_warps(f->hd, rows);
+    if (f->kv_chunk > 0) {  // the caller's chunks
+        f->kv_chunk = (int)std::min(((long long)f->kv_chunk + tile - 1) / tile * tile, most);
+        f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
+        consider(4, f->n_splits);
+        if (big > 4) consider(big, f->n_splits);
+        return;
     }
+    for (int warps = 4; warps <= big; warps += big > 4 ? big - 4 : 4) {
+        consider(warps, 1);
+        const long long slots = sms * (f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps));
+        for (long long n = 2; n <= 16; n *= 2) consider(warps, n);
+        for (int w = 1; w <= 4; ++w) consider(warps, slots * w / std::max(1LL, units));  // whole waves
+    }
+    f->kv_chunk = (int)std::min((tiles + best_n - 1) / best_n * tile, most);
     f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
 }
 

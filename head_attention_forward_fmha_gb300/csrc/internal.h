@@ -173,11 +173,13 @@ struct Kv4Fwd {
     int batch, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, causal;
     int kv_chunk, n_splits;  // keys per chunk (a multiple of the kernel's key tile) and their number
     bool tc;                 // the tensor-core kernel
+    int warps;               // warps per block of the other
     unsigned* status;
 };
 int kv4_kv_tile(int hd);                       // keys per tile
 int kv4_rows_per_cta(int hd, long long rows);  // query rows per thread block, given the rows per KV head
-int kv4_ctas_per_sm(int hd, int rows_per_cta);
+int kv4_big_warps(int hd, int rows_per_cta);   // warps of the larger of the two block sizes (the other has 4)
+int kv4_ctas_per_sm(int hd, int rows_per_cta, int warps);
 cudaError_t launch_kv4_fwd(const Kv4Fwd& a, cudaStream_t stream);
 // 128-row query tiles on the tcgen05 tensor cores (kv4_tc_kernel.cu)
 int kv4_tc_kv_tile(int hd);

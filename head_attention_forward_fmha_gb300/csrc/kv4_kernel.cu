@@ -12,7 +12,7 @@
 // bf16 output's 8).
 //
 // One thread block takes RT = 8 NB query rows that share a KV head and one chunk
-// of that sequence's keys; each of its four warps takes every fourth tile of KT
+// of that sequence's keys; each of its W warps takes every W-th tile of KT
 // keys through a ring of its own (four bulk copies per tile: K and V codes and
 // scales, each contiguous over keys), so no warp waits for another before the
 // end.  Per 16 keys a warp computes S^T = K Q^T and O^T += V^T P^T with
@@ -44,11 +44,11 @@
 namespace fmha {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry
 
-template <int HD, int NB>
+template <int HD, int NB, int W>
 struct K4Cfg {
+    static constexpr int WARPS = W;
     static constexpr int RT = 8 * NB;                  // query rows per block
     static constexpr int KT = HD >= 256 ? 16 : 32;     // keys per tile
     static constexpr int GR = KT / 16;                 // 16-key groups per tile
@@ -58,7 +58,7 @@ struct K4Cfg {
     static constexpr int OFF_VC = OFF_KS + KT * SB;
     static constexpr int OFF_VS = OFF_VC + KT * CB;
     static constexpr int STAGE = OFF_VS + KT * SB;
-    static constexpr int STAGES = HD == 256 ? 4 : 3;
+    static constexpr int STAGES = W > 4 || HD == 512 ? 2 : HD == 256 ? 4 : 3;
     static constexpr int RING = STAGES * STAGE;        // per warp
     static constexpr int NCH = HD >= 128 ? HD / 128 : 1;  // 128-column chunks
     static constexpr int TW = HD >= 128 ? 32 : 16;     // columns of a chunk per lane in S^T
@@ -66,12 +66,12 @@ struct K4Cfg {
     static constexpr int ODB = HD / 16;                // MMAs of O^T
     static constexpr bool QREG = HD * NB <= 256;       // Q fragments in registers, else in shared memory
     static constexpr int Q_BYTES = QREG ? 0 : QSTEPS * NB * 256;
-    static constexpr int COMB = kWarps * RT * HD * 4;  // epilogue: fp32 O of each warp
-    static constexpr int BODY = kWarps * RING > COMB ? kWarps * RING : COMB;
+    static constexpr int COMB = W * RT * HD * 4;  // epilogue: fp32 O of each warp
+    static constexpr int BODY = W * RING > COMB ? W * RING : COMB;
     static constexpr int OFF_Q = BODY;
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
-    static constexpr int OFF_ML = OFF_BAR + kWarps * STAGES * 8;   // [kWarps][RT] (reference, sum)
-    static constexpr int OFF_FLAG = OFF_ML + kWarps * RT * 8;
+    static constexpr int OFF_ML = OFF_BAR + W * STAGES * 8;   // [W][RT] (reference, sum)
+    static constexpr int OFF_FLAG = OFF_ML + W * RT * 8;
     static constexpr int SMEM = OFF_FLAG + 16;
     static_assert(STAGE % 16 == 0 && OFF_KS % 16 == 0 && OFF_VC % 16 == 0, "bulk copies are 16-byte aligned");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -141,9 +141,10 @@ __device__ __forceinline__ void key_pairs(uint32_t x, uint32_t y, uint32_t s, ui
     }
 }
 
-template <int HD, int NB, bool SINK>
-__global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
-    using C = K4Cfg<HD, NB>;
+template <int HD, int NB, int W>
+__global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv4_fwd_kernel(const K4Args a) {
+    using C = K4Cfg<HD, NB, W>;
+    constexpr int kWarps = W;
     constexpr int KT = C::KT, GR = C::GR;
     const Kv4Fwd& f = a.f;
     launch_dependents();  // the merge grid may be scheduled now; it waits for this grid's results
@@ -158,12 +159,37 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
     const int r_begin = blockIdx.x * C::RT;
     const int r_end = min(a.R, r_begin + C::RT);
     const long long row0 = ((long long)b * f.n_h + (long long)kvh * a.group) * f.T;  // slab's first query row
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * C::STAGES; ++i) mbar_init(&bars[i], 1);
-        *abort_flag = 0;
+    auto row_t = [&](int r) { return f.T == 1 ? 0 : r % f.T; };
+    if (threadIdx.x < 32) {
+        for (int i = threadIdx.x; i < kWarps * C::STAGES; i += 32) mbar_init(&bars[i], 1);
+        if (threadIdx.x == 0) *abort_flag = 0;
         mbar_fence_init();
     }
+    __syncthreads();         // barriers initialised
     grid_dependency_wait();  // every global access below follows the preceding kernel
+
+    // Q's loads are issued before the sequence's length is known (NB = 1: all of them).
+    auto q_row = [&](int nb) {
+        const int r = r_begin + nb * 8 + g;
+        return reinterpret_cast<const uint2*>(f.q + (row0 + (r < r_end ? r : r_begin)) * HD);
+    };
+    uint2 early[C::QSTEPS];
+    {
+        const uint2* src = q_row(0);
+#pragma unroll
+        for (int i = 0; i < C::QSTEPS; ++i)
+            early[i] = __ldg(src + (128 * (i / (C::TW / 4)) + C::TW * t4 + 4 * (i % (C::TW / 4))) / 4);
+    }
+    auto load_q = [&](int nb, uint2 (&raw)[C::QSTEPS]) {
+        const bool live = r_begin + nb * 8 + g < r_end;
+        const uint2* src = q_row(nb);
+#pragma unroll
+        for (int i = 0; i < C::QSTEPS; ++i) {
+            raw[i] = nb == 0 ? early[i]
+                             : __ldg(src + (128 * (i / (C::TW / 4)) + C::TW * t4 + 4 * (i % (C::TW / 4))) / 4);
+            if (!live) raw[i] = make_uint2(0u, 0u);
+        }
+    };
 
     // Keys.  Row t sits at position len - T + t.  The chunks divide a virtual
     // key axis: the first keys (rounded up to whole tiles), then the keys from
@@ -199,11 +225,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
 
     const uint32_t ring = smem_u32(smem) + warp * C::RING;
     uint64_t* full = bars + warp * C::STAGES;
-    // this slab's rows
-    const uint8_t* const kc = f.k_codes + (long long)slab * f.cap * C::CB;
-    const uint8_t* const ks = f.k_scales + (long long)slab * f.cap * C::SB;
-    const uint8_t* const vc = f.v_codes + (long long)slab * f.cap * C::CB;
-    const uint8_t* const vs = f.v_scales + (long long)slab * f.cap * C::SB;
     const uint64_t pol = l2_policy_evict_first();
     const int my_tiles = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
 
@@ -218,25 +239,28 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             end = b_hi;
         }
     };
-    auto issue = [&](int i, int s) {  // one lane; tile i into stage s = i % STAGES, which is free
+    // Lanes 0 .. 3 copy a tile's K codes, K scales, V codes and V scales, one each.
+    const bool copier = lane < 4;
+    const uint8_t* my_src = lane == 0 ? f.k_codes : lane == 1 ? f.k_scales : lane == 2 ? f.v_codes : f.v_scales;
+    const int my_row = (lane & 1) ? C::SB : C::CB;
+    my_src += (long long)slab * f.cap * my_row;
+    const uint32_t my_dst = ring + (lane == 0 ? 0 : lane == 1 ? C::OFF_KS : lane == 2 ? C::OFF_VC : C::OFF_VS);
+    auto issue = [&](int i, int s) {  // the copying lanes; tile i into stage s = i % STAGES, which is free
         int key, end;
         tile_of(i, key, end);
         const int n = min(KT, ((warp + i * kWarps) < n_head ? head_end16 : body_end16) - key);
         if (!FMHA_IN_BOUNDS(key >= 0 && key % 16 == 0 && n > 0 && n % 16 == 0 && key + n <= f.cap, kSiteKv4Copy, f.status))
             return false;
-        const uint32_t dst = ring + s * C::STAGE;
-        const unsigned long long r = (unsigned)key;
-        mbar_arrive_expect_tx(&full[s], n * 2 * (C::CB + C::SB));
-        bulk_load_hint(dst, kc + r * C::CB, n * C::CB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_KS, ks + r * C::SB, n * C::SB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_VC, vc + r * C::CB, n * C::CB, &full[s], pol);
-        bulk_load_hint(dst + C::OFF_VS, vs + r * C::SB, n * C::SB, &full[s], pol);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], n * 2 * (C::CB + C::SB));
+        bulk_load_hint(my_dst + s * C::STAGE, my_src + (unsigned long long)(unsigned)key * my_row, n * my_row, &full[s], pol);
         return true;
     };
-    __syncthreads();  // barriers initialised
-    int issued = 0;   // lane 0: tiles issued
-    if (lane == 0)
-        while (issued < min(C::STAGES, my_tiles) && issue(issued, issued)) ++issued;
+    int issued = 0;  // copying lanes: tiles issued
+    if (copier) {
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i)
+            if (issued == i && i < my_tiles && issue(i, i)) ++issued;
+    }
 
     // Q fragments: for step s of chunk c, row n = g: columns 128 c + TW t + 4 s ..+3.
     uint2 qf[C::QREG ? C::QSTEPS : 1][NB];
@@ -245,18 +269,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         float fac_g[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int r = r_begin + nb * 8 + g;
-            const bool live = r < r_end;
-            const uint2* src = reinterpret_cast<const uint2*>(f.q + (row0 + (live ? r : r_begin)) * HD);
             uint2 raw[C::QSTEPS];
+            load_q(nb, raw);
             uint32_t mx = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
-            for (int i = 0; i < C::QSTEPS; ++i) {
-                const int c = i / (C::TW / 4), s = i % (C::TW / 4);
-                raw[i] = live ? __ldg(src + (128 * c + C::TW * t4 + 4 * s) / 4) : make_uint2(0u, 0u);
-                mx = max(mx, max(max(raw[i].x & 0x7FFFu, (raw[i].x >> 16) & 0x7FFFu),
-                                 max(raw[i].y & 0x7FFFu, (raw[i].y >> 16) & 0x7FFFu)));
-            }
+            for (int i = 0; i < C::QSTEPS; ++i)
+                mx = __vmaxu2(mx, __vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu));
+            mx = max(mx & 0xFFFFu, mx >> 16);
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             // 2^k takes the largest magnitude into [2^14, 2^15); rows of zeros,
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             const int r = r_begin + nb * 8 + 2 * t4 + i;
             int lo = INT_MAX, hi = -1;
             if (r < r_end) {
-                const int p = len - f.T + r % f.T;
+                const int p = len - f.T + row_t(r);
                 lo = u_lo;
                 hi = b_hi - 1;
                 if (f.causal) hi = min(hi, p);
@@ -334,8 +353,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
             for (int nb = 0; nb < NB; ++nb) sc[gr][nb][0] = sc[gr][nb][1] = sc[gr][nb][2] = sc[gr][nb][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c) {
-                constexpr int W = C::TW / 8;
-                uint32_t wa[W], wb[W], ra[W][4], rb[W][4];
+                constexpr int WD = C::TW / 8;
+                uint32_t wa[WD], wb[WD], ra[WD][4], rb[WD][4];
                 const uint32_t pa = st + (gr * 16 + row_a) * C::CB + c * 64 + t4 * (C::TW / 2);
                 const uint32_t pb = pa + 8 * C::CB;
                 const uint32_t qa = st + C::OFF_KS + (gr * 16 + row_a) * C::SB + c * 8 + t4 * (C::TW / 16);
@@ -353,10 +372,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                     sa = lds8(qa);
                     sb = lds8(qa + 8 * C::SB);
                 }
-                scaled_row<W>(wa, sa, ra);
-                scaled_row<W>(wb, sb, rb);
+                scaled_row<WD>(wa, sa, ra);
+                scaled_row<WD>(wb, sb, rb);
 #pragma unroll
-                for (int w = 0; w < W; ++w)
+                for (int w = 0; w < WD; ++w)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int step = c * (C::TW / 4) + 2 * w + h;
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                         bool in = key >= jlo[nb][e & 1] && key <= jhi[nb][e & 1];
                         if (head) {
                             const int r = r_begin + nb * 8 + 2 * t4 + (e & 1);
-                            in = r < r_end && key < n_first && (!f.causal || key <= len - f.T + r % f.T);
+                            in = r < r_end && key < n_first && (!f.causal || key <= len - f.T + row_t(r));
                         }
                         sc[gr][nb][e] = in ? sc[gr][nb][e] : -INFINITY;
                     }
@@ -466,10 +485,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                     s3 = in_y8 ? s3 : 0u;
                 }
                 const uint32_t sp = e4m3x2_to_f16(s0 | (s1 << 8)), sq = e4m3x2_to_f16(s2 | (s3 << 8));
-                constexpr int W = HD >= 128 ? 2 : 1;
-                const uint32_t cv = st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * W);
-                uint32_t x[W], y[W], x8[W], y8[W];
-                if constexpr (W == 2) {
+                constexpr int WV = HD >= 128 ? 2 : 1;
+                const uint32_t cv = st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * WV);
+                uint32_t x[WV], y[WV], x8[WV], y8[WV];
+                if constexpr (WV == 2) {
                     const uint2 u0 = lds64(cv + key_x * C::CB), u1 = lds64(cv + key_y * C::CB);
                     const uint2 u2 = lds64(cv + (key_x + 8) * C::CB), u3 = lds64(cv + (key_y + 8) * C::CB);
                     x[0] = u0.x; x[1] = u0.y;
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                     y8[0] = lds32(cv + (key_y + 8) * C::CB);
                 }
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
+                for (int w = 0; w < WV; ++w) {
                     uint32_t lo[4], hi[4], lo8[4], hi8[4];
                     key_pairs(x[w], y[w], sp, lo, hi);
                     key_pairs(x8[w], y8[w], sq, lo8, hi8);
@@ -491,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
-                            mma_f16_16816(o[(c * W + w) * 4 + j][nb], lo[j], hi[j], lo8[j], hi8[j], pb[gr][nb][0],
+                            mma_f16_16816(o[(c * WV + w) * 4 + j][nb], lo[j], hi[j], lo8[j], hi8[j], pb[gr][nb][0],
                                           pb[gr][nb][1]);
                 }
             }
@@ -513,7 +532,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
         else
             tile_step(std::true_type{}, ring + s * C::STAGE, key0, end, head);
         __syncwarp();  // every lane is done with the stage
-        if (lane == 0 && issued == i + C::STAGES && issued < my_tiles && issue(issued, s)) ++issued;
+        if (copier && issued == i + C::STAGES && issued < my_tiles && issue(issued, s)) ++issued;
         if (++s == C::STAGES) {
             s = 0;
             phase ^= 1;
@@ -521,8 +540,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
     }
 
     // ------------------------------------------------------------ epilogue
-    if (lane == 0) drain_ring(full, C::STAGES, issued, f.status);
-    if (!ok) atomicOr(abort_flag, 1);
+    // Every copy that was waited for has landed; after a wait that gave up the
+    // others are waited for here.
+    if (!ok) {
+        if (lane == 0) {
+            drain_ring(full, C::STAGES, issued, f.status);
+            atomicOr(abort_flag, 1);
+        }
+        __syncwarp();
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -540,75 +566,79 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_fwd_kernel(const K4Args a) {
     __syncthreads();  // every warp is done with its ring
     if (*abort_flag) return;
 
-    // Rescale this warp's O to the rows' maxima over the warps and park it.
-    float* comb = reinterpret_cast<float*>(smem);  // [kWarps][RT][HD]
+    // Each warp parks its O as it lies in the fragments: [warp][MMA d][nb][i][lane],
+    // the column pair of row nb * 8 + 2 t + i, so that neither the stores nor the
+    // loads below meet a bank twice.
+    constexpr int WV = HD >= 128 ? 2 : 1;
+    float2* comb = reinterpret_cast<float2*>(smem);
+    constexpr int SLICE = C::ODB * NB * 2 * 32;  // one warp's share
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int d = 0; d < C::ODB; ++d)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = nb * 8 + 2 * t4 + i;
-            float M = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * C::RT + r].x);
-            const float fac = exp2f(m_ref[nb][i] - ((M == -INFINITY) ? 0.f : M));
-#pragma unroll
-            for (int d = 0; d < C::ODB; ++d) {
-                constexpr int W = HD >= 128 ? 2 : 1;
-                const int c = d / (4 * W), w = (d / 4) % W, j = d % 4;
-                const int col = 128 * c + g * (8 * W) + 8 * w + 2 * j;
-                const int ci = (warp * C::RT + r) * HD + col;
-                if (!FMHA_IN_BOUNDS(ci >= 0 && ci + 2 <= kWarps * C::RT * HD, kSiteKv4Comb, f.status)) continue;
-                *reinterpret_cast<float2*>(comb + ci) = make_float2(o[d][nb][i] * fac, o[d][nb][2 + i] * fac);
+            for (int i = 0; i < 2; ++i) {
+                const int at = warp * SLICE + ((d * NB + nb) * 2 + i) * 32 + lane;
+                if (FMHA_IN_BOUNDS(at < W * SLICE, kSiteKv4Comb, f.status)) comb[at] = make_float2(o[d][nb][i], o[d][nb][2 + i]);
             }
-        }
     __syncthreads();
-    for (int item = threadIdx.x; item < C::RT * (HD / 8); item += kWarps * 32) {
-        const int r = item / (HD / 8), d8 = item - r * (HD / 8);
+    // A job is 8 neighbouring columns (four MMAs) of the 32 lanes' rows: sum the warps,
+    // weighted by their references, divide, write out.
+    constexpr int JOBS = C::NCH * WV * NB * 2;
+    for (int job = warp; job < JOBS; job += kWarps) {
+        const int i = job & 1, nb = (job >> 1) % NB, cw = job / (2 * NB);  // cw: 8-column half of a block (with its chunk)
+        const int r = nb * 8 + 2 * t4 + i;
         if (r_begin + r >= r_end) continue;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * C::RT + r].x);
         const float Mu = (M == -INFINITY) ? 0.f : M;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) L += ml[w * C::RT + r].y * exp2f(ml[w * C::RT + r].x - Mu);
-        float inv, lse;
-        finish_row(M - kPBias, L,
-                   SINK ? sink_log2_of(f.sink, kvh * a.group + (r_begin + r) / f.T, f.n_h, f.status) : -INFINITY, inv, lse);
-        inv *= f.v_global;
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4* src = reinterpret_cast<const float4*>(comb + (w * C::RT + r) * HD + d8 * 8);
-            const float4 u0 = src[0], u1 = src[1];
-            acc[0] += u0.x; acc[1] += u0.y; acc[2] += u0.z; acc[3] += u0.w;
-            acc[4] += u1.x; acc[5] += u1.y; acc[6] += u1.z; acc[7] += u1.w;
+            const float2 v = ml[w * C::RT + r];
+            const float fac = exp2f(v.x - Mu);  // 0 for a warp without keys
+            L += v.y * fac;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = comb[w * SLICE + (((cw * 4 + j) * NB + nb) * 2 + i) * 32 + lane];
+                acc[2 * j] += u.x * fac;
+                acc[2 * j + 1] += u.y * fac;
+            }
         }
+        float inv, lse;
+        finish_row(M - kPBias, L,
+                   f.sink && f.n_splits == 1 ? sink_log2_of(f.sink, kvh * a.group + (r_begin + r) / f.T, f.n_h, f.status)
+                                             : -INFINITY,
+                   inv, lse);
+        inv *= f.v_global;
+        const int col = 128 * (cw / WV) + g * (8 * WV) + 8 * (cw % WV);
         const long long grow = row0 + r_begin + r;
-        if (!FMHA_IN_BOUNDS(grow >= 0 && grow < a.rows_total && split < f.n_splits, kSiteKv4Out, f.status)) continue;
+        if (!FMHA_IN_BOUNDS(grow >= 0 && grow < a.rows_total && split < f.n_splits && col + 8 <= HD, kSiteKv4Out, f.status)) continue;
         if (f.n_splits == 1) {
             uint4 pk;
             pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
             pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
             pk.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
             pk.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-            *reinterpret_cast<uint4*>(f.o + grow * HD + d8 * 8) = pk;
-            if (d8 == 0) f.lse[grow] = lse;
+            *reinterpret_cast<uint4*>(f.o + grow * HD + col) = pk;
+            if (col == 0) f.lse[grow] = lse;
         } else {
             const long long prow = (long long)split * a.rows_total + grow;
-            float4* dst = reinterpret_cast<float4*>(f.o_part + prow * HD + d8 * 8);
+            float4* dst = reinterpret_cast<float4*>(f.o_part + prow * HD + col);
             dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
             dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
-            if (d8 == 0) f.lse_part[prow] = lse;
+            if (col == 0) f.lse_part[prow] = lse;
         }
     }
 }
 
-template <int HD, int NB, bool SINK>
+template <int HD, int NB, int W>
 cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
-    using C = K4Cfg<HD, NB>;
-    auto kern = kv4_fwd_kernel<HD, NB, SINK>;
+    using C = K4Cfg<HD, NB, W>;
+    auto kern = kv4_fwd_kernel<HD, NB, W>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -628,7 +658,7 @@ cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
     a.rows_total = (long long)f.batch * f.n_h * f.T;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.R + C::RT - 1) / C::RT, f.n_splits, f.batch * f.n_kv_h);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(W * 32);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
@@ -637,25 +667,21 @@ cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int HD, bool SINK>
+constexpr int big_warps(int hd, int rows) { return hd * rows <= 1024 ? 16 : 8; }
+
+template <int HD, int NB>
+cudaError_t launch_w(const Kv4Fwd& f, cudaStream_t stream) {
+    return f.warps > 4 ? launch_t<HD, NB, big_warps(HD, 8 * NB)>(f, stream) : launch_t<HD, NB, 4>(f, stream);
+}
+
+template <int HD>
 cudaError_t launch_hd(const Kv4Fwd& f, cudaStream_t stream) {
     const int rows = kv4_rows_per_cta(HD, (long long)f.n_h / f.n_kv_h * f.T);
     if constexpr (HD <= 128)
-        if (rows == 32) return launch_t<HD, 4, SINK>(f, stream);
+        if (rows == 32) return launch_w<HD, 4>(f, stream);
     if constexpr (HD <= 256)
-        if (rows == 16) return launch_t<HD, 2, SINK>(f, stream);
-    return launch_t<HD, 1, SINK>(f, stream);
-}
-
-template <bool SINK>
-cudaError_t launch_s(const Kv4Fwd& f, cudaStream_t stream) {
-    switch (f.hd) {
-        case 64: return launch_hd<64, SINK>(f, stream);
-        case 128: return launch_hd<128, SINK>(f, stream);
-        case 256: return launch_hd<256, SINK>(f, stream);
-        case 512: return launch_hd<512, SINK>(f, stream);
-        default: return cudaErrorInvalidValue;
-    }
+        if (rows == 16) return launch_w<HD, 2>(f, stream);
+    return launch_w<HD, 1>(f, stream);
 }
 
 }  // namespace
@@ -667,14 +693,21 @@ int kv4_rows_per_cta(int hd, long long rows) {
     return rows > 8 && hd <= 256 ? 16 : 8;
 }
 
-int kv4_ctas_per_sm(int hd, int rows_per_cta) {
-    if (hd == 512) return 2;
-    if (hd * rows_per_cta <= 128 * 8) return 4;
-    return hd * rows_per_cta >= 128 * 32 ? 2 : 3;
+int kv4_big_warps(int hd, int rows_per_cta) { return big_warps(hd, rows_per_cta); }
+
+int kv4_ctas_per_sm(int hd, int rows_per_cta, int warps) {
+    if (warps > 4) return 1;
+    return hd * rows_per_cta <= 128 * 8 ? 4 : 2;  // by registers and shared memory
 }
 
 cudaError_t launch_kv4_fwd(const Kv4Fwd& f, cudaStream_t stream) {
-    return f.sink && f.n_splits == 1 ? launch_s<true>(f, stream) : launch_s<false>(f, stream);
+    switch (f.hd) {
+        case 64: return launch_hd<64>(f, stream);
+        case 128: return launch_hd<128>(f, stream);
+        case 256: return launch_hd<256>(f, stream);
+        case 512: return launch_hd<512>(f, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace fmha

@@ -79,17 +79,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
         : "memory");
 }
 
-// One lane of the (converged) warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
 // Instruction descriptor, kind::f16 with fp16 A and B, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
     return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -304,7 +293,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         // NBUF tiles of K and V are held in registers, their loads in flight
         // while others are converted.
         const int tid = threadIdx.x - 5 * 32;
-        constexpr int NBUF = HD <= 128 ? 3 : 2;
+        constexpr int NBUF = 2;
         constexpr int KPPR = C::KCH / 32, VPPR = C::HDV / 32, RP = HD / 32;
         Pieces<C::KP, KPPR, RP, C::CT> kb[NBUF][C::NKC];
         Pieces<C::VP, VPPR, RP, C::CT> vb[NBUF];
@@ -471,61 +460,71 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             const bool full = key0 >= lo && key0 + BN - 1 <= hi;
             const uint32_t p_addr = t_lane + C::P_COL + pb * (BN / 2);
             float alpha = 1.f;
-            // P of the whole tile against the present reference, its sum, and the
-            // tile's largest score; S stays as it is.  Usually the reference stands;
-            // where a row of the warp has none yet or exceeds it by more than 8, it
-            // moves to the tile's maximum and the tile is done once more.  The P
+            // 32 scores of the row, those outside [lo, hi] at -inf
+            auto load_scores = [&](int c, float (&x)[32]) {
+                tmem_ld32(s_addr + c * 32, x);
+                tmem_wait_ld();
+                if (!full) {
+                    const int k0 = max(0, lo - key0 - c * 32), k1 = min(31, hi - key0 - c * 32);
+                    const uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = (in >> i) & 1u ? x[i] : -INFINITY;
+                }
+            };
+            // P against the present reference; S stays as it is.  Usually the reference
+            // stands; where a row of the warp has none yet, or a P came out above
+            // 2^14 (a score above the reference by more than 8), it moves to the
+            // tile's maximum first and the tile is done (again).  The loops are kept
+            // small: unrolled over the tile, this one ran at 0.6 of its speed.  The P
             // buffer is free: S_j's QK was queued after PV_{j-NSB}, which read it.
-            bool exps = !__any_sync(0xffffffffu, m_ref == -INFINITY);
+            bool move = m_ref == -INFINITY;
 #pragma unroll 1
-            for (int again = 0;; ++again) {
+            for (int again = 0; again < 2; ++again) {
+                if (__any_sync(0xffffffffu, move)) {
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < BN / 32; ++c) {
+                        float x[32];
+                        load_scores(c, x);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
+                    }
+                    const float mt = mx * qs;
+                    if (mt > m_ref + 8.f) {
+                        alpha = ex2_approx(m_ref - mt);  // 0 when the reference was -inf
+                        m_ref = mt;
+                        l *= alpha;
+                    }
+                    again = 1;  // within 8 of the maximum now
+                }
                 const float mu = kPBias - (m_ref == -INFINITY ? 0.f : m_ref);
-                float mx = -INFINITY;
                 uint64_t s2[2] = {0ull, 0ull};
+                uint32_t top = 0u;
                 const uint64_t q2 = f32x2(qs, qs), mu2 = f32x2(mu, mu);
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
                     float x[32];
-                    tmem_ld32(s_addr + c * 32, x);
-                    tmem_wait_ld();
-                    if (!full) {
+                    load_scores(c, x);
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int key = key0 + c * 32 + i;
-                            x[i] = (key >= lo && key <= hi) ? x[i] : -INFINITY;
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        float y0, y1;
+                        f32x2_split(fma_f32x2(f32x2(x[2 * i], x[2 * i + 1]), q2, mu2), y0, y1);
+                        y0 = ex2_approx(y0);
+                        y1 = ex2_approx(y1);
+                        pk[i] = pack_f16x2(y0, y1);
+                        top = __vmaxu2(top, pk[i]);  // not negative: fp16 bits compare as integers
+                        s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
-                    if (exps) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float y0, y1;
-                            f32x2_split(fma_f32x2(f32x2(x[2 * i], x[2 * i + 1]), q2, mu2), y0, y1);
-                            y0 = ex2_approx(y0);
-                            y1 = ex2_approx(y1);
-                            pk[i] = pack_f16x2(y0, y1);
-                            s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
-                        }
-                        tmem_st16u(p_addr + c * 16, pk);
-                    }
+                    tmem_st16u(p_addr + c * 16, pk);
                 }
-                const float mt = mx * qs;
-                const bool move = again == 0 && mt > m_ref + 8.f;
-                if (again > 0 || (exps && !__any_sync(0xffffffffu, move))) {
-                    float a0, a1, b0, b1;
-                    f32x2_split(s2[0], a0, a1);
-                    f32x2_split(s2[1], b0, b1);
-                    l += (a0 + a1) + (b0 + b1);
-                    break;
-                }
-                if (move) {
-                    alpha = ex2_approx(m_ref - mt);  // 0 when the reference was -inf
-                    m_ref = mt;
-                    l *= alpha;
-                }
-                exps = true;
+                move = max(top & 0xFFFFu, top >> 16) > 0x7400u;  // 2^14
+                if (again == 0 && __any_sync(0xffffffffu, move)) continue;
+                float a0, a1, b0, b1;
+                f32x2_split(s2[0], a0, a1);
+                f32x2_split(s2[1], b0, b1);
+                l += (a0 + a1) + (b0 + b1);
+                break;
             }
             // a rescale of O needs PV_{j-1}
             const bool rescale = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
@@ -561,6 +560,10 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         const bool store = valid && ok && FMHA_IN_BOUNDS(gr >= 0 && gr < a.rows_total && split < f.n_splits, kSiteKv4Out, f.status);
         const long long prow = (long long)split * a.rows_total + gr;
         if (ok) {
+            // fp32 partials go through a 4 KB corner of Q's place per warp (its MMAs
+            // are done), so that a store covers 128 bytes of a row
+            uint8_t* stage = sq + warp * 4096;
+            const unsigned rows_live = __ballot_sync(0xffffffffu, store);
 #pragma unroll 1
             for (int c = 0; c < C::HDV / 32; ++c) {
                 float ov[32];
@@ -571,9 +574,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 #pragma unroll
                     for (int i = 0; i < 32; ++i) ov[i] = 0.f;
                 }
-                if (!store) continue;
                 const int col = part * C::HDV + c * 32;
                 if (f.n_splits == 1) {
+                    if (!store) continue;
                     uint4* dst = reinterpret_cast<uint4*>(f.o + gr * HD + col);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -582,10 +585,20 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                                             pack_bf16x2(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
                                             pack_bf16x2(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(f.o_part + prow * HD + col);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(ov[4 * q] * inv, ov[4 * q + 1] * inv, ov[4 * q + 2] * inv, ov[4 * q + 3] * inv);
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                            make_float4(ov[4 * q] * inv, ov[4 * q + 1] * inv, ov[4 * q + 2] * inv, ov[4 * q + 3] * inv);
+                    __syncwarp();
+                    float* dst = f.o_part + ((long long)split * a.rows_total + row0 + r_begin + warp * 32) * HD + col;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // 4 rows of 8 x 16 bytes
+                        const int r = i * 4 + (lane >> 3), q = lane & 7;
+                        if ((rows_live >> r) & 1u)
+                            *reinterpret_cast<float4*>(dst + (long long)r * HD + q * 4) =
+                                *reinterpret_cast<const float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+                    }
+                    __syncwarp();
                 }
             }
         }

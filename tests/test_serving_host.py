@@ -101,7 +101,7 @@ def test_binding_refusals():
         binding.fmha_fwd_kv4(bf, *cache, s_k=64)
     with pytest.raises(TypeError):
         binding.fmha_kv4_append(bf[:, :1], bf[:, :1], *cache, torch.zeros(1, dtype=torch.int32))
-    with pytest.raises(ValueError):
-        binding.fmha_fwd_kv4(bf[0], *cache)
+    with pytest.raises(TypeError):
+        binding.fmha_fwd_first(bf, bf, bf, 4, window=8)
     with pytest.raises(ValueError):
         binding.fmha_kv4_cache(1, 1, 40, 128, device="cpu")

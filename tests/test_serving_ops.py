@@ -469,6 +469,37 @@ def test_kv4_many_rows(hd):
     check_kv4(hd, 3, 1, 100, 256, [100, 256, 30], causal=True, kv_chunk=64)
 
 
+def test_threads_on_one_stream_keep_their_partials_apart():
+    """Four threads run split calls on the same (default) stream at once; each checks its own results."""
+    import threading
+
+    sets = [state(60 + i, b=1, T=1, n_h=8, n_kv=1, cap=8192) for i in range(4)]
+    for s in sets:
+        s["lens"].fill_(8100)
+    torch.cuda.synchronize()
+    assert binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 8192, 128)[0] > 1
+
+    def work(s):
+        for _ in range(50):
+            binding.fmha_fwd_kv4(s["q"], *s["cache"], s["lens"], o=s["o"], lse=s["lse"])
+
+    for s in sets:
+        s["q"].copy_(normal(gen(70), *s["q"].shape))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(s,)) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for s in sets:
+        c = s["cache"]
+        ref.assert_attention((s["o"], s["lse"]), ref.attend(s["q"], ref.dequantise(c[0], c[1], 1.0), ref.dequantise(c[2], c[3], 1.0),
+                                                            [8100], 128 ** -0.5))
+    binding.fmha_release()
+    assert not binding._workspaces
+
+
 def test_kv4_same_call_twice_is_bitwise_the_same():
     r = gen(40)
     cache = filled(r, 2, 2, 4096, 128)
