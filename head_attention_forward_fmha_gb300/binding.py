@@ -59,7 +59,7 @@ SIGNATURES = {
     "fmha_qk_norm_rope": ([_vp, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp, _f32, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
                            _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
     "fmha_kv4_append": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
-    "fmha_fwd_kv4_plan": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)], _i32),
+    "fmha_fwd_kv4_plan": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)], _i32),
     "fmha_fwd_kv4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                       _f32, _i32, _i32, _i32, _i32, _vp, _sz, _vp], _i32),
     "fmha_fwd_first_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
@@ -585,11 +585,12 @@ def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=
 _kv4_plans = {}  # (chunk length, workspace bytes) by shape, for the kernel path that is set
 
 
-def fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, window=0, n_first=0, causal=False, kv_chunk=0):
-    """(n_splits, kv_chunk) that fmha_fwd_kv4 uses for sequences of up to s_k keys (kv_chunk 0: its own choice)."""
+def fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, window=0, n_first=0, causal=False, kv_chunk=0, ragged=True):
+    """(n_splits, kv_chunk) that fmha_fwd_kv4 uses for sequences of up to s_k keys (kv_chunk 0: its own choice; ragged:
+    whether seq_lens is given)."""
     chunk = ctypes.c_int(int(kv_chunk))
     n = (_lib or load()).fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, int(window), int(n_first), int(bool(causal)),
-                                           ctypes.byref(chunk))
+                                           int(bool(ragged)), ctypes.byref(chunk))
     _check(n if n < 0 else 0, "fmha_fwd_kv4_plan")
     return n, chunk.value
 
@@ -615,7 +616,7 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
         o = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((b, n_h, T), dtype=_FP32, device=dev)
-    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk)
+    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk, seq_lens is not None)
     plan = _kv4_plans.get(key)
     if plan is None:
         n, chunk = fmha_fwd_kv4_plan(*key)

@@ -924,8 +924,16 @@ bool kv4_use_tc(int hd, long long R) {
 // mma.sync kernel: a warp needs at least ~0.8 us for a tile of 4096 K and V codes
 // whatever else runs, an SM at least ~0.13 us (35 KB of cache per us), a block
 // ~3 us before and after; the merge kernel ~2.5 us and its partials.
-// Tensor-core kernel: ~1.4 us per tile, ~6 us before and after.
-void plan_kv4(Kv4Fwd* f) {
+// Tensor-core kernel: ~1.1 us per tile and ~7 us before and after, at hd 512 2.1
+// and 9.
+//
+// Ragged sequences are taken to hold half of s_k on average: of n chunks each,
+// (n + 1) / 2 blocks then start and do n / 2 blocks' work, and what decides is that
+// work over the slots and half a block's time at the end, rather than whole
+// waves (32 sequences of up to 32768 keys at hd 128: 16 chunks 123 us, 7 chunks
+// 131 us; 16 of up to 4096 at hd 512, one KV head: 8 chunks 33 us, 4 chunks 39 us; a
+// prompt chunk of 128 tokens over 4: one chunk 41 us, two 53 us).
+void plan_kv4(Kv4Fwd* f, bool ragged) {
     const long long R = (long long)f->n_h / f->n_kv_h * f->T;
     f->tc = kv4_use_tc(f->hd, R);
     const int tile = f->tc ? kv4_tc_kv_tile(f->hd) : kv4_kv_tile(f->hd);
@@ -950,15 +958,21 @@ void plan_kv4(Kv4Fwd* f) {
         const int per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps);
         const long long blocks = units * n, slots = sms * per_sm, waves = (blocks + slots - 1) / slots;
         const long long mine = (tiles + n - 1) / n;  // tiles of a block
-        double us;
+        double fixed = 3.0, body;
         if (f->tc) {
-            us = (double)waves * (6.0 + (double)mine * 1.4);
+            fixed = f->hd == 512 ? 9.0 : 7.0;
+            body = (double)mine * (f->hd == 512 ? 2.1 : 1.1);
         } else {
             const long long resident = std::min<long long>(per_sm, (blocks + sms - 1) / sms);
             const double busy = (double)std::min<long long>(warps, mine) * (double)resident;
-            us = (double)waves * (3.0 + (double)((mine + warps - 1) / warps) * std::max(lat, busy * thr));
+            body = (double)((mine + warps - 1) / warps) * std::max(lat, busy * thr);
         }
-        if (n > 1) us += 2.5 + parts_us * (double)n;
+        double us = (double)waves * (fixed + body);
+        if (ragged && f->batch > 1) {
+            const double work = (double)units / (double)slots * ((double)(n + 1) * fixed + (double)n * body) / 2;
+            us = std::max(fixed + body, work + (fixed + body) / 2);
+        }
+        if (n > 1) us += 2.5 + parts_us * (double)n * (f->tc && f->hd == 512 ? 0.5 : 1.0);
         if (us < best * 0.98) {
             best = us;
             best_n = n;
@@ -977,7 +991,10 @@ void plan_kv4(Kv4Fwd* f) {
         consider(warps, 1);
         const long long slots = sms * (f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps));
         for (long long n = 2; n <= 16; n *= 2) consider(warps, n);
-        for (int w = 1; w <= 4; ++w) consider(warps, slots * w / std::max(1LL, units));  // whole waves
+        for (int w = 1; w <= 4; ++w) {  // whole waves; the merge reads partials in fours
+            const long long n = slots * w / std::max(1LL, units);
+            consider(warps, n > 4 ? n & ~3LL : n);
+        }
     }
     f->kv_chunk = (int)std::min((tiles + best_n - 1) / best_n * tile, most);
     f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
@@ -1084,14 +1101,15 @@ extern "C" int fmha_kv4_append(const void* k, const void* v, void* k_codes, void
 }
 
 extern "C" int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, int window, int n_first, int causal,
-                                 int* kv_chunk) try {
+                                 int ragged, int* kv_chunk) try {
     Kv4Fwd f;
     const int cap = s_k > 0 && s_k < INT_MAX - 16 ? (s_k + 15) / 16 * 16 : s_k;
     const int rc = check_kv4(batch, n_h, n_kv_h, T, s_k, cap, hd, 1.f, window, n_first, causal, &f);
     if (rc) return rc;
+    if (ragged != 0 && ragged != 1) return fail(FMHA_ERR_SHAPE, "ragged must be 0 or 1 (got %d)", ragged);
     if (kv_chunk && *kv_chunk < 0) return fail(FMHA_ERR_SHAPE, "kv_chunk=%d must be >= 0", *kv_chunk);
     if (kv_chunk) f.kv_chunk = *kv_chunk;
-    plan_kv4(&f);
+    plan_kv4(&f, ragged != 0);
     if (kv_chunk) *kv_chunk = f.kv_chunk;
     return f.n_splits;
 } catch (...) {
@@ -1128,24 +1146,27 @@ extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_sc
     f.v_global = v_global;
     if (kv_chunk < 0) return fail(FMHA_ERR_SHAPE, "kv_chunk=%d must be >= 0", kv_chunk);
     f.kv_chunk = kv_chunk;
-    plan_kv4(&f);
+    plan_kv4(&f, seq_lens != nullptr);
     if (f.n_splits > 65535) return fail(FMHA_ERR_SHAPE, "too many KV chunks (%d)", f.n_splits);
+    bool f16 = false;
     if (f.n_splits > 1) {
         const size_t need = partial_bytes(rows, hd, f.n_splits);
         if (!workspace || workspace_bytes < need)
             return fail(FMHA_ERR_WORKSPACE, "fmha_fwd_kv4: %zu bytes of workspace needed for %d chunks, %zu given", need,
                         f.n_splits, workspace ? workspace_bytes : (size_t)0);
         if (!aligned(workspace, 16)) return fail(FMHA_ERR_ALIGN, "workspace must be 16-byte aligned");
-        const PartialViews pv = partial_views(workspace, rows, hd, f.n_splits, false);
-        f.o_part = static_cast<float*>(pv.o_part);
+        f16 = f.tc && hd == 512;  // as fmha_fwd: half the partials' bytes where they are many
+        const PartialViews pv = partial_views(workspace, rows, hd, f.n_splits, f16);
+        f.o_part = pv.o_part;
         f.lse_part = pv.lse_part;
+        f.range_part = pv.range_part;
     }
     f.status = device_status_word();
     if (!f.status) return fail(FMHA_ERR_LAUNCH, "cannot resolve the device status word");
     cudaError_t e = f.tc ? launch_kv4_tc(f, stream) : launch_kv4_fwd(f, stream);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit attention kernel launch");
     if (f.n_splits > 1) {
-        e = launch_merge(f.o_part, f.lse_part, nullptr, f.n_splits, rows, hd, false, o, lse, stream, sink, T, n_h);
+        e = launch_merge(f.o_part, f.lse_part, f.range_part, f.n_splits, rows, hd, f16, o, lse, stream, sink, T, n_h);
         if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
     }
     return FMHA_OK;

@@ -168,7 +168,8 @@ struct Kv4Fwd {
     const float* sink;    // [n_h] or NULL
     __nv_bfloat16* o;
     float* lse;
-    float *o_part, *lse_part;  // n_splits > 1
+    void* o_part;        // n_splits > 1: fp32, or fp16 with range factors (tensor-core kernel at hd 512)
+    float *lse_part, *range_part;
     float k_global, v_global, scale;
     int batch, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, causal;
     int kv_chunk, n_splits;  // keys per chunk (a multiple of the kernel's key tile) and their number

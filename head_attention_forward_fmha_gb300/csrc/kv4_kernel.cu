@@ -39,12 +39,12 @@
 #include <atomic>
 #include <type_traits>
 #include "internal.h"
+#include "kv4_common.cuh"
 #include "ptx.cuh"
 
 namespace fmha {
 namespace {
 
-constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry
 
 template <int HD, int NB, int W>
 struct K4Cfg {
@@ -221,6 +221,11 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
     const int k16 = u_lo & ~15;  // >= body16: chunks are multiples of 16 keys
     const int n_body = b_hi > u_lo ? (b_hi - k16 + KT - 1) / KT : 0;
     const int n_tiles = n_head + n_body;
+    if (n_tiles == 0) {  // nothing to attend in this chunk
+        write_empty_rows(f, a.rows_total, row0 + r_begin, r_end - r_begin, split, 0, HD, true,
+                         f.sink && f.n_splits == 1 ? kvh * a.group : -1, r_begin);
+        return;
+    }
     const int body_end16 = (b_hi + 15) & ~15, head_end16 = (n_first + 15) & ~15;
 
     const uint32_t ring = smem_u32(smem) + warp * C::RING;
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
             if (col == 0) f.lse[grow] = lse;
         } else {
             const long long prow = (long long)split * a.rows_total + grow;
-            float4* dst = reinterpret_cast<float4*>(f.o_part + prow * HD + col);
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(f.o_part) + prow * HD + col);
             dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
             dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
             if (col == 0) f.lse_part[prow] = lse;

@@ -24,12 +24,11 @@
 #include <climits>
 #include <atomic>
 #include "internal.h"
+#include "kv4_common.cuh"
 #include "ptx.cuh"
 
 namespace fmha {
 namespace {
-
-constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry (kv4_kernel.cu)
 
 template <int HD>
 struct K4TCfg {
@@ -198,14 +197,6 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         mbar_init(mma_drain, 1);
         mbar_fence_init();
     }
-    if (warp == 4) {
-        tmem_alloc(tmem_slot, C::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();  // every global access below follows the preceding kernel
 
     // Keys: the virtual axis of kv4_kernel.cu, with tiles of BN keys and a
@@ -233,6 +224,19 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
     }
     const int n_body = b_hi > u_lo ? (b_hi - u_lo + BN - 1) / BN : 0;
     const int n_tiles = n_head + n_body;
+    if (n_tiles == 0) {  // nothing to attend in this chunk: no tensor memory, no Q
+        write_empty_rows(f, a.rows_total, row0 + r_begin, r_end - r_begin, split, part * C::HDV, C::HDV, part == 0,
+                         SINK ? kvh * a.group : -1, r_begin);
+        return;
+    }
+    if (warp == 4) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     auto tile_key = [&](int j) { return j < n_head ? h_lo + j * BN : u_lo + (j - n_head) * BN; };
     auto tile_end = [&](int j) { return j < n_head ? n_first : b_hi; };
 
@@ -324,11 +328,11 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 fetch_k(kb[i], i);
                 fetch_v(vb[i], i);
             }
-        if (n_tiles > 0) load_q(warp - 1);
+        load_q(warp - 1);
         bool ok = true;
         // K_j and then V_{j-1}, for j up to n_tiles (where there is no K_j)
 #pragma unroll 1
-        for (int j0 = 0; ok && j0 <= n_tiles && n_tiles > 0; j0 += NBUF) {
+        for (int j0 = 0; ok && j0 <= n_tiles; j0 += NBUF) {
 #pragma unroll
             for (int i = 0; i < NBUF; ++i) {
                 const int j = j0 + i;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         // The whole warp walks the loop and one elected lane issues, so that the
         // descriptors stay in uniform registers: issued by `lane == 0` alone, each MMA
         // took ~95 clocks (hd 512: 3000 per tile of 32) however small it was.
-        if (n_tiles > 0) {
+        {
             constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, 0);
             constexpr uint32_t idesc_o = idesc_f16_f32(BM, C::HDV, 1);
             // A descriptor's low word holds the address in units of 16 bytes: the
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             mbar_wait(mma_drain, 0, f.status);
         }
     } else {
-        if (n_tiles > 0) load_q(warp);
+        load_q(warp);
         // ------------------------------------------------------------ softmax
         const int row = threadIdx.x;  // tile row and TMEM lane
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
@@ -445,8 +449,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             if (f.window > 0) jlo = max(jlo, p - f.window + 1);
         }
         float m_ref = -INFINITY, l = 0.f;
-        bool ok = n_tiles == 0 || mbar_wait(q_full, 0, f.status);
-        const float qs = n_tiles > 0 && ok ? row_fac[row] : 1.f;
+        bool ok = mbar_wait(q_full, 0, f.status);
+        const float qs = ok ? row_fac[row] : 1.f;
         for (int j = 0; ok && j < n_tiles; ++j) {
             const int pb = j % NSB;
             if (!mbar_wait(&s_full[pb], (j / NSB) & 1, f.status)) {
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             mbar_arrive(&p_ready[pb]);
         }
         // ------------------------------------------------------------ epilogue
-        if (ok && n_tiles > 0) ok = mbar_wait(&o_done[(n_tiles - 1) % NSB], ((n_tiles - 1) / NSB) & 1, f.status);
+        if (ok) ok = mbar_wait(&o_done[(n_tiles - 1) % NSB], ((n_tiles - 1) / NSB) & 1, f.status);
         ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below is warp-collective
         tc_fence_after();
         float inv, lse;
@@ -560,20 +564,39 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         const bool store = valid && ok && FMHA_IN_BOUNDS(gr >= 0 && gr < a.rows_total && split < f.n_splits, kSiteKv4Out, f.status);
         const long long prow = (long long)split * a.rows_total + gr;
         if (ok) {
-            // fp32 partials go through a 4 KB corner of Q's place per warp (its MMAs
-            // are done), so that a store covers 128 bytes of a row
+            float range = 1.f;
+            if constexpr (HD == 512) {
+                if (f.n_splits > 1) {
+                    // fp16 partials, scaled per row half so that the largest |O| lies in
+                    // [2^14, 2^15), and the factor that undoes it
+                    float mx = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < C::HDV / 32; ++c) {
+                        float ov[32];
+                        tmem_ld32(t_lane + C::O_COL + c * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(ov[i]));
+                    }
+                    mx *= inv;
+                    const int e = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+                    if (mx > 0.f && e < 128) {  // leave zero, inf and NaN rows as they are
+                        const int k = min(max(e - 14, -100), 100);
+                        inv *= __uint_as_float((uint32_t)(127 - k) << 23);
+                        range = __uint_as_float((uint32_t)(127 + k) << 23);
+                    }
+                    if (store) f.range_part[prow * 2 + part] = range;
+                }
+            }
+            // partials go through a 4 KB corner of Q's place per warp (its MMAs are
+            // done), so that a store covers 128 (fp16: 64) bytes of a row
             uint8_t* stage = sq + warp * 4096;
             const unsigned rows_live = __ballot_sync(0xffffffffu, store);
 #pragma unroll 1
             for (int c = 0; c < C::HDV / 32; ++c) {
                 float ov[32];
-                if (n_tiles > 0) {
-                    tmem_ld32(t_lane + C::O_COL + c * 32, ov);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) ov[i] = 0.f;
-                }
+                tmem_ld32(t_lane + C::O_COL + c * 32, ov);
+                tmem_wait_ld();
                 const int col = part * C::HDV + c * 32;
                 if (f.n_splits == 1) {
                     if (!store) continue;
@@ -590,13 +613,17 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
                             make_float4(ov[4 * q] * inv, ov[4 * q + 1] * inv, ov[4 * q + 2] * inv, ov[4 * q + 3] * inv);
                     __syncwarp();
-                    float* dst = f.o_part + ((long long)split * a.rows_total + row0 + r_begin + warp * 32) * HD + col;
+                    const long long at = ((long long)split * a.rows_total + row0 + r_begin + warp * 32) * HD + col;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {  // 4 rows of 8 x 16 bytes
                         const int r = i * 4 + (lane >> 3), q = lane & 7;
-                        if ((rows_live >> r) & 1u)
-                            *reinterpret_cast<float4*>(dst + (long long)r * HD + q * 4) =
-                                *reinterpret_cast<const float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+                        if (!((rows_live >> r) & 1u)) continue;
+                        const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+                        if constexpr (HD == 512)
+                            *reinterpret_cast<uint2*>(static_cast<__half*>(f.o_part) + at + (long long)r * HD + q * 4) =
+                                make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+                        else
+                            *reinterpret_cast<float4*>(static_cast<float*>(f.o_part) + at + (long long)r * HD + q * 4) = v;
                     }
                     __syncwarp();
                 }

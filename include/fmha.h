@@ -428,12 +428,12 @@ int fmha_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales,
 
 /*
  * The plan of fmha_fwd_kv4: returns the number of KV chunks for sequences of up
- * to s_k keys.  *kv_chunk (may be NULL) holds the chunk length asked for, in
- * keys, 0 for the library's choice, and receives the one used (a multiple of
- * the kernel's key tile).
+ * to s_k keys; ragged: 1 when the call gives seq_lens, else 0.  *kv_chunk (may
+ * be NULL) holds the chunk length asked for, in keys, 0 for the library's choice,
+ * and receives the one used (a multiple of the kernel's key tile).
  */
 int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, int window, int n_first, int causal,
-                      int* kv_chunk);
+                      int ragged, int* kv_chunk);
 
 /*
  * The forward over a 4-bit cache: O (bf16) and LSE (fp32) as fmha_fwd_sink, with

@@ -89,6 +89,11 @@ def test_kv4_plan():
     assert binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 0, 128)[0] == 1
     with pytest.raises(binding.FmhaError):
         binding.fmha_fwd_kv4_plan(1, 8, 3, 1, 64, 128)
+    # chunks cover the longest axis whatever the sequences' lengths are taken to be
+    for ragged in (False, True):
+        for T in (1, 128):
+            n, chunk = binding.fmha_fwd_kv4_plan(32, 64, 8, T, 32768, 128, ragged=ragged)
+            assert n * chunk >= 32768 > (n - 1) * chunk
 
 
 def test_binding_refusals():

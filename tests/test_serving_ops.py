@@ -250,6 +250,8 @@ def test_kv4_sink_scales_and_bounds(hd, kernel):
     check_kv4(hd, 8, 2, 2, 256, [0, 7, 200], g=3.0, s_k=200)
     check_kv4(hd, 8, 2, 1, 256, [0, 7, 256], scale=-0.2)          # a negative scale turns the order round
     check_kv4(hd, 8, 2, 1, 256, [0, 7, 256], scale=0.0)           # every key the same weight
+    check_kv4(hd, 8, 2, 2, 256, [0, 7, 256], g=2.0 ** -40, kv_chunk=64)   # tiny and huge values through partials
+    check_kv4(hd, 8, 2, 2, 256, [0, 7, 256], g=2.0 ** 30, scale=2.0 ** -34, kv_chunk=64)
     check_kv4(hd, 8, 2, 1, 256, [5, 256], q_mult=2.0 ** 60, scale=2.0 ** -63)
     check_kv4(hd, 8, 2, 1, 256, [5, 256], q_mult=2.0 ** -70, scale=2.0 ** 67)
 
