@@ -907,23 +907,27 @@ int check_kv4(int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, f
     return FMHA_OK;
 }
 
-// Kernel and chunks of the 4-bit attention.  The tensor-core kernel takes over
-// where a KV head has so many query rows that the other one, which converts the
-// cache again for every 8 to 32 rows, costs more; fmha_set_kernel_path applies
-// here too (1: never, 2 to 4: always).
+// The 4-bit attention's kernel.  The mma.sync kernel converts the cache again for
+// every 8 to 32 rows of a KV head, the tensor-core kernel once for 128 but with more
+// work per tile; measured over 16384 keys (8 sequences, 8 heads): hd 64 48 rows 89
+// against 116 us, hd 128 32 rows 82 against 121 and 48 rows 146 against 126, hd
+// 256 16 rows 98 against 171 and 24 rows 181 against 172, hd 512 24 rows 315 against
+// 408, each 8 rows more adding ~80.  fmha_set_kernel_path applies here too (1:
+// never, 2 to 4: always).
 bool kv4_use_tc(int hd, long long R) {
     const int ov = g_path_override.load();
     if (ov != 0) return ov >= 2;
-    return R >= (hd <= 128 ? 48 : 24);
+    return R > (hd == 64 ? 64 : hd == 128 ? 32 : hd == 256 ? 16 : 24);
 }
 
 // How fmha_fwd_kv4 divides its work: the virtual key axis (first keys rounded up
 // to tiles, then the window) of sequences of s_k keys into n chunks, and for the
 // mma.sync kernel the warps per block; the candidate with the least estimated time.
 //
-// mma.sync kernel: a warp needs at least ~0.8 us for a tile of 4096 K and V codes
-// whatever else runs, an SM at least ~0.13 us (35 KB of cache per us), a block
-// ~3 us before and after; the merge kernel ~2.5 us and its partials.
+// mma.sync kernel: for a tile of 4096 K and 4096 V codes a warp needs at least ~1
+// us whatever else runs (1.4 with 16 rows, 1.8 with 32), an SM at least ~0.13 us (0.2,
+// 0.3), a block ~3 us before and after; the merge kernel ~2.5 us, ~0.04 per chunk
+// and its partials.
 // Tensor-core kernel: ~1.1 us per tile and ~7 us before and after, at hd 512 2.1
 // and 9.
 //
@@ -946,13 +950,14 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
     if (span < 1) span = 1;
     f->warps = 4;
     const long long most = INT_MAX / 2 / tile * tile;
-    const long long units =
-        (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
     const long long sms = sm_count(), tiles = (span + tile - 1) / tile;
     const double parts_us = (double)R * f->batch * f->n_kv_h * f->hd * 4.0 / 8e6;  // one chunk's partials, written and read
-    const double size = tile * f->hd / 4096.0, lat = 0.8 * size * (0.75 + rows / 32.0), thr = 0.13 * size * (0.9 + rows / 80.0);
+    const double size = tile * f->hd / 4096.0;
     double best = 1e30;
     long long best_n = 1;
+    const double lat = size * (rows == 32 ? 1.8 : rows == 16 ? 1.4 : 1.0), thr = size * (rows == 32 ? 0.3 : rows == 16 ? 0.2 : 0.13);
+    const long long units =
+        (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
     auto consider = [&](int warps, long long n) {
         if (n < 1 || n > 256 || (n > 1 && n > tiles)) return;
         const int per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps);
@@ -972,30 +977,31 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
             const double work = (double)units / (double)slots * ((double)(n + 1) * fixed + (double)n * body) / 2;
             us = std::max(fixed + body, work + (fixed + body) / 2);
         }
-        if (n > 1) us += 2.5 + parts_us * (double)n * (f->tc && f->hd == 512 ? 0.5 : 1.0);
+        if (n > 1) us += 2.5 + 0.04 * (double)n + parts_us * (double)n * (f->tc && f->hd == 512 ? 0.5 : 1.0);
         if (us < best * 0.98) {
             best = us;
             best_n = n;
             f->warps = warps;
         }
     };
-    const int big = f->tc ? 4 : kv4_big_warps(f->hd, rows);
     if (f->kv_chunk > 0) {  // the caller's chunks
         f->kv_chunk = (int)std::min(((long long)f->kv_chunk + tile - 1) / tile * tile, most);
         f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
-        consider(4, f->n_splits);
-        if (big > 4) consider(big, f->n_splits);
-        return;
     }
+    const int big = f->tc ? 4 : kv4_big_warps(f->hd, rows);
     for (int warps = 4; warps <= big; warps += big > 4 ? big - 4 : 4) {
-        consider(warps, 1);
+        if (f->kv_chunk > 0) {
+            consider(warps, f->n_splits);
+            continue;
+        }
         const long long slots = sms * (f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps));
-        for (long long n = 2; n <= 16; n *= 2) consider(warps, n);
+        for (long long n = 1; n <= 16; n *= 2) consider(warps, n);
         for (int w = 1; w <= 4; ++w) {  // whole waves; the merge reads partials in fours
             const long long n = slots * w / std::max(1LL, units);
             consider(warps, n > 4 ? n & ~3LL : n);
         }
     }
+    if (f->kv_chunk > 0) return;
     f->kv_chunk = (int)std::min((tiles + best_n - 1) / best_n * tile, most);
     f->n_splits = (int)((span + f->kv_chunk - 1) / f->kv_chunk);
 }

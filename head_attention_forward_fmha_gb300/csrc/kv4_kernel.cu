@@ -682,7 +682,7 @@ cudaError_t launch_w(const Kv4Fwd& f, cudaStream_t stream) {
 template <int HD>
 cudaError_t launch_hd(const Kv4Fwd& f, cudaStream_t stream) {
     const int rows = kv4_rows_per_cta(HD, (long long)f.n_h / f.n_kv_h * f.T);
-    if constexpr (HD <= 128)
+    if constexpr (HD == 64)
         if (rows == 32) return launch_w<HD, 4>(f, stream);
     if constexpr (HD <= 256)
         if (rows == 16) return launch_w<HD, 2>(f, stream);
@@ -694,7 +694,7 @@ cudaError_t launch_hd(const Kv4Fwd& f, cudaStream_t stream) {
 int kv4_kv_tile(int hd) { return hd >= 256 ? 16 : 32; }
 
 int kv4_rows_per_cta(int hd, long long rows) {
-    if (rows > 16 && hd <= 128) return 32;
+    if (rows > 16 && hd == 64) return 32;  // at hd 128 its accumulators do not fit the registers
     return rows > 8 && hd <= 256 ? 16 : 8;
 }
 
