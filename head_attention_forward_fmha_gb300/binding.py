@@ -7,6 +7,7 @@ kernels; there is no CPU fallback, and a missing library raises.
 """
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -65,6 +66,11 @@ SIGNATURES = {
     "fmha_fwd_first_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "fmha_fwd_first": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp, _sz,
                         _vp], _i32),
+    # arguments in one struct, packed here into bytes
+    "fmha_qk_norm_rope_packed": ([ctypes.c_char_p], _i32),
+    "fmha_kv4_append_packed": ([ctypes.c_char_p], _i32),
+    "fmha_fwd_kv4_packed": ([ctypes.c_char_p], _i32),
+    "fmha_fwd_first_packed": ([ctypes.c_char_p], _i32),
 }
 # Size of the fixed split-KV scratch fmha_fwd_noalloc uses (FMHA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -459,15 +465,30 @@ def _device(t, name):
     return t.get_device()
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) of the library with device `dev` current; stream None is that device's current stream."""
+def _run(fn, dev, pack, *args):
+    """Call `fn`_packed with these arguments, device `dev` current."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _call(fn, dev, stream, *args)
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    rc = getattr(_lib or load(), fn)(*args, handle)
+            return _run(fn, dev, pack, *args)
+    try:
+        block = pack(*args)
+    except struct.error as e:
+        raise ValueError("%s: %s" % (fn, e)) from None
+    rc = getattr(_lib or load(), fn + "_packed")(block)
     if rc:
         _check(rc, fn)
+
+
+def _handle(stream, dev):
+    """The stream's handle; None is the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+# The argument structs of include/fmha.h: pointers and 64-bit numbers, floats, ints (0 for an absent pointer).
+_NORM_ROPE = struct.Struct("=10Q2qf9i").pack
+_APPEND = struct.Struct("=10Q2f6i").pack
+_KV4 = struct.Struct("=12Q3f11i").pack
+_FIRST = struct.Struct("=9Qf9i").pack
 
 
 _workspaces = {}  # uint8 tensor by (thread, device, stream)
@@ -522,8 +543,7 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     if (k is None) != (v is None) or (k is not None and k.dim() != 4):
         raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
     if cos_sin is None:
-        cs_ptr = pos_ptr = None
-        max_pos = rot = 0
+        cs_ptr = pos_ptr = max_pos = rot = 0
     else:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin [max_pos, rot] expected, got %s" % (tuple(cos_sin.shape),))
@@ -537,12 +557,12 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
         v = torch.empty_like(k)
     rows = k.shape[2]
     kv_shape = (b, n_kv_h, rows, hd)
-    _call("fmha_qk_norm_rope", dev, stream, qkv.data_ptr(), sb, st,
-          None if q_weight is None else _ptr(q_weight, "q_weight", _FP32, (hd,), dev),
-          None if k_weight is None else _ptr(k_weight, "k_weight", _FP32, (hd,), dev), eps, cs_ptr, pos_ptr, max_pos, rot,
-          bool(interleaved), _ptr(q, "q", _BF16, (b, n_h, T, hd), dev), _ptr(k, "k", _BF16, kv_shape, dev),
-          _ptr(v, "v", _BF16, kv_shape, dev), None if kv_start is None else _ptr(kv_start, "kv_start", _I32, (b,), dev), rows,
-          b, T, n_h, n_kv_h, hd)
+    _run("fmha_qk_norm_rope", dev, _NORM_ROPE, qkv.data_ptr(),
+         0 if q_weight is None else _ptr(q_weight, "q_weight", _FP32, (hd,), dev),
+         0 if k_weight is None else _ptr(k_weight, "k_weight", _FP32, (hd,), dev), cs_ptr, pos_ptr,
+         _ptr(q, "q", _BF16, (b, n_h, T, hd), dev), _ptr(k, "k", _BF16, kv_shape, dev), _ptr(v, "v", _BF16, kv_shape, dev),
+         0 if kv_start is None else _ptr(kv_start, "kv_start", _I32, (b,), dev), _handle(stream, dev), sb, st, eps, max_pos, rot,
+         bool(interleaved), rows, b, T, n_h, n_kv_h, hd)
     return q, k, v
 
 
@@ -576,10 +596,11 @@ def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=
     shape = k.shape
     b, n_kv_h, T, hd = shape
     cap = _kv4_heads_rows(k_codes)[1]
-    _call("fmha_kv4_append", dev, stream, _ptr(k, "k", _BF16, shape, dev), _ptr(v, "v", _BF16, shape, dev),
-          *_kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev), _ptr(start, "start", _I32, (b,), dev),
-          k_global, v_global, None if k_out is None else _ptr(k_out, "k_out", _BF16, shape, dev),
-          None if v_out is None else _ptr(v_out, "v_out", _BF16, shape, dev), b, n_kv_h, T, cap, hd)
+    _run("fmha_kv4_append", dev, _APPEND, _ptr(k, "k", _BF16, shape, dev), _ptr(v, "v", _BF16, shape, dev),
+         *_kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev), _ptr(start, "start", _I32, (b,), dev),
+         0 if k_out is None else _ptr(k_out, "k_out", _BF16, shape, dev),
+         0 if v_out is None else _ptr(v_out, "v_out", _BF16, shape, dev), _handle(stream, dev), k_global, v_global, b, n_kv_h, T,
+         cap, hd, 0)
 
 
 _kv4_plans = {}  # (chunk length, workspace bytes) by shape, for the kernel path that is set
@@ -624,17 +645,17 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
     kv_chunk, need = plan
     q_ptr = _ptr(q, "q", _BF16, shape, dev)
     cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev)
-    ws = None
+    ws = 0
     if workspace is not None:
         ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
         need = workspace.numel()
     elif need:
         workspace = _workspace(need, dev, stream)
         ws = workspace.data_ptr()
-    _call("fmha_fwd_kv4", dev, stream, q_ptr, *cache, None if seq_lens is None else _ptr(seq_lens, "seq_lens", _I32, (b,), dev),
-          _ptr(o, "o", _BF16, shape, dev), _ptr(lse, "lse", _FP32, (b, n_h, T), dev),
-          None if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), k_global, v_global, b, n_h, n_kv_h, T, s_k, cap, hd,
-          hd ** -0.5 if scale is None else scale, window, n_first, bool(causal), kv_chunk, ws, need)
+    _run("fmha_fwd_kv4", dev, _KV4, q_ptr, *cache, 0 if seq_lens is None else _ptr(seq_lens, "seq_lens", _I32, (b,), dev),
+         _ptr(o, "o", _BF16, shape, dev), _ptr(lse, "lse", _FP32, (b, n_h, T), dev),
+         0 if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), ws, need, _handle(stream, dev), k_global, v_global,
+         hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, bool(causal), kv_chunk)
     return o, lse
 
 
@@ -664,14 +685,14 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
         need = _first_plans[key] = fmha_fwd_first_workspace_bytes(*key)
     q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
     q_ptr, k_ptr = _ptr(q, "q", _BF16, q_shape, dev), _ptr(k, "k", _BF16, kv_shape, dev)
-    ws = None
+    ws = 0
     if workspace is not None:
         ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
         need = workspace.numel()
     elif need:
         workspace = _workspace(need, dev, stream)
         ws = workspace.data_ptr()
-    _call("fmha_fwd_first", dev, stream, q_ptr, k_ptr, _ptr(v, "v", _BF16, kv_shape, dev), _ptr(o, "o", _BF16, q_shape, dev),
-          _ptr(lse, "lse", _FP32, (b, n_h, T), dev), None if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev),
-          b, n_h, n_kv_h, T, s_k, hd, hd ** -0.5 if scale is None else scale, window, n_first, bool(causal), ws, need)
+    _run("fmha_fwd_first", dev, _FIRST, q_ptr, k_ptr, _ptr(v, "v", _BF16, kv_shape, dev), _ptr(o, "o", _BF16, q_shape, dev),
+         _ptr(lse, "lse", _FP32, (b, n_h, T), dev), 0 if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), ws, need,
+         _handle(stream, dev), hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
     return o, lse

@@ -1240,3 +1240,30 @@ extern "C" int fmha_fwd_first(const void* q, const void* k, const void* v, void*
 } catch (...) {
     return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_first");
 }
+
+// ---------------------------------------------------------------- arguments in one struct
+extern "C" int fmha_qk_norm_rope_packed(const struct fmha_qk_norm_rope_args* a) {
+    if (!a) return fail(FMHA_ERR_NULL, "fmha_qk_norm_rope_packed: NULL arguments");
+    return fmha_qk_norm_rope(a->qkv, a->batch_stride, a->token_stride, a->q_weight, a->k_weight, a->eps, a->cos_sin,
+                             a->positions, a->max_pos, a->rot, a->interleaved, a->q, a->k, a->v, a->kv_start, a->kv_rows,
+                             a->batch, a->T, a->n_h, a->n_kv_h, a->hd, a->stream);
+}
+
+extern "C" int fmha_kv4_append_packed(const struct fmha_kv4_append_args* a) {
+    if (!a) return fail(FMHA_ERR_NULL, "fmha_kv4_append_packed: NULL arguments");
+    return fmha_kv4_append(a->k, a->v, a->k_codes, a->k_scales, a->v_codes, a->v_scales, a->start, a->k_global, a->v_global,
+                           a->k_out, a->v_out, a->batch, a->n_kv_h, a->T, a->cap, a->hd, a->stream);
+}
+
+extern "C" int fmha_fwd_kv4_packed(const struct fmha_fwd_kv4_args* a) {
+    if (!a) return fail(FMHA_ERR_NULL, "fmha_fwd_kv4_packed: NULL arguments");
+    return fmha_fwd_kv4(a->q, a->k_codes, a->k_scales, a->v_codes, a->v_scales, a->seq_lens, a->o, a->lse, a->sink,
+                        a->k_global, a->v_global, a->batch, a->n_h, a->n_kv_h, a->T, a->s_k, a->cap, a->hd, a->scale,
+                        a->window, a->n_first, a->causal, a->kv_chunk, a->workspace, a->workspace_bytes, a->stream);
+}
+
+extern "C" int fmha_fwd_first_packed(const struct fmha_fwd_first_args* a) {
+    if (!a) return fail(FMHA_ERR_NULL, "fmha_fwd_first_packed: NULL arguments");
+    return fmha_fwd_first(a->q, a->k, a->v, a->o, a->lse, a->sink, a->batch, a->n_h, a->n_kv_h, a->T, a->s_k, a->hd, a->scale,
+                          a->window, a->n_first, a->causal, a->workspace, a->workspace_bytes, a->stream);
+}

@@ -70,6 +70,32 @@ def test_first_refusals(lib, change, code):
     assert lib.fmha_fwd_first(*{**FIRST, **change}.values()) == code
 
 
+def test_argument_structs_are_laid_out_as_packed_here(tmp_path):
+    """The binding packs the structs of include/fmha.h itself: sizes and the offsets of the last fields."""
+    import os
+    import struct
+    import subprocess
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    last = [("qk_norm_rope", "hd", "=10Q2qf9i"), ("kv4_append", "reserved", "=10Q2f6i"), ("fwd_kv4", "kv_chunk", "=12Q3f11i"),
+            ("fwd_first", "causal", "=9Qf9i")]
+    lines = "".join('printf("%%zu ", offsetof(struct fmha_%s_args, %s));' % (n, f) for n, f, _ in last)
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "fmha.h"\nint main(void) {%s return 0;}\n' % lines)
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "s")], check=True)
+    got = subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(x) for x in got] == [struct.calcsize(f) - 4 for _, _, f in last]
+
+
+def test_packed_calls_refuse_like_the_others(lib):
+    assert lib.fmha_fwd_kv4_packed(None) == -1 and lib.fmha_fwd_first_packed(None) == -1
+    assert lib.fmha_qk_norm_rope_packed(None) == -1 and lib.fmha_kv4_append_packed(None) == -1
+    assert lib.fmha_fwd_kv4_packed(binding._KV4(*[P] * 5, 0, P, P, 0, 0, 0, 0, 1.0, 1.0, 0.1, 1, 8, 1, 1, 64, 64, 80, 0, 0, 0, 0)) == -3
+    assert lib.fmha_fwd_first_packed(binding._FIRST(*[P] * 5, 0, 0, 0, 0, 0.1, 1, 8, 1, 1, 64, 128, 16, -1, 0)) == -5
+    assert lib.fmha_kv4_append_packed(binding._APPEND(*[P] * 7, 0, 0, 0, 1.0, 1.0, 1, 1, 1, 40, 128, 0)) == -5
+    assert lib.fmha_qk_norm_rope_packed(binding._NORM_ROPE(*[P] * 8, 0, 0, 0, 1280, 1e-6, 64, 4, 0, 1, 1, 1, 8, 1, 128)) == -5
+
+
 def test_first_workspace():
     f = binding.fmha_fwd_first_workspace_bytes
     assert f(1, 8, 1, 1, 64, 128, 16, 4) == 0          # one chunk
