@@ -924,10 +924,13 @@ bool kv4_use_tc(int hd, long long R) {
 // to tiles, then the window) of sequences of s_k keys into n chunks, and for the
 // mma.sync kernel the warps per block; the candidate with the least estimated time.
 //
-// mma.sync kernel: for a tile of 4096 K and 4096 V codes a warp needs at least ~1
-// us whatever else runs (1.4 with 16 rows, 1.8 with 32), an SM at least ~0.13 us (0.2,
-// 0.3), a block ~3 us before and after; the merge kernel ~2.5 us, ~0.04 per chunk
-// and its partials.
+// mma.sync kernel: a tile of 4096 K and 4096 V codes takes a warp ~0.55 us plus 0.095
+// for every warp that its SM has at work (16 warps: 2.1 us, 35 KB of cache per us; a
+// half more with 16 rows, 2.2 times with 32; a tile at hd 64, half as large, 0.75),
+// a block ~3 us before and after; blocks beyond a wave of small ones start as others
+// end; the merge kernel ~2.5 us, ~0.04 per chunk and its partials.  Without such
+// terms for half-filled SMs, 16 sequences of 32768 keys went to two chunks at
+// 189 us instead of eight at 113.
 // Tensor-core kernel: ~1.1 us per tile and ~7 us before and after, at hd 512 2.1
 // and 9.
 //
@@ -952,16 +955,17 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
     const long long most = INT_MAX / 2 / tile * tile;
     const long long sms = sm_count(), tiles = (span + tile - 1) / tile;
     const double parts_us = (double)R * f->batch * f->n_kv_h * f->hd * 4.0 / 8e6;  // one chunk's partials, written and read
-    const double size = tile * f->hd / 4096.0;
-    double best = 1e30;
-    long long best_n = 1;
-    const double lat = size * (rows == 32 ? 1.8 : rows == 16 ? 1.4 : 1.0), thr = size * (rows == 32 ? 0.3 : rows == 16 ? 0.2 : 0.13);
+    const double size = (f->hd == 64 ? 0.75 : tile * f->hd / 4096.0) * (rows == 32 ? 2.2 : rows == 16 ? 1.5 : 1.0);
     const long long units =
         (long long)f->batch * f->n_kv_h * ((R + rows - 1) / rows) * (f->tc ? kv4_tc_blocks_per_row_tile(f->hd) : 1);
+    double best = 1e30;
+    long long best_n = 1;
     auto consider = [&](int warps, long long n) {
         if (n < 1 || n > 256 || (n > 1 && n > tiles)) return;
         const int per_sm = f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps);
-        const long long blocks = units * n, slots = sms * per_sm, waves = (blocks + slots - 1) / slots;
+        const long long blocks = units * n, slots = sms * per_sm;
+        const double ratio = (double)blocks / (double)slots, whole = std::ceil(ratio);
+        const double waves = std::max(1.0, ratio + (per_sm == 1 ? 1.0 : per_sm == 2 ? 0.5 : 0.15) * (whole - ratio));
         const long long mine = (tiles + n - 1) / n;  // tiles of a block
         double fixed = 3.0, body;
         if (f->tc) {
@@ -970,9 +974,9 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
         } else {
             const long long resident = std::min<long long>(per_sm, (blocks + sms - 1) / sms);
             const double busy = (double)std::min<long long>(warps, mine) * (double)resident;
-            body = (double)((mine + warps - 1) / warps) * std::max(lat, busy * thr);
+            body = (double)((mine + warps - 1) / warps) * size * (0.55 + 0.095 * busy);
         }
-        double us = (double)waves * (fixed + body);
+        double us = waves * (fixed + body);
         if (ragged && f->batch > 1) {
             const double work = (double)units / (double)slots * ((double)(n + 1) * fixed + (double)n * body) / 2;
             us = std::max(fixed + body, work + (fixed + body) / 2);
