@@ -2,7 +2,8 @@
 
 ``O = softmax(scale * Q K^T + mask) V`` with online softmax, fp32 LSE, split-KV
 partials merged by LSE, MHA/MQA/GQA, head dims 64/128/256/512, decode and short
-prefill, sliding-window and bottom-right causal masks.
+prefill, sliding-window and bottom-right causal masks; around it norm and rotation
+of queries and keys, a KV cache in 4 bits, and windows that keep first tokens.
 
 Every step runs in the CUDA kernels of ``libfmha_gb300.so`` behind a C ABI
 (``include/fmha.h``).  ``binding`` marshals torch tensors into that ABI; there

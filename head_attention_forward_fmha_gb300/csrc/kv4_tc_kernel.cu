@@ -14,13 +14,23 @@
 //
 // Warp roles (13 warps): 0..3 Q's conversion to fp16 (scaled by a power of two
 // per row), then softmax and epilogue, one query row per thread; 4 tensor memory
-// and MMA issue; 5..12 the conversion.  A conversion thread
-// holds its share of two or three tiles in registers, so that their loads are in
-// flight while it converts another.
+// and MMA issue; 5..12 the conversion.  A conversion thread holds its share of two
+// tiles in registers, so that their loads are in flight while it converts another.
 //
-// Bounded by the tensor cores and the softmax beside the conversion: per 128 keys
-// at hd 128 the MMAs take ~1000 clocks, the exponentials 512 and the
-// conversion's stores 512 of the SM's shared-memory writes.
+// Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 90 us, 766
+// TFLOP/s; over a window of 2048 with ragged lengths 41 us; 128 heads of 512 on one
+// KV head, 16 ragged sequences up to 4096 keys 33 us.  A clock trace says what bounds
+// it.  At hd 128 a tile of 128 keys took ~2200 clocks, of which the softmax warps 2075
+// (the exponentials alone 512), with MMAs and conversion beside them; at hd 512 a
+// tile of 64 keys took 2950, of which the 32 MMAs of S 2000: with N = 64 they read Q
+// (4 KB of shared memory each) for half as many keys as at N = 128, for which there
+// is no room.  What mattered on the way: at hd 512 no spilled register, descriptors
+// by addition among them (with 227 KB of shared memory there is hardly an L1, and
+// each reload is a trip to L2), and conversion in coalesced pieces (75 -> 49 us);
+// MMAs issued by an elected lane of a converged warp (49 -> 41); partials in fp16
+// (39 -> 33).  Small loops in the softmax (unrolled over the tile, the 4 x 4096 keys
+// took 156 us instead of 94).  Two threads per row (17 warps, 96 registers) were
+// slower: 113 us instead of 95 there, at hd 512 64 instead of 41.
 #include <climits>
 #include <atomic>
 #include "internal.h"

@@ -21,6 +21,14 @@
 // columns, out = x A + x' B with A, B made of the weights, cosines and sines;
 // a warp forms A and B once and applies them to all its heads, two columns per
 // instruction (packed fp32 pairs).
+//
+// Measured on GB300: four prompts of 4095 tokens, 64 + 2 x 8 heads of 128 (679 MB)
+// 109 us, 6.2 TB/s, 92 % of the measured copy rate, 65 % of the issue slots; one
+// token of the same 1.7 us.  With weight, norm and rotation applied one after
+// the other to single elements the prompts took 138 us, with 64-bit task
+// arithmetic and plain stores 121.  Four row sets per warp instead of one take 256
+// tokens of 96 heads of 256 from 8.5 to 5.8 us; below 16384 rows one set is taken, which
+// spreads the few rows over more warps.
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -379,7 +379,8 @@ int fmha_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float
  * Serving operators around the forward (no counterpart on the pages the method
  * comes from).  All of them are stream-ordered, allocate nothing and keep
  * nothing between calls; a NULL-able argument says so.  Tensors are contiguous
- * device memory; 16-byte alignment unless said otherwise.
+ * device memory, 16-byte aligned unless said otherwise, and outputs may not
+ * overlap inputs.
  */
 
 /*
@@ -400,7 +401,7 @@ int fmha_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float
  * q: [batch, n_h, T, hd]; k, v: [batch, n_kv_h, kv_rows, hd], the token's row at
  *   kv_start[b] + t (kv_start NULL: 0); a row outside [0, kv_rows) is not
  *   written.  Norm and rotation are computed in fp32 and rounded to bf16 once;
- *   V is copied bit for bit.  Outputs may not overlap qkv.
+ *   V is copied bit for bit.
  */
 int fmha_qk_norm_rope(const void* qkv, long long batch_stride, long long token_stride,
                       const float* q_weight, const float* k_weight, float eps,

@@ -510,3 +510,50 @@ def test_kv4_same_call_twice_is_bitwise_the_same():
     ws = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=DEV)
     b = binding.fmha_fwd_kv4(q, *cache, workspace=ws)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_torch_ops():
+    """The custom ops run the same calls, and trace under fake tensors."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from head_attention_forward_fmha_gb300 import torch_op  # noqa: F401  (registers them)
+
+    r = gen(80)
+    q, k, v = normal(r, 1, 8, 2, 128), normal(r, 1, 2, 400, 128), normal(r, 1, 2, 400, 128)
+    a = torch.ops.fmha_gb300.fwd_first(q, k, v, 4, 128 ** -0.5, 100, True)
+    b = binding.fmha_fwd_first(q, k, v, 4, window=100, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    cache = filled(r, 1, 2, 256, 128)
+    lens = torch.tensor([200], dtype=torch.int32, device=DEV)
+    a = torch.ops.fmha_gb300.fwd_kv4(q, *cache, lens, 1.0, 2.0, 128 ** -0.5, 100, 4, True)
+    b = binding.fmha_fwd_kv4(q, *cache, lens, v_global=2.0, window=100, n_first=4, causal=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with FakeTensorMode() as mode:
+        f = [mode.from_tensor(t) for t in (q, *cache, lens)]
+        o, lse = torch.ops.fmha_gb300.fwd_kv4(*f, 1.0, 2.0, 128 ** -0.5, 100, 4, True)
+        assert o.shape == q.shape and o.dtype == torch.bfloat16 and lse.shape == (1, 8, 2) and lse.dtype == torch.float32
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+def test_long_chunks_of_queries(hd):
+    """More query rows than a tile holds, several times over, and odd counts."""
+    check_kv4(hd, 6, 2, 301, 640, [301, 640, 5], causal=True, window=123, n_first=9)
+    check_first(hd, 1, 3, 1, 301, 640, 123, 9, True, sink=True)
+
+
+def test_no_rows_and_no_keys():
+    r = gen(81)
+    cache = filled(r, 2, 1, 64, 64)
+    o, lse = binding.fmha_fwd_kv4(torch.empty(2, 4, 0, 64, dtype=torch.bfloat16, device=DEV), *cache)
+    assert o.numel() == 0 and lse.numel() == 0
+    empty = binding.fmha_kv4_cache(2, 1, 0, 64)
+    sink = torch.tensor([1.0, -2.0, 0.5, 3.0], device=DEV)
+    o, lse = binding.fmha_fwd_kv4(normal(r, 2, 4, 3, 64), *empty, sink=sink)
+    assert (o == 0).all() and torch.equal(lse, sink[None, :, None].expand(2, 4, 3))
+    o, lse = binding.fmha_fwd_first(normal(r, 1, 2, 2, 64), torch.empty(1, 1, 0, 64, dtype=torch.bfloat16, device=DEV),
+                                    torch.empty(1, 1, 0, 64, dtype=torch.bfloat16, device=DEV), 4, window=8)
+    assert (o == 0).all() and torch.isinf(lse).all()
+    binding.fmha_kv4_append(*[torch.empty(2, 1, 0, 64, dtype=torch.bfloat16, device=DEV)] * 2, *cache,
+                            torch.zeros(2, dtype=torch.int32, device=DEV))
+    q, k, v = binding.fmha_qk_norm_rope(torch.empty(2, 0, 192, dtype=torch.bfloat16, device=DEV), None, None, 1, 1)
+    assert q.shape == (2, 1, 0, 64)
