@@ -603,6 +603,14 @@ def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=
          cap, hd, 0)
 
 
+def _remember(plans, key, value):
+    """Keep a plan; lengths that grow with every call would otherwise fill the memory."""
+    if len(plans) >= 4096:
+        plans.clear()
+    plans[key] = value
+    return value
+
+
 _kv4_plans = {}  # (chunk length, workspace bytes) by shape, for the kernel path that is set
 
 
@@ -641,7 +649,7 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
     plan = _kv4_plans.get(key)
     if plan is None:
         n, chunk = fmha_fwd_kv4_plan(*key)
-        plan = _kv4_plans[key] = chunk, (fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0)
+        plan = _remember(_kv4_plans, key, (chunk, fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0))
     kv_chunk, need = plan
     q_ptr = _ptr(q, "q", _BF16, shape, dev)
     cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev)
@@ -682,7 +690,7 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal)
     need = _first_plans.get(key)
     if need is None:
-        need = _first_plans[key] = fmha_fwd_first_workspace_bytes(*key)
+        need = _remember(_first_plans, key, fmha_fwd_first_workspace_bytes(*key))
     q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
     q_ptr, k_ptr = _ptr(q, "q", _BF16, q_shape, dev), _ptr(k, "k", _BF16, kv_shape, dev)
     ws = 0

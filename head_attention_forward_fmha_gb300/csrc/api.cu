@@ -891,6 +891,9 @@ int check_kv4(int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, f
     if (cap < s_k || cap % 16 != 0)
         return fail(FMHA_ERR_SHAPE, "cap=%d must be a multiple of 16 and at least s_k=%d", cap, s_k);
     if (s_k > INT_MAX - 4096) return fail(FMHA_ERR_SHAPE, "s_k=%d is too long", s_k);
+    // the kernels form positions len - T - window in 32 bits, with len down to 0
+    if (window < s_k && (long long)T + window > INT_MAX - 4096)
+        return fail(FMHA_ERR_SHAPE, "T=%d and window=%d together are too long", T, window);
     Kv4Fwd& f = *out;
     f = Kv4Fwd{};
     f.batch = batch;
@@ -1136,6 +1139,8 @@ extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_sc
     if (rc) return rc;
     if (!(k_global > 0.f) || !std::isfinite(k_global) || !(v_global > 0.f) || !std::isfinite(v_global))
         return fail(FMHA_ERR_SHAPE, "k_global and v_global must be finite and > 0");
+    if (!std::isfinite(2.f * scale * k_global))  // log2(e) < 2: the factor of the scores
+        return fail(FMHA_ERR_SHAPE, "scale * k_global is too large");
     const long long rows = (long long)batch * n_h * T;
     if (rows == 0) return FMHA_OK;
     if (!q || !o || !lse || (s_k > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)))

@@ -388,14 +388,16 @@ int fmha_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float
  *
  * qkv: [batch, T] rows of (n_h + 2 n_kv_h) * hd bf16 elements (the query
  *   heads, the key heads, the value heads), row (b, t) at element
- *   b * batch_stride + t * token_stride; both strides multiples of 8.
+ *   b * batch_stride + t * token_stride; both strides multiples of 8,
+ *   token_stride at least a row.
  * q_weight, k_weight: [hd] fp32.  With a weight each head row x of that kind
  *   becomes x * rsqrt(mean(x^2) + eps) * weight; NULL leaves it as it is.
  * cos_sin: [max_pos, rot] fp32, row p the rot / 2 cosines and then the rot / 2
  *   sines of position p's angles.  Pair i of a query or key row is columns (i,
  *   rot / 2 + i), or (2 i, 2 i + 1) when interleaved is 1, and becomes
  *   (lo cos_i - hi sin_i, hi cos_i + lo sin_i); columns from rot on stay.  rot is
- *   a multiple of 8 up to hd; 0 is no rotation (cos_sin and positions NULL).
+ *   a multiple of 8 up to hd; 0 is no rotation (cos_sin and positions are not
+ *   read then, and no token is padding).
  * positions: [batch, T] int32.  A token whose position is outside
  *   [0, max_pos) is padding: none of its outputs is written.
  * q: [batch, n_h, T, hd]; k, v: [batch, n_kv_h, kv_rows, hd], the token's row at
@@ -442,7 +444,8 @@ int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, in
  *
  * seq_lens: [batch] int32, the keys of each sequence (clamped to [0, s_k]), or
  *   NULL: s_k each.  s_k <= cap bounds them on the host and shapes the launch.
- *   Rows of the cache from a sequence's length on are not read into any result.
+ *   Rows of the cache from a sequence's length on, and keys that no row attends,
+ *   reach no result; V's scales have to be numbers at keys that some row attends.
  * Query row t of a sequence with len keys sits at position len - T + t; with
  *   causal, a row at a negative position attends nothing (O = 0, LSE = -inf, or
  *   the sink's).

@@ -136,3 +136,19 @@ def test_binding_refusals():
         binding.fmha_fwd_first(bf, bf, bf, 4, window=8)
     with pytest.raises(ValueError):
         binding.fmha_kv4_cache(1, 1, 40, 128, device="cpu")
+
+
+def test_kv4_refuses_what_its_arithmetic_does_not_hold(lib):
+    """Positions len - T - window and the factor scale * k_global * log2(e) past 32 bits."""
+    big = (1 << 31) - 8192
+    assert lib.fmha_fwd_kv4(*{**KV4, **dict(T=8192, s_k=big, cap=big, window=big - 1)}.values()) == -5
+    assert lib.fmha_fwd_kv4_plan(1, 8, 1, 8192, big, 128, big - 1, 0, 1, 1, None) == -5
+    assert lib.fmha_fwd_kv4_plan(1, 8, 1, 8192, big, 128, big, 0, 1, 1, None) > 0  # holds every key: no window
+    assert lib.fmha_fwd_kv4(*{**KV4, **dict(scale=1e30, kg=1e30)}.values()) == -5
+
+
+def test_plans_are_kept_within_bounds():
+    plans = {}
+    for i in range(10000):
+        assert binding._remember(plans, i, -i) == -i and plans[i] == -i
+    assert len(plans) <= 4096

@@ -532,6 +532,8 @@ def test_torch_ops():
         f = [mode.from_tensor(t) for t in (q, *cache, lens)]
         o, lse = torch.ops.fmha_gb300.fwd_kv4(*f, 1.0, 2.0, 128 ** -0.5, 100, 4, True)
         assert o.shape == q.shape and o.dtype == torch.bfloat16 and lse.shape == (1, 8, 2) and lse.dtype == torch.float32
+        o, lse = torch.ops.fmha_gb300.fwd_first(*[mode.from_tensor(t) for t in (q, k, v)], 4, 128 ** -0.5, 100, True)
+        assert o.shape == q.shape and lse.shape == (1, 8, 2)
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256, 512])
