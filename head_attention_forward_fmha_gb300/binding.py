@@ -7,7 +7,6 @@ kernels; there is no CPU fallback, and a missing library raises.
 """
 import ctypes
 import os
-import struct
 import threading
 
 import torch
@@ -66,7 +65,7 @@ SIGNATURES = {
     "fmha_fwd_first_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "fmha_fwd_first": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp, _sz,
                         _vp], _i32),
-    # arguments in one struct, packed here into bytes
+    # arguments in one struct
     "fmha_qk_norm_rope_packed": ([ctypes.c_char_p], _i32),
     "fmha_kv4_append_packed": ([ctypes.c_char_p], _i32),
     "fmha_fwd_kv4_packed": ([ctypes.c_char_p], _i32),
@@ -77,6 +76,8 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
 _lib = None
+_call = None      # _tensor_args.call (csrc/tensor_args.cpp)
+_packed = {}      # address of each *_packed entry
 
 
 class FmhaError(RuntimeError):
@@ -86,8 +87,8 @@ class FmhaError(RuntimeError):
 
 
 def load(path=None):
-    """Load the shared library (once).  Raises if it has not been built."""
-    global _lib
+    """Load the shared library and the argument packer (once).  Raises if they have not been built."""
+    global _lib, _call
     if _lib is not None and path is None:
         return _lib
     p = path or LIB_PATH
@@ -99,6 +100,10 @@ def load(path=None):
         fn.argtypes = args
         fn.restype = res
     if path is None:
+        from . import _tensor_args
+
+        _packed.update((n[:-7], ctypes.cast(getattr(lib, n), _vp).value) for n in SIGNATURES if n.endswith("_packed"))
+        _call = _tensor_args.call
         _lib = lib
     return lib
 
@@ -439,23 +444,18 @@ def fmha_fwd_noalloc(q, k, v, o, lse, scale=None, window=0, causal=False, stream
 # ---------------------------------------------------------------------------
 # Serving operators around the forward: norm and rotation, 4-bit cache, window
 # with first keys.  Their smallest calls take a few microseconds on the GPU, so
-# the checks here are written for few Python steps per tensor.
+# the tensors are checked and packed by csrc/tensor_args.cpp.
 # ---------------------------------------------------------------------------
-_BF16, _FP32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_BF16, _FP32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
-
-def _ptr(t, name, dtype, shape, dev):
-    """Data pointer of a contiguous tensor of this dtype and shape on CUDA device `dev` (an index)."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous CUDA %s tensor" % (name, dtype))
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s must be on cuda:%d" % (name, dev))
+# The argument structs of include/fmha.h: entry, a character per field (tensor_args.cpp has their meaning), tensor names.
+_NORM_ROPE = ("fmha_qk_norm_rope", b"SfffiBBBiqqqrnnnnnnnnn",
+              ("qkv", "q_weight", "k_weight", "cos_sin", "positions", "q", "k", "v", "kv_start"))
+_APPEND = ("fmha_kv4_append", b"BBUUUUIbbqrrnnnnnn",
+           ("k", "v", "k_codes", "k_scales", "v_codes", "v_scales", "start", "k_out", "v_out"))
+_KV4 = ("fmha_fwd_kv4", b"BUUUUiBFfuqqrrrnnnnnnnnnnn",
+        ("q", "k_codes", "k_scales", "v_codes", "v_scales", "seq_lens", "o", "lse", "sink", "workspace"))
+_FIRST = ("fmha_fwd_first", b"BBBBFfuqqrnnnnnnnnn", ("q", "k", "v", "o", "lse", "sink", "workspace"))
 
 
 def _device(t, name):
@@ -465,16 +465,15 @@ def _device(t, name):
     return t.get_device()
 
 
-def _run(fn, dev, pack, *args):
-    """Call `fn`_packed with these arguments, device `dev` current."""
+def _run(entry, dev, *values):
+    """Call an entry with the values of its struct's fields (tensors each with their shape), device `dev` current."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _run(fn, dev, pack, *args)
-    try:
-        block = pack(*args)
-    except struct.error as e:
-        raise ValueError("%s: %s" % (fn, e)) from None
-    rc = getattr(_lib or load(), fn + "_packed")(block)
+            return _run(entry, dev, *values)
+    if _lib is None:
+        load()
+    fn, layout, names = entry
+    rc = _call(_packed[fn], layout, names, dev, *values)
     if rc:
         _check(rc, fn)
 
@@ -482,13 +481,6 @@ def _run(fn, dev, pack, *args):
 def _handle(stream, dev):
     """The stream's handle; None is the device's current stream."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-# The argument structs of include/fmha.h: pointers and 64-bit numbers, floats, ints (0 for an absent pointer).
-_NORM_ROPE = struct.Struct("=10Q2qf9i").pack
-_APPEND = struct.Struct("=10Q2f6i").pack
-_KV4 = struct.Struct("=12Q3f11i").pack
-_FIRST = struct.Struct("=9Qf9i").pack
 
 
 _workspaces = {}  # uint8 tensor by (thread, device, stream)
@@ -525,11 +517,10 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     k and v given with more rows than T are written at rows kv_start[b] + t (int32 [b]; None: 0).
     Returns q [b, n_h, T, hd], k and v [b, n_kv_h, rows, hd]; what is not given is allocated."""
     dev = _device(qkv, "qkv")
-    if qkv.dtype is not _BF16:
-        raise TypeError("qkv must be a CUDA bf16 tensor")
-    if qkv.dim() != 3 or n_h < 1 or n_kv_h < 1 or qkv.shape[2] % (n_h + 2 * n_kv_h):
-        raise ValueError("qkv [b, T, (n_h + 2 n_kv_h) * hd] expected, got %s" % (tuple(qkv.shape),))
-    b, T, width = qkv.shape
+    shape = qkv.shape
+    if len(shape) != 3 or n_h < 1 or n_kv_h < 1 or shape[2] % (n_h + 2 * n_kv_h):
+        raise ValueError("qkv [b, T, (n_h + 2 n_kv_h) * hd] expected, got %s" % (tuple(shape),))
+    b, T, width = shape
     hd = width // (n_h + 2 * n_kv_h)
     sb, st, se = qkv.stride()
     if se != 1 and width > 1:
@@ -543,26 +534,21 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     if (k is None) != (v is None) or (k is not None and k.dim() != 4):
         raise ValueError("k and v [b, n_kv_h, rows, hd] are given together or not at all")
     if cos_sin is None:
-        cs_ptr = pos_ptr = max_pos = rot = 0
+        max_pos = rot = 0
+    elif cos_sin.dim() != 2:
+        raise ValueError("cos_sin [max_pos, rot] expected, got %s" % (tuple(cos_sin.shape),))
     else:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin [max_pos, rot] expected, got %s" % (tuple(cos_sin.shape),))
         max_pos, rot = cos_sin.shape
-        cs_ptr = _ptr(cos_sin, "cos_sin", _FP32, (max_pos, rot), dev)
-        pos_ptr = _ptr(positions, "positions", _I32, (b, T), dev)
     if q is None:
         q = torch.empty((b, n_h, T, hd), dtype=_BF16, device=dev)
     if k is None:
         k = torch.empty((b, n_kv_h, T, hd), dtype=_BF16, device=dev)
         v = torch.empty_like(k)
     rows = k.shape[2]
-    kv_shape = (b, n_kv_h, rows, hd)
-    _run("fmha_qk_norm_rope", dev, _NORM_ROPE, qkv.data_ptr(),
-         0 if q_weight is None else _ptr(q_weight, "q_weight", _FP32, (hd,), dev),
-         0 if k_weight is None else _ptr(k_weight, "k_weight", _FP32, (hd,), dev), cs_ptr, pos_ptr,
-         _ptr(q, "q", _BF16, (b, n_h, T, hd), dev), _ptr(k, "k", _BF16, kv_shape, dev), _ptr(v, "v", _BF16, kv_shape, dev),
-         0 if kv_start is None else _ptr(kv_start, "kv_start", _I32, (b,), dev), _handle(stream, dev), sb, st, eps, max_pos, rot,
-         bool(interleaved), rows, b, T, n_h, n_kv_h, hd)
+    kv_shape, w_shape = (b, n_kv_h, rows, hd), (hd,)
+    _run(_NORM_ROPE, dev, qkv, q_weight, w_shape, k_weight, w_shape, cos_sin, None, positions, (b, T), q, (b, n_h, T, hd),
+         k, kv_shape, v, kv_shape, kv_start, (b,), _handle(stream, dev), sb, st, eps, max_pos, rot, bool(interleaved), rows, b, T,
+         n_h, n_kv_h, hd)
     return q, k, v
 
 
@@ -572,12 +558,6 @@ def fmha_kv4_cache(batch, n_kv_h, cap, hd, device="cuda"):
     if hd not in (64, 128, 256, 512) or cap % 16:
         raise ValueError("hd must be 64, 128, 256 or 512 and cap a multiple of 16 (got hd=%d cap=%d)" % (hd, cap))
     return tuple(torch.zeros((batch, n_kv_h, cap, hd // w), dtype=_U8, device=device) for w in (2, 16, 2, 16))
-
-
-def _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev):
-    cs, ss = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
-    return (_ptr(k_codes, "k_codes", _U8, cs, dev), _ptr(k_scales, "k_scales", _U8, ss, dev),
-            _ptr(v_codes, "v_codes", _U8, cs, dev), _ptr(v_scales, "v_scales", _U8, ss, dev))
 
 
 def _kv4_heads_rows(k_codes):
@@ -591,16 +571,14 @@ def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=
     """Quantise k, v (bf16 [b, n_kv_h, T, hd]) into a 4-bit cache (fmha_kv4_cache) at rows start[b] + t (int32 [b]; rows
     outside the cache are left out).  k_out and v_out, bf16 like k, receive the values that the written rows stand for."""
     dev = _device(k, "k")
-    if k.dim() != 4:
-        raise ValueError("k [b, n_kv_h, T, hd] expected, got %s" % (tuple(k.shape),))
     shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("k [b, n_kv_h, T, hd] expected, got %s" % (tuple(shape),))
     b, n_kv_h, T, hd = shape
     cap = _kv4_heads_rows(k_codes)[1]
-    _run("fmha_kv4_append", dev, _APPEND, _ptr(k, "k", _BF16, shape, dev), _ptr(v, "v", _BF16, shape, dev),
-         *_kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev), _ptr(start, "start", _I32, (b,), dev),
-         0 if k_out is None else _ptr(k_out, "k_out", _BF16, shape, dev),
-         0 if v_out is None else _ptr(v_out, "v_out", _BF16, shape, dev), _handle(stream, dev), k_global, v_global, b, n_kv_h, T,
-         cap, hd, 0)
+    codes, scales = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
+    _run(_APPEND, dev, k, shape, v, shape, k_codes, codes, k_scales, scales, v_codes, codes, v_scales, scales, start, (b,),
+         k_out, shape, v_out, shape, _handle(stream, dev), k_global, v_global, b, n_kv_h, T, cap, hd, 0)
 
 
 def _remember(plans, key, value):
@@ -634,9 +612,9 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
     partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call uses the
     binding's own (one per thread and stream; a new one under graph capture)."""
     dev = _device(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q [b, n_h, T, hd] expected, got %s" % (tuple(q.shape),))
     shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q [b, n_h, T, hd] expected, got %s" % (tuple(shape),))
     b, n_h, T, hd = shape
     n_kv_h, cap = _kv4_heads_rows(k_codes)
     if s_k is None:
@@ -651,18 +629,13 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
         n, chunk = fmha_fwd_kv4_plan(*key)
         plan = _remember(_kv4_plans, key, (chunk, fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0))
     kv_chunk, need = plan
-    q_ptr = _ptr(q, "q", _BF16, shape, dev)
-    cache = _kv4_ptrs(k_codes, k_scales, v_codes, v_scales, b, n_kv_h, cap, hd, dev)
-    ws = 0
     if workspace is not None:
-        ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
         need = workspace.numel()
     elif need:
         workspace = _workspace(need, dev, stream)
-        ws = workspace.data_ptr()
-    _run("fmha_fwd_kv4", dev, _KV4, q_ptr, *cache, 0 if seq_lens is None else _ptr(seq_lens, "seq_lens", _I32, (b,), dev),
-         _ptr(o, "o", _BF16, shape, dev), _ptr(lse, "lse", _FP32, (b, n_h, T), dev),
-         0 if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), ws, need, _handle(stream, dev), k_global, v_global,
+    codes, scales = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
+    _run(_KV4, dev, q, shape, k_codes, codes, k_scales, scales, v_codes, codes, v_scales, scales, seq_lens, (b,), o, shape,
+         lse, (b, n_h, T), sink, (n_h,), workspace, None, need, _handle(stream, dev), k_global, v_global,
          hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, bool(causal), kv_chunk)
     return o, lse
 
@@ -691,16 +664,11 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     need = _first_plans.get(key)
     if need is None:
         need = _remember(_first_plans, key, fmha_fwd_first_workspace_bytes(*key))
-    q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
-    q_ptr, k_ptr = _ptr(q, "q", _BF16, q_shape, dev), _ptr(k, "k", _BF16, kv_shape, dev)
-    ws = 0
     if workspace is not None:
-        ws = _ptr(workspace, "workspace", _U8, workspace.shape, dev)
         need = workspace.numel()
     elif need:
         workspace = _workspace(need, dev, stream)
-        ws = workspace.data_ptr()
-    _run("fmha_fwd_first", dev, _FIRST, q_ptr, k_ptr, _ptr(v, "v", _BF16, kv_shape, dev), _ptr(o, "o", _BF16, q_shape, dev),
-         _ptr(lse, "lse", _FP32, (b, n_h, T), dev), 0 if sink is None else _ptr(sink, "sink", _FP32, (n_h,), dev), ws, need,
+    q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
+    _run(_FIRST, dev, q, q_shape, k, kv_shape, v, kv_shape, o, q_shape, lse, (b, n_h, T), sink, (n_h,), workspace, None, need,
          _handle(stream, dev), hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
     return o, lse

@@ -4,7 +4,9 @@ Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel
 (``-gencode arch=compute_103a,code=sm_103a -lineinfo -O3``) and linked into one
 shared library next to this file.  The checked build compiles the same sources
 with ``-DFMHA_CHECKED`` (every computed index of the kernels is tested before
-its access, see ``include/fmha.h``) into ``libfmha_gb300_checked.so``.  Usage:
+its access, see ``include/fmha.h``) into ``libfmha_gb300_checked.so``.  The Python
+binding's argument packer, ``csrc/tensor_args.cpp``, is built by g++ against the installed
+torch into the extension module ``_tensor_args.so``.  Usage:
 ``python -m head_attention_forward_fmha_gb300.build [--force] [--verbose]
 [--checked | --all]``.
 """
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libfmha_gb300.so")
 CHECKED_LIB_PATH = os.path.join(PKG, "libfmha_gb300_checked.so")
+ARGS_SRC = os.path.join(CSRC, "tensor_args.cpp")
+ARGS_PATH = os.path.join(PKG, "_tensor_args.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -57,7 +62,34 @@ def up_to_date(checked=False):
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _build_args(force):
+    """The argument packer; against another torch than it was built with (a stamp says which) it is built again."""
+    import torch
+
+    stamp = os.path.join(BUILD_DIR, "tensor_args.torch")
+    if not force and os.path.exists(ARGS_PATH) and os.path.exists(stamp) and open(stamp).read() == torch.__version__ and \
+            os.path.getmtime(ARGS_PATH) >= max(os.path.getmtime(ARGS_SRC), os.path.getmtime(os.path.abspath(__file__))):
+        return
+    gxx = os.environ.get("CXX") or shutil.which("g++")
+    if not gxx:
+        raise RuntimeError("g++ not found (set CXX)")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    inc, lib = os.path.join(home, "include"), os.path.join(home, "lib")
+    tmp = "%s.%d.tmp" % (ARGS_PATH, os.getpid())
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", sysconfig.get_paths()["include"], "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), ARGS_SRC,
+           "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on tensor_args.cpp:\n%s" % r.stdout)
+    os.replace(tmp, ARGS_PATH)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+
+
 def _build_variants(variants, force, verbose, extra_flags):
+    _build_args(force)
     todo = [c for c in variants if force or not up_to_date(c)]
     if not todo:
         return

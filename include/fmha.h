@@ -488,8 +488,8 @@ int fmha_fwd_first(const void* q, const void* k, const void* v, void* o, float* 
 /*
  * The serving operators with their arguments in one struct: the same calls, for
  * bindings in which every argument of a foreign call costs time (from Python's
- * ctypes, 26 arguments took 2.7 us, one takes 0.4).  Fields as the arguments of the
- * call of the same name.
+ * ctypes, 26 arguments took 2.7 us, one takes 0.4; the Python binding packs them in
+ * csrc/tensor_args.cpp).  Fields as the arguments of the call of the same name.
  */
 struct fmha_qk_norm_rope_args {
     const void* qkv;

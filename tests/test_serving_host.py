@@ -1,5 +1,8 @@
 """Refusals of the serving operators, without a GPU: the C entry points' argument
 checks (nothing is launched on an error), the 4-bit plan, and the binding's own checks."""
+import re
+import struct
+
 import pytest
 import torch
 
@@ -73,7 +76,6 @@ def test_first_refusals(lib, change, code):
 def test_argument_structs_are_laid_out_as_packed_here(tmp_path):
     """The binding packs the structs of include/fmha.h itself: sizes and the offsets of the last fields."""
     import os
-    import struct
     import subprocess
 
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -85,15 +87,22 @@ def test_argument_structs_are_laid_out_as_packed_here(tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "s")], check=True)
     got = subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == [struct.calcsize(f) - 4 for _, _, f in last]
+    # the binding's layouts have the same fields (a pointer for each tensor)
+    for (name, layout, tensors), (n, _, f) in zip((binding._NORM_ROPE, binding._APPEND, binding._KV4, binding._FIRST), last):
+        kinds = {**dict.fromkeys("BFIUbfiuS", "Q"), "q": "q", "n": "i", "r": "f"}
+        fields = "".join(kinds[c] for c in layout.decode())
+        assert name == "fmha_" + n and struct.calcsize("=" + fields) == struct.calcsize(f)
+        assert sum(c in "BFIUbfiuS" for c in layout.decode()) == len(tensors)
+        assert fields.replace("q", "Q") == "".join((c * int(k or 1)).replace("q", "Q") for k, c in re.findall(r"(\d*)([Qqfi])", f))
 
 
 def test_packed_calls_refuse_like_the_others(lib):
     assert lib.fmha_fwd_kv4_packed(None) == -1 and lib.fmha_fwd_first_packed(None) == -1
     assert lib.fmha_qk_norm_rope_packed(None) == -1 and lib.fmha_kv4_append_packed(None) == -1
-    assert lib.fmha_fwd_kv4_packed(binding._KV4(*[P] * 5, 0, P, P, 0, 0, 0, 0, 1.0, 1.0, 0.1, 1, 8, 1, 1, 64, 64, 80, 0, 0, 0, 0)) == -3
-    assert lib.fmha_fwd_first_packed(binding._FIRST(*[P] * 5, 0, 0, 0, 0, 0.1, 1, 8, 1, 1, 64, 128, 16, -1, 0)) == -5
-    assert lib.fmha_kv4_append_packed(binding._APPEND(*[P] * 7, 0, 0, 0, 1.0, 1.0, 1, 1, 1, 40, 128, 0)) == -5
-    assert lib.fmha_qk_norm_rope_packed(binding._NORM_ROPE(*[P] * 8, 0, 0, 0, 1280, 1e-6, 64, 4, 0, 1, 1, 1, 8, 1, 128)) == -5
+    assert lib.fmha_fwd_kv4_packed(struct.pack("=12Q3f11i", *[P] * 5, 0, P, P, 0, 0, 0, 0, 1.0, 1.0, 0.1, 1, 8, 1, 1, 64, 64, 80, 0, 0, 0, 0)) == -3
+    assert lib.fmha_fwd_first_packed(struct.pack("=9Qf9i", *[P] * 5, 0, 0, 0, 0, 0.1, 1, 8, 1, 1, 64, 128, 16, -1, 0)) == -5
+    assert lib.fmha_kv4_append_packed(struct.pack("=10Q2f6i", *[P] * 7, 0, 0, 0, 1.0, 1.0, 1, 1, 1, 40, 128, 0)) == -5
+    assert lib.fmha_qk_norm_rope_packed(struct.pack("=10Q2qf9i", *[P] * 8, 0, 0, 0, 1280, 1e-6, 64, 4, 0, 1, 1, 1, 8, 1, 128)) == -5
 
 
 def test_first_workspace():
@@ -152,3 +161,32 @@ def test_plans_are_kept_within_bounds():
     for i in range(10000):
         assert binding._remember(plans, i, -i) == -i and plans[i] == -i
     assert len(plans) <= 4096
+
+
+def test_argument_packer():
+    """What the packer refuses, and the bytes that it passes on (read back by a callback)."""
+    import ctypes
+
+    from head_attention_forward_fmha_gb300 import _tensor_args
+
+    got = []
+
+    @ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p)
+    def entry(p):
+        got.append(ctypes.string_at(p, 32))
+        return 7
+
+    fn = ctypes.cast(entry, ctypes.c_void_p).value
+    call = _tensor_args.call
+    assert call(fn, b"bqnrnn", ("x",), 0, None, None, -5, 1 << 30, 0.25, -1, True) == 7
+    assert got[0] == struct.pack("=Qqifii", 0, -5, 1 << 30, 0.25, -1, 1)
+    t = torch.zeros(2, 3, dtype=torch.bfloat16)
+    for bad, err in ((("B", ("x",), t, (2, 3)), TypeError),             # not on a GPU
+                     (("B", ("x",), None, (2, 3)), TypeError),          # needed
+                     (("S", ("x",), "text"), TypeError),
+                     (("n", (), 1 << 31), ValueError), (("n", (), -(1 << 31) - 1), ValueError), (("q", (), 1 << 63), ValueError),
+                     (("n", (), 1.5), TypeError), (("r", (), "1"), TypeError), (("n", ()), TypeError), (("n", (), 1, 2), TypeError),
+                     (("z", (), 1), TypeError), (("b", (), None, None), TypeError), (("n" * 70, (), *range(70)), TypeError)):
+        with pytest.raises(err):
+            call(fn, bad[0].encode(), bad[1], 0, *bad[2:])
+    assert len(got) == 1
