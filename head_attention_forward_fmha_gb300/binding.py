@@ -655,7 +655,11 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call uses the
     binding's own (one per thread and stream; a new one under graph capture)."""
     dev = _device(q, "q")
-    b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
+    q_shape, kv_shape = q.shape, k.shape
+    if len(q_shape) != 4 or len(kv_shape) != 4:
+        raise ValueError("q [b,n_h,T,hd] and k, v [b,n_kv_h,s_k,hd] expected")
+    b, n_h, T, hd = q_shape
+    n_kv_h, s_k = kv_shape[1:3]
     if o is None:
         o = torch.empty_like(q)
     if lse is None:
@@ -668,7 +672,7 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
         need = workspace.numel()
     elif need:
         workspace = _workspace(need, dev, stream)
-    q_shape, kv_shape = (b, n_h, T, hd), (b, n_kv_h, s_k, hd)
+    kv_shape = (b, n_kv_h, s_k, hd)
     _run(_FIRST, dev, q, q_shape, k, kv_shape, v, kv_shape, o, q_shape, lse, (b, n_h, T), sink, (n_h,), workspace, None, need,
          _handle(stream, dev), hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
     return o, lse

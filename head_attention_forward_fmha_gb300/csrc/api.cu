@@ -931,7 +931,8 @@ bool kv4_use_tc(int hd, long long R) {
 // for every warp that its SM has at work (16 warps: 2.1 us, 35 KB of cache per us; a
 // half more with 16 rows, 2.2 times with 32; a tile at hd 64, half as large, 0.75),
 // a block ~3 us before and after; blocks beyond a wave of small ones start as others
-// end; the merge kernel ~2.5 us, ~0.04 per chunk and its partials.  Without such
+// end; the merge kernel ~2.5 us, ~0.04 per chunk, from 16 on 0.12 (16 rows over 8192
+// keys at hd 256: 128 chunks 22 us, 32 chunks 14), and its partials.  Without such
 // terms for half-filled SMs, 16 sequences of 32768 keys went to two chunks at
 // 189 us instead of eight at 113.
 // Tensor-core kernel: ~1.1 us per tile and ~7 us before and after, at hd 512 2.1
@@ -984,7 +985,7 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
             const double work = (double)units / (double)slots * ((double)(n + 1) * fixed + (double)n * body) / 2;
             us = std::max(fixed + body, work + (fixed + body) / 2);
         }
-        if (n > 1) us += 2.5 + 0.04 * (double)n + parts_us * (double)n * (f->tc && f->hd == 512 ? 0.5 : 1.0);
+        if (n > 1) us += 2.5 + 0.04 * (double)n + 0.08 * (double)std::max(0LL, n - 16) + parts_us * (double)n * (f->tc && f->hd == 512 ? 0.5 : 1.0);
         if (us < best * 0.98) {
             best = us;
             best_n = n;
@@ -1002,7 +1003,7 @@ void plan_kv4(Kv4Fwd* f, bool ragged) {
             continue;
         }
         const long long slots = sms * (f->tc ? 1 : kv4_ctas_per_sm(f->hd, rows, warps));
-        for (long long n = 1; n <= 16; n *= 2) consider(warps, n);
+        for (long long n = 1; n <= 64; n *= 2) consider(warps, n);
         for (int w = 1; w <= 4; ++w) {  // whole waves; the merge reads partials in fours
             const long long n = slots * w / std::max(1LL, units);
             consider(warps, n > 4 ? n & ~3LL : n);
