@@ -17,11 +17,12 @@
 // and MMA issue; 5..12 the conversion.  A conversion thread holds its share of two
 // tiles in registers, so that their loads are in flight while it converts another.
 //
-// Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 90 us, 766
-// TFLOP/s; over a window of 2048 with ragged lengths 41 us; 128 heads of 512 on one
+// Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 83 us, 823
+// TFLOP/s; over a window of 2048 with ragged lengths 39 us; 128 heads of 512 on one
 // KV head, 16 ragged sequences up to 4096 keys 33 us.  A clock trace says what bounds
 // it.  At hd 128 a tile of 128 keys took ~2200 clocks, of which the softmax warps 2075
-// (the exponentials alone 512), with MMAs and conversion beside them; at hd 512 a
+// (the exponentials alone 512), with MMAs and conversion beside them (before its
+// scores were read 64 at a time); at hd 512 a
 // tile of 64 keys took 2950, of which the 32 MMAs of S 2000: with N = 64 they read Q
 // (4 KB of shared memory each) for half as many keys as at N = 128, for which there
 // is no room.  What mattered on the way: at hd 512 no spilled register, descriptors
@@ -474,15 +475,24 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             const bool full = key0 >= lo && key0 + BN - 1 <= hi;
             const uint32_t p_addr = t_lane + C::P_COL + pb * (BN / 2);
             float alpha = 1.f;
-            // 32 scores of the row, those outside [lo, hi] at -inf
-            auto load_scores = [&](int c, float (&x)[32]) {
-                tmem_ld32(s_addr + c * 32, x);
+            // The row's scores from column `col` of the tile on, those outside [lo, hi] at
+            // -inf.  64 at a time: each wait for tensor memory costs (by 32, 4 x 4096 keys at hd
+            // 128 take 90 instead of 84 us); the maximum by 32 where there is one pass
+            // of 64 anyway (by 64 it spills at hd 512, 46 instead of 41 us).
+            auto load_scores = [&](int col, auto& x) {
+                constexpr int N = sizeof(x) / sizeof(x[0]);
+#pragma unroll
+                for (int h = 0; h < N; ++h) tmem_ld32(s_addr + col + h * 32, x[h]);
                 tmem_wait_ld();
                 if (!full) {
-                    const int k0 = max(0, lo - key0 - c * 32), k1 = min(31, hi - key0 - c * 32);
-                    const uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = (in >> i) & 1u ? x[i] : -INFINITY;
+                    for (int h = 0; h < N; ++h) {
+                        const int first = key0 + col + h * 32;
+                        const int k0 = max(0, lo - first), k1 = min(31, hi - first);
+                        const uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[h][i] = (in >> i) & 1u ? x[h][i] : -INFINITY;
+                    }
                 }
             };
             // P against the present reference; S stays as it is.  Usually the reference
@@ -497,11 +507,13 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 if (__any_sync(0xffffffffu, move)) {
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < BN / 32; ++c) {
-                        float x[32];
-                        load_scores(c, x);
+                    for (int col = 0; col < BN; col += BN / 2) {
+                        float x[BN / 64][32];
+                        load_scores(col, x);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
+                        for (int h = 0; h < BN / 64; ++h)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[h][i], x[h][i + 1]));
                     }
                     const float mt = mx * qs;
                     if (mt > m_ref + 8.f) {
@@ -516,21 +528,24 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 uint32_t top = 0u;
                 const uint64_t q2 = f32x2(qs, qs), mu2 = f32x2(mu, mu);
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
-                    float x[32];
-                    load_scores(c, x);
-                    uint32_t pk[16];
+                for (int col = 0; col < BN; col += 64) {
+                    float x[2][32];
+                    load_scores(col, x);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float y0, y1;
-                        f32x2_split(fma_f32x2(f32x2(x[2 * i], x[2 * i + 1]), q2, mu2), y0, y1);
-                        y0 = ex2_approx(y0);
-                        y1 = ex2_approx(y1);
-                        pk[i] = pack_f16x2(y0, y1);
-                        top = __vmaxu2(top, pk[i]);  // not negative: fp16 bits compare as integers
-                        s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float y0, y1;
+                            f32x2_split(fma_f32x2(f32x2(x[h][2 * i], x[h][2 * i + 1]), q2, mu2), y0, y1);
+                            y0 = ex2_approx(y0);
+                            y1 = ex2_approx(y1);
+                            pk[i] = pack_f16x2(y0, y1);
+                            top = __vmaxu2(top, pk[i]);  // not negative: fp16 bits compare as integers
+                            s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
+                        }
+                        tmem_st16u(p_addr + col / 2 + h * 16, pk);
                     }
-                    tmem_st16u(p_addr + c * 16, pk);
                 }
                 move = max(top & 0xFFFFu, top >> 16) > 0x7400u;  // 2^14
                 if (again == 0 && __any_sync(0xffffffffu, move)) continue;
