@@ -18,7 +18,7 @@
 // tiles in registers, so that their loads are in flight while it converts another.
 //
 // Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 83 us, 823
-// TFLOP/s; over a window of 2048 with ragged lengths 39 us; 128 heads of 512 on one
+// TFLOP/s; over a window of 2048 with ragged lengths 34 us; 128 heads of 512 on one
 // KV head, 16 ragged sequences up to 4096 keys 33 us.  A clock trace says what bounds
 // it.  At hd 128 a tile of 128 keys took ~2200 clocks, of which the softmax warps 2075
 // (the exponentials alone 512), with MMAs and conversion beside them (before its
@@ -184,9 +184,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rt = blockIdx.x / C::PARTS, part = blockIdx.x % C::PARTS;
-    const int split = blockIdx.y, slab = blockIdx.z;
-    const int b = slab / f.n_kv_h, kvh = slab - b * f.n_kv_h;
-    const long long row0 = ((long long)b * f.n_h + (long long)kvh * a.group) * f.T;  // slab's first query row
+    const int split = blockIdx.y;
+    int b = blockIdx.z / f.n_kv_h;
+    const int kvh = blockIdx.z - b * f.n_kv_h;
     const int r_begin = rt * BM;
     const int r_end = min(a.R, r_begin + BM);
 
@@ -212,7 +212,25 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 
     // Keys: the virtual axis of kv4_kernel.cu, with tiles of BN keys and a
     // window part that starts at its first key.
-    const int len = f.seq_lens ? min(max(__ldg(f.seq_lens + b), 0), f.s_k) : f.s_k;
+    int len = f.s_k;
+    if (f.seq_lens && f.n_splits == 1 && f.batch <= 32) {
+        // Blocks start in the order of their index: with the longest sequence first,
+        // the shortest fill the last gaps (chunks of 128 tokens over four ragged
+        // sequences 38.6 -> 33.6 us).  Slot b holds the sequence that b others exceed.
+        // Chunks are even without it (16 sequences in 8 chunks at hd 512: 33.0, sorted 36.6 us).
+        const int mine = lane < f.batch ? min(max(__ldg(f.seq_lens + lane), 0), f.s_k) : -1;
+        int ahead = 0;
+        for (int i = 0; i < f.batch; ++i) {
+            const int other = __shfl_sync(0xffffffffu, mine, i);
+            ahead += other > mine || (other == mine && i < lane);
+        }
+        b = __ffs(__ballot_sync(0xffffffffu, lane < f.batch && ahead == b)) - 1;
+        len = __shfl_sync(0xffffffffu, mine, b);
+    } else if (f.seq_lens) {
+        len = min(max(__ldg(f.seq_lens + b), 0), f.s_k);
+    }
+    const int slab = b * f.n_kv_h + kvh;
+    const long long row0 = ((long long)b * f.n_h + (long long)kvh * a.group) * f.T;  // slab's first query row
     const int n_first = f.window > 0 ? min(f.n_first, len) : 0;
     const int head_span = (n_first + BN - 1) / BN * BN;
     int body = 0;

@@ -559,3 +559,13 @@ def test_no_rows_and_no_keys():
                             torch.zeros(2, dtype=torch.int32, device=DEV))
     q, k, v = binding.fmha_qk_norm_rope(torch.empty(2, 0, 192, dtype=torch.bfloat16, device=DEV), None, None, 1, 1)
     assert q.shape == (2, 1, 0, 64)
+
+
+@pytest.mark.parametrize("b", [2, 7, 32, 33])
+def test_kv4_order_of_lengths(b, kernel):
+    """Sequences in rising, falling and mixed order of length, with equal ones and empty ones; more of them than lanes."""
+    rising = [3 * i for i in range(b)]
+    mixed = [(37 * i) % 5 * 20 for i in range(b)]
+    for lens in (rising, rising[::-1], mixed, [50] * b, [0] * b):
+        check_kv4(64, 4, 2, 3, 112, lens, causal=True, window=40, n_first=2)
+    check_kv4(128, 4, 1, 2, 512, [(131 * i) % 513 for i in range(b)], kv_chunk=128)
