@@ -1182,7 +1182,7 @@ extern "C" int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_sc
     cudaError_t e = f.tc ? launch_kv4_tc(f, stream) : launch_kv4_fwd(f, stream);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit attention kernel launch");
     if (f.n_splits > 1) {
-        e = launch_merge(f.o_part, f.lse_part, f.range_part, f.n_splits, rows, hd, f16, o, lse, stream, sink, T, n_h);
+        e = launch_merge(f.o_part, f.lse_part, f.range_part, f.n_splits, rows, hd, f16, o, lse, stream, sink, T, n_h, true);
         if (e != cudaSuccess) return cuda_fail(e, "merge kernel launch");
     }
     return FMHA_OK;

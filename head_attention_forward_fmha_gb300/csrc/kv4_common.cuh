@@ -11,11 +11,12 @@ constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry
 // Output of a block whose rows attend no key of their chunk, by all of its
 // threads: rows first .. first + n - 1, columns col0 .. col0 + ncol - 1: O = 0 and
 // LSE = -inf, or the row's sink in a final output (sink_head0 >= 0: the query
-// head of row_in_slab 0; the first row is row r0 of its slab).
+// head of row_in_slab 0; the first row is row r0 of its slab).  Of a partial's O
+// the merge reads nothing then, unless there are few chunks.
 __device__ __forceinline__ void write_empty_rows(const Kv4Fwd& f, long long rows_total, long long first, int n, int split,
                                                  int col0, int ncol, bool with_lse, int sink_head0, int r0) {
     const int threads = blockDim.x, per_row = ncol / 8;
-    for (int i = threadIdx.x; i < n * per_row; i += threads) {
+    for (int i = threadIdx.x; f.n_splits <= kMergeReadsAll && i < n * per_row; i += threads) {
         const int r = i / per_row, c = col0 + (i - r * per_row) * 8;
         if (!FMHA_IN_BOUNDS(first + r >= 0 && first + r < rows_total && c + 8 <= f.hd && split < f.n_splits, kSiteKv4Out,
                             f.status))
@@ -25,12 +26,13 @@ __device__ __forceinline__ void write_empty_rows(const Kv4Fwd& f, long long rows
         } else if (f.range_part) {
             *reinterpret_cast<uint4*>(static_cast<__half*>(f.o_part) + (split * rows_total + first + r) * f.hd + c) =
                 make_uint4(0u, 0u, 0u, 0u);
-            if (c == col0) f.range_part[(split * rows_total + first + r) * 2 + c / 256] = 1.f;
         } else {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(f.o_part) + (split * rows_total + first + r) * f.hd + c);
             dst[0] = dst[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
+    if (f.n_splits > 1 && f.range_part)
+        for (int r = threadIdx.x; r < n; r += threads) f.range_part[(split * rows_total + first + r) * 2 + col0 / 256] = 1.f;
     if (!with_lse) return;
     for (int r = threadIdx.x; r < n; r += threads) {
         if (f.n_splits == 1)

@@ -19,7 +19,7 @@
 //
 // Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 83 us, 823
 // TFLOP/s; over a window of 2048 with ragged lengths 34 us; 128 heads of 512 on one
-// KV head, 16 ragged sequences up to 4096 keys 33 us.  A clock trace says what bounds
+// KV head, 16 ragged sequences up to 4096 keys 31 us.  A clock trace says what bounds
 // it.  At hd 128 a tile of 128 keys took ~2200 clocks, of which the softmax warps 2075
 // (the exponentials alone 512), with MMAs and conversion beside them (before its
 // scores were read 64 at a time); at hd 512 a
@@ -29,7 +29,7 @@
 // by addition among them (with 227 KB of shared memory there is hardly an L1, and
 // each reload is a trip to L2), and conversion in coalesced pieces (75 -> 49 us);
 // MMAs issued by an elected lane of a converged warp (49 -> 41); partials in fp16
-// (39 -> 33).  Small loops in the softmax (unrolled over the tile, the 4 x 4096 keys
+// (39 -> 33), of empty chunks none (33 -> 31).  Small loops in the softmax (unrolled over the tile, the 4 x 4096 keys
 // took 156 us instead of 94).  Two threads per row (17 warps, 96 registers) were
 // slower: 113 us instead of 95 there, at hd 512 64 instead of 41.
 #include <climits>

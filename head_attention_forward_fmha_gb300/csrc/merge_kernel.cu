@@ -86,7 +86,11 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&acc)
     }
 }
 
-template <int HD, typename PT, bool SINK>
+// SKIP (more than kMergeReadsAll chunks): the O of a chunk with LSE = -inf is not
+// read, and need not be written; with ragged lengths half the chunks may be such
+// (16 sequences in 8 chunks at hd 512: 33.4 -> 31.1 us).  An instantiation of its own:
+// as a test at run time it cost the MQA decode step of four chunks 11.6 -> 11.8 us.
+template <int HD, typename PT, bool SINK, bool SKIP>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     merge_lse_kernel(const PT* __restrict__ o_parts, const float* __restrict__ lse_parts,
                      const float* __restrict__ range_parts, int n_splits, long long rows,
@@ -111,8 +115,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     // Up to kFast chunks: every load (LSEs, range factors, the partial
     // slices) is issued before any arithmetic, so the warp waits for one
     // memory round trip instead of two.
-    constexpr int kFast = 4;
-    if (n_splits <= kFast) {
+    constexpr int kFast = kMergeReadsAll;
+    if (!SKIP && n_splits <= kFast) {
         const float lv = (lane < n_splits) ? __ldg(lse_parts + (long long)lane * rows + row) : -INFINITY;
         float rv = 1.f;
         if constexpr (sizeof(PT) == 2) {
@@ -183,6 +187,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                 if (mine < n_splits && FMHA_IN_BOUNDS(col / 256 < 2, kSiteMergeRange, status))
                     w_mine *= __ldg(range_parts + ((long long)mine * rows + row) * 2 + col / 256);
             }
+            unsigned live = 0xffffffffu;
+            if constexpr (SKIP)
+                live = __ballot_sync(0xffffffffu, mine < n_splits && __ldg(lse_parts + (long long)mine * rows + row) != -INFINITY);
             float wsum = w_den;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, s);
@@ -192,6 +199,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
             int i = 0;
             for (; i + 4 <= cnt; i += 4) {
                 float v0[V], v1[V], v2[V], v3[V];
+                const unsigned four = (live >> i) & 15u;
+                if (SKIP && four == 0u) continue;
+                if (SKIP && four != 15u) {
+                    for (int k = i; k < i + 4; ++k) {
+                        if (!((live >> k) & 1u)) continue;
+                        load_vec<V>(o_parts + ((long long)(base + k) * rows + row) * HD + col, v0);
+                        const float w = __shfl_sync(0xffffffffu, w_mine, k);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[e] += w * v0[e];
+                    }
+                    continue;
+                }
                 load_vec<V>(o_parts + ((long long)(base + i) * rows + row) * HD + col, v0);
                 load_vec<V>(o_parts + ((long long)(base + i + 1) * rows + row) * HD + col, v1);
                 load_vec<V>(o_parts + ((long long)(base + i + 2) * rows + row) * HD + col, v2);
@@ -204,6 +223,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                 for (int e = 0; e < V; ++e) acc[e] += w0 * v0[e] + w1 * v1[e] + w2 * v2[e] + w3 * v3[e];
             }
             for (; i < cnt; ++i) {
+                if (SKIP && !((live >> i) & 1u)) continue;
                 float v0[V];
                 load_vec<V>(o_parts + ((long long)(base + i) * rows + row) * HD + col, v0);
                 const float w0 = __shfl_sync(0xffffffffu, w_mine, i);
@@ -221,7 +241,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 template <int HD, typename PT>
 cudaError_t launch_t(const PT* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                      long long rows, void* o, float* lse, cudaStream_t stream, const float* sink, int T, int n_h,
-                     unsigned* status) {
+                     bool skip_empty, unsigned* status) {
     const long long tasks = rows * MCfg<HD, PT>::NSLICE;
     const long long blocks = (tasks + kMergeWarps - 1) / kMergeWarps;
     cudaLaunchConfig_t cfg = {};
@@ -232,24 +252,24 @@ cudaError_t launch_t(const PT* o_parts, const float* lse_parts, const float* ran
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (sink)
-        return cudaLaunchKernelEx(&cfg, merge_lse_kernel<HD, PT, true>, o_parts, lse_parts, range_parts, n_splits,
-                                  rows, static_cast<__nv_bfloat16*>(o), lse, sink, T, n_h, status);
-    return cudaLaunchKernelEx(&cfg, merge_lse_kernel<HD, PT, false>, o_parts, lse_parts, range_parts, n_splits, rows,
+    const bool skip = skip_empty && n_splits > kMergeReadsAll;
+    auto kern = sink ? (skip ? merge_lse_kernel<HD, PT, true, true> : merge_lse_kernel<HD, PT, true, false>)
+                     : (skip ? merge_lse_kernel<HD, PT, false, true> : merge_lse_kernel<HD, PT, false, false>);
+    return cudaLaunchKernelEx(&cfg, kern, o_parts, lse_parts, range_parts, n_splits, rows,
                               static_cast<__nv_bfloat16*>(o), lse, sink, T, n_h, status);
 }
 
 template <int HD>
 cudaError_t launch_hd(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                       long long rows, bool f16, void* o, float* lse, cudaStream_t stream, const float* sink, int T,
-                      int n_h, unsigned* status) {
+                      int n_h, bool skip_empty, unsigned* status) {
     if (f16) {
         if (HD != 512 || range_parts == nullptr) return cudaErrorInvalidValue;
         return launch_t<HD>(static_cast<const __half*>(o_parts), lse_parts, range_parts, n_splits, rows, o, lse,
-                            stream, sink, T, n_h, status);
+                            stream, sink, T, n_h, skip_empty, status);
     }
     return launch_t<HD>(static_cast<const float*>(o_parts), lse_parts, nullptr, n_splits, rows, o, lse, stream,
-                        sink, T, n_h, status);
+                        sink, T, n_h, skip_empty, status);
 }
 
 // The merge with an NVFP4 final output: one thread per (row, 16-column
@@ -345,16 +365,17 @@ cudaError_t launch_merge_nvfp4(const void* o_parts, const float* lse_parts, cons
 
 cudaError_t launch_merge(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                          long long rows, int hd, bool f16, void* o, float* lse, cudaStream_t stream,
-                         const float* sink, int T, int n_h) {
+                         const float* sink, int T, int n_h,
+                         bool skip_empty) {
     if (rows <= 0) return cudaSuccess;
     if (sink && (T < 1 || n_h < 1)) return cudaErrorInvalidValue;
     unsigned* status = device_status_word();
     if (!status) return cudaErrorInvalidDevicePointer;
     switch (hd) {
-        case 64: return launch_hd<64>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, status);
-        case 128: return launch_hd<128>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, status);
-        case 256: return launch_hd<256>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, status);
-        case 512: return launch_hd<512>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, status);
+        case 64: return launch_hd<64>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
+        case 128: return launch_hd<128>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
+        case 256: return launch_hd<256>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
+        case 512: return launch_hd<512>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
         default: return cudaErrorInvalidValue;
     }
 }

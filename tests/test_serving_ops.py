@@ -569,3 +569,22 @@ def test_kv4_order_of_lengths(b, kernel):
     for lens in (rising, rising[::-1], mixed, [50] * b, [0] * b):
         check_kv4(64, 4, 2, 3, 112, lens, causal=True, window=40, n_first=2)
     check_kv4(128, 4, 1, 2, 512, [(131 * i) % 513 for i in range(b)], kv_chunk=128)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+@pytest.mark.parametrize("kv_chunk", [128, 256])
+def test_kv4_chunks_without_keys_are_not_read(hd, kv_chunk, kernel):
+    """8 or 4 chunks, most of them empty, over a workspace of NaN: empty chunks reach no result, whatever lies there."""
+    lens = [0, 1, 130, 300, 1024, 640]
+    want = check_kv4(hd, 4, 2, 2, 1024, lens, sink=True, kv_chunk=kv_chunk, causal=True)
+    r = gen(hd)
+    cache = filled(r, len(lens), 2, 1024, hd)
+    spoil(cache, lens)
+    q = normal(r, len(lens), 4, 2, hd)
+    sink = torch.randn(4, generator=r, device=DEV) * 2
+    n, _ = binding.fmha_fwd_kv4_plan(len(lens), 4, 2, 2, 1024, hd, causal=True, kv_chunk=kv_chunk)
+    assert n == 1024 // kv_chunk
+    ws = torch.full((binding.fmha_workspace_bytes(len(lens), 4, 2, hd, n),), 0xFF, dtype=torch.uint8, device=DEV)
+    got = binding.fmha_fwd_kv4(q, *cache, torch.tensor(lens, dtype=torch.int32, device=DEV), v_global=2.0, sink=sink, kv_chunk=kv_chunk,
+                               causal=True, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
