@@ -14,8 +14,10 @@
 // which is the correctly rounded quotient (Markstein 1990) as long as nothing
 // overflows or underflows, and the roundings to E4M3 and E2M1 are the
 // hardware's conversions, which go to nearest, ties to even, and saturate, as
-// the format asks.  A block with a NaN, an infinity or a scale g s outside
-// [2^-90, 2^90] takes the quantiser of nvfp4.cuh, and all of them give its codes.
+// the format asks.  A block with a NaN, an infinity, a scale g s outside
+// [2^-90, 2^90] or a value above 2^30 g s (its scale saturates then, and x r might
+// overflow: the correction makes that a NaN, whose conversion has no sign) takes the
+// quantiser of nvfp4.cuh, and all of them give its codes.
 //
 // Measured on GB300: four prompts of 4095 tokens, 8 heads of 128, with the values
 // (153 MB) 30.4 us, 5.0 TB/s; with IEEE divisions and comparisons 68 us, with
@@ -66,7 +68,7 @@ __device__ __forceinline__ void quantise8(const uint4& u, const __nv_bfloat16* b
     const float gs = __fmul_rn(g, s);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     codes = 0u;
-    if (top < 0x7F80u && (s == 0.f || (gs >= 0x1p-90f && gs <= 0x1p90f))) {
+    if (top < 0x7F80u && (s == 0.f || (gs >= 0x1p-90f && gs <= 0x1p90f && __uint_as_float(top << 16) <= gs * 0x1p30f))) {
         if (s > 0.f) {
             const float r = __frcp_rn(gs);
             const uint64_t r2 = f32x2(r, r), n2 = f32x2(-gs, -gs);

@@ -17,3 +17,11 @@ def test_serving_suite_passes_with_index_checks():
     r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_serving_ops.py", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"],
                        env=env, cwd=ROOT, capture_output=True, text=True, timeout=1200)
     assert r.returncode == 0, "\n".join((r.stdout + r.stderr).splitlines()[-30:])
+
+
+@pytest.mark.gpu
+def test_serving_edges_pass_with_index_checks():
+    env = dict(os.environ, FMHA_GB300_LIB=build.build(checked=True))
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_serving_edges.py", "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider"],
+                       env=env, cwd=ROOT, capture_output=True, text=True, timeout=1200)
+    assert r.returncode == 0, "\n".join((r.stdout + r.stderr).splitlines()[-30:])
