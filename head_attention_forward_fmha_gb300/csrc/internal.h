@@ -123,11 +123,12 @@ inline cudaLaunchAttribute programmatic_launch_attr() {
 // ---- split-KV merge (merge_kernel.cu) -------------------------------------
 // sink: [n_h] attention-sink logits added once to the merged denominator
 // (NULL: none); row r belongs to head (r / T) % n_h.
-// skip_empty: of more than kMergeReadsAll chunks, the O of those with LSE = -inf is not read.
+// kv4: the 4-bit attention's partials: of more than kMergeReadsAll chunks, the O of those with
+// LSE = -inf is not read; a chunk with LSE = NaN makes O and LSE of its row NaN.
 constexpr int kMergeReadsAll = 4;
 cudaError_t launch_merge(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                          long long rows, int hd, bool f16_parts, void* o, float* lse, cudaStream_t stream,
-                         const float* sink = nullptr, int T = 1, int n_h = 1, bool skip_empty = false);
+                         const float* sink = nullptr, int T = 1, int n_h = 1, bool kv4 = false);
 // The merge writing NVFP4 O (fp4.codes / fp4.scales) instead of bf16 O; no sink.
 cudaError_t launch_merge_nvfp4(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                                long long rows, int hd, bool f16_parts, Fp4Out fp4, float* lse, cudaStream_t stream);

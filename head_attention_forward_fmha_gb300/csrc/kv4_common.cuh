@@ -8,6 +8,14 @@ namespace fmha {
 
 constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry
 
+// End of a row: finish_row, but where a NaN score has made the sum NaN, so are O and
+// LSE.  (finish_row gives such a row LSE = -inf, which marks an empty chunk: the merge
+// would leave it out, and whether the NaN shows would depend on the number of chunks.)
+__device__ __forceinline__ void finish_row_nan(float m, float l, float sink_l2, float& inv, float& lse) {
+    finish_row(m, l, sink_l2, inv, lse);
+    if (l != l) inv = lse = l;
+}
+
 // Output of a block whose rows attend no key of their chunk, by all of its
 // threads: rows first .. first + n - 1, columns col0 .. col0 + ncol - 1: O = 0 and
 // LSE = -inf, or the row's sink in a final output (sink_head0 >= 0: the query

@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
             }
         }
         float inv, lse;
-        finish_row(M - kPBias, L,
+        finish_row_nan(M - kPBias, L,
                    f.sink && f.n_splits == 1 ? sink_log2_of(f.sink, kvh * a.group + (r_begin + r) / f.T, f.n_h, f.status)
                                              : -INFINITY,
                    inv, lse);

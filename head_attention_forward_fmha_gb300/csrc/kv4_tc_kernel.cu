@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld below is warp-collective
         tc_fence_after();
         float inv, lse;
-        finish_row(m_ref - kPBias, l,
+        finish_row_nan(m_ref - kPBias, l,
                    (SINK && valid) ? sink_log2_of(f.sink, kvh * a.group + grow / f.T, f.n_h, f.status) : -INFINITY, inv, lse);
         inv *= f.v_global;
         const long long gr = row0 + grow;

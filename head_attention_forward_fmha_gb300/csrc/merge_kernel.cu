@@ -86,11 +86,29 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&acc)
     }
 }
 
-// SKIP (more than kMergeReadsAll chunks): the O of a chunk with LSE = -inf is not
-// read, and need not be written; with ragged lengths half the chunks may be such
-// (16 sequences in 8 chunks at hd 512: 33.4 -> 31.1 us).  An instantiation of its own:
-// as a test at run time it cost the MQA decode step of four chunks 11.6 -> 11.8 us.
-template <int HD, typename PT, bool SINK, bool SKIP>
+// The merge of the 4-bit attention's partials.  Of more than kMergeReadsAll chunks, the O
+// of those with LSE = -inf is not read, and need not be written; with ragged lengths
+// half the chunks may be such (16 sequences in 8 chunks at hd 512: 33.4 -> 31.1 us).
+// A chunk with LSE = NaN had a NaN score: O and LSE of the row are NaN.  Instantiations of
+// their own: as a test at run time the first cost the MQA decode step of four chunks
+// 11.6 -> 11.8 us.
+enum MergeKind { kMergePlain, kMergeKv4Few, kMergeKv4Many };
+
+// 1 / den, 0 without any weight; NaN stays NaN for the 4-bit attention.
+template <int KIND>
+__device__ __forceinline__ float merge_inv(float den) {
+    if constexpr (KIND != kMergePlain)
+        if (den != den) return den;
+    return (den > 0.f) ? 1.f / den : 0.f;
+}
+template <int KIND>
+__device__ __forceinline__ float merge_lse(float m, float den) {
+    if constexpr (KIND != kMergePlain)
+        if (den != den) return den;
+    return (den > 0.f) ? m + log2f(den) * 0.693147180559945309f : -INFINITY;
+}
+
+template <int HD, typename PT, bool SINK, int KIND>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     merge_lse_kernel(const PT* __restrict__ o_parts, const float* __restrict__ lse_parts,
                      const float* __restrict__ range_parts, int n_splits, long long rows,
@@ -110,13 +128,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         if (!__all_sync(0xffffffffu, in)) return;
     }
     constexpr float kLog2e = 1.4426950408889634f;
-    constexpr float kLn2 = 0.693147180559945309f;
 
     // Up to kFast chunks: every load (LSEs, range factors, the partial
     // slices) is issued before any arithmetic, so the warp waits for one
     // memory round trip instead of two.
     constexpr int kFast = kMergeReadsAll;
-    if (!SKIP && n_splits <= kFast) {
+    if (KIND == kMergeKv4Few || (KIND == kMergePlain && n_splits <= kFast)) {
         const float lv = (lane < n_splits) ? __ldg(lse_parts + (long long)lane * rows + row) : -INFINITY;
         float rv = 1.f;
         if constexpr (sizeof(PT) == 2) {
@@ -156,14 +173,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += wi * pv[i][e];
         }
-        const float inv = (den > 0.f) ? 1.f / den : 0.f;
-        store_row<V>(o + row * HD + col, acc, inv);
-        if (lane == 0 && col == 0) lse[row] = (den > 0.f) ? m + log2f(den) * kLn2 : -INFINITY;
+        if constexpr (KIND != kMergePlain)
+            if (__any_sync(0xffffffffu, lv != lv)) den = NAN;
+        store_row<V>(o + row * HD + col, acc, merge_inv<KIND>(den));
+        if (lane == 0 && col == 0) lse[row] = merge_lse<KIND>(m, den);
         return;
     }
 
+    constexpr bool SKIP = KIND == kMergeKv4Many;
     float mx = -INFINITY;
-    for (int i = lane; i < n_splits; i += 32) mx = fmaxf(mx, __ldg(lse_parts + (long long)i * rows + row));
+    bool nan = false;
+    for (int i = lane; i < n_splits; i += 32) {
+        const float lv = __ldg(lse_parts + (long long)i * rows + row);
+        mx = fmaxf(mx, lv);
+        if constexpr (SKIP) nan |= lv != lv;
+    }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     // attention sink: one more term exp(sigma) of the denominator (no value)
@@ -233,15 +257,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         }
     }
     if (SINK && sg != -INFINITY) den += exp2f((sg - mx) * kLog2e);
-    const float inv = (den > 0.f) ? 1.f / den : 0.f;
-    store_row<V>(o + row * HD + col, acc, inv);
-    if (lane == 0 && col == 0) lse[row] = (den > 0.f) ? mx + log2f(den) * kLn2 : -INFINITY;
+    if constexpr (SKIP)
+        if (__any_sync(0xffffffffu, nan)) den = NAN;
+    store_row<V>(o + row * HD + col, acc, merge_inv<KIND>(den));
+    if (lane == 0 && col == 0) lse[row] = merge_lse<KIND>(mx, den);
 }
 
 template <int HD, typename PT>
 cudaError_t launch_t(const PT* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                      long long rows, void* o, float* lse, cudaStream_t stream, const float* sink, int T, int n_h,
-                     bool skip_empty, unsigned* status) {
+                     bool kv4, unsigned* status) {
     const long long tasks = rows * MCfg<HD, PT>::NSLICE;
     const long long blocks = (tasks + kMergeWarps - 1) / kMergeWarps;
     cudaLaunchConfig_t cfg = {};
@@ -252,9 +277,10 @@ cudaError_t launch_t(const PT* o_parts, const float* lse_parts, const float* ran
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool skip = skip_empty && n_splits > kMergeReadsAll;
-    auto kern = sink ? (skip ? merge_lse_kernel<HD, PT, true, true> : merge_lse_kernel<HD, PT, true, false>)
-                     : (skip ? merge_lse_kernel<HD, PT, false, true> : merge_lse_kernel<HD, PT, false, false>);
+    auto kern = !kv4  ? (sink ? merge_lse_kernel<HD, PT, true, kMergePlain> : merge_lse_kernel<HD, PT, false, kMergePlain>)
+                : n_splits <= kMergeReadsAll
+                    ? (sink ? merge_lse_kernel<HD, PT, true, kMergeKv4Few> : merge_lse_kernel<HD, PT, false, kMergeKv4Few>)
+                    : (sink ? merge_lse_kernel<HD, PT, true, kMergeKv4Many> : merge_lse_kernel<HD, PT, false, kMergeKv4Many>);
     return cudaLaunchKernelEx(&cfg, kern, o_parts, lse_parts, range_parts, n_splits, rows,
                               static_cast<__nv_bfloat16*>(o), lse, sink, T, n_h, status);
 }
@@ -262,14 +288,14 @@ cudaError_t launch_t(const PT* o_parts, const float* lse_parts, const float* ran
 template <int HD>
 cudaError_t launch_hd(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                       long long rows, bool f16, void* o, float* lse, cudaStream_t stream, const float* sink, int T,
-                      int n_h, bool skip_empty, unsigned* status) {
+                      int n_h, bool kv4, unsigned* status) {
     if (f16) {
         if (HD != 512 || range_parts == nullptr) return cudaErrorInvalidValue;
         return launch_t<HD>(static_cast<const __half*>(o_parts), lse_parts, range_parts, n_splits, rows, o, lse,
-                            stream, sink, T, n_h, skip_empty, status);
+                            stream, sink, T, n_h, kv4, status);
     }
     return launch_t<HD>(static_cast<const float*>(o_parts), lse_parts, nullptr, n_splits, rows, o, lse, stream,
-                        sink, T, n_h, skip_empty, status);
+                        sink, T, n_h, kv4, status);
 }
 
 // The merge with an NVFP4 final output: one thread per (row, 16-column
@@ -366,16 +392,16 @@ cudaError_t launch_merge_nvfp4(const void* o_parts, const float* lse_parts, cons
 cudaError_t launch_merge(const void* o_parts, const float* lse_parts, const float* range_parts, int n_splits,
                          long long rows, int hd, bool f16, void* o, float* lse, cudaStream_t stream,
                          const float* sink, int T, int n_h,
-                         bool skip_empty) {
+                         bool kv4) {
     if (rows <= 0) return cudaSuccess;
     if (sink && (T < 1 || n_h < 1)) return cudaErrorInvalidValue;
     unsigned* status = device_status_word();
     if (!status) return cudaErrorInvalidDevicePointer;
     switch (hd) {
-        case 64: return launch_hd<64>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
-        case 128: return launch_hd<128>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
-        case 256: return launch_hd<256>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
-        case 512: return launch_hd<512>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, skip_empty, status);
+        case 64: return launch_hd<64>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, kv4, status);
+        case 128: return launch_hd<128>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, kv4, status);
+        case 256: return launch_hd<256>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, kv4, status);
+        case 512: return launch_hd<512>(o_parts, lse_parts, range_parts, n_splits, rows, f16, o, lse, stream, sink, T, n_h, kv4, status);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -446,6 +446,8 @@ int fmha_fwd_kv4_plan(int batch, int n_h, int n_kv_h, int T, int s_k, int hd, in
  *   NULL: s_k each.  s_k <= cap bounds them on the host and shapes the launch.
  *   Rows of the cache from a sequence's length on, and keys that no row attends,
  *   reach no result; V's scales have to be numbers at keys that some row attends.
+ *   A NaN score of an attended key (a NaN in the query row or in a K scale) makes
+ *   O and LSE of its row NaN, whatever the number of chunks.
  * Query row t of a sequence with len keys sits at position len - T + t; with
  *   causal, a row at a negative position attends nothing (O = 0, LSE = -inf, or
  *   the sink's).

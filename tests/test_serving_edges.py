@@ -34,3 +34,35 @@ def test_append_of_values_far_above_saturation(hd, g):
         values = ref.dequantise(c, s, 1.0).float() * torch.tensor(g, dtype=torch.float32, device=DEV)
         assert torch.equal(o, values.to(torch.bfloat16))
     assert (cache[0][0, 1, 0] == 0xFF).all() and (cache[0][0, 1, 1] == 0x77).all()
+
+
+# ------------------------------------------------------------------ NaN in attended places
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+@pytest.mark.parametrize("kv_chunk", [1024, 512, 256, 128])
+@pytest.mark.parametrize("sink", [False, True])
+def test_kv4_nan_scores_show_whatever_the_chunks(hd, kv_chunk, sink, kernel):
+    """A NaN in a query row, or in the scale of an attended key: NaN in O and in LSE of the rows that meet it, and only
+    there, with 1, 2, 4 and 8 chunks.  Sequences of one chunk beside it leave the others empty."""
+    r = ops.gen(hd)
+    lens, cap, n_h, n_kv, T = [1024, 700, 100, 0], 1024, 4, 2, 2
+    cache = ops.filled(r, len(lens), n_kv, cap, hd)
+    q = ops.normal(r, len(lens), n_h, T, hd)
+    sg = torch.randn(n_h, generator=r, device=DEV) * 2 if sink else None
+    want = ref.attend(q, ref.dequantise(cache[0], cache[1], 1.0), ref.dequantise(cache[2], cache[3], 2.0), lens, hd ** -0.5, causal=True, sink=sg)
+    ops.spoil(cache, lens)
+    bad = torch.zeros((len(lens), n_h, T), dtype=torch.bool, device=DEV)
+    q[1, 2, 1, 5] = float("nan")
+    q[2, 1, 0] = float("nan")
+    cache[1][0, 1, 300, 2] = 0x7F
+    bad[1, 2, 1] = bad[2, 1, 0] = bad[0, 2:] = True
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    n, _ = binding.fmha_fwd_kv4_plan(len(lens), n_h, n_kv, T, cap, hd, causal=True, kv_chunk=kv_chunk)
+    assert n == cap // kv_chunk
+    o, lse = binding.fmha_fwd_kv4(q, *cache, ln, v_global=2.0, causal=True, sink=sg, kv_chunk=kv_chunk)
+    assert torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    keep = ~bad
+    (ro, rl, o_tol, l_tol) = want
+    assert ((o.double() - ro).abs() <= o_tol)[keep].all()
+    fin = keep & torch.isfinite(rl)
+    assert torch.equal(torch.isinf(lse[keep]), torch.isinf(rl[keep])) and ((lse.double() - rl).abs() <= l_tol)[fin].all()
