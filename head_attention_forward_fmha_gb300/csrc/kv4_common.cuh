@@ -1,12 +1,42 @@
 // kv4_common.cuh -- pieces shared by the two kernels of the attention over a
 // 4-bit cache (kv4_kernel.cu, kv4_tc_kernel.cu).
 #pragma once
+#include <cmath>
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace fmha {
 
 constexpr float kPBias = 6.f;  // log2 of the factor that P and its sum carry
+
+// |scale| * k_global * log2(e) as mant * 2^expo, mant in [1, 2), and the scale's sign
+// (0 for a product of zero: mant 1, expo 0).  Apart because a row's factor, this times
+// the power of two that undoes Q's scaling, may pass fp32's range on either side.
+struct ScoreScale {
+    float mant, sign;
+    int expo;
+};
+
+inline ScoreScale score_scale(const Kv4Fwd& f) {
+    const double s = (double)f.scale * f.k_global * 1.4426950408889634;
+    ScoreScale r{1.f, 0.f, 0};
+    if (s == 0) return r;
+    r.sign = s > 0 ? 1.f : -1.f;
+    r.mant = 2.f * (float)std::frexp(std::fabs(s), &r.expo);  // 2 if it was rounded up to 1
+    r.expo -= 1;
+    if (r.mant >= 2.f) {
+        r.mant = 1.f;
+        r.expo += 1;
+    }
+    return r;
+}
+
+// The row's factor mant * 2^e, e kept within fp32's normal numbers: neither 0, which would turn
+// the masked scores' -inf into NaN, nor infinite, which would turn scores of 0 into NaN.
+// Below 2^-126 it makes all weights equal as it should (products are below 2^36).
+__device__ __forceinline__ float score_factor(float mant, int e) {
+    return __uint_as_float(__float_as_uint(mant) + ((uint32_t)min(max(e, -126), 127) << 23));
+}
 
 // End of a row: finish_row, but where a NaN score has made the sum NaN, so are O and
 // LSE.  (finish_row gives such a row LSE = -inf, which marks an empty chunk: the merge

@@ -88,8 +88,7 @@ struct K4Cfg {
 struct K4Args {
     Kv4Fwd f;
     int group, R;
-    float sl2;       // |scale| * k_global * log2(e), 1 for a scale of zero
-    float sl2_sign;  // of the scale: -1, 0 or 1
+    ScoreScale sl2;
     long long rows_total;
 };
 
@@ -296,8 +295,8 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
             const int e = (int)(mx >> 7);
             const int k = (e > 0 && e < 255) ? min(max(14 - (e - 127), -120), 120) : 0;
             // the sign of the scale goes into Q, so that a larger product is a larger score
-            const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2_sign;
-            fac_g[nb] = __uint_as_float((uint32_t)(127 - k) << 23);
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2.sign;
+            fac_g[nb] = score_factor(a.sl2.mant, a.sl2.expo - k);
 #pragma unroll
             for (int i = 0; i < C::QSTEPS; ++i) {
                 const uint2 v = make_uint2(pack_f16x2(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up),
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) qs[nb][i] = __shfl_sync(0xffffffffu, fac_g[nb], (2 * t4 + i) * 4) * a.sl2;
+            for (int i = 0; i < 2; ++i) qs[nb][i] = __shfl_sync(0xffffffffu, fac_g[nb], (2 * t4 + i) * 4);
         if constexpr (!C::QREG) __syncthreads();
     }
 
@@ -665,9 +664,7 @@ cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
     a.f = f;
     a.group = f.n_h / f.n_kv_h;
     a.R = a.group * f.T;
-    const double sl2 = (double)f.scale * f.k_global * 1.4426950408889634;
-    a.sl2_sign = sl2 > 0 ? 1.f : sl2 < 0 ? -1.f : 0.f;
-    a.sl2 = sl2 != 0 ? (float)(sl2 < 0 ? -sl2 : sl2) : 1.f;
+    a.sl2 = score_scale(f);
     a.rows_total = (long long)f.batch * f.n_h * f.T;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.R + C::RT - 1) / C::RT, f.n_splits, f.batch * f.n_kv_h);

@@ -75,7 +75,7 @@ struct K4TCfg {
 struct K4TArgs {
     Kv4Fwd f;
     int group, R;
-    float sl2, sl2_sign;  // as in kv4_kernel.cu
+    ScoreScale sl2;
     long long rows_total;
 };
 
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 for (int m = LPR / 2; m > 0; m >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, m));
                 const int e = (int)(mx >> 7);
                 const int k = (e > 0 && e < 255) ? min(max(14 - (e - 127), -120), 120) : 0;
-                const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2_sign;
+                const float up = __uint_as_float((uint32_t)(127 + k) << 23) * a.sl2.sign;
                 if (row >= BM) continue;
-                if (lc == 0) row_fac[row] = __uint_as_float((uint32_t)(127 - k) << 23) * a.sl2;
+                if (lc == 0) row_fac[row] = score_factor(a.sl2.mant, a.sl2.expo - k);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const int col = v * 256 + lc * 8;
@@ -704,9 +704,7 @@ cudaError_t launch_t(const Kv4Fwd& f, cudaStream_t stream) {
     a.f = f;
     a.group = f.n_h / f.n_kv_h;
     a.R = a.group * f.T;
-    const double sl2 = (double)f.scale * f.k_global * 1.4426950408889634;
-    a.sl2_sign = sl2 > 0 ? 1.f : sl2 < 0 ? -1.f : 0.f;
-    a.sl2 = sl2 != 0 ? (float)(sl2 < 0 ? -sl2 : sl2) : 1.f;
+    a.sl2 = score_scale(f);
     a.rows_total = (long long)f.batch * f.n_h * f.T;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.R + C::BM - 1) / C::BM * C::PARTS, f.n_splits, f.batch * f.n_kv_h);

@@ -66,3 +66,29 @@ def test_kv4_nan_scores_show_whatever_the_chunks(hd, kv_chunk, sink, kernel):
     assert ((o.double() - ro).abs() <= o_tol)[keep].all()
     fin = keep & torch.isfinite(rl)
     assert torch.equal(torch.isinf(lse[keep]), torch.isinf(rl[keep])) and ((lse.double() - rl).abs() <= l_tol)[fin].all()
+
+
+# ------------------------------------------------------------------ factors of the scores at the ends of fp32
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+@pytest.mark.parametrize("kv_chunk", [0, 64])
+def test_kv4_score_factors_past_the_range_of_fp32(hd, kv_chunk, kernel):
+    """Rows so small that their factor underflows (every key weighs the same then), masked keys beside them; and products of
+    scale and global scale below fp32's smallest number."""
+    lens = [0, 7, 200, 256]
+    ops.check_kv4(hd, 8, 2, 2, 256, lens, g=2.0 ** -40, q_mult=2.0 ** -100, causal=True, kv_chunk=kv_chunk)
+    ops.check_kv4(hd, 8, 2, 2, 256, lens, g=2.0 ** -40, q_mult=2.0 ** -100, window=50, n_first=3, kv_chunk=kv_chunk)
+    ops.check_kv4(hd, 8, 2, 2, 256, lens, g=2.0 ** -40, scale=2.0 ** -130, causal=True, sink=True, kv_chunk=kv_chunk)
+    ops.check_kv4(hd, 8, 2, 2, 256, lens, g=2.0 ** -40, scale=2.0 ** -115, q_mult=2.0 ** 110, causal=True, kv_chunk=kv_chunk)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+def test_kv4_keys_of_zero_under_a_factor_past_fp32(hd, kernel):
+    """K is zero and every score 0, however large Q, scale and global scale are: the mean of V."""
+    r = ops.gen(hd)
+    lens = [5, 256, 130]
+    cache = ops.filled(r, 3, 2, 256, hd)
+    cache[0].zero_()
+    q = ops.normal(r, 3, 8, 2, hd) * 2.0 ** 110
+    got = binding.fmha_fwd_kv4(q, *cache, torch.tensor(lens, dtype=torch.int32, device=DEV), k_global=2.0 ** 60, v_global=2.0, scale=2.0 ** 20)
+    want = ref.attend(q, torch.zeros(3, 2, 256, hd, device=DEV), ref.dequantise(cache[2], cache[3], 2.0), lens, 1.0)
+    ref.assert_attention(got, want)
