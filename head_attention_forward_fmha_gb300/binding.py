@@ -122,6 +122,29 @@ def _stream(stream):
     return int(stream)
 
 
+def _stream_object(stream, dev):
+    """The torch stream of a call's `stream` argument, a Stream or a handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)  # ExternalStream(0) would be one of torch's own streams
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor that a call on `stream` (None: the current one) writes.
+
+    On another stream it takes that stream's memory: what tensors of the current stream have left may still be in use by
+    work queued there.  It counts as used by the current stream too, where the caller may read it and then drop it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    side, here = _stream_object(stream, dev), torch.cuda.current_stream(dev)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if side.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def _bf16(t, name):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
         raise TypeError("%s must be a contiguous CUDA bf16 tensor" % name)
@@ -168,11 +191,11 @@ def fmha_fwd(q, k, v, o=None, lse=None, scale=None, window=0, causal=False, stre
     """O (bf16 [b,n_h,T,hd]) and LSE (fp32 [b,n_h,T]); allocates them if not given.
     sink: optional fp32 CUDA tensor of n_h attention-sink logits (fmha_fwd_sink)."""
     b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=q.device)
     qp, kp, vp = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+    if o is None:
+        o = _empty(q.shape, torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _empty((b, n_h, T), torch.float32, q.device, stream)
     _check_outputs(q, o, lse)
     if scale is None:
         scale = hd ** -0.5
@@ -245,15 +268,16 @@ def fmha_fwd_splitkv(q, k, v, kv_chunk, o_parts=None, lse_parts=None, scale=None
     """fp32 partials O_i [n,b,n_h,T,hd] and lse_i [n,b,n_h,T] for chunks of kv_chunk keys."""
     b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
     _, n = fmha_split_layout(T, s_k, window, kv_chunk)
+    qp, kp, vp = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     if o_parts is None:
-        o_parts = torch.empty((n, b, n_h, T, hd), dtype=torch.float32, device=q.device)
+        o_parts = _empty((n, b, n_h, T, hd), torch.float32, q.device, stream)
     if lse_parts is None:
-        lse_parts = torch.empty((n, b, n_h, T), dtype=torch.float32, device=q.device)
+        lse_parts = _empty((n, b, n_h, T), torch.float32, q.device, stream)
     if o_parts.numel() < n * b * n_h * T * hd or lse_parts.numel() < n * b * n_h * T:
         raise ValueError("partial buffers too small for %d chunks" % n)
     if scale is None:
         scale = hd ** -0.5
-    rc = load().fmha_fwd_splitkv(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _f32(o_parts, "o_parts"),
+    rc = load().fmha_fwd_splitkv(qp, kp, vp, _f32(o_parts, "o_parts"),
                                  _f32(lse_parts, "lse_parts"), int(kv_chunk), b, n_h, n_kv_h, T, s_k, hd,
                                  float(scale), int(window), int(bool(causal)), _stream(stream))
     _check(rc, "fmha_fwd_splitkv")
@@ -266,16 +290,16 @@ def fmha_merge(o_parts, lse_parts, o=None, lse=None, stream=None, sink=None):
     if o_parts.dim() != 5 or lse_parts.dim() != 4 or tuple(o_parts.shape[:4]) != tuple(lse_parts.shape):
         raise ValueError("o_parts [n,b,n_h,T,hd] and lse_parts [n,b,n_h,T] expected")
     n, b, n_h, T, hd = o_parts.shape
+    op, lp = _f32(o_parts, "o_parts"), _f32(lse_parts, "lse_parts")
     if o is None:
-        o = torch.empty((b, n_h, T, hd), dtype=torch.bfloat16, device=o_parts.device)
+        o = _empty((b, n_h, T, hd), torch.bfloat16, o_parts.device, stream)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=o_parts.device)
+        lse = _empty((b, n_h, T), torch.float32, o_parts.device, stream)
     if sink is None:
-        rc = load().fmha_merge(_f32(o_parts, "o_parts"), _f32(lse_parts, "lse_parts"), n, _bf16(o, "o"),
-                               _f32(lse, "lse"), b, n_h, T, hd, _stream(stream))
+        rc = load().fmha_merge(op, lp, n, _bf16(o, "o"), _f32(lse, "lse"), b, n_h, T, hd, _stream(stream))
         _check(rc, "fmha_merge")
     else:
-        rc = load().fmha_merge_ex(_f32(o_parts, "o_parts"), _f32(lse_parts, "lse_parts"), None, PARTS_F32, n,
+        rc = load().fmha_merge_ex(op, lp, None, PARTS_F32, n,
                                   _sink_ptr(sink, n_h), _bf16(o, "o"), _f32(lse, "lse"), b, n_h, T, hd,
                                   _stream(stream))
         _check(rc, "fmha_merge_ex")
@@ -288,19 +312,20 @@ def fmha_fwd_splitkv_f16(q, k, v, kv_chunk, o_parts=None, lse_parts=None, range_
     factors 2^k fp32 [n,b,n_h,T,2] (one per 256-column half row).  hd-512 tensor-core kernel only."""
     b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
     _, n = fmha_split_layout(T, s_k, window, kv_chunk)
+    qp, kp, vp = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     if o_parts is None:
-        o_parts = torch.empty((n, b, n_h, T, hd), dtype=torch.float16, device=q.device)
+        o_parts = _empty((n, b, n_h, T, hd), torch.float16, q.device, stream)
     if lse_parts is None:
-        lse_parts = torch.empty((n, b, n_h, T), dtype=torch.float32, device=q.device)
+        lse_parts = _empty((n, b, n_h, T), torch.float32, q.device, stream)
     if range_parts is None:
-        range_parts = torch.empty((n, b, n_h, T, 2), dtype=torch.float32, device=q.device)
+        range_parts = _empty((n, b, n_h, T, 2), torch.float32, q.device, stream)
     if (o_parts.dtype != torch.float16 or not o_parts.is_cuda or not o_parts.is_contiguous()
             or o_parts.numel() < n * b * n_h * T * hd or lse_parts.numel() < n * b * n_h * T
             or range_parts.numel() < n * b * n_h * T * 2):
         raise ValueError("fp16 partial buffers too small or of the wrong type for %d chunks" % n)
     if scale is None:
         scale = hd ** -0.5
-    rc = load().fmha_fwd_splitkv_ex(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), o_parts.data_ptr(),
+    rc = load().fmha_fwd_splitkv_ex(qp, kp, vp, o_parts.data_ptr(),
                                     _f32(lse_parts, "lse_parts"), _f32(range_parts, "range_parts"), PARTS_F16,
                                     int(kv_chunk), b, n_h, n_kv_h, T, s_k, hd, float(scale), int(window),
                                     int(bool(causal)), _stream(stream))
@@ -315,11 +340,12 @@ def fmha_merge_f16(o_parts, lse_parts, range_parts, o=None, lse=None, stream=Non
     n, b, n_h, T, hd = o_parts.shape
     if tuple(lse_parts.shape) != (n, b, n_h, T) or tuple(range_parts.shape) != (n, b, n_h, T, 2):
         raise ValueError("lse_parts [n,b,n_h,T] and range_parts [n,b,n_h,T,2] expected")
+    lp, rp = _f32(lse_parts, "lse_parts"), _f32(range_parts, "range_parts")
     if o is None:
-        o = torch.empty((b, n_h, T, hd), dtype=torch.bfloat16, device=o_parts.device)
+        o = _empty((b, n_h, T, hd), torch.bfloat16, o_parts.device, stream)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=o_parts.device)
-    rc = load().fmha_merge_ex(o_parts.data_ptr(), _f32(lse_parts, "lse_parts"), _f32(range_parts, "range_parts"),
+        lse = _empty((b, n_h, T), torch.float32, o_parts.device, stream)
+    rc = load().fmha_merge_ex(o_parts.data_ptr(), lp, rp,
                               PARTS_F16, n, _sink_ptr(sink, n_h), _bf16(o, "o"), _f32(lse, "lse"), b, n_h, T, hd,
                               _stream(stream))
     _check(rc, "fmha_merge_ex")
@@ -355,13 +381,13 @@ def fmha_fwd_nvfp4(q, k, v, codes=None, scales=None, lse=None, global_scale=1.0,
     """fmha_fwd with O quantised to NVFP4 (see include/fmha.h): returns
     (codes uint8 [b,n_h,T,hd/2], scales uint8 [b,n_h,T,hd/16] E4M3, lse fp32 [b,n_h,T])."""
     b, n_h, n_kv_h, T, s_k, hd = _shapes(q, k, v)
-    if codes is None:
-        codes = torch.empty((b, n_h, T, hd // 2), dtype=torch.uint8, device=q.device)
-    if scales is None:
-        scales = torch.empty((b, n_h, T, hd // 16), dtype=torch.uint8, device=q.device)
-    if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=torch.float32, device=q.device)
     qp, kp, vp = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+    if codes is None:
+        codes = _empty((b, n_h, T, hd // 2), torch.uint8, q.device, stream)
+    if scales is None:
+        scales = _empty((b, n_h, T, hd // 16), torch.uint8, q.device, stream)
+    if lse is None:
+        lse = _empty((b, n_h, T), torch.float32, q.device, stream)
     if (tuple(codes.shape) != (b, n_h, T, hd // 2) or tuple(scales.shape) != (b, n_h, T, hd // 16)
             or tuple(lse.shape) != (b, n_h, T)):
         raise ValueError("codes [b,n_h,T,hd/2], scales [b,n_h,T,hd/16] and lse [b,n_h,T] expected")
@@ -381,10 +407,10 @@ def fmha_quantize_nvfp4(x, global_scale=1.0, stream=None):
     if x.dim() < 1 or x.shape[-1] % 16 != 0:
         raise ValueError("x [..., hd] with hd a multiple of 16 expected")
     hd = x.shape[-1]
-    rows = x.numel() // hd
-    codes = torch.empty(tuple(x.shape[:-1]) + (hd // 2,), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(tuple(x.shape[:-1]) + (hd // 16,), dtype=torch.uint8, device=x.device)
-    rc = load().fmha_quantize_nvfp4(_f32(x, "x"), rows, hd, float(global_scale), _u8(codes, "codes"),
+    rows, xp = x.numel() // hd, _f32(x, "x")
+    codes = _empty(tuple(x.shape[:-1]) + (hd // 2,), torch.uint8, x.device, stream)
+    scales = _empty(tuple(x.shape[:-1]) + (hd // 16,), torch.uint8, x.device, stream)
+    rc = load().fmha_quantize_nvfp4(xp, rows, hd, float(global_scale), _u8(codes, "codes"),
                                     _u8(scales, "scales"), _stream(stream))
     _check(rc, "fmha_quantize_nvfp4")
     return codes, scales
@@ -493,9 +519,7 @@ def _workspace(nbytes, dev, stream):
     costs the host more than the rest of a call.  A call that is being captured into a graph gets a new one, which the
     graph's memory pool holds: graphs captured on one stream may be replayed at the same time."""
     if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_stream_object(stream, dev)):
             return _workspace(nbytes, dev, None)
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=_U8, device=dev)
@@ -540,10 +564,9 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     else:
         max_pos, rot = cos_sin.shape
     if q is None:
-        q = torch.empty((b, n_h, T, hd), dtype=_BF16, device=dev)
+        q = _empty((b, n_h, T, hd), _BF16, dev, stream)
     if k is None:
-        k = torch.empty((b, n_kv_h, T, hd), dtype=_BF16, device=dev)
-        v = torch.empty_like(k)
+        k, v = (_empty((b, n_kv_h, T, hd), _BF16, dev, stream) for _ in range(2))
     rows = k.shape[2]
     kv_shape, w_shape = (b, n_kv_h, rows, hd), (hd,)
     _run(_NORM_ROPE, dev, qkv, q_weight, w_shape, k_weight, w_shape, cos_sin, None, positions, (b, T), q, (b, n_h, T, hd),
@@ -620,9 +643,9 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
     if s_k is None:
         s_k = cap
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(shape, _BF16, dev, stream)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=_FP32, device=dev)
+        lse = _empty((b, n_h, T), _FP32, dev, stream)
     key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk, seq_lens is not None)
     plan = _kv4_plans.get(key)
     if plan is None:
@@ -661,9 +684,9 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     b, n_h, T, hd = q_shape
     n_kv_h, s_k = kv_shape[1:3]
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q_shape, _BF16, dev, stream)
     if lse is None:
-        lse = torch.empty((b, n_h, T), dtype=_FP32, device=dev)
+        lse = _empty((b, n_h, T), _FP32, dev, stream)
     key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal)
     need = _first_plans.get(key)
     if need is None:

@@ -92,3 +92,86 @@ def test_kv4_keys_of_zero_under_a_factor_past_fp32(hd, kernel):
     got = binding.fmha_fwd_kv4(q, *cache, torch.tensor(lens, dtype=torch.int32, device=DEV), k_global=2.0 ** 60, v_global=2.0, scale=2.0 ** 20)
     want = ref.attend(q, torch.zeros(3, 2, 256, hd, device=DEV), ref.dequantise(cache[2], cache[3], 2.0), lens, 1.0)
     ref.assert_attention(got, want)
+
+
+# ------------------------------------------------------------------ other streams
+def _calls(r, hd=128):
+    """Calls that allocate their outputs, each as a function of the stream: (name, outputs)."""
+    q, k, v = ops.normal(r, 2, 8, 1, hd), ops.normal(r, 2, 2, 600, hd), ops.normal(r, 2, 2, 600, hd)
+    cache = ops.filled(r, 2, 2, 608, hd)
+    qkv, tab = ops.normal(r, 2, 1, 12 * hd), ops.table(16, hd)
+    pos = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    parts = binding.fmha_fwd_splitkv(q, k, v, 200)
+    q5, k5, v5 = ops.normal(r, 1, 64, 1, 512), ops.normal(r, 1, 1, 600, 512), ops.normal(r, 1, 1, 600, 512)
+    parts16 = binding.fmha_fwd_splitkv_f16(q5, k5, v5, 256)
+    return {
+        "norm_rope": lambda s: binding.fmha_qk_norm_rope(qkv, tab, pos, 8, 2, stream=s),
+        "kv4": lambda s: binding.fmha_fwd_kv4(q, *cache, stream=s),
+        "first": lambda s: binding.fmha_fwd_first(q, k, v, 4, window=500, stream=s),
+        "fwd": lambda s: binding.fmha_fwd(q, k, v, stream=s),
+        "nvfp4": lambda s: binding.fmha_fwd_nvfp4(q, k, v, stream=s),
+        "splitkv": lambda s: binding.fmha_fwd_splitkv(q, k, v, 200, stream=s),
+        "merge": lambda s: binding.fmha_merge(*parts, stream=s),
+        "splitkv_f16": lambda s: binding.fmha_fwd_splitkv_f16(q5, k5, v5, 256, stream=s),
+        "merge_f16": lambda s: binding.fmha_merge_f16(*parts16, stream=s),
+        "quantize": lambda s: binding.fmha_quantize_nvfp4(parts[0], stream=s),
+    }
+
+
+CALLS = ["norm_rope", "kv4", "first", "fwd", "nvfp4", "splitkv", "merge", "splitkv_f16", "merge_f16", "quantize"]
+STREAMS = ["stream", "handle", "default handle"]
+
+
+def _lanes(how):
+    """(the current stream of the test, what a call is given as its stream, that as a Stream)"""
+    if how == "default handle":
+        return torch.cuda.Stream(), 0, torch.cuda.default_stream()
+    side = torch.cuda.Stream()
+    return torch.cuda.default_stream(), side if how == "stream" else side.cuda_stream, side
+
+
+def _bits(out):
+    return [t.clone().view(torch.uint8) for t in out]
+
+
+@pytest.mark.parametrize("how", STREAMS)
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_do_not_take_memory_that_the_current_stream_still_uses(name, how):
+    """Blocks freed on the current stream, which copies from them later, beside a call on another stream that allocates."""
+    here, given, side = _lanes(how)
+    call = _calls(ops.gen(90))[name]
+    sizes = [t.shape + (t.element_size(),) for t in call(None)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        olds = [torch.full(s, 7, dtype=torch.uint8, device=DEV) for s in sizes]
+        news = [torch.empty_like(t) for t in olds]
+        here.synchronize()
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        for o, n in zip(olds, news):
+            n.copy_(o)
+        del o, olds
+        outs = call(given)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert len(outs) == len(news) and all((n == 7).all() for n in news)
+
+
+@pytest.mark.parametrize("how", STREAMS)
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_are_kept_for_the_current_stream_too(name, how):
+    """Outputs of a call on another stream, read on the current one, dropped before that has happened, and the same call again."""
+    here, given, side = _lanes(how)
+    call = _calls(ops.gen(91))[name]
+    want = _bits(call(None))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        outs = call(given)
+        here.wait_stream(side)
+        torch.cuda._sleep(200_000_000)
+        got = _bits(outs)
+        del outs
+        with torch.cuda.stream(side):
+            other = [torch.full_like(w, 9) for w in want]  # takes such blocks if they are free
+        side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want)) and all((t == 9).all() for t in other)
