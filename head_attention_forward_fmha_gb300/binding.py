@@ -7,7 +7,6 @@ kernels; there is no CPU fallback, and a missing library raises.
 """
 import ctypes
 import os
-import threading
 
 import torch
 
@@ -417,9 +416,8 @@ def fmha_quantize_nvfp4(x, global_scale=1.0, stream=None):
 
 
 def fmha_release():
-    """Free the library's workspaces and the binding's."""
+    """Free the library's workspaces."""
     load().fmha_release()
-    _workspaces.clear()
 
 
 def fmha_version():
@@ -509,25 +507,10 @@ def _handle(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-_workspaces = {}  # uint8 tensor by (thread, device, stream)
-
-
-def _workspace(nbytes, dev, stream):
-    """A tensor of at least nbytes for the partials of one call on `stream`.
-
-    Calls of one thread on one stream follow each other, so they share one that is kept (and grown): allocating it anew
-    costs the host more than the rest of a call.  A call that is being captured into a graph gets a new one, which the
-    graph's memory pool holds: graphs captured on one stream may be replayed at the same time."""
-    if stream is not None:
-        with torch.cuda.stream(_stream_object(stream, dev)):
-            return _workspace(nbytes, dev, None)
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(nbytes, dtype=_U8, device=dev)
-    key = threading.get_ident(), dev, torch._C._cuda_getCurrentRawStream(dev)
-    t = _workspaces.get(key)
-    if t is None or t.numel() < nbytes:
-        t = _workspaces[key] = torch.empty(nbytes, dtype=_U8, device=dev)
-    return t
+# Workspaces that outlive a call: none.  Those of split calls are allocated by csrc/tensor_args.cpp for the call alone, in
+# the memory of its stream (of the graph's pool while torch.cuda.graph captures it).  Kept ones would stay behind threads
+# and streams that are gone, and could lie in a pool that is not theirs.
+_workspaces = ()
 
 
 def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -632,8 +615,8 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
 
     seq_lens: int32 [b], the keys of each sequence (None: s_k each); s_k: their bound, at most the cache's rows (the
     default).  With a window, the keys j < n_first stay attended.  workspace: an optional uint8 tensor for the split-KV
-    partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call uses the
-    binding's own (one per thread and stream; a new one under graph capture)."""
+    partials (fmha_workspace_bytes of fmha_fwd_kv4_plan's n_splits); without one the call allocates
+    its own (under capture by torch.cuda.graph in the graph's pool; give one under any other capture)."""
     dev = _device(q, "q")
     shape = q.shape
     if len(shape) != 4:
@@ -652,13 +635,14 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
         n, chunk = fmha_fwd_kv4_plan(*key)
         plan = _remember(_kv4_plans, key, (chunk, fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0))
     kv_chunk, need = plan
+    handle = at = _handle(stream, dev)
     if workspace is not None:
-        need = workspace.numel()
-    elif need:
-        workspace = _workspace(need, dev, stream)
+        need, at = workspace.numel(), None
+    elif need:  # the call's own, of its stream's memory
+        workspace = need
     codes, scales = (b, n_kv_h, cap, hd // 2), (b, n_kv_h, cap, hd // 16)
     _run(_KV4, dev, q, shape, k_codes, codes, k_scales, scales, v_codes, codes, v_scales, scales, seq_lens, (b,), o, shape,
-         lse, (b, n_h, T), sink, (n_h,), workspace, None, need, _handle(stream, dev), k_global, v_global,
+         lse, (b, n_h, T), sink, (n_h,), workspace, at, need, handle, k_global, v_global,
          hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, cap, hd, window, n_first, bool(causal), kv_chunk)
     return o, lse
 
@@ -675,8 +659,8 @@ def fmha_fwd_first_workspace_bytes(batch, n_h, n_kv_h, T, s_k, hd, window, n_fir
 def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, causal=False, sink=None, workspace=None,
                    stream=None):
     """fmha_fwd with the keys j < n_first attended outside the window too (fmha_fwd_first in include/fmha.h).
-    workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call uses the
-    binding's own (one per thread and stream; a new one under graph capture)."""
+    workspace: an optional uint8 tensor of fmha_fwd_first_workspace_bytes; without one the call allocates
+    its own (under capture by torch.cuda.graph in the graph's pool; give one under any other capture)."""
     dev = _device(q, "q")
     q_shape, kv_shape = q.shape, k.shape
     if len(q_shape) != 4 or len(kv_shape) != 4:
@@ -691,11 +675,12 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     need = _first_plans.get(key)
     if need is None:
         need = _remember(_first_plans, key, fmha_fwd_first_workspace_bytes(*key))
+    handle = at = _handle(stream, dev)
     if workspace is not None:
-        need = workspace.numel()
-    elif need:
-        workspace = _workspace(need, dev, stream)
+        need, at = workspace.numel(), None
+    elif need:  # the call's own, of its stream's memory
+        workspace = need
     kv_shape = (b, n_kv_h, s_k, hd)
-    _run(_FIRST, dev, q, q_shape, k, kv_shape, v, kv_shape, o, q_shape, lse, (b, n_h, T), sink, (n_h,), workspace, None, need,
-         _handle(stream, dev), hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
+    _run(_FIRST, dev, q, q_shape, k, kv_shape, v, kv_shape, o, q_shape, lse, (b, n_h, T), sink, (n_h,), workspace, at, need,
+         handle, hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
     return o, lse

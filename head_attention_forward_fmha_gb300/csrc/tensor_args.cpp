@@ -11,13 +11,16 @@
 // per field of the struct, in its order and without padding:
 //   B F I U   the address of a contiguous bf16, fp32, int32 or uint8 tensor; takes two
 //             values, the tensor and its shape (None: any)
-//   b f i u   the same, or None for a null pointer
+//   b f i u   the same, or None for a null pointer; for u also a number of bytes and the handle of a
+//             stream of the current device: the address of as many of that stream's, from torch's
+//             allocator, which has them back when the call returns
 //   S         the address of a bf16 tensor of any strides, one value
 //   q         a 64-bit integer      n   a 32-bit integer      r   an fp32 number
 // names: a name for each tensor, in order, for the errors.  A tensor of another type, or
 // not contiguous, or not on a GPU raises TypeError; of another shape or on another
 // GPU than `device`, or a number out of range, ValueError.
 #include <Python.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -35,6 +38,15 @@ const char* dtype_name(at::ScalarType t) {
         default: return "torch.uint8";
     }
 }
+
+// Memory of one call: the work that the call has queued on `stream` is done with it before what the
+// stream is given later.
+struct CallMemory {
+    void* ptr = nullptr;
+    ~CallMemory() {
+        if (ptr) c10::cuda::CUDACachingAllocator::raw_delete(ptr);
+    }
+};
 
 // The address of `obj`, checked; false with a Python error set.
 bool tensor_address(PyObject* obj, PyObject* shape, at::ScalarType type, bool contiguous, long long device, PyObject* name,
@@ -94,6 +106,7 @@ PyObject* call_checked(PyObject* const* args, Py_ssize_t nargs) {
     alignas(8) unsigned char block[kMaxBytes];
     size_t at = 0;
     Py_ssize_t next = 4, tensor = 0;
+    CallMemory own;
     for (const char* c = PyBytes_AS_STRING(args[1]); *c; ++c) {
         const bool has_shape = std::strchr("BFIUbfiu", *c) != nullptr, strided = *c == 'S';
         if (next + (has_shape ? 2 : 1) > nargs || at + 8 > kMaxBytes) {
@@ -109,7 +122,17 @@ PyObject* call_checked(PyObject* const* args, Py_ssize_t nargs) {
             }
             PyObject* name = PyTuple_GET_ITEM(args[2], tensor++);
             uint64_t p = 0;
-            if (obj != Py_None || strided || (*c >= 'A' && *c <= 'Z')) {
+            if (*c == 'u' && PyLong_CheckExact(obj)) {
+                const long long n = PyLong_AsLongLong(obj);
+                void* stream = n < 0 ? nullptr : PyLong_AsVoidPtr(shape);
+                if (PyErr_Occurred()) return nullptr;
+                if (n < 0 || own.ptr) {
+                    PyErr_SetString(PyExc_ValueError, "one number of bytes, not negative, expected");
+                    return nullptr;
+                }
+                own.ptr = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream((size_t)n, (cudaStream_t)stream);
+                p = reinterpret_cast<uint64_t>(own.ptr);
+            } else if (obj != Py_None || strided || (*c >= 'A' && *c <= 'Z')) {
                 const char k = *c | 0x20;
                 const at::ScalarType type = k == 'f' ? at::kFloat : k == 'i' ? at::kInt : k == 'u' ? at::kByte : at::kBFloat16;
                 if (!tensor_address(obj, shape, type, !strided, device, name, &p)) return nullptr;
@@ -152,6 +175,13 @@ PyObject* call_checked(PyObject* const* args, Py_ssize_t nargs) {
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     try {
         return call_checked(args, nargs);
+    } catch (const c10::OutOfMemoryError& e) {
+        PyObject* torch = PyImport_ImportModule("torch");
+        PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (type) PyErr_SetString(type, e.what_without_backtrace());
+        Py_XDECREF(type);
+        Py_XDECREF(torch);
+        return nullptr;
     } catch (const std::exception& e) {  // a tensor without storage, for example
         PyErr_SetString(PyExc_TypeError, e.what());
         return nullptr;

@@ -175,3 +175,72 @@ def test_outputs_are_kept_for_the_current_stream_too(name, how):
         side.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(got, want)) and all((t == 9).all() for t in other)
+
+
+# ------------------------------------------------------------------ memory that outlives a call
+@pytest.mark.parametrize("name", ["kv4", "first"])
+def test_split_calls_keep_no_memory(name):
+    """Partials belong to the call: threads and streams that come and go leave nothing behind, nor does a call whose
+    allocations go to a pool of their own, as in a compiled program's graph mode."""
+    import threading
+
+    r = ops.gen(92)
+    q, o, lse = ops.normal(r, 1, 8, 1, 128), torch.empty(1, 8, 1, 128, dtype=torch.bfloat16, device=DEV), torch.empty(1, 8, 1, device=DEV)
+    k, v = ops.normal(r, 1, 1, 8192, 128), ops.normal(r, 1, 1, 8192, 128)
+    cache = ops.filled(r, 1, 1, 8192, 128)
+    assert binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 8192, 128, ragged=False)[0] > 1
+    assert binding.fmha_fwd_first_workspace_bytes(1, 8, 1, 1, 8192, 128, 8000, 4) > 0
+
+    def call(stream=None):
+        if name == "kv4":
+            binding.fmha_fwd_kv4(q, *cache, o=o, lse=lse, stream=stream)
+        else:
+            binding.fmha_fwd_first(q, k, v, 4, window=8000, o=o, lse=lse, stream=stream)
+
+    call()
+    torch.cuda.synchronize()
+    binding.fmha_release()
+    before = torch.cuda.memory_allocated()
+
+    def work():
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()  # this thread's context
+        call()
+        call(side)
+        with torch.cuda.stream(side):
+            call()
+        side.synchronize()
+
+    for _ in range(3):
+        threads = [threading.Thread(target=work) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    pool = torch.cuda.MemPool()
+    with torch.cuda.use_mem_pool(pool):
+        call()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+
+
+def test_split_calls_in_a_compiled_program_with_graphs():
+    """torch.compile's graph mode (a warm-up in its own memory pool, a capture, replays), eager calls in between."""
+    from head_attention_forward_fmha_gb300 import torch_op  # noqa: F401  (registers the ops)
+
+    r = ops.gen(94)
+    cache, k, v = ops.filled(r, 1, 1, 8192, 128), ops.normal(r, 1, 1, 8192, 128), ops.normal(r, 1, 1, 8192, 128)
+    lens = torch.tensor([8100], dtype=torch.int32, device=DEV)
+
+    def program(q):
+        a = torch.ops.fmha_gb300.fwd_kv4(q * 1.0, *cache, lens, 1.0, 2.0, 128 ** -0.5, 0, 0, False)
+        b = torch.ops.fmha_gb300.fwd_first(q * 1.0, k, v, 4, 128 ** -0.5, 8000, False)
+        return a[0] * 1.0, a[1], b[0] * 1.0, b[1]
+
+    compiled = torch.compile(program, mode="reduce-overhead", fullgraph=True)
+    for _ in range(6):
+        q = ops.normal(r, 1, 8, 1, 128)
+        torch.compiler.cudagraph_mark_step_begin()
+        got = [t.clone() for t in compiled(q)]
+        want = program(q)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))

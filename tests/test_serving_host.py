@@ -190,3 +190,13 @@ def test_argument_packer():
         with pytest.raises(err):
             call(fn, bad[0].encode(), bad[1], 0, *bad[2:])
     assert len(got) == 1
+
+
+def test_argument_packer_refuses_bad_numbers_of_bytes():
+    """A number of bytes in a workspace's place goes with a stream's handle, and only there."""
+    from head_attention_forward_fmha_gb300 import _tensor_args
+
+    for layout, value, stream, err in ((b"uq", -1, 0, ValueError), (b"uq", 1 << 70, 0, OverflowError), (b"uq", 4096, None, TypeError),
+                                       (b"uq", True, 0, TypeError), (b"Uq", 4096, 0, TypeError), (b"fq", 4096, 0, TypeError)):
+        with pytest.raises(err):
+            _tensor_args.call(1, layout, ("workspace",), 0, value, stream, 0)
