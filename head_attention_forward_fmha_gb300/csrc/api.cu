@@ -61,6 +61,22 @@ bool tensor_map_encoder() {
     return g_encode != nullptr;
 }
 
+// Encodes a 3-D map with 128-byte swizzle.  The encoder is a driver call and needs a current
+// context, which a host thread has from its first runtime call that makes one
+// current: if this is the thread's first use of CUDA, that is done here.
+CUresult encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t elem[3] = {1, 1, 1};
+    auto encode = [&] {
+        return g_encode(m, type, 3, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    return r;
+}
+
 // K or V [slabs, s_k, hd] bf16 viewed as a 3-D tensor (hd fastest); boxes of
 // 64 head-dim columns (128 bytes, 128-byte swizzle) x box_rows keys x 1 slab.
 // slab_rows: rows from one slab to the next, when the map covers only the first s_k of them.
@@ -71,10 +87,7 @@ int make_kv_map(CUtensorMap* m, const void* base, int hd, int s_k, long long sla
     cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)s_k, (cuuint64_t)slabs};
     cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)(slab_rows ? slab_rows : s_k) * hd * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-    cuuint32_t elem[3] = {1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box);
     if (r != CUDA_SUCCESS) return fail(FMHA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return FMHA_OK;
 }
@@ -401,11 +414,7 @@ int make_rows_map(CUtensorMap* m, const void* base, int hd, int R, long long sla
     cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)R, (cuuint64_t)slabs};
     cuuint64_t strides[2] = {(cuuint64_t)hd * esz, (cuuint64_t)R * hd * esz};
     cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_rows, 1};
-    cuuint32_t elem[3] = {1, 1, 1};
-    CUresult r = g_encode(m, dt, 3,
-                          const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = encode_map(m, dt, base, dims, strides, box);
     if (r != CUDA_SUCCESS) return fail(FMHA_ERR_LAUNCH, "cuTensorMapEncodeTiled (%s) failed (CUresult %d)", what, (int)r);
     return FMHA_OK;
 }

@@ -244,3 +244,43 @@ def test_split_calls_in_a_compiled_program_with_graphs():
         got = [t.clone() for t in compiled(q)]
         want = program(q)
         assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("name", ["norm_rope", "append", "kv4", "first", "fwd", "splitkv", "noalloc", "nvfp4"])
+def test_first_call_of_a_fresh_thread(name):
+    """A thread that has made no CUDA call yet."""
+    import threading
+
+    r = ops.gen(95)
+    q, k, v = ops.normal(r, 1, 8, 1, 128), ops.normal(r, 1, 1, 8192, 128), ops.normal(r, 1, 1, 8192, 128)
+    o, lse, cache = torch.empty_like(q), torch.empty(1, 8, 1, device=DEV), ops.filled(r, 1, 1, 8192, 128)
+    qkv, pos, tab = ops.normal(r, 1, 1, 10 * 128), torch.zeros(1, 1, dtype=torch.int32, device=DEV), ops.table(16, 128)
+    start, ws = torch.zeros(1, dtype=torch.int32, device=DEV), torch.empty(16 << 20, dtype=torch.uint8, device=DEV)
+    k1, v1 = (torch.empty(1, 1, 1, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    parts = torch.empty(8, 1, 8, 1, 128, device=DEV), torch.empty(8, 1, 8, 1, device=DEV)
+    codes = [torch.empty(1, 8, 1, 128 // w, dtype=torch.uint8, device=DEV) for w in (2, 16)]
+    here = torch.cuda.current_stream().cuda_stream
+    calls = {
+        "norm_rope": lambda: binding.fmha_qk_norm_rope(qkv, tab, pos, 8, 1, q=q, k=k1, v=v1, stream=here),
+        "append": lambda: binding.fmha_kv4_append(k, v, *cache, start, stream=here),
+        "kv4": lambda: binding.fmha_fwd_kv4(q, *cache, o=o, lse=lse, workspace=ws, stream=here),
+        "first": lambda: binding.fmha_fwd_first(q, k, v, 4, window=8000, o=o, lse=lse, workspace=ws, stream=here),
+        "fwd": lambda: binding.fmha_fwd(q, k, v, o=o, lse=lse, stream=here),
+        "splitkv": lambda: binding.fmha_fwd_splitkv(q, k, v, 1024, *parts, stream=here),
+        "noalloc": lambda: binding.fmha_fwd_noalloc(q, k, v, o, lse, stream=here),
+        "nvfp4": lambda: binding.fmha_fwd_nvfp4(q, k, v, *codes, lse, stream=here),
+    }
+    torch.cuda.synchronize()
+    raised = []
+
+    def work():
+        try:
+            calls[name]()
+        except Exception as e:  # shown by the test
+            raised.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not raised, raised
