@@ -587,6 +587,14 @@ def fmha_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, start, k_global=
          k_out, shape, v_out, shape, _handle(stream, dev), k_global, v_global, b, n_kv_h, T, cap, hd, 0)
 
 
+def _planned(dev, query, *args):
+    """What `query`, a plan, says on device `dev`: it depends on the number of SMs."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return query(*args)
+    return query(*args)
+
+
 def _remember(plans, key, value):
     """Keep a plan; lengths that grow with every call would otherwise fill the memory."""
     if len(plans) >= 4096:
@@ -595,7 +603,7 @@ def _remember(plans, key, value):
     return value
 
 
-_kv4_plans = {}  # (chunk length, workspace bytes) by shape, for the kernel path that is set
+_kv4_plans = {}  # (chunk length, workspace bytes) by shape and device, for the kernel path that is set
 
 
 def fmha_fwd_kv4_plan(batch, n_h, n_kv_h, T, s_k, hd, window=0, n_first=0, causal=False, kv_chunk=0, ragged=True):
@@ -629,10 +637,10 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
         o = _empty(shape, _BF16, dev, stream)
     if lse is None:
         lse = _empty((b, n_h, T), _FP32, dev, stream)
-    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk, seq_lens is not None)
+    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, kv_chunk, seq_lens is not None, dev)
     plan = _kv4_plans.get(key)
     if plan is None:
-        n, chunk = fmha_fwd_kv4_plan(*key)
+        n, chunk = _planned(dev, fmha_fwd_kv4_plan, *key[:-1])
         plan = _remember(_kv4_plans, key, (chunk, fmha_workspace_bytes(b, n_h, T, hd, n) if n > 1 else 0))
     kv_chunk, need = plan
     handle = at = _handle(stream, dev)
@@ -647,7 +655,7 @@ def fmha_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, seq_lens=None, o=None,
     return o, lse
 
 
-_first_plans = {}  # workspace bytes by shape, for the kernel path that is set
+_first_plans = {}  # workspace bytes by shape and device, for the kernel path that is set
 
 
 def fmha_fwd_first_workspace_bytes(batch, n_h, n_kv_h, T, s_k, hd, window, n_first, causal=False):
@@ -671,10 +679,10 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
         o = _empty(q_shape, _BF16, dev, stream)
     if lse is None:
         lse = _empty((b, n_h, T), _FP32, dev, stream)
-    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal)
+    key = (b, n_h, n_kv_h, T, s_k, hd, window, n_first, causal, dev)
     need = _first_plans.get(key)
     if need is None:
-        need = _remember(_first_plans, key, fmha_fwd_first_workspace_bytes(*key))
+        need = _remember(_first_plans, key, _planned(dev, fmha_fwd_first_workspace_bytes, *key[:-1]))
     handle = at = _handle(stream, dev)
     if workspace is not None:
         need, at = workspace.numel(), None

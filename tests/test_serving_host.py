@@ -200,3 +200,44 @@ def test_argument_packer_refuses_bad_numbers_of_bytes():
                                        (b"uq", True, 0, TypeError), (b"Uq", 4096, 0, TypeError), (b"fq", 4096, 0, TypeError)):
         with pytest.raises(err):
             _tensor_args.call(1, layout, ("workspace",), 0, value, stream, 0)
+
+
+@pytest.mark.parametrize("name", ["kv4", "first"])
+def test_plans_are_those_of_the_tensors_device(name, monkeypatch):
+    """Two devices of which the second plans twice the chunks: each call asks with its device current, and a plan kept for one
+    is not taken on the other."""
+    state = {"current": 0}
+
+    class On:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.old, state["current"] = state["current"], self.dev
+
+        def __exit__(self, *_):
+            state["current"] = self.old
+
+    got = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(binding, "_run", lambda entry, dev, *values: got.append((dev, values)))
+    monkeypatch.setattr(binding, "_handle", lambda stream, dev: 0)
+    monkeypatch.setattr(binding, "fmha_fwd_kv4_plan", lambda *a: (2 * (1 + state["current"]), 512))
+    monkeypatch.setattr(binding, "fmha_fwd_first_workspace_bytes", lambda *a: 1000 * (1 + state["current"]))
+    monkeypatch.setattr(binding, "_kv4_plans", {})
+    monkeypatch.setattr(binding, "_first_plans", {})
+    q, o, lse = torch.zeros(1, 8, 1, 128), torch.zeros(1, 8, 1, 128), torch.zeros(1, 8, 1)
+    kv, cache = torch.zeros(1, 1, 64, 128), torch.zeros(1, 1, 64, 64)
+    for dev in (0, 1, 0, 1):
+        monkeypatch.setattr(binding, "_device", lambda t, name: dev)
+        if name == "kv4":
+            binding.fmha_fwd_kv4(q, cache, cache, cache, cache, o=o, lse=lse)
+            need = binding.fmha_workspace_bytes(1, 8, 1, 128, 2 * (1 + dev))
+        else:
+            binding.fmha_fwd_first(q, kv, kv, 4, o=o, lse=lse, window=16)
+            need = 1000 * (1 + dev)
+        assert got[-1][0] == dev and need in [x for x in got[-1][1] if isinstance(x, int)]
+        assert state["current"] == 0
+    kept = binding._kv4_plans if name == "kv4" else binding._first_plans
+    assert len(kept) == 2
