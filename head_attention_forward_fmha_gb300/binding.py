@@ -75,7 +75,7 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
 _lib = None
-_call = None      # _tensor_args.call (csrc/tensor_args.cpp)
+_call = None      # _tensor_args.call (csrc/tensor_args.cpp), from the first call that needs it on
 _packed = {}      # address of each *_packed entry
 
 
@@ -86,8 +86,8 @@ class FmhaError(RuntimeError):
 
 
 def load(path=None):
-    """Load the shared library and the argument packer (once).  Raises if they have not been built."""
-    global _lib, _call
+    """Load the shared library (once).  Raises if it has not been built."""
+    global _lib
     if _lib is not None and path is None:
         return _lib
     p = path or LIB_PATH
@@ -99,12 +99,21 @@ def load(path=None):
         fn.argtypes = args
         fn.restype = res
     if path is None:
-        from . import _tensor_args
-
         _packed.update((n[:-7], ctypes.cast(getattr(lib, n), _vp).value) for n in SIGNATURES if n.endswith("_packed"))
-        _call = _tensor_args.call
         _lib = lib
     return lib
+
+
+def _load_packer():
+    """Load the argument packer (once), which the serving operators' calls need and no other."""
+    global _call
+    load()
+    try:
+        from . import _tensor_args
+    except ImportError as e:
+        raise ImportError("the argument packer _tensor_args.so is missing or was built against another torch (%s): run "
+                          "head_attention_forward_fmha_gb300.build" % e) from e
+    _call = _tensor_args.call
 
 
 def _check(rc, fn):
@@ -494,8 +503,8 @@ def _run(entry, dev, *values):
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _run(entry, dev, *values)
-    if _lib is None:
-        load()
+    if _call is None:
+        _load_packer()
     fn, layout, names = entry
     rc = _call(_packed[fn], layout, names, dev, *values)
     if rc:

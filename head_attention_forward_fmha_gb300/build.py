@@ -6,7 +6,8 @@ shared library next to this file.  The checked build compiles the same sources
 with ``-DFMHA_CHECKED`` (every computed index of the kernels is tested before
 its access, see ``include/fmha.h``) into ``libfmha_gb300_checked.so``.  The Python
 binding's argument packer, ``csrc/tensor_args.cpp``, is built by g++ against the installed
-torch into the extension module ``_tensor_args.so``.  Usage:
+torch into the extension module ``_tensor_args.so``; the libraries need neither, and are
+built where it cannot be.  Usage:
 ``python -m head_attention_forward_fmha_gb300.build [--force] [--verbose]
 [--checked | --all]``.
 """
@@ -18,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -62,14 +64,14 @@ def up_to_date(checked=False):
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _build_args(force):
-    """The argument packer; against another torch than it was built with (a stamp says which) it is built again."""
+def build_args(force=False):
+    """The argument packer; against another torch or Python than it was built with (a stamp says which) it is built again."""
     import torch
 
-    stamp = os.path.join(BUILD_DIR, "tensor_args.torch")
-    if not force and os.path.exists(ARGS_PATH) and os.path.exists(stamp) and open(stamp).read() == torch.__version__ and \
+    stamp, built_for = os.path.join(BUILD_DIR, "tensor_args.torch"), "%s %s" % (torch.__version__, sys.version)
+    if not force and os.path.exists(ARGS_PATH) and os.path.exists(stamp) and open(stamp).read() == built_for and \
             os.path.getmtime(ARGS_PATH) >= max(os.path.getmtime(ARGS_SRC), os.path.getmtime(os.path.abspath(__file__))):
-        return
+        return ARGS_PATH
     gxx = os.environ.get("CXX") or shutil.which("g++")
     if not gxx:
         raise RuntimeError("g++ not found (set CXX)")
@@ -86,11 +88,19 @@ def _build_args(force):
         raise RuntimeError("g++ failed on tensor_args.cpp:\n%s" % r.stdout)
     os.replace(tmp, ARGS_PATH)
     with open(stamp, "w") as f:
-        f.write(torch.__version__)
+        f.write(built_for)
+    return ARGS_PATH
 
 
 def _build_variants(variants, force, verbose, extra_flags):
-    _build_args(force)
+    _build_libraries(variants, force, verbose, extra_flags)
+    try:
+        build_args(force)
+    except (ImportError, RuntimeError) as e:
+        warnings.warn("the serving operators' argument packer was not built: %s" % e)
+
+
+def _build_libraries(variants, force, verbose, extra_flags):
     todo = [c for c in variants if force or not up_to_date(c)]
     if not todo:
         return

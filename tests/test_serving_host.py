@@ -241,3 +241,38 @@ def test_plans_are_those_of_the_tensors_device(name, monkeypatch):
         assert state["current"] == 0
     kept = binding._kv4_plans if name == "kv4" else binding._first_plans
     assert len(kept) == 2
+
+
+def test_older_calls_need_no_argument_packer():
+    """Without the packer the library loads and its other calls work; the serving calls say what is missing."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys
+sys.modules["head_attention_forward_fmha_gb300._tensor_args"] = None  # importing it raises ImportError
+import torch
+from head_attention_forward_fmha_gb300 import binding
+assert binding.fmha_fwd_plan(1, 8, 1, 1, 4096, 128)[0] >= 1 and binding.fmha_fwd_kv4_plan(1, 8, 1, 1, 4096, 128)[0] >= 1
+torch._C._cuda_getDevice = lambda: 0
+for entry in (binding._NORM_ROPE, binding._APPEND, binding._KV4, binding._FIRST):
+    try:
+        binding._run(entry, 0)
+        raise SystemExit("no error")
+    except ImportError as e:
+        assert "_tensor_args" in str(e) and "build" in str(e), e
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_libraries_are_built_without_a_host_compiler(monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "ARGS_PATH", str(tmp_path / "_tensor_args.so"))
+    monkeypatch.setenv("CXX", "/bin/false")
+    with pytest.warns(UserWarning, match="packer was not built"):
+        assert build.build() == build.LIB_PATH
+    with pytest.raises(RuntimeError):
+        build.build_args()
