@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Append a, int 
     // The two threads of a block are neighbours in a warp and live or die together.
     long long at = -1;
     uint4 uk = make_uint4(0u, 0u, 0u, 0u), uv = uk;
-    if (row < rows) {
+    if (row < rows && FMHA_IN_BOUNDS(i >= 0 && i < (long long)rows << log_tpr && slab / (unsigned)a.n_kv_h < (unsigned)a.batch,
+                                     kSiteKv4Append, a.status)) {
         uk = __ldcs(reinterpret_cast<const uint4*>(a.k + i * 8));
         uv = __ldcs(reinterpret_cast<const uint4*>(a.v + i * 8));
         at = __ldg(a.start + slab / (unsigned)a.n_kv_h) + (long long)t;

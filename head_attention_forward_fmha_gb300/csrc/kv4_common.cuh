@@ -38,6 +38,12 @@ __device__ __forceinline__ float score_factor(float mant, int e) {
     return __uint_as_float(__float_as_uint(mant) + ((uint32_t)min(max(e, -126), 127) << 23));
 }
 
+// Sequence b's length.
+__device__ __forceinline__ int seq_len(const Kv4Fwd& f, int b) {
+    if (!FMHA_IN_BOUNDS(b >= 0 && b < f.batch, kSiteKv4Copy, f.status)) return 0;
+    return min(max(__ldg(f.seq_lens + b), 0), f.s_k);
+}
+
 // End of a row: finish_row, but where a NaN score has made the sum NaN, so are O and
 // LSE.  (finish_row gives such a row LSE = -inf, which marks an empty chunk: the merge
 // would leave it out, and whether the NaN shows would depend on the number of chunks.)
@@ -70,9 +76,15 @@ __device__ __forceinline__ void write_empty_rows(const Kv4Fwd& f, long long rows
         }
     }
     if (f.n_splits > 1 && f.range_part)
-        for (int r = threadIdx.x; r < n; r += threads) f.range_part[(split * rows_total + first + r) * 2 + col0 / 256] = 1.f;
+        for (int r = threadIdx.x; r < n; r += threads)
+            if (FMHA_IN_BOUNDS(first + r >= 0 && first + r < rows_total && split < f.n_splits && col0 / 256 < 2, kSiteKv4Range, f.status))
+                f.range_part[(split * rows_total + first + r) * 2 + col0 / 256] = 1.f;
     if (!with_lse) return;
     for (int r = threadIdx.x; r < n; r += threads) {
+        if (!FMHA_IN_BOUNDS(first + r >= 0 && first + r < rows_total && split < f.n_splits &&
+                                (sink_head0 < 0 || sink_head0 + (r0 + r) / f.T < f.n_h),
+                            kSiteKv4Out, f.status))
+            continue;
         if (f.n_splits == 1)
             f.lse[first + r] = sink_head0 >= 0 ? __ldg(f.sink + sink_head0 + (r0 + r) / f.T) : -INFINITY;
         else

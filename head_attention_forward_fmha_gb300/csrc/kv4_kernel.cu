@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
     // Q's loads are issued before the sequence's length is known (NB = 1: all of them).
     auto q_row = [&](int nb) {
         const int r = r_begin + nb * 8 + g;
-        return reinterpret_cast<const uint2*>(f.q + (row0 + (r < r_end ? r : r_begin)) * HD);
+        const long long row = row0 + (r < r_end ? r : r_begin);
+        return reinterpret_cast<const uint2*>(
+            f.q + (FMHA_IN_BOUNDS(row >= 0 && row < a.rows_total, kSiteKv4Q, f.status) ? row * HD : 0));
     };
     uint2 early[C::QSTEPS];
     {
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
     // Keys.  Row t sits at position len - T + t.  The chunks divide a virtual
     // key axis: the first keys (rounded up to whole tiles), then the keys from
     // the first one that row 0's window holds (rounded down to 16, the copies' unit).
-    const int len = f.seq_lens ? min(max(__ldg(f.seq_lens + b), 0), f.s_k) : f.s_k;
+    const int len = f.seq_lens ? seq_len(f, b) : f.s_k;
     const int n_first = f.window > 0 ? min(f.n_first, len) : 0;
     const int head_span = (n_first + KT - 1) / KT * KT;
     int body = 0;
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
                 if constexpr (C::QREG) {
                     qf[i][nb] = v;
                 } else {
-                    if (warp == 0) *reinterpret_cast<uint2*>(smem + C::OFF_Q + (i * NB + nb) * 256 + lane * 8) = v;
+                    if (warp == 0 && FMHA_IN_BOUNDS((i * NB + nb) * 256 + lane * 8 + 8 <= C::Q_BYTES, kSiteKv4Q, f.status))
+                        *reinterpret_cast<uint2*>(smem + C::OFF_Q + (i * NB + nb) * 256 + lane * 8) = v;
                 }
             }
         }
@@ -355,9 +358,14 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
 
     const int row_a = key_of_row(g), row_b = row_a + 8;            // S^T rows of this lane
     const int key_x = key_of_row(2 * t4), key_y = key_of_row(2 * t4 + 1);  // P's keys (and + 8)
+    // A shared-memory address inside [lo, hi), of `bytes` bytes (checked build: lo if it is not).
+    auto inside = [&](uint32_t addr, uint32_t bytes, uint32_t lo, uint32_t hi) {
+        return FMHA_IN_BOUNDS(addr >= lo && addr + bytes <= hi, kSiteKv4Key, f.status) ? addr : lo;
+    };
     // One tile.  EDGE: some key of it is masked for some row, or holds no data.
     auto tile_step = [&](auto edge, uint32_t st, int key0, int end, bool head) {
         constexpr bool EDGE = decltype(edge)::value;
+        st = inside(st, C::STAGE, ring, ring + C::RING);
         float sc[GR][NB][4];
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
@@ -367,9 +375,11 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
             for (int c = 0; c < C::NCH; ++c) {
                 constexpr int WD = C::TW / 8;
                 uint32_t wa[WD], wb[WD], ra[WD][4], rb[WD][4];
-                const uint32_t pa = st + (gr * 16 + row_a) * C::CB + c * 64 + t4 * (C::TW / 2);
+                const uint32_t pa = inside(st + (gr * 16 + row_a) * C::CB + c * 64 + t4 * (C::TW / 2), 8 * C::CB + C::TW / 2,
+                                           st, st + C::OFF_KS);
                 const uint32_t pb = pa + 8 * C::CB;
-                const uint32_t qa = st + C::OFF_KS + (gr * 16 + row_a) * C::SB + c * 8 + t4 * (C::TW / 16);
+                const uint32_t qa = inside(st + C::OFF_KS + (gr * 16 + row_a) * C::SB + c * 8 + t4 * (C::TW / 16),
+                                           8 * C::SB + C::TW / 16, st + C::OFF_KS, st + C::OFF_VC);
                 uint32_t sa, sb;
                 if constexpr (C::TW == 32) {
                     const uint4 u = lds128(pa), v = lds128(pb);
@@ -395,7 +405,8 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
                         for (int nb = 0; nb < NB; ++nb) {
                             uint2 q;
                             if constexpr (C::QREG) q = qf[step][nb];
-                            else q = lds64(smem_u32(smem) + C::OFF_Q + (step * NB + nb) * 256 + lane * 8);
+                            else q = lds64(inside(smem_u32(smem) + C::OFF_Q + (step * NB + nb) * 256 + lane * 8, 8,
+                                                  smem_u32(smem) + C::OFF_Q, smem_u32(smem) + C::OFF_Q + C::Q_BYTES));
                             mma_f16_16816(sc[gr][nb], ra[w][2 * h], rb[w][2 * h], ra[w][2 * h + 1], rb[w][2 * h + 1], q.x,
                                           q.y);
                         }
@@ -487,7 +498,9 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
             }
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c) {
-                const uint32_t sv = st + C::OFF_VS + gr * 16 * C::SB + c * 8 + (HD >= 128 ? g : g >> 1);
+                const int last = max(key_x, key_y) + 8;
+                const uint32_t sv = inside(st + C::OFF_VS + gr * 16 * C::SB + c * 8 + (HD >= 128 ? g : g >> 1), last * C::SB + 1,
+                                           st + C::OFF_VS, st + C::STAGE);
                 uint32_t s0 = lds8(sv + key_x * C::SB), s1 = lds8(sv + key_y * C::SB);
                 uint32_t s2 = lds8(sv + (key_x + 8) * C::SB), s3 = lds8(sv + (key_y + 8) * C::SB);
                 if constexpr (EDGE) {
@@ -498,7 +511,8 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
                 }
                 const uint32_t sp = e4m3x2_to_f16(s0 | (s1 << 8)), sq = e4m3x2_to_f16(s2 | (s3 << 8));
                 constexpr int WV = HD >= 128 ? 2 : 1;
-                const uint32_t cv = st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * WV);
+                const uint32_t cv = inside(st + C::OFF_VC + gr * 16 * C::CB + c * 64 + g * (4 * WV), last * C::CB + 4 * WV,
+                                           st + C::OFF_VC, st + C::OFF_VS);
                 uint32_t x[WV], y[WV], x8[WV], y8[WV];
                 if constexpr (WV == 2) {
                     const uint2 u0 = lds64(cv + key_x * C::CB), u1 = lds64(cv + key_y * C::CB);
@@ -573,7 +587,10 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) ml[warp * C::RT + nb * 8 + 2 * t4 + i] = make_float2(m_ref[nb][i], l[nb][i]);
+            for (int i = 0; i < 2; ++i) {
+                const int at = warp * C::RT + nb * 8 + 2 * t4 + i;
+                if (FMHA_IN_BOUNDS(at < W * C::RT, kSiteKv4Comb, f.status)) ml[at] = make_float2(m_ref[nb][i], l[nb][i]);
+            }
     }
     __syncthreads();  // every warp is done with its ring
     if (*abort_flag) return;
@@ -601,6 +618,7 @@ __global__ void __launch_bounds__(W * 32, (HD * NB <= 128 && W == 4) ? 4 : 1) kv
         const int i = job & 1, nb = (job >> 1) % NB, cw = job / (2 * NB);  // cw: 8-column half of a block (with its chunk)
         const int r = nb * 8 + 2 * t4 + i;
         if (r_begin + r >= r_end) continue;
+        if (!FMHA_IN_BOUNDS(r < C::RT && (((cw * 4 + 3) * NB + nb) * 2 + i) * 32 + lane < SLICE, kSiteKv4Comb, f.status)) continue;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * C::RT + r].x);

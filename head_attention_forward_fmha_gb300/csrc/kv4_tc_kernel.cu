@@ -104,13 +104,14 @@ struct Pieces {
     uint4 codes[N];
     uint32_t scales[N];  // packing them would wait for the loads
 
-    // c, s: piece 0 of the tile's first key; `keys` of them are there.
-    __device__ __forceinline__ void load(int tid, const uint4* c, const unsigned short* s, int keys) {
+    // c, s: piece 0 of the tile's first key; `keys` of them are there, `left` pieces up to the cache's end.
+    __device__ __forceinline__ void load(int tid, const uint4* c, const unsigned short* s, int keys, long long left,
+                                         unsigned* status) {
 #pragma unroll
         for (int p = 0; p < N; ++p) {
             const int idx = p * CT + tid, key = idx / PPR;
             const int at = STRIDE == PPR ? idx : key * STRIDE + idx % PPR;
-            const bool live = key < keys;
+            const bool live = key < keys && FMHA_IN_BOUNDS(at >= 0 && at < left, kSiteKv4Copy, status);
             codes[p] = live ? __ldg(c + at) : make_uint4(0u, 0u, 0u, 0u);
             scales[p] = live ? __ldg(s + at) : 0u;
         }
@@ -120,7 +121,7 @@ struct Pieces {
     // chunk c of row r at chunk c ^ (r % 8)).  A piece is four chunks; lanes take
     // theirs in different orders, c ^ x, so that eight lanes always store to eight
     // different chunk positions (bank groups).
-    __device__ __forceinline__ void store(int tid, uint8_t* tile, int rows) const {
+    __device__ __forceinline__ void store(int tid, uint8_t* tile, int rows, unsigned* status) const {
 #pragma unroll
         for (int p = 0; p < N; ++p) {
             const int idx = p * CT + tid;
@@ -144,7 +145,9 @@ struct Pieces {
                 s1 = swap ? s0 : s1;
                 s0 = u;
             }
-            uint8_t* row = tile + (i >> 1) * rows * 128 + key * 128;
+            const int off = (i >> 1) * rows * 128 + key * 128;
+            if (!FMHA_IN_BOUNDS(key < rows && off >= 0 && off + 128 <= rows * ((PPR + 1) / 2) * 128, kSiteKv4Key, status)) continue;
+            uint8_t* row = tile + off;
             const int pos = ((i & 1) * 4) ^ x ^ (key & 7);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         // the shortest fill the last gaps (chunks of 128 tokens over four ragged
         // sequences 38.6 -> 33.6 us).  Slot b holds the sequence that b others exceed.
         // Chunks are even without it (16 sequences in 8 chunks at hd 512: 33.0, sorted 36.6 us).
-        const int mine = lane < f.batch ? min(max(__ldg(f.seq_lens + lane), 0), f.s_k) : -1;
+        const int mine = lane < f.batch ? seq_len(f, lane) : -1;
         int ahead = 0;
         for (int i = 0; i < f.batch; ++i) {
             const int other = __shfl_sync(0xffffffffu, mine, i);
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         b = __ffs(__ballot_sync(0xffffffffu, lane < f.batch && ahead == b)) - 1;
         len = __shfl_sync(0xffffffffu, mine, b);
     } else if (f.seq_lens) {
-        len = min(max(__ldg(f.seq_lens + b), 0), f.s_k);
+        len = seq_len(f, b);
     }
     const int slab = b * f.n_kv_h + kvh;
     const long long row0 = ((long long)b * f.n_h + (long long)kvh * a.group) * f.T;  // slab's first query row
@@ -283,7 +286,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int row = (base + 12 * i) * RPI + lr;
-                const bool live = row < BM && r_begin + row < r_end;
+                const bool live = row < BM && r_begin + row < r_end &&
+                                  FMHA_IN_BOUNDS(row0 + r_begin + row >= 0 && row0 + r_begin + row < a.rows_total, kSiteKv4Q, f.status);
                 const uint4* src = reinterpret_cast<const uint4*>(f.q + (row0 + r_begin + (live ? row : 0)) * HD);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) u[i][v] = live ? __ldg(src + v * 32 + lc) : make_uint4(0u, 0u, 0u, 0u);
@@ -311,8 +315,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                     uint32_t h[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) h[y] = pack_f16x2(bf16_lo(x[y]) * up, bf16_hi(x[y]) * up);
-                    *reinterpret_cast<uint4*>(sq + (col >> 6) * BM * 128 + row * 128 +
-                                              ((((col & 63) >> 3) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    const int at = (col >> 6) * BM * 128 + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+                    if (FMHA_IN_BOUNDS(at >= 0 && at + 16 <= C::Q_BYTES, kSiteKv4Q, f.status))
+                        *reinterpret_cast<uint4*>(sq + at) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
         }
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         constexpr int KPPR = C::KCH / 32, VPPR = C::HDV / 32, RP = HD / 32;
         Pieces<C::KP, KPPR, RP, C::CT> kb[NBUF][C::NKC];
         Pieces<C::VP, VPPR, RP, C::CT> vb[NBUF];
-        const long long base = (long long)slab * f.cap * RP;
+        const long long base = (long long)slab * f.cap * RP, total = (long long)f.batch * f.n_kv_h * f.cap * RP;
         const uint4* const kc = reinterpret_cast<const uint4*>(f.k_codes) + base;
         const uint4* const vc = reinterpret_cast<const uint4*>(f.v_codes) + base + part * VPPR;
         const unsigned short* const ks = reinterpret_cast<const unsigned short*>(f.k_scales) + base;
@@ -344,12 +349,13 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             long long at;
             const int n = keys_of(j, at);
 #pragma unroll
-            for (int c = 0; c < C::NKC; ++c) p[c].load(tid, kc + at + c * KPPR, ks + at + c * KPPR, n);
+            for (int c = 0; c < C::NKC; ++c)
+                p[c].load(tid, kc + at + c * KPPR, ks + at + c * KPPR, n, total - base - at - c * KPPR, f.status);
         };
         auto fetch_v = [&](auto& p, int j) {
             long long at;
             const int n = keys_of(j, at);
-            p.load(tid, vc + at, vs + at, n);
+            p.load(tid, vc + at, vs + at, n, total - base - at - part * VPPR, f.status);
         };
 #pragma unroll
         for (int i = 0; i < NBUF; ++i)
@@ -372,8 +378,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                     for (int c = 0; c < C::NKC; ++c) {
                         const int q = s * C::NKC + c;
                         ok = ok && (j < STG || mbar_wait(&k_empty[q], ((j / STG) - 1) & 1, f.status));
-                        if (ok) {
-                            kb[i][c].store(tid, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), BN);
+                        if (ok && FMHA_IN_BOUNDS(s < STG, kSiteKv4Key, f.status)) {
+                            kb[i][c].store(tid, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), BN, f.status);
                             fence_proxy_async_smem();
                             mbar_arrive(&k_full[q]);
                         }
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                     auto& v = vb[i == 0 ? LAST : i - 1];
                     const int jv = j - 1, sv_ = STG == 1 ? 0 : jv & 1;
                     ok = ok && (jv < STG || mbar_wait(&v_empty[sv_], ((jv / STG) - 1) & 1, f.status));
-                    if (ok) {
-                        v.store(tid, sv + sv_ * C::V_TILE, BN);
+                    if (ok && FMHA_IN_BOUNDS(sv_ < STG, kSiteKv4Key, f.status)) {
+                        v.store(tid, sv + sv_ * C::V_TILE, BN, f.status);
                         fence_proxy_async_smem();
                         mbar_arrive(&v_full[sv_]);
                         if (jv + NBUF < n_tiles) fetch_v(v, jv + NBUF);
@@ -412,6 +418,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             auto issue_qk = [&](int j) -> bool {
                 const int s = STG == 1 ? 0 : j & 1;
                 const uint32_t d = tmem + (j % NSB) * BN;
+                if (!FMHA_IN_BOUNDS(s >= 0 && s < STG && C::OFF_K + (s + 1) * C::K_TILE <= C::OFF_V, kSiteKv4Desc, f.status) ||
+                    !FMHA_IN_BOUNDS(d - tmem + BN <= C::O_COL, kSiteKv4Tmem, f.status))
+                    return false;
                 const uint64_t b0 = k_desc + s * (C::K_TILE / 16);
 #pragma unroll 1
                 for (int c = 0; c < C::NKC; ++c) {
@@ -441,6 +450,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                 tc_fence_after();
                 const uint64_t b0 = v_desc + s * (C::V_TILE / 16);
                 const uint32_t p_col = tmem + C::P_COL + pb * (BN / 2);
+                if (!FMHA_IN_BOUNDS(s >= 0 && s < STG && C::OFF_V + (s + 1) * C::V_TILE <= C::OFF_BAR, kSiteKv4Desc, f.status) ||
+                    !FMHA_IN_BOUNDS(p_col - tmem + BN / 2 <= C::TMEM_COLS, kSiteKv4Tmem, f.status))
+                    break;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BN / 16; ++kk)
@@ -463,6 +475,9 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         // ------------------------------------------------------------ softmax
         const int row = threadIdx.x;  // tile row and TMEM lane
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+        auto o_addr = [&](int c) {  // columns 32 c .. 32 c + 31 of O
+            return t_lane + C::O_COL + (FMHA_IN_BOUNDS(warp < 4 && c * 32 + 32 <= C::HDV, kSiteKv4Tmem, f.status) ? c * 32 : 0);
+        };
         const int grow = r_begin + row;
         const bool valid = grow < r_end;
         int jlo = INT_MAX, jhi = -1, fhi = -1;
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
         }
         float m_ref = -INFINITY, l = 0.f;
         bool ok = mbar_wait(q_full, 0, f.status);
-        const float qs = ok ? row_fac[row] : 1.f;
+        const float qs = ok && FMHA_IN_BOUNDS(row >= 0 && row < BM, kSiteKv4Q, f.status) ? row_fac[row] : 1.f;
         for (int j = 0; ok && j < n_tiles; ++j) {
             const int pb = j % NSB;
             if (!mbar_wait(&s_full[pb], (j / NSB) & 1, f.status)) {
@@ -500,7 +515,10 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
             auto load_scores = [&](int col, auto& x) {
                 constexpr int N = sizeof(x) / sizeof(x[0]);
 #pragma unroll
-                for (int h = 0; h < N; ++h) tmem_ld32(s_addr + col + h * 32, x[h]);
+                for (int h = 0; h < N; ++h) {
+                    const bool in = FMHA_IN_BOUNDS(pb * BN + col + h * 32 + 32 <= C::O_COL, kSiteKv4Tmem, f.status);
+                    tmem_ld32(s_addr + (in ? col + h * 32 : 0), x[h]);
+                }
                 tmem_wait_ld();
                 if (!full) {
 #pragma unroll
@@ -562,7 +580,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                             top = __vmaxu2(top, pk[i]);  // not negative: fp16 bits compare as integers
                             s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
                         }
-                        tmem_st16u(p_addr + col / 2 + h * 16, pk);
+                        const bool in = FMHA_IN_BOUNDS(col / 2 + h * 16 + 16 <= BN / 2 && pb < NSB, kSiteKv4Tmem, f.status);
+                        tmem_st16u(p_addr + (in ? col / 2 + h * 16 : 0), pk);
                     }
                 }
                 move = max(top & 0xFFFFu, top >> 16) > 0x7400u;  // 2^14
@@ -584,11 +603,11 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 #pragma unroll 1
                 for (int c = 0; c < C::HDV / 32; ++c) {
                     float ov[32];
-                    tmem_ld32(t_lane + C::O_COL + c * 32, ov);
+                    tmem_ld32(o_addr(c), ov);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-                    tmem_st32(t_lane + C::O_COL + c * 32, ov);
+                    tmem_st32(o_addr(c), ov);
                 }
             }
             tmem_wait_st();
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 #pragma unroll 1
                     for (int c = 0; c < C::HDV / 32; ++c) {
                         float ov[32];
-                        tmem_ld32(t_lane + C::O_COL + c * 32, ov);
+                        tmem_ld32(o_addr(c), ov);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(ov[i]));
@@ -628,7 +647,8 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                         inv *= __uint_as_float((uint32_t)(127 - k) << 23);
                         range = __uint_as_float((uint32_t)(127 + k) << 23);
                     }
-                    if (store) f.range_part[prow * 2 + part] = range;
+                    if (store && FMHA_IN_BOUNDS(prow >= 0 && prow < f.n_splits * a.rows_total && part < 2, kSiteKv4Range, f.status))
+                        f.range_part[prow * 2 + part] = range;
                 }
             }
             // partials go through a 4 KB corner of Q's place per warp (its MMAs are
@@ -638,11 +658,11 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 #pragma unroll 1
             for (int c = 0; c < C::HDV / 32; ++c) {
                 float ov[32];
-                tmem_ld32(t_lane + C::O_COL + c * 32, ov);
+                tmem_ld32(o_addr(c), ov);
                 tmem_wait_ld();
                 const int col = part * C::HDV + c * 32;
                 if (f.n_splits == 1) {
-                    if (!store) continue;
+                    if (!store || !FMHA_IN_BOUNDS(col + 32 <= HD, kSiteKv4Out, f.status)) continue;
                     uint4* dst = reinterpret_cast<uint4*>(f.o + gr * HD + col);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -650,7 +670,7 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                                             pack_bf16x2(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
                                             pack_bf16x2(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
                                             pack_bf16x2(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
-                } else {
+                } else if (FMHA_IN_BOUNDS(col + 32 <= HD && warp * 4096 + 4096 <= C::Q_BYTES, kSiteKv4Comb, f.status)) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =

@@ -62,7 +62,6 @@ enum CheckSite : unsigned {
     kSiteWideVSlots = 0x203,  // the V_ITEMS slots of a PV MMA are consecutive
     kSiteWideQKDesc = 0x204,  // Q and K slots the QK MMA reads
     kSiteWideSCol = 0x205,
-    kSiteWidePRow = 0x206,
     kSiteWideLse = 0x207,
     kSiteWideRange = 0x208,  // range factor index of an fp16 partial
     kSiteWideFp4 = 0x209,    // NVFP4 output row
@@ -90,13 +89,18 @@ enum CheckSite : unsigned {
     kSitePairKDesc = 0x704,  // K stage the QK MMAs read
     kSitePairVDesc = 0x705,  // V stage the PV MMAs read
     kSitePairLse = 0x706,    // LSE / partial LSE index
-    kSitePairFp4 = 0x707,    // NVFP4 output row
-    kSiteNrCol = 0x801,      // norm-and-rotation kernel: column of a stored vector
-    kSiteKv4Append = 0x802,  // 4-bit append kernel: cache block index
-    kSiteKv4Copy = 0x803,    // 4-bit attention: keys of a bulk copy
-    kSiteKv4Key = 0x804,     // 4-bit attention: shared-memory offset of a key row
-    kSiteKv4Comb = 0x805,    // 4-bit attention: combine buffer index
-    kSiteKv4Out = 0x806,     // 4-bit attention: output / partial row
+    kSiteNrCol = 0x801,      // norm-and-rotation kernel: columns of a head row
+    kSiteKv4Append = 0x802,  // 4-bit append kernel: row loaded, cache block index, value row
+    kSiteKv4Copy = 0x803,    // 4-bit attention: keys copied or loaded from the cache, index of a length
+    kSiteKv4Key = 0x804,     // 4-bit attention: shared-memory offset of a key row (codes and scales, or converted)
+    kSiteKv4Comb = 0x805,    // 4-bit attention: combine buffer, its (reference, sum) pairs, staging of a row
+    kSiteKv4Out = 0x806,     // 4-bit attention: output / partial row, LSE, sink
+    kSiteKv4Q = 0x807,       // 4-bit attention: query row, its place and factor in shared memory
+    kSiteKv4Tmem = 0x808,    // 4-bit attention: tensor-memory columns of S, P and O
+    kSiteKv4Desc = 0x809,    // 4-bit attention: K and V stages the MMAs read
+    kSiteKv4Range = 0x80a,   // 4-bit attention: range factor index of an fp16 partial
+    kSiteNrRow = 0x80b,      // norm-and-rotation kernel: head row loaded or stored, index of a position or start
+    kSiteNrTable = 0x80c,    // norm-and-rotation kernel: row of the cosines and sines
 };
 
 static __device__ __noinline__ bool bounds_failed(unsigned site, unsigned* status) {

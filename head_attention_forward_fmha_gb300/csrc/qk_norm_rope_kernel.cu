@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNor
         col[k][1] = turned[k] && !inter ? half + 4 * u : 8 * u + 4;
     }
     grid_dependency_wait();  // every global access below follows the preceding kernel
+    if (!FMHA_IN_BOUNDS(b >= 0 && b < a.batch && t >= 0 && t < a.T && set >= 0, kSiteNrRow, a.status)) return;
 
     // Every load is issued before any arithmetic.
     const __nv_bfloat16* src = a.qkv + b * a.batch_stride + t * a.token_stride +
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNor
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 raw[i][k][f] = make_uint2(0u, 0u);
-                if (h0 + i * C::RPW < heads)
+                if (h0 + i * C::RPW < heads && FMHA_IN_BOUNDS(col[k][f] >= 0 && col[k][f] + 4 <= HD, kSiteNrCol, a.status))
                     raw[i][k][f] = __ldcs(reinterpret_cast<const uint2*>(src + i * C::RPW * HD + col[k][f]));
             }
     const int pos = a.rot > 0 ? __ldg(a.positions + token) : 0;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNor
                 const float4 v = w ? __ldg(reinterpret_cast<const float4*>(w + col[k][f])) : make_float4(1.f, 1.f, 1.f, 1.f);
                 w4[f][0] = v.x; w4[f][1] = v.y; w4[f][2] = v.z; w4[f][3] = v.w;
             }
-            if (turned[k]) {
+            if (turned[k] && FMHA_IN_BOUNDS(pos >= 0 && pos < a.max_pos && 4 * (u0 + k * C::LANES) + 4 <= half, kSiteNrTable, a.status)) {
                 const float* tab = a.cos_sin + (long long)pos * a.rot + 4 * (u0 + k * C::LANES);
                 const float4 c = __ldg(reinterpret_cast<const float4*>(tab));
                 const float4 s = __ldg(reinterpret_cast<const float4*>(tab + half));
@@ -194,6 +195,10 @@ __global__ void __launch_bounds__(kNrWarps * 32) qk_norm_rope_kernel(const QkNor
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
         if (h0 + i * C::RPW >= heads) break;
+        const long long at = dst + i * C::RPW * step - (type == 0 ? a.q : type == 1 ? a.k : a.v);
+        if (!FMHA_IN_BOUNDS(at >= 0 && at + HD <= (long long)a.batch * HD * (type == 0 ? (long long)a.n_h * a.T : (long long)a.n_kv_h * a.kv_rows),
+                            kSiteNrRow, a.status))
+            break;
 #pragma unroll
         for (int k = 0; k < C::UNITS; ++k)
 #pragma unroll

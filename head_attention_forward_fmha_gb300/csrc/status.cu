@@ -32,12 +32,18 @@ static_assert(kStatusBitTimeout == kStatusBarrierTimeout && kStatusBitBounds == 
 
 const char* check_site_name(unsigned site) {
     switch (site) {
-        case kSiteNrCol: return "norm-and-rotation kernel: column of a stored vector";
-        case kSiteKv4Append: return "4-bit append kernel: cache block";
-        case kSiteKv4Copy: return "4-bit attention: keys of a bulk copy";
+        case kSiteNrCol: return "norm-and-rotation kernel: columns of a head row";
+        case kSiteKv4Append: return "4-bit append kernel: row or cache block";
+        case kSiteKv4Copy: return "4-bit attention: keys copied or loaded";
         case kSiteKv4Key: return "4-bit attention: shared-memory offset of a key row";
-        case kSiteKv4Comb: return "4-bit attention: combine buffer";
+        case kSiteKv4Comb: return "4-bit attention: combine or staging buffer";
         case kSiteKv4Out: return "4-bit attention: output row";
+        case kSiteKv4Q: return "4-bit attention: query row";
+        case kSiteKv4Tmem: return "4-bit attention: TMEM columns";
+        case kSiteKv4Desc: return "4-bit attention: K/V stage of an MMA";
+        case kSiteKv4Range: return "4-bit attention: range factor";
+        case kSiteNrRow: return "norm-and-rotation kernel: head row";
+        case kSiteNrTable: return "norm-and-rotation kernel: row of the table";
         case kSiteTcQLoad: return "row-tile kernel: Q box coordinates";
         case kSiteTcKLoad: return "row-tile kernel: K tile key / stage";
         case kSiteTcVLoad: return "row-tile kernel: V tile key / stage";
@@ -53,7 +59,6 @@ const char* check_site_name(unsigned site) {
         case kSiteWideVSlots: return "hd-512 kernel: V slots of a PV MMA not consecutive";
         case kSiteWideQKDesc: return "hd-512 kernel: Q / K slot of the QK MMA";
         case kSiteWideSCol: return "hd-512 kernel: TMEM columns of S";
-        case kSiteWidePRow: return "hd-512 kernel: P row";
         case kSiteWideLse: return "hd-512 kernel: LSE index";
         case kSiteWideRange: return "hd-512 kernel: range factor index";
         case kSiteWideFp4: return "hd-512 kernel: NVFP4 output row";
@@ -81,7 +86,6 @@ const char* check_site_name(unsigned site) {
         case kSitePairKDesc: return "two-row-tile kernel: K stage of the QK MMAs";
         case kSitePairVDesc: return "two-row-tile kernel: V stage of the PV MMAs";
         case kSitePairLse: return "two-row-tile kernel: LSE index";
-        case kSitePairFp4: return "two-row-tile kernel: NVFP4 output row";
         default: return "unknown site";
     }
 }

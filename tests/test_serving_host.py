@@ -276,3 +276,26 @@ def test_libraries_are_built_without_a_host_compiler(monkeypatch, tmp_path):
         assert build.build() == build.LIB_PATH
     with pytest.raises(RuntimeError):
         build.build_args()
+
+
+def test_index_check_sites_are_named_and_used():
+    """Every site code stands at some check of a kernel and has a description; the serving kernels check what they access."""
+    import glob
+    import os
+
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    text = {os.path.basename(p): open(p).read() for p in glob.glob(os.path.join(csrc, "*.cu*"))}
+    enum = text["ptx.cuh"][text["ptx.cuh"].index("enum CheckSite") :]
+    enum = enum[: enum.index("};")]
+    sites = re.findall(r"^\s*(kSite\w+) = 0x", enum, re.M)
+    assert len(sites) == len(set(sites)) > 40
+    elsewhere = "".join(text.values()).replace(enum, "").replace(text["status.cu"], "")
+    for site in sites:
+        assert "case %s:" % site in text["status.cu"], site + " has no description"
+        if site != "kSiteSelfTest":  # its check stands in status.cu
+            assert re.search(r"\b%s\b" % site, elsewhere), site + " is checked nowhere"
+    kv4 = {"Copy", "Key", "Comb", "Out", "Q"}
+    for name, want in (("kv4_kernel.cu", kv4), ("kv4_tc_kernel.cu", kv4 | {"Tmem", "Desc", "Range"}), ("kv4_append_kernel.cu", {"Append"})):
+        have = set(re.findall(r"kSiteKv4(\w+)", text[name] + text["kv4_common.cuh"]))
+        assert want <= have, "%s: no check for %s" % (name, want - have)
+    assert {"Col", "Row", "Table"} <= set(re.findall(r"kSiteNr(\w+)", text["qk_norm_rope_kernel.cu"]))
