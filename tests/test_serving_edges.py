@@ -284,3 +284,18 @@ def test_first_call_of_a_fresh_thread(name):
     t.join()
     torch.cuda.synchronize()
     assert not raised, raised
+
+
+def test_smoke_runs_a_kernel_with_first_keys(monkeypatch):
+    """The smoke run's call with first keys has a window that hides some of them."""
+    import __graft_entry__ as entry
+
+    seen, real = [], binding.fmha_fwd_first
+
+    def record(q, k, v, n_first, **kw):
+        seen.append(0 < n_first < k.shape[2] - q.shape[2] - kw.get("window", 0) + 1 and kw.get("window", 0) > 0)
+        return real(q, k, v, n_first, **kw)
+
+    monkeypatch.setattr(binding, "fmha_fwd_first", record)
+    entry.smoke()
+    assert seen and all(seen)
