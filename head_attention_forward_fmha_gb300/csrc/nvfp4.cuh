@@ -51,14 +51,6 @@ __device__ __forceinline__ uint32_t e2m1_code(float a) {
            (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
 }
 
-// The value of an E2M1 code: magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6, sign in bit 3.
-// Exponent field 0 is m / 2; otherwise (2 + m) * 2^(e - 2).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float a = e == 0 ? 0.5f * (float)m : (float)(2u + m) * __uint_as_float((125u + e) << 23);
-    return (c & 8u) ? -a : a;
-}
-
 // One 16-element block: returns the E4M3 scale code and packs the 16 element
 // codes into two 32-bit words (element i in bits 4 (i % 8) of word i / 8).
 __device__ __forceinline__ uint32_t nvfp4_block(const float (&x)[16], float g, uint32_t (&packed)[2]) {
