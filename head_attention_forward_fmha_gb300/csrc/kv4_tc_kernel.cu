@@ -585,7 +585,10 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
                     }
                 }
                 move = max(top & 0xFFFFu, top >> 16) > 0x7400u;  // 2^14
-                if (again == 0 && __any_sync(0xffffffffu, move)) continue;
+                if (again == 0 && __any_sync(0xffffffffu, move)) {
+                    tmem_wait_st();  // P is written to the same columns once more
+                    continue;
+                }
                 float a0, a1, b0, b1;
                 f32x2_split(s2[0], a0, a1);
                 f32x2_split(s2[1], b0, b1);

@@ -94,6 +94,21 @@ def test_kv4_keys_of_zero_under_a_factor_past_fp32(hd, kernel):
     ref.assert_attention(got, want)
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256, 512])
+def test_kv4_scores_that_rise_within_every_tile(hd, kernel):
+    """The reference moves in every tile after its weights have been written once, for some rows of a warp and not for others."""
+    n, rows = 1024, 40
+    r = ops.gen(93)
+    k, v, q = ops.normal(r, 1, 1, n, hd) * 0.1, ops.normal(r, 1, 1, n, hd), ops.normal(r, 1, rows, 1, hd)
+    k[0, 0, :, 0] = torch.linspace(0, 96, n, device=DEV).to(torch.bfloat16)
+    q[0, :, 0, 0] = torch.linspace(-4, 0.5 * hd ** 0.5 * 4, rows, device=DEV).to(torch.bfloat16)
+    cache = binding.fmha_kv4_cache(1, 1, n, hd)
+    binding.fmha_kv4_append(k, v, *cache, torch.zeros(1, dtype=torch.int32, device=DEV))
+    want = ref.attend(q, ref.dequantise(cache[0], cache[1], 1.0), ref.dequantise(cache[2], cache[3], 1.0), [n], hd ** -0.5)
+    for chunk in (0, 1024):
+        ref.assert_attention(binding.fmha_fwd_kv4(q, *cache, kv_chunk=chunk), want)
+
+
 # ------------------------------------------------------------------ other streams
 def _calls(r, hd=128):
     """Calls that allocate their outputs, each as a function of the stream: (name, outputs)."""
