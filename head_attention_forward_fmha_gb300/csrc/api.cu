@@ -921,10 +921,10 @@ int check_kv4(int batch, int n_h, int n_kv_h, int T, int s_k, int cap, int hd, f
 
 // The 4-bit attention's kernel.  The mma.sync kernel converts the cache again for
 // every 8 to 32 rows of a KV head, the tensor-core kernel once for 128 but with more
-// work per tile; measured over 16384 keys (8 sequences, 8 heads): hd 64 48 rows 89
-// against 116 us, hd 128 32 rows 82 against 121 and 48 rows 146 against 126, hd
-// 256 16 rows 98 against 171 and 24 rows 181 against 172, hd 512 24 rows 315 against
-// 408, each 8 rows more adding ~80.  fmha_set_kernel_path applies here too (1:
+// work per tile; measured over 16384 keys (8 sequences, 8 KV heads), mma.sync against
+// tensor cores in us: hd 64 32 rows 67 / 106, 64 rows 115 / 106, 72 rows 147 / 108 (about
+// equal from 40 to 64 rows); hd 128 32 rows 105 / 120, 40 rows 135 / 122; hd 256 16 rows
+// 117 / 188, 24 rows 201 / 195; hd 512 24 rows 326 / 421, 32 rows 462 / 416.  fmha_set_kernel_path applies here too (1:
 // never, 2 to 4: always).
 bool kv4_use_tc(int hd, long long R) {
     const int ov = g_path_override.load();

@@ -20,7 +20,7 @@
 // quantiser of nvfp4.cuh, and all of them give its codes.
 //
 // Measured on GB300: four prompts of 4095 tokens, 8 heads of 128, with the values
-// (153 MB) 30.4 us, 5.0 TB/s; with IEEE divisions and comparisons 68 us, with
+// (153 MB) 31.0 us, 4.9 TB/s; with IEEE divisions and comparisons 68 us, with
 // 64-bit index arithmetic repeated for K and for V 40 us.  At 72 % of the issue
 // slots (363 instructions per 16 elements) the arithmetic still stands beside the
 // memory.  32 single tokens 2.2 us.

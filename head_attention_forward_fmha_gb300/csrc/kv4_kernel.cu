@@ -32,7 +32,7 @@
 // each) where HBM delivers 24 bytes per clock and SM, 42 codes.  Measured on GB300
 // (hd 128, 8 rows per KV head): 19 sequences of 32768 keys 120 us, 5.97 TB/s, 88 % of
 // the measured copy rate (152 blocks of 16 warps); 32 of them 216 us, 5.6 TB/s;
-// ragged lengths up to that 121 us; one sequence of 8191 keys 9.3 us with its
+// ragged lengths up to that 115 to 127 us (eight sets of lengths); one sequence of 8191 keys 9.3 us with its
 // merge, of which set-up, first copies and the merge are the larger part.  A tile
 // without masked keys has code of its own (159 -> 140 us for the ragged batch), the four
 // copies of a tile come from four lanes, and each warp parks its O in fragment

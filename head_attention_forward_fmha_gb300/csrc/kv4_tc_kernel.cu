@@ -18,14 +18,15 @@
 // tiles in registers, so that their loads are in flight while it converts another.
 //
 // Measured on GB300: 128 tokens of 64/8 heads of 128 over 4 x 4096 keys 83 us, 823
-// TFLOP/s; over a window of 2048 with ragged lengths 34 us; 128 heads of 512 on one
-// KV head, 16 ragged sequences up to 4096 keys 31 us.  A clock trace says what bounds
-// it.  At hd 128 a tile of 128 keys took ~2200 clocks, of which the softmax warps 2075
-// (the exponentials alone 512), with MMAs and conversion beside them (before its
-// scores were read 64 at a time); at hd 512 a
-// tile of 64 keys took 2950, of which the 32 MMAs of S 2000: with N = 64 they read Q
-// (4 KB of shared memory each) for half as many keys as at N = 128, for which there
-// is no room.  What mattered on the way: at hd 512 no spilled register, descriptors
+// TFLOP/s; over a window of 2048 with four ragged lengths 29 to 51 us (eight sets of
+// lengths; a sequence's chunk is one block's chain of tiles); 128 heads of 512 on one KV head,
+// 16 ragged sequences up to 4096 keys 31 to 35 us.  A clock trace of a block says what
+// bounds it.  At hd 128 a tile of 128 keys takes ~1900 clocks, of which the softmax
+// warps ~1750 (the exponentials alone 512), with MMAs and conversion beside them; a tile
+// in which the reference moves takes up to twice that.  At hd 512 a tile of 64 keys
+// takes ~3000, the softmax ~1170 of them, and it waits ~1850 for S: with N = 64 its 32
+// MMAs read Q (4 KB of shared memory each) for half as many keys as at N = 128, for
+// which there is no room.  What mattered on the way: at hd 512 no spilled register, descriptors
 // by addition among them (with 227 KB of shared memory there is hardly an L1, and
 // each reload is a trip to L2), and conversion in coalesced pieces (75 -> 49 us);
 // MMAs issued by an elected lane of a converged warp (49 -> 41); partials in fp16

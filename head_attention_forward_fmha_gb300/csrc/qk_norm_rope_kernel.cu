@@ -26,9 +26,15 @@
 // 109 us, 6.2 TB/s, 92 % of the measured copy rate, 65 % of the issue slots; one
 // token of the same 1.7 us.  With weight, norm and rotation applied one after
 // the other to single elements the prompts took 138 us, with 64-bit task
-// arithmetic and plain stores 121.  Four row sets per warp instead of one take 256
-// tokens of 96 heads of 256 from 8.5 to 5.8 us; below 16384 rows one set is taken, which
-// spreads the few rows over more warps.
+// arithmetic and plain stores 121.
+//
+// Four row sets per warp or one: four form A and B once for more heads and keep more loads
+// in flight, one spreads few rows over more warps.  They cross between 8192 and 32768 head
+// rows (one / four, us, 64 query and 8 KV heads): hd 64 16320 rows
+// 2.7 / 3.0, 32720 rows 3.9 / 3.5, 262080 rows 21.8 / 14.3; hd 128 8160 rows 2.7 / 2.7,
+// 16320 rows 4.0 / 3.8, 262080 rows 41.4 / 23.5; hd 256 4080 rows 2.7 / 2.8, 16320 rows
+// 6.6 / 5.0; hd 512 4080 rows 3.1 / 3.9, 16320 rows 9.9 / 9.0, 262080 rows 128 / 89.  So four
+// from 16384 rows on, at every head dim.
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -473,7 +473,8 @@ int fmha_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const
  * Without a window (0, or one of at least s_k keys) n_first changes nothing.
  * Only the first keys' tiles and the window's keys are read.  Keys that no row
  * of the call attends do not reach any result, whatever memory holds there; V
- * has to be finite at keys that some row of the sequence attends.
+ * has to be finite at keys that some row of the sequence attends.  A NaN score leaves
+ * its row's O and LSE undefined, as in fmha_fwd (fmha_fwd_kv4 makes both NaN).
  * sink: [n_h] fp32 logits or NULL.  Kernels, plan and partial format are those of
  * fmha_fwd; the partials live in `workspace`, of at least
  * fmha_fwd_first_workspace_bytes(same shape) bytes (0: none needed; also 0 for an
