@@ -25,6 +25,7 @@
 
 #include <climits>
 #include <cstring>
+#include <string>
 
 namespace {
 
@@ -44,7 +45,31 @@ const char* dtype_name(at::ScalarType t) {
 struct CallMemory {
     void* ptr = nullptr;
     ~CallMemory() {
-        if (ptr) c10::cuda::CUDACachingAllocator::raw_delete(ptr);
+        try {
+            if (ptr) c10::cuda::CUDACachingAllocator::raw_delete(ptr);
+        } catch (...) {  // after a CUDA error, which the call itself or the next one reports
+        }
+    }
+
+    // False with a Python error set: torch.OutOfMemoryError, or RuntimeError for any other failure.
+    bool allocate(size_t bytes, void* stream) {
+        bool out_of_memory = false;
+        std::string what;
+        try {
+            ptr = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, (cudaStream_t)stream);
+            return true;
+        } catch (const c10::OutOfMemoryError& e) {
+            out_of_memory = true;
+            what = e.what_without_backtrace();
+        } catch (const std::exception& e) {
+            what = e.what();
+        }
+        PyObject* torch = out_of_memory ? PyImport_ImportModule("torch") : nullptr;
+        PyObject* error = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (!PyErr_Occurred()) PyErr_SetString(error ? error : PyExc_RuntimeError, what.c_str());
+        Py_XDECREF(error);
+        Py_XDECREF(torch);
+        return false;
     }
 };
 
@@ -130,7 +155,7 @@ PyObject* call_checked(PyObject* const* args, Py_ssize_t nargs) {
                     PyErr_SetString(PyExc_ValueError, "one number of bytes, not negative, expected");
                     return nullptr;
                 }
-                own.ptr = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream((size_t)n, (cudaStream_t)stream);
+                if (!own.allocate((size_t)n, stream)) return nullptr;
                 p = reinterpret_cast<uint64_t>(own.ptr);
             } else if (obj != Py_None || strided || (*c >= 'A' && *c <= 'Z')) {
                 const char k = *c | 0x20;
@@ -175,13 +200,6 @@ PyObject* call_checked(PyObject* const* args, Py_ssize_t nargs) {
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     try {
         return call_checked(args, nargs);
-    } catch (const c10::OutOfMemoryError& e) {
-        PyObject* torch = PyImport_ImportModule("torch");
-        PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
-        if (type) PyErr_SetString(type, e.what_without_backtrace());
-        Py_XDECREF(type);
-        Py_XDECREF(torch);
-        return nullptr;
     } catch (const std::exception& e) {  // a tensor without storage, for example
         PyErr_SetString(PyExc_TypeError, e.what());
         return nullptr;

@@ -261,6 +261,22 @@ def test_split_calls_in_a_compiled_program_with_graphs():
         assert all(torch.equal(g, w) for g, w in zip(got, want))
 
 
+def test_a_workspace_that_does_not_fit_is_torchs_error():
+    """More partials than the device has memory for: torch.OutOfMemoryError, nothing launched, and the next call works."""
+    r = ops.gen(96)
+    q, cache = ops.normal(r, 1, 8, 1, 128), ops.filled(r, 1, 1, 256, 128)
+    entry, names = binding._packed["fmha_fwd_kv4"], binding._KV4[2]
+    binding.fmha_fwd_kv4(q, *cache)
+    o, lse = torch.zeros_like(q), torch.zeros(1, 8, 1, device=DEV)
+    with pytest.raises(torch.OutOfMemoryError):
+        binding._call(entry, binding._KV4[1], names, 0, q, None, *[x for t in cache for x in (t, None)], None, None, o, None, lse, None,
+                      None, None, 1 << 45, 0, 1 << 45, 0, 1.0, 1.0, 0.1, 1, 8, 1, 1, 256, 256, 128, 0, 0, 0, 0)
+    torch.cuda.synchronize()
+    assert (o == 0).all() and (lse == 0).all()
+    a, b = binding.fmha_fwd_kv4(q, *cache), binding.fmha_fwd_kv4(q, *cache)
+    assert torch.equal(a[0], b[0])
+
+
 @pytest.mark.parametrize("name", ["norm_rope", "append", "kv4", "first", "fwd", "splitkv", "noalloc", "nvfp4"])
 def test_first_call_of_a_fresh_thread(name):
     """A thread that has made no CUDA call yet."""
