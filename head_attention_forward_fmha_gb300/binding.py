@@ -530,8 +530,10 @@ def fmha_qk_norm_rope(qkv, cos_sin, positions, n_h, n_kv_h, q_weight=None, k_wei
     qkv: bf16 [b, T, (n_h + 2 n_kv_h) * hd], rows contiguous, tokens and sequences at any stride of a multiple of 8
     elements.  cos_sin: fp32 [max_pos, rot], the cosines and then the sines of each position; positions: int32 [b, T]
     (a token outside [0, max_pos) is padding, its outputs are left as they are); both None: no rotation.
-    k and v given with more rows than T are written at rows kv_start[b] + t (int32 [b]; None: 0).
-    Returns q [b, n_h, T, hd], k and v [b, n_kv_h, rows, hd]; what is not given is allocated."""
+    k and v given with more rows than T are written at rows kv_start[b] + t (int32 [b]; None: 0); fmha_fwd and
+    fmha_fwd_first count every row of such a buffer as a key.
+    Returns q [b, n_h, T, hd], k and v [b, n_kv_h, rows, hd]; what is not given is allocated, and undefined where
+    nothing is written."""
     dev = _device(qkv, "qkv")
     shape = qkv.shape
     if len(shape) != 3 or n_h < 1 or n_kv_h < 1 or shape[2] % (n_h + 2 * n_kv_h):

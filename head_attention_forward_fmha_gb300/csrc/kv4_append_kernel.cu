@@ -14,13 +14,13 @@
 // which is the correctly rounded quotient (Markstein 1990) as long as nothing
 // overflows or underflows, and the roundings to E4M3 and E2M1 are the
 // hardware's conversions, which go to nearest, ties to even, and saturate, as
-// the format asks.  A block with a NaN, an infinity, a scale g s outside
-// [2^-90, 2^90] or a value above 2^30 g s (its scale saturates then, and x r might
-// overflow: the correction makes that a NaN, whose conversion has no sign) takes the
-// quantiser of nvfp4.cuh, and all of them give its codes.
+// the format asks.  A block whose scale code is the largest (0x7E, where it may have
+// saturated, and x r overflow: the correction makes that a NaN, whose conversion has no
+// sign; infinities are there too) or a NaN, or whose scale g s lies outside [2^-90,
+// 2^90], takes the quantiser of nvfp4.cuh, and all of them give its codes.
 //
 // Measured on GB300: four prompts of 4095 tokens, 8 heads of 128, with the values
-// (153 MB) 31.0 us, 4.9 TB/s; with IEEE divisions and comparisons 68 us, with
+// (153 MB) 30.4 us, 5.0 TB/s; with IEEE divisions and comparisons 68 us, with
 // 64-bit index arithmetic repeated for K and for V 40 us.  At 72 % of the issue
 // slots (363 instructions per 16 elements) the arithmetic still stands beside the
 // memory.  32 single tokens 2.2 us.
@@ -68,7 +68,7 @@ __device__ __forceinline__ void quantise8(const uint4& u, const __nv_bfloat16* b
     const float gs = __fmul_rn(g, s);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     codes = 0u;
-    if (top < 0x7F80u && (s == 0.f || (gs >= 0x1p-90f && gs <= 0x1p90f && __uint_as_float(top << 16) <= gs * 0x1p30f))) {
+    if (sc < 0x7Eu && (s == 0.f || (gs >= 0x1p-90f && gs <= 0x1p90f))) {
         if (s > 0.f) {
             const float r = __frcp_rn(gs);
             const uint64_t r2 = f32x2(r, r), n2 = f32x2(-gs, -gs);

@@ -402,7 +402,8 @@ int fmha_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float
  *   [0, max_pos) is padding: none of its outputs is written.
  * q: [batch, n_h, T, hd]; k, v: [batch, n_kv_h, kv_rows, hd], the token's row at
  *   kv_start[b] + t (kv_start NULL: 0); a row outside [0, kv_rows) is not
- *   written.  Norm and rotation are computed in fp32 and rounded to bf16 once;
+ *   written.  (fmha_fwd and fmha_fwd_first take every row of K and V as a key.)
+ *   Norm and rotation are computed in fp32 and rounded to bf16 once;
  *   V is copied bit for bit.
  */
 int fmha_qk_norm_rope(const void* qkv, long long batch_stride, long long token_stride,

@@ -25,6 +25,8 @@ def test_append_of_values_far_above_saturation(hd, g):
         v[0, 1, t, :16] *= -big
     k[0, 1, 0], k[0, 1, 1] = -3e38, 3e38
     k[0, 1, 2, ::2], k[0, 1, 3] = -float("inf"), float("inf")
+    k[0, 1, 4, 5], k[0, 1, 5] = float("nan"), float("nan")
+    k[0, 1, 6], k[0, 1, 7] = (k[0, 1, 6].float() * 700 * g).to(k.dtype), -2688 * g  # around the largest scale, and at it
     cache = binding.fmha_kv4_cache(1, 2, cap, hd)
     out = torch.zeros_like(k), torch.zeros_like(v)
     binding.fmha_kv4_append(k, v, *cache, torch.zeros(1, dtype=torch.int32, device=DEV), k_global=g, v_global=g, k_out=out[0], v_out=out[1])
