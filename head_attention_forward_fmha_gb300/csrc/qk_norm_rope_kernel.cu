@@ -23,7 +23,7 @@
 // instruction (packed fp32 pairs).
 //
 // Measured on GB300: four prompts of 4095 tokens, 64 + 2 x 8 heads of 128 (679 MB)
-// 109 us, 6.2 TB/s, 92 % of the measured copy rate, 65 % of the issue slots; one
+// 109 us, 6.2 TB/s, 92 % of the measured copy rate, 60 % of the issue slots; one
 // token of the same 1.7 us.  With weight, norm and rotation applied one after
 // the other to single elements the prompts took 138 us, with 64-bit task
 // arithmetic and plain stores 121.
