@@ -518,7 +518,8 @@ def _handle(stream, dev):
 
 # Workspaces that outlive a call: none.  Those of split calls are allocated by csrc/tensor_args.cpp for the call alone, in
 # the memory of its stream (of the graph's pool while torch.cuda.graph captures it).  Kept ones would stay behind threads
-# and streams that are gone, and could lie in a pool that is not theirs.
+# and streams that are gone, and could lie in a pool that is not theirs.  (That allocator takes the per-thread default
+# stream, handle 2, for one stream: threads that run on it give workspaces and outputs of their own.)
 _workspaces = ()
 
 
