@@ -194,6 +194,28 @@ def test_outputs_are_kept_for_the_current_stream_too(name, how):
     assert all(torch.equal(g, w) for g, w in zip(got, want)) and all((t == 9).all() for t in other)
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_a_stream_that_a_capture_forks(name):
+    """Captured on a side stream that joins the capture, outputs and workspaces allocated by the calls; replayed twice."""
+    call = _calls(ops.gen(97))[name]
+    want = _bits(call(None))
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        outs = [call(side) for _ in range(2)]
+        here.wait_stream(side)
+    for _ in range(2):
+        for out in outs:
+            for t in out:
+                t.view(torch.uint8).fill_(0xA5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(g, w) for g, w in zip(_bits(out), want))
+
+
 # ------------------------------------------------------------------ memory that outlives a call
 @pytest.mark.parametrize("name", ["kv4", "first"])
 def test_split_calls_keep_no_memory(name):
