@@ -69,6 +69,11 @@ SIGNATURES = {
     "fmha_kv4_append_packed": ([ctypes.c_char_p], _i32),
     "fmha_fwd_kv4_packed": ([ctypes.c_char_p], _i32),
     "fmha_fwd_first_packed": ([ctypes.c_char_p], _i32),
+    # a cache in pages: arguments in one struct
+    "fmha_paged_append": ([ctypes.c_char_p], _i32),
+    "fmha_paged_gather": ([ctypes.c_char_p], _i32),
+    "fmha_fwd_paged": ([ctypes.c_char_p], _i32),
+    "fmha_fwd_paged_plan": ([_i32] * 13, _i32),
 }
 # Size of the fixed split-KV scratch fmha_fwd_noalloc uses (FMHA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -76,7 +81,7 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _lib = None
 _call = None      # _tensor_args.call (csrc/tensor_args.cpp), from the first call that needs it on
-_packed = {}      # address of each *_packed entry
+_packed = {}      # address of each entry that takes its arguments in one struct
 
 
 class FmhaError(RuntimeError):
@@ -99,7 +104,8 @@ def load(path=None):
         fn.argtypes = args
         fn.restype = res
     if path is None:
-        _packed.update((n[:-7], ctypes.cast(getattr(lib, n), _vp).value) for n in SIGNATURES if n.endswith("_packed"))
+        _packed.update((n[:-7] if n.endswith("_packed") else n, ctypes.cast(getattr(lib, n), _vp).value)
+                       for n, (args, _) in SIGNATURES.items() if args == [ctypes.c_char_p])
         _lib = lib
     return lib
 
@@ -703,4 +709,165 @@ def fmha_fwd_first(q, k, v, n_first, o=None, lse=None, scale=None, window=0, cau
     kv_shape = (b, n_kv_h, s_k, hd)
     _run(_FIRST, dev, q, q_shape, k, kv_shape, v, kv_shape, o, q_shape, lse, (b, n_h, T), sink, (n_h,), workspace, at, need,
          handle, hd ** -0.5 if scale is None else scale, b, n_h, n_kv_h, T, s_k, hd, window, n_first, bool(causal))
+    return o, lse
+
+
+# ---------------------------------------------------------------------------
+# KV cache in pages
+# ---------------------------------------------------------------------------
+# As above, by the form of the pages: bf16, or codes with scales.
+_PAGED_APPEND = {c: ("fmha_paged_append", b"SS" + p + s + b"IIiqqqqqqqnnnnnnnn",
+                     ("k", "v", "k_pages", "v_pages", "k_scales", "v_scales", "block_table", "start", "cu_q"))
+                 for c, p, s in ((False, b"BB", b"uu"), (True, b"UU", b"UU"))}
+_PAGED_GATHER = {c: ("fmha_paged_gather", p + s + b"IIiBBqnnnnnnnn",
+                     ("k_pages", "v_pages", "k_scales", "v_scales", "block_table", "seq_lens", "start", "k", "v"))
+                 for c, p, s in ((False, b"BB", b"uu"), (True, b"UU", b"UU"))}
+_PAGED_FWD = {c: ("fmha_fwd_paged", b"S" + p + s + b"IIiBFfuqqqqqrnnnnnnnnnnnnnnn",
+                  ("q", "k_pages", "v_pages", "k_scales", "v_scales", "block_table", "seq_lens", "cu_q", "o", "lse", "sink", "workspace"))
+              for c, p, s in ((False, b"BB", b"uu"), (True, b"UU", b"UU"))}
+
+
+def fmha_paged_cache(n_pages, n_kv_h, page, hd, dtype=_BF16, device="cuda"):
+    """A pool of pages of `page` rows (a power of two, 16 at least): (k_pages, v_pages, k_scales, v_scales), zeros.
+    dtype bfloat16: rows as they are, and no scales (None); float8_e4m3fn: E4M3 codes (uint8) and a scale byte for each
+    row and head."""
+    if hd not in (64, 128, 256, 512) or page < 16 or page > 65536 or page & (page - 1):
+        raise ValueError("hd must be 64, 128, 256 or 512 and page a power of two from 16 to 65536 (got hd=%d page=%d)" % (hd, page))
+    if dtype not in (_BF16, torch.float8_e4m3fn):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float8_e4m3fn, got %s" % (dtype,))
+    kind = _BF16 if dtype == _BF16 else _U8
+    k, v = (torch.zeros((n_pages, n_kv_h, page, hd), dtype=kind, device=device) for _ in range(2))
+    if kind == _BF16:
+        return k, v, None, None
+    return (k, v) + tuple(torch.zeros((n_pages, n_kv_h, page), dtype=_U8, device=device) for _ in range(2))
+
+
+def _pages(k_pages, k_scales, v_scales, block_table):
+    """(n_pages, n_kv_h, page, hd, batch, table width) of a cache and whether it holds codes."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages [n_pages, n_kv_h, page, hd] expected")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table [b, pages of a sequence] expected")
+    codes = k_scales is not None
+    if codes != (v_scales is not None) or codes != (k_pages.dtype == _U8):
+        raise ValueError("k_scales and v_scales go with uint8 pages, and only with them")
+    return tuple(k_pages.shape) + tuple(block_table.shape) + (codes,)
+
+
+def _token_strides(x, heads, hd, batch, ragged, name):
+    """(T or total, strides of the sequence, the token and the head) of x, [b, heads, T, hd] or ragged [total, heads, hd]."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    shape, stride = x.shape, x.stride()
+    if ragged:
+        if len(shape) != 3 or shape[1] != heads or shape[2] != hd:
+            raise ValueError("%s [total, %d, %d] expected with cu_q, got %s" % (name, heads, hd, tuple(shape)))
+        n, sb, st, sh, one = shape[0], 0, stride[0], stride[1], stride[2]
+    else:
+        if len(shape) != 4 or shape[0] != batch or shape[1] != heads or shape[3] != hd:
+            raise ValueError("%s [%d, %d, T, %d] expected, got %s" % (name, batch, heads, hd, tuple(shape)))
+        n, sb, st, sh, one = shape[2], stride[0], stride[2], stride[1], stride[3]
+    if one != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    # strides of dimensions of one element say nothing
+    return n, 0 if batch <= 1 else sb, 0 if n <= 1 else st, 0 if heads <= 1 else sh
+
+
+def fmha_paged_append(k, v, k_pages, v_pages, k_scales, v_scales, block_table, start, cu_q=None, stream=None):
+    """New K and V rows into a cache in pages (fmha_paged_append in include/fmha.h): token t of sequence b goes to row
+    start[b] + t (int32 [b]) of the pages that block_table (int32 [b, n]; entries outside the pool are no pages) lists for it.
+
+    k, v: bf16 [b, n_kv_h, T, hd], or with cu_q (int32 [b + 1]) [total, n_kv_h, hd], sequence b having the rows from cu_q[b]
+    to cu_q[b + 1] - 1; rows of hd contiguous, the other strides multiples of 8 elements.
+    k_pages, v_pages, k_scales, v_scales: fmha_paged_cache."""
+    dev = _device(k, "k")
+    n_pages, heads, page, hd, b, width, codes = _pages(k_pages, k_scales, v_scales, block_table)
+    n, *ks = _token_strides(k, heads, hd, b, cu_q is not None, "k")
+    nv, *vs = _token_strides(v, heads, hd, b, cu_q is not None, "v")
+    if n != nv:
+        raise ValueError("k and v must have the same shape, got %s and %s" % (tuple(k.shape), tuple(v.shape)))
+    pool, scales = (n_pages, heads, page, hd), (n_pages, heads, page)
+    _run(_PAGED_APPEND[codes], dev, k, v, k_pages, pool, v_pages, pool, k_scales, scales, v_scales, scales, block_table, (b, width),
+         start, (b,), cu_q, (b + 1,), _handle(stream, dev), *ks, *vs, b, n, n, heads, hd, page, n_pages, width)
+
+
+def fmha_paged_gather(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, rows, start=None, k=None, v=None, stream=None):
+    """Rows of a cache in pages as contiguous bf16 (fmha_paged_gather in include/fmha.h): k and v [b, n_kv_h, rows, hd], row i
+    being row start[b] + i (int32 [b]; None: i) of sequence b.  Rows from its length seq_lens[b] on, and rows whose page
+    is not there, are left as they are (zeros in tensors allocated here)."""
+    dev = _device(k_pages, "k_pages")
+    n_pages, heads, page, hd, b, width, codes = _pages(k_pages, k_scales, v_scales, block_table)
+    shape = (b, heads, rows, hd)
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together or not at all")
+    if k is None:
+        k, v = (_empty(shape, _BF16, dev, stream) for _ in range(2))
+        with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else _stream_object(stream, dev)):
+            k.zero_()
+            v.zero_()
+    pool, scales = (n_pages, heads, page, hd), (n_pages, heads, page)
+    _run(_PAGED_GATHER[codes], dev, k_pages, pool, v_pages, pool, k_scales, scales, v_scales, scales, block_table, (b, width),
+         seq_lens, (b,), start, (b,), k, shape, v, shape, _handle(stream, dev), b, rows, heads, hd, page, n_pages, width, 0)
+    return k, v
+
+
+_paged_plans = {}  # (chunks, workspace bytes) by shape and device
+
+
+def fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window=0, n_first=0, causal=False, total=None, n_splits=0):
+    """The number of chunks that fmha_fwd_paged uses for sequences of up to s_k keys and T new tokens (total: the rows of a
+    ragged q; n_splits 0: its own choice)."""
+    n = (_lib or load()).fmha_fwd_paged_plan(batch, T, int(total or 0), n_h, n_kv_h, hd, page, s_k, int(window), int(n_first),
+                                             int(bool(causal)), int(total is not None), int(n_splits))
+    _check(n if n < 0 else 0, "fmha_fwd_paged_plan")
+    return n
+
+
+def _paged_plan(batch, T, total, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, n_splits):
+    n = fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, total, n_splits)
+    rows = batch * T if total is None else total
+    return n, rows * n_h * n * (hd + 1) * 4 if n > 1 else 0
+
+
+def fmha_fwd_paged(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q=None, max_q=None, o=None, lse=None, s_k=None,
+                   scale=None, window=0, n_first=0, causal=False, sink=None, n_splits=0, workspace=None, stream=None):
+    """O (bf16) and LSE (fp32) of new tokens over a cache in pages (fmha_fwd_paged in include/fmha.h).
+
+    q: bf16 [b, n_h, T, hd], or with cu_q (int32 [b + 1]) [total, n_h, hd], where sequence b has the rows from cu_q[b] to
+    cu_q[b + 1] - 1 (other rows of o and lse are left as they are); rows contiguous, other strides multiples of 8.  max_q: the
+    most new tokens that a sequence has, if known (with cu_q; it chooses the kernel).  o and lse: contiguous, the shape of q and that without hd.
+    seq_lens: int32 [b], the keys of each sequence, the new tokens' included; s_k: their bound (what the block table
+    holds by default).  Keys on pages that are not there are not attended; with a window, the keys j < n_first stay
+    attended.  n_splits: chunks per sequence, 0: the library's choice.  workspace: an optional uint8 tensor for the chunks'
+    partials; without one the call allocates its own (under capture by torch.cuda.graph in the graph's pool; give one
+    under any other capture)."""
+    dev = _device(q, "q")
+    n_pages, n_kv_h, page, hd, b, width, codes = _pages(k_pages, k_scales, v_scales, block_table)
+    ragged = cu_q is not None
+    shape = q.shape
+    if len(shape) < 2:
+        raise ValueError("q [b, n_h, T, hd] or [total, n_h, hd] expected, got %s" % (tuple(shape),))
+    n_h = shape[1]
+    n, *qs = _token_strides(q, n_h, hd, b, ragged, "q")
+    total, T = (n, n if max_q is None else min(max_q, n)) if ragged else (None, n)
+    if s_k is None:
+        s_k = min(width * page, 1 << 30)
+    if o is None:
+        o = _empty(shape, _BF16, dev, stream)
+    if lse is None:
+        lse = _empty(shape[:-1], _FP32, dev, stream)
+    key = (b, T, total, n_h, n_kv_h, hd, page, min(s_k, width * page), window, n_first, causal, n_splits, dev)
+    plan = _paged_plans.get(key)
+    if plan is None:
+        plan = _remember(_paged_plans, key, _planned(dev, _paged_plan, *key[:-1]))
+    chunks, need = plan
+    handle = at = _handle(stream, dev)
+    if workspace is not None:
+        need, at = workspace.numel(), None
+    elif need:  # the call's own, of its stream's memory
+        workspace = need
+    pool, scales = (n_pages, n_kv_h, page, hd), (n_pages, n_kv_h, page)
+    _run(_PAGED_FWD[codes], dev, q, k_pages, pool, v_pages, pool, k_scales, scales, v_scales, scales, block_table, (b, width), seq_lens, (b,),
+         cu_q, (b + 1,), o, tuple(shape), lse, tuple(shape[:-1]), sink, (n_h,), workspace, at, need, handle, *qs,
+         hd ** -0.5 if scale is None else scale, b, T, n, n_h, n_kv_h, hd, page, n_pages, width, s_k, window, n_first, bool(causal), n_splits, 0)
     return o, lse

@@ -77,6 +77,15 @@ CUresult encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, 
     return r;
 }
 
+}  // namespace
+
+CUresult fmha::encode_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box) {
+    return tensor_map_encoder() ? encode_map(m, type, base, dims, strides, box) : CUDA_ERROR_NOT_SUPPORTED;
+}
+
+namespace {
+
 // K or V [slabs, s_k, hd] bf16 viewed as a 3-D tensor (hd fastest); boxes of
 // 64 head-dim columns (128 bytes, 128-byte swizzle) x box_rows keys x 1 slab.
 // slab_rows: rows from one slab to the next, when the map covers only the first s_k of them.
@@ -161,7 +170,9 @@ SplitPlan split_layout(int T, int s_k, int window, int chunk) {
     return sp;
 }
 
-int sm_count() {
+}  // namespace
+
+int fmha::sm_count() {
     // Per-device cache; any host thread may fill an entry (the value it stores
     // is the same whichever thread wins).  Without a device (planning on a
     // host) the count is GB300's 152 SMs.
@@ -175,6 +186,8 @@ int sm_count() {
     }
     return n;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- planning
 // Kernel families: the decode kernel (8 or 16 query rows per thread block,

@@ -190,6 +190,74 @@ int kv4_tc_kv_tile(int hd);
 int kv4_tc_blocks_per_row_tile(int hd);
 cudaError_t launch_kv4_tc(const Kv4Fwd& a, cudaStream_t stream);
 
+// ---- KV cache in pages (paged_api.cu and the paged_*.cu kernels) -----------
+// K and V pages [n_pages, n_kv_h, page, hd], bf16, or E4M3 codes under a power of two per
+// row and head (scale bytes [n_pages, n_kv_h, page]; byte e: 2^(e - 127), 255: the row is NaN).
+struct PagedCache {
+    void *k_pages, *v_pages;
+    uint8_t *k_scales, *v_scales;  // both NULL: bf16 pages
+    const int* table;              // [batch, width] page of each sequence's keys; outside [0, n_pages): not there
+    int width, n_pages, n_kv_h, page, log_page, hd;
+};
+
+// New tokens: token t of sequence b at element b * batch_stride + t * token_stride of its
+// tensor (cu NULL: T tokens each), or (cu[b] + t) * token_stride (`total` tokens, [batch + 1] bounds cu).
+struct PagedTokens {
+    const int* cu;
+    int batch, T, total;
+};
+
+struct PagedAppend {
+    PagedCache c;
+    PagedTokens t;
+    const __nv_bfloat16 *k, *v;
+    long long k_strides[3], v_strides[3];  // sequence, token, head; elements
+    const int* start;                      // [batch] position of each sequence's first new token
+    unsigned* status;
+};
+cudaError_t launch_paged_append(const PagedAppend& a, cudaStream_t stream);
+
+struct PagedGather {
+    PagedCache c;
+    const int *start, *seq_lens;  // [batch]; start NULL: 0
+    __nv_bfloat16 *k, *v;         // [batch, n_kv_h, rows, hd]
+    int batch, rows;
+    unsigned* status;
+};
+cudaError_t launch_paged_gather(const PagedGather& a, cudaStream_t stream);
+
+struct PagedFwd {
+    PagedCache c;
+    PagedTokens t;
+    const __nv_bfloat16* q;
+    long long q_strides[3];  // sequence, token, head; elements
+    const int* seq_lens;     // [batch] keys of each sequence, new tokens included
+    const float* sink;       // [n_h] or NULL
+    __nv_bfloat16* o;        // [batch, n_h, T, hd], or [total, n_h, hd] with cu
+    float* lse;              // the same rows
+    float *o_part, *lse_part;  // n_splits > 1: [n_splits, rows, hd], [n_splits, rows]
+    float scale_log2;        // scale * log2(e)
+    int n_h, s_k, window, n_first, causal;
+    int group;                  // n_h / n_kv_h
+    long long rows;             // of o
+    int row_tiles;              // of the launch, over all sequences
+    int chunk_tiles, n_splits;  // key tiles per chunk (the last chunk takes what is left) and their number
+    unsigned* status;
+};
+int paged_decode_kv_tile(int hd);                 // keys per tile
+int paged_decode_rows(int hd, long long rows);    // query rows per thread block, given the rows per KV head of a sequence
+cudaError_t launch_paged_decode(const PagedFwd& a, int rows_per_cta, cudaStream_t stream);
+int paged_tc_kv_tile(int hd);
+int paged_tc_rows(int hd);                        // query rows per thread block (two tiles of 128 at hd 64 and 128)
+cudaError_t launch_paged_tc(const PagedFwd& a, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedFwd& a, cudaStream_t stream);
+
+// ---- shared by the API files (api.cu) --------------------------------------
+int sm_count();
+// A 3-D tensor map with 128-byte swizzle (dims and box innermost first; strides in bytes of the outer two).
+CUresult encode_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box);
+
 // ---- host-side errors (api.cu): set the calling thread's message, return code
 int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t e, const char* what);

@@ -1,0 +1,562 @@
+// paged_decode_kernel.cu -- attention over a cache in pages for few query rows per KV head.
+//
+// One thread block handles RT (8 or 16) query rows of one sequence that share a KV head, and
+// one chunk of that sequence's key tiles.  A producer warp streams the tiles from HBM through a ring
+// of TMA boxes (128-byte swizzle): its lanes look the tile's pages up in the block table, one
+// tile ahead, and each issues the boxes of its page (a page that is not there is a box
+// behind the pool, which the TMA fills with zeros).  Four consumer warps each take 16 keys
+// of a tile, which lie in one page:
+//   S^T = K Q^T     mma.sync m16n8k16, keys as M, so that 8 query rows fill N = 8
+//   O^T += V^T P^T  keys as the reduction dimension; P transposed in registers (movmatrix)
+// with the online softmax between them, and merge their partial states at the end.
+//
+// 8-bit pages: the codes are expanded in registers to bf16 (paged_common.cuh, 7 integer and 2
+// multiply instructions for 4 codes), K's as fp32-exact multiples whose row scale goes to the scores,
+// V's to P, both in fp32.  Expansion takes bytes 0 and 2, then 1 and 3 of a word: for K the
+// order of the columns does not matter as long as Q has the same one (Q is stored so), for V the
+// pairs are two keys of one column.  V's operand is loaded by ldmatrix with transposition on pairs of
+// codes, so that rows g and g + 8 of the A operand are columns 2 g and 2 g + 1.
+#include <atomic>
+#include "internal.h"
+#include "paged_common.cuh"
+#include "ptx.cuh"
+
+namespace fmha {
+namespace {
+
+template <int HD, int NB, bool CODES>
+struct PDCfg {
+    static constexpr int RT = 8 * NB;                  // query rows per block
+    static constexpr int KW = HD <= 128 ? 4 : 2;       // key groups of 16 keys
+    static constexpr int DW = 4 / KW;                  // warps that share a key group's columns in P V
+    static constexpr int KT = 16 * KW;                 // keys per tile
+    static constexpr int HDW = HD / DW;                // columns of O per warp
+    static constexpr int NCW = 4;
+    static constexpr int THREADS = (NCW + 1) * 32;
+    static constexpr int ROW = CODES ? HD : HD * 2;    // bytes of a stored row
+    static constexpr int TILE_BYTES = KT * ROW;
+    static constexpr int BOX_BYTES = ROW < 128 ? TILE_BYTES : KT * 128;  // 128 bytes wide
+    static constexpr int NBOX = TILE_BYTES / BOX_BYTES;
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int STAGES = STAGE_BYTES <= 16384 ? 6 : 3;
+    static constexpr int Q_STRIDE = HD * 2 + 16;       // padded row
+    static constexpr int Q_BYTES = RT * Q_STRIDE;
+    static constexpr int SC_BYTES = CODES ? 2 * KT : 0;  // scale bytes of a stage: K's, then V's
+    static constexpr int OFF_Q = STAGES * STAGE_BYTES;
+    static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
+    static constexpr int OFF_LIVE = OFF_BAR + 2 * STAGES * 8;  // per stage: a bit for each 16 keys that are there
+    static constexpr int OFF_SC = OFF_LIVE + (STAGES * 4 + 15) / 16 * 16;
+    static constexpr int OFF_ML = OFF_SC + STAGES * SC_BYTES;
+    static constexpr int SMEM = 1024 + OFF_ML + KW * RT * 8 + 16;
+    static_assert(KW * RT * HD * 4 <= STAGES * STAGE_BYTES, "the combine buffer reuses the ring");
+};
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// One arrival on the barrier when this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+template <int HD, int NB, bool CODES, bool SINK>
+__global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const PagedFwd f) {
+    using C = PDCfg<HD, NB, CODES>;
+    launch_dependents();  // the merge grid may be scheduled now; it waits for this grid's results
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stages = smem;
+    uint8_t* qs = smem + C::OFF_Q;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::STAGES;
+    uint32_t* live = reinterpret_cast<uint32_t*>(smem + C::OFF_LIVE);
+    uint8_t* scales = smem + C::OFF_SC;
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [KW][RT] (max, sum) per key group
+    int* abort_flag = reinterpret_cast<int*>(ml + C::KW * C::RT);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kvh = blockIdx.x % f.c.n_kv_h, split = blockIdx.y;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], CODES ? 33 : 1);
+            mbar_init(&empty[s], C::NCW);
+        }
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    grid_dependency_wait();  // every global access below follows the preceding kernel
+    const PagedTile t = paged_tile(f, blockIdx.x / f.c.n_kv_h, C::RT, f.status);
+    if (t.n <= 0) return;
+    // A tile's boxes: of min(page, KT) keys each, from a multiple of that on.
+    const int box_keys = min(f.c.page, C::KT);
+    const PagedKeys k = paged_keys(f, t, split, C::KT, box_keys);
+    if (k.n <= 0) {
+        paged_write_empty(f, t, kvh, split, 0, HD);
+        return;
+    }
+    __syncthreads();
+
+    // ------------------------------------------------------------ producer
+    if (warp == C::NCW) {
+        // Lane = (K or V, page of the tile, 128-byte column box): at most 2 * 4 * 4 of them
+        // (hd 512 in bf16, 8 column boxes, takes two boxes a lane).
+        const int pages = C::KT / box_keys;
+        const int my_page = lane & 3, my_col = (lane >> 2) & 3, my_v = lane >> 4;
+        const bool mine = my_page < pages && my_col < C::NBOX;
+        const int box_rows = CODES && HD == 64 ? box_keys / 2 : box_keys;  // rows of 128 bytes (two keys at 64 bytes each)
+        if (lane == 0) {
+            tma_prefetch_desc(&tmk);
+            tma_prefetch_desc(&tmv);
+        }
+        const uint64_t pol = l2_policy_evict_first();
+        // the lanes' pages one tile ahead, by 16 keys: granule lane & 3
+        auto entry = [&](int it) {
+            if (it >= k.n) return -1;
+            const int key = k.key(it, C::KT) + 16 * (lane & 3);
+            return 16 * (lane & 3) < C::KT && key < k.to(it) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
+        };
+        int issued = 0, ahead = entry(0);
+        for (int it = 0; it < k.n; ++it) {
+            const int s = it % C::STAGES, page = ahead, key = k.key(it, C::KT);
+            ahead = entry(it + 1);
+            // (all lanes go on or none: collectives follow)
+            if (it >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1, f.status))) break;
+            const unsigned there = __ballot_sync(0xffffffffu, lane < 4 && page >= 0);
+            // the box of page my_page starts at granule my_page * box_keys / 16
+            const int bp = __shfl_sync(0xffffffffu, page, my_page * (box_keys >> 4) & 3);
+            uint8_t* kst = stages + s * C::STAGE_BYTES;
+            if (lane == 0) {
+                live[s] = there;
+                mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+            }
+            __syncwarp();
+            if (mine) {
+                const int bkey = key + my_page * box_keys;
+                const int slab = bp < 0 ? f.c.n_pages * f.c.n_kv_h : bp * f.c.n_kv_h + kvh;  // behind the pool: zeros
+                const int row = (bkey & (f.c.page - 1)) / (box_keys / box_rows);
+                uint8_t* dst = kst + my_v * C::TILE_BYTES + my_page * box_rows * 128;
+                for (int col = my_col; col < C::NBOX; col += 4)
+                    if (FMHA_IN_BOUNDS(s < C::STAGES && row >= 0 && row + box_rows <= f.c.page / (box_keys / box_rows) &&
+                                           my_v * C::TILE_BYTES + col * C::BOX_BYTES + (my_page + 1) * box_rows * 128 <= C::STAGE_BYTES,
+                                       kSitePagedKv, f.status))
+                        tma_load_3d_hint(dst + col * C::BOX_BYTES, my_v ? &tmv : &tmk, col * (CODES ? 128 : 64), row, slab, &full[s], pol);
+            }
+            if constexpr (CODES) {
+                // scale bytes, four keys a lane: lanes 0 .. KT / 4 - 1 K's, the next V's
+                constexpr int PER = C::KT / 4;
+                const int four = (lane % PER) * 4;
+                const int sp = __shfl_sync(0xffffffffu, page, four >> 4);
+                if (lane < 2 * PER) {
+                    const int row = paged_row(f.c, sp, kvh, key + (four & ~15)) + (four & 15);
+                    const bool ok = sp >= 0 && FMHA_IN_BOUNDS(paged_row_ok(f.c, row + 3), kSitePagedRow, f.status);
+                    const uint8_t* src = lane < PER ? f.c.k_scales : f.c.v_scales;
+                    cp_async4(scales + s * C::SC_BYTES + lane * 4, src + (ok ? row : 0), ok);
+                }
+                cp_async_arrive(&full[s]);
+            }
+            ++issued;
+        }
+        // Exit drain: what this warp loaded has landed before the block may exit.
+        drain_ring(full, C::STAGES, issued, f.status);
+        return;
+    }
+
+    // ------------------------------------------------------------ consumers
+    const int kw = warp / C::DW, dw = warp - kw * C::DW;
+
+    // Q rows -> shared memory (zero rows past the end); for codes with columns 1 and 2 of each four exchanged
+    for (int i = threadIdx.x; i < C::RT * (HD / 8); i += C::NCW * 32) {
+        const int r = i / (HD / 8), c8 = i - r * (HD / 8);
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (r < t.n) val = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + c8 * 8));
+        if constexpr (CODES)
+            val = make_uint4(__byte_perm(val.x, val.y, 0x5410), __byte_perm(val.x, val.y, 0x7632), __byte_perm(val.z, val.w, 0x5410),
+                             __byte_perm(val.z, val.w, 0x7632));
+        if (FMHA_IN_BOUNDS(r * C::Q_STRIDE + c8 * 16 + 16 <= C::Q_BYTES, kSitePagedQ, f.status))
+            *reinterpret_cast<uint4*>(qs + r * C::Q_STRIDE + c8 * 16) = val;
+    }
+
+    // Keys of each accumulator row of this thread (rows nb * 8 + 2 * (lane % 4) + i), and those that every row attends.
+    int jlo[NB][2], jhi[NB][2], fhi[NB][2];
+    int all_lo = 0, all_hi = INT_MAX, all_f = INT_MAX;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = t.r0 + nb * 8 + 2 * (lane & 3) + i;
+            paged_row_keys(f, t, k, r, jlo[nb][i], jhi[nb][i], fhi[nb][i]);
+            if (r < t.r0 + t.n) {
+                all_lo = max(all_lo, jlo[nb][i]);
+                all_hi = min(all_hi, jhi[nb][i]);
+                all_f = min(all_f, fhi[nb][i]);
+            }
+        }
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1) {
+        all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, s));
+        all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, s));
+        all_f = min(all_f, __shfl_xor_sync(0xffffffffu, all_f, s));
+    }
+
+    float m[NB][2], l[NB][2];
+    float o[C::HDW / 16][NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+        for (int db = 0; db < C::HDW / 16; ++db) o[db][nb][0] = o[db][nb][1] = o[db][nb][2] = o[db][nb][3] = 0.f;
+    }
+    named_barrier_sync(1, C::NCW * 32);  // Q staged
+
+    const float sl2 = f.scale_log2;
+    const uint32_t qs_addr = smem_u32(qs);
+    const int g = lane >> 2, t4 = lane & 3;
+    bool ok = true;
+
+    for (int it = 0; it < k.n; ++it) {
+        const int s = it % C::STAGES;
+        if (!mbar_wait(&full[s], (it / C::STAGES) & 1, f.status)) {
+            ok = false;
+            break;
+        }
+        const uint32_t kst = smem_u32(stages + s * C::STAGE_BYTES);
+        const uint32_t vst = kst + C::TILE_BYTES;
+        const int kb = k.key(it, C::KT) + 16 * kw;  // this warp's first key
+        const bool there = (live[s] >> kw) & 1u;
+
+        // S^T (16 keys x RT rows) = K Q^T
+        float sc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+        if constexpr (!CODES) {
+            const int k_row = 16 * kw + (lane & 15), k_c8 = lane >> 4;
+            const uint32_t q_addr = qs_addr + ((lane & 7) + (NB >= 2 ? 8 * (lane >> 4) : 0)) * C::Q_STRIDE + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const int d = 16 * kk + 8 * k_c8;
+                uint32_t ka = kst + (d >> 6) * C::BOX_BYTES + k_row * 128 + ((((d & 63) >> 3) ^ (k_row & 7)) << 4);
+                if (!FMHA_IN_BOUNDS(ka >= kst && ka + 16 <= kst + C::TILE_BYTES, kSitePagedLds, f.status)) ka = kst;
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(ka, a0, a1, a2, a3);
+                uint32_t qa = q_addr + kk * 32;
+                if (!FMHA_IN_BOUNDS(qa >= qs_addr && qa + 16 <= qs_addr + C::Q_BYTES, kSitePagedLds, f.status)) qa = qs_addr;
+                uint32_t bq[NB][2];
+                if constexpr (NB == 1)
+                    ldsm_x2(qa, bq[0][0], bq[0][1]);
+                else
+                    ldsm_x4(qa, bq[0][0], bq[0][1], bq[1][0], bq[1][1]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(sc[nb], a0, a1, a2, a3, bq[nb][0], bq[nb][1]);
+            }
+        } else {
+            // Thread (g, t4) takes columns 32 kk + 8 t4 .. + 7 of keys g and g + 8, and of query rows g.
+#pragma unroll
+            for (int kk = 0; kk < HD / 32; ++kk) {
+                uint2 w[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int key = 16 * kw + g + 8 * y, d = 32 * kk + 8 * t4;
+                    const int row = HD == 64 ? key >> 1 : key, byte = HD == 64 ? (key & 1) * 64 + d : d & 127;
+                    uint32_t ka = kst + (HD == 64 ? 0 : d >> 7) * C::BOX_BYTES + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 8);
+                    if (!FMHA_IN_BOUNDS(ka >= kst && ka + 8 <= kst + C::TILE_BYTES, kSitePagedLds, f.status)) ka = kst;
+                    w[y] = lds64(ka);
+                }
+                uint32_t a[2][4];
+                a[0][0] = mul_bf16x2(e4m3x2_raw<true>(w[0].x), kBf16x2Two120);
+                a[0][1] = mul_bf16x2(e4m3x2_raw<true>(w[1].x), kBf16x2Two120);
+                a[0][2] = mul_bf16x2(e4m3x2_raw<false>(w[0].x), kBf16x2Two120);
+                a[0][3] = mul_bf16x2(e4m3x2_raw<false>(w[1].x), kBf16x2Two120);
+                a[1][0] = mul_bf16x2(e4m3x2_raw<true>(w[0].y), kBf16x2Two120);
+                a[1][1] = mul_bf16x2(e4m3x2_raw<true>(w[1].y), kBf16x2Two120);
+                a[1][2] = mul_bf16x2(e4m3x2_raw<false>(w[0].y), kBf16x2Two120);
+                a[1][3] = mul_bf16x2(e4m3x2_raw<false>(w[1].y), kBf16x2Two120);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    uint32_t qa = qs_addr + (nb * 8 + g) * C::Q_STRIDE + (32 * kk + 8 * t4) * 2;
+                    if (!FMHA_IN_BOUNDS(qa + 16 <= qs_addr + C::Q_BYTES, kSitePagedLds, f.status)) qa = qs_addr;
+                    const uint4 q = lds128(qa);
+                    mma_bf16_16816(sc[nb], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                    mma_bf16_16816(sc[nb], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                }
+            }
+        }
+
+        // scale, mask, online softmax (log2 domain)
+        float k0 = 1.f, k1 = 1.f, v0 = 1.f, v1 = 1.f;  // factors of keys g and g + 8
+        if constexpr (CODES) {
+            const uint8_t* ks = scales + s * C::SC_BYTES + 16 * kw + g;
+            k0 = paged_scale(ks[0]);
+            k1 = paged_scale(ks[8]);
+            v0 = paged_scale(ks[C::KT]);
+            v1 = paged_scale(ks[C::KT + 8]);
+        }
+        const bool in_head = k.head(it);
+        const int need_lo = in_head ? 0 : all_lo, need_hi = in_head ? all_f : all_hi;
+        const bool edge = !there || kb < need_lo || kb + 15 > need_hi;
+        const int j0 = kb + g, j1 = j0 + 8;
+        if (edge) {
+            // a key that no row attends has no factor, whatever memory holds there
+            if (!there || j0 < k.from(it) || j0 >= k.to(it)) v0 = 0.f;
+            if (!there || j1 < k.from(it) || j1 >= k.to(it)) v1 = 0.f;
+        }
+        uint32_t pb[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float mx[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x0 = sc[nb][i] * k0 * sl2, x1 = sc[nb][2 + i] * k1 * sl2;
+                if (edge) {
+                    const int lo = in_head ? 0 : jlo[nb][i], hi = in_head ? fhi[nb][i] : jhi[nb][i];
+                    x0 = (there && j0 >= lo && j0 <= hi) ? x0 : -INFINITY;
+                    x1 = (there && j1 >= lo && j1 <= hi) ? x1 : -INFINITY;
+                }
+                sc[nb][i] = x0;
+                sc[nb][2 + i] = x1;
+                mx[i] = fmaxf(x0, x1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 4));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 8));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 16));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float mn = fmaxf(m[nb][i], mx[i]);
+                const float mu = (mn == -INFINITY) ? 0.f : mn;
+                const float alpha = exp2f(m[nb][i] - mu);
+                m[nb][i] = mn;
+                const float p0 = exp2f(sc[nb][i] - mu);
+                const float p1 = exp2f(sc[nb][2 + i] - mu);
+                l[nb][i] = l[nb][i] * alpha + p0 + p1;
+                sc[nb][i] = p0 * v0;
+                sc[nb][2 + i] = p1 * v1;
+#pragma unroll
+                for (int db = 0; db < C::HDW / 16; ++db) {
+                    o[db][nb][i] *= alpha;
+                    o[db][nb][2 + i] *= alpha;
+                }
+            }
+            pb[nb][0] = movmatrix_t(pack_bf16x2(sc[nb][0], sc[nb][1]));
+            pb[nb][1] = movmatrix_t(pack_bf16x2(sc[nb][2], sc[nb][3]));
+        }
+
+        // O^T (columns x RT rows) += V^T P^T
+        // keys 2 t4, 2 t4 + 1 and those 8 further on: which of them V's operand keeps
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (edge) {
+            auto pair = [&](int key) {
+                const bool a = there && key >= k.from(it) && key < k.to(it), b = there && key + 1 >= k.from(it) && key + 1 < k.to(it);
+                return (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
+            };
+            keep0 = pair(kb + 2 * t4);
+            keep1 = pair(kb + 2 * t4 + 8);
+        }
+        if constexpr (!CODES) {
+            const int v_row = 16 * kw + (lane & 7) + 8 * (lane >> 4), v_c8 = (lane >> 3) & 1;
+#pragma unroll
+            for (int db = 0; db < C::HDW / 16; ++db) {
+                const int d = dw * C::HDW + 16 * db + 8 * v_c8;
+                uint32_t va = vst + (d >> 6) * C::BOX_BYTES + v_row * 128 + ((((d & 63) >> 3) ^ (v_row & 7)) << 4);
+                if (!FMHA_IN_BOUNDS(va >= vst && va + 16 <= vst + C::TILE_BYTES, kSitePagedLds, f.status)) va = vst;
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4_t(va, a0, a1, a2, a3);
+                if (edge) {
+                    a0 &= keep0;
+                    a1 &= keep0;
+                    a2 &= keep1;
+                    a3 &= keep1;
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(o[db][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+            }
+        } else {
+            // matrices of ldmatrix: keys 0 .. 7 and 8 .. 15, of 16 columns and of the next 16
+            const int key = 16 * kw + (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+            for (int db = 0; db < C::HDW / 32; ++db) {
+                const int d = dw * C::HDW + 32 * db + 16 * (lane >> 4);
+                const int row = HD == 64 ? key >> 1 : key, byte = HD == 64 ? (key & 1) * 64 + d : d & 127;
+                uint32_t va = vst + (HD == 64 ? 0 : d >> 7) * C::BOX_BYTES + row * 128 + (((byte >> 4) ^ (row & 7)) << 4);
+                if (!FMHA_IN_BOUNDS(va >= vst && va + 16 <= vst + C::TILE_BYTES, kSitePagedLds, f.status)) va = vst;
+                uint32_t r[4];
+                ldsm_x4_t(va, r[0], r[1], r[2], r[3]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    // (any E4M3 code is a finite number in this form: what P multiplies by zero stays zero)
+                    const uint32_t a0 = mul_bf16x2(e4m3x2_raw<true>(r[2 * y]), kBf16x2Two120);
+                    const uint32_t a1 = mul_bf16x2(e4m3x2_raw<false>(r[2 * y]), kBf16x2Two120);
+                    const uint32_t a2 = mul_bf16x2(e4m3x2_raw<true>(r[2 * y + 1]), kBf16x2Two120);
+                    const uint32_t a3 = mul_bf16x2(e4m3x2_raw<false>(r[2 * y + 1]), kBf16x2Two120);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(o[2 * db + y][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ------------------------------------------------------------ epilogue
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 4);
+            l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 8);
+            l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 16);
+        }
+    if (!ok) atomicOr(abort_flag, 1);
+    named_barrier_sync(1, C::NCW * 32);  // every warp is done with the ring
+    if (*abort_flag) return;
+
+    if (dw == 0 && lane < 4) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int mi = kw * C::RT + nb * 8 + 2 * lane + i;
+                if (FMHA_IN_BOUNDS(mi >= 0 && mi < C::KW * C::RT, kSitePagedComb, f.status)) ml[mi] = make_float2(m[nb][i], l[nb][i]);
+            }
+    }
+    named_barrier_sync(1, C::NCW * 32);
+
+    // This warp's O, relative to the row's maximum over all key groups
+    float* comb = reinterpret_cast<float*>(stages);  // [KW][RT][HD]
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = nb * 8 + 2 * t4 + i;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < C::KW; ++w) M = fmaxf(M, ml[w * C::RT + r].x);
+            const float fac = exp2f(m[nb][i] - ((M == -INFINITY) ? 0.f : M));
+#pragma unroll
+            for (int db = 0; db < C::HDW / 16; ++db) {
+                // rows g and g + 8 of the operand: columns g and g + 8 of 16, for codes 2 g and 2 g + 1
+                const int d = dw * C::HDW + 16 * db + (CODES ? 2 * g : g);
+                const int ci = (kw * C::RT + r) * HD + d;
+                if (!FMHA_IN_BOUNDS(ci >= 0 && ci + (CODES ? 1 : 8) < C::KW * C::RT * HD, kSitePagedComb, f.status)) continue;
+                comb[ci] = o[db][nb][i] * fac;
+                comb[ci + (CODES ? 1 : 8)] = o[db][nb][2 + i] * fac;
+            }
+        }
+    named_barrier_sync(1, C::NCW * 32);
+
+    // Sum of the key groups, one divide by the running sum (plus the sink)
+    for (int item = threadIdx.x; item < C::RT * (HD / 8); item += C::NCW * 32) {
+        const int r = item / (HD / 8), d8 = item - r * (HD / 8);
+        if (r >= t.n) continue;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::KW; ++w) M = fmaxf(M, ml[w * C::RT + r].x);
+        const float Mu = (M == -INFINITY) ? 0.f : M;
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::KW; ++w) L += ml[w * C::RT + r].y * exp2f(ml[w * C::RT + r].x - Mu);
+        int head;
+        const long long row = paged_out_row(f, t, kvh, t.r0 + r, head);
+        float inv, lse;
+        paged_finish(M, L, SINK ? sink_log2_of(f.sink, head, f.n_h, f.status) : -INFINITY, inv, lse);
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::KW; ++w) {
+            const float4* src = reinterpret_cast<const float4*>(comb + (w * C::RT + r) * HD + d8 * 8);
+            const float4 u0 = src[0], u1 = src[1];
+            acc[0] += u0.x; acc[1] += u0.y; acc[2] += u0.z; acc[3] += u0.w;
+            acc[4] += u1.x; acc[5] += u1.y; acc[6] += u1.z; acc[7] += u1.w;
+        }
+        if (!FMHA_IN_BOUNDS(row >= 0 && row < f.rows && split < f.n_splits, kSitePagedOut, f.status)) continue;
+        if (f.n_splits == 1) {
+            uint4 pk;
+            pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+            pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+            pk.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+            pk.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
+            *reinterpret_cast<uint4*>(f.o + row * HD + d8 * 8) = pk;
+            if (d8 == 0) f.lse[row] = lse;
+        } else {
+            const long long prow = split * f.rows + row;
+            float4* dst = reinterpret_cast<float4*>(f.o_part + prow * HD + d8 * 8);
+            dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
+            if (d8 == 0) f.lse_part[prow] = lse;
+        }
+    }
+}
+
+template <int HD, int NB, bool CODES, bool SINK>
+cudaError_t launch_t(const PagedFwd& f, cudaStream_t stream) {
+    using C = PDCfg<HD, NB, CODES>;
+    auto kern = paged_decode_kernel<HD, NB, CODES, SINK>;
+    static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 128 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 128) attr_set[dev] = true;
+    }
+    // The pool as rows of 64 bf16 or 128 codes per box; rows of 64 codes in pairs.
+    const int box_keys = f.c.page < C::KT ? f.c.page : C::KT, per_row = CODES && HD == 64 ? 2 : 1;
+    const cuuint64_t row_bytes = (cuuint64_t)C::ROW * per_row;
+    const cuuint64_t dims[3] = {CODES ? row_bytes : (cuuint64_t)HD, (cuuint64_t)(f.c.page / per_row), (cuuint64_t)f.c.n_pages * f.c.n_kv_h};
+    const cuuint64_t strides[2] = {row_bytes, (cuuint64_t)f.c.page * C::ROW};
+    const cuuint32_t box[3] = {CODES ? 128u : 64u, (cuuint32_t)(box_keys / per_row), 1};
+    const CUtensorMapDataType type = CODES ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap tmk = {}, tmv = {};  // without keys nothing is loaded
+    if (f.s_k > 0 && (encode_map_3d(&tmk, type, f.c.k_pages, dims, strides, box) != CUDA_SUCCESS ||
+        encode_map_3d(&tmv, type, f.c.v_pages, dims, strides, box) != CUDA_SUCCESS))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(f.row_tiles * f.c.n_kv_h), f.n_splits);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmk, tmv, f);
+}
+
+template <bool CODES, bool SINK>
+cudaError_t launch_s(const PagedFwd& f, int rows, cudaStream_t stream) {
+    switch (f.c.hd) {
+        case 64: return rows == 16 ? launch_t<64, 2, CODES, SINK>(f, stream) : launch_t<64, 1, CODES, SINK>(f, stream);
+        case 128: return rows == 16 ? launch_t<128, 2, CODES, SINK>(f, stream) : launch_t<128, 1, CODES, SINK>(f, stream);
+        case 256: return rows == 16 ? launch_t<256, 2, CODES, SINK>(f, stream) : launch_t<256, 1, CODES, SINK>(f, stream);
+        case 512: return launch_t<512, 1, CODES, SINK>(f, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int paged_decode_kv_tile(int hd) { return hd <= 128 ? 64 : 32; }
+int paged_decode_rows(int hd, long long rows) { return rows > 8 && hd <= 256 ? 16 : 8; }
+
+cudaError_t launch_paged_decode(const PagedFwd& f, int rows, cudaStream_t stream) {
+    const bool sink = f.sink && f.n_splits == 1, codes = f.c.k_scales != nullptr;
+    if (codes) return sink ? launch_s<true, true>(f, rows, stream) : launch_s<true, false>(f, rows, stream);
+    return sink ? launch_s<false, true>(f, rows, stream) : launch_s<false, false>(f, rows, stream);
+}
+
+}  // namespace fmha

@@ -45,7 +45,7 @@ constexpr bool kCheckedBuild = false;
 // Site codes: 0x1nn row-tile kernel, 0x2nn hd-512 kernel, 0x3nn decode
 // kernel, 0x4nn merge, 0x5nn shared epilogue / softmax helpers, 0x7nn
 // two-row-tile kernel, 0x8nn norm-and-rotation, 4-bit cache append, 4-bit
-// cache attention.
+// cache attention, 0x9nn cache in pages.
 enum CheckSite : unsigned {
     kSiteTcQLoad = 0x101,   // Q box coordinates
     kSiteTcKLoad = 0x102,   // K tile: first key, stage offset
@@ -101,6 +101,16 @@ enum CheckSite : unsigned {
     kSiteKv4Range = 0x80a,   // 4-bit attention: range factor index of an fp16 partial
     kSiteNrRow = 0x80b,      // norm-and-rotation kernel: head row loaded or stored, index of a position or start
     kSiteNrTable = 0x80c,    // norm-and-rotation kernel: row of the cosines and sines
+    kSitePagedSeq = 0x901,   // paged cache: index of a length, a bound, a start or a block-table entry
+    kSitePagedRow = 0x902,   // paged cache: row of a page (and its scale byte)
+    kSitePagedIo = 0x903,    // paged append and gather: row of new tokens or of the contiguous output
+    kSitePagedQ = 0x904,     // paged attention: query row and its place in shared memory
+    kSitePagedKv = 0x905,    // paged attention: shared-memory offset of a key row, or box coordinates
+    kSitePagedLds = 0x906,   // paged attention: shared-memory operand of an mma.sync
+    kSitePagedTmem = 0x907,  // paged attention: tensor-memory columns of S, P and O
+    kSitePagedDesc = 0x908,  // paged attention: K and V stages the MMAs read
+    kSitePagedComb = 0x909,  // paged attention: combine or staging buffer
+    kSitePagedOut = 0x90a,   // paged attention and merge: output or partial row, sink
 };
 
 static __device__ __noinline__ bool bounds_failed(unsigned site, unsigned* status) {

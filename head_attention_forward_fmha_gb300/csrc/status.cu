@@ -44,6 +44,16 @@ const char* check_site_name(unsigned site) {
         case kSiteKv4Range: return "4-bit attention: range factor";
         case kSiteNrRow: return "norm-and-rotation kernel: head row";
         case kSiteNrTable: return "norm-and-rotation kernel: row of the table";
+        case kSitePagedSeq: return "paged cache: length, bound, start or block-table index";
+        case kSitePagedRow: return "paged cache: row of a page";
+        case kSitePagedIo: return "paged append / gather: contiguous row";
+        case kSitePagedQ: return "paged attention: query row";
+        case kSitePagedKv: return "paged attention: key row in shared memory / box coordinates";
+        case kSitePagedLds: return "paged attention: shared-memory operand";
+        case kSitePagedTmem: return "paged attention: TMEM columns";
+        case kSitePagedDesc: return "paged attention: K/V stage of an MMA";
+        case kSitePagedComb: return "paged attention: combine or staging buffer";
+        case kSitePagedOut: return "paged attention: output row";
         case kSiteTcQLoad: return "row-tile kernel: Q box coordinates";
         case kSiteTcKLoad: return "row-tile kernel: K tile key / stage";
         case kSiteTcVLoad: return "row-tile kernel: V tile key / stage";

@@ -543,6 +543,104 @@ int fmha_kv4_append_packed(const struct fmha_kv4_append_args* args);
 int fmha_fwd_kv4_packed(const struct fmha_fwd_kv4_args* args);
 int fmha_fwd_first_packed(const struct fmha_fwd_first_args* args);
 
+/*
+ * A KV cache in pages.  Sequences share a pool of pages of `page` rows each, a power of
+ * two from 16 to 65536:
+ *   k_pages, v_pages [n_pages, n_kv_h, page, hd], in one of two forms:
+ *     bf16 (k_scales and v_scales NULL), or 8 bits: E4M3 codes and a scale byte for every row,
+ *     k_scales, v_scales [n_pages, n_kv_h, page], where byte e stands for 2^(e - 127).  A row's
+ *     scale is the smallest power of two, from 2^-127 on, that brings its largest magnitude to 448 or
+ *     less; code = E4M3(x / scale), to nearest, ties to even (x / scale is exact, so each value is
+ *     rounded once); the row stands for scale * code, which is a bf16 value again (below 2^-133 the
+ *     nearest one).  A row with a NaN or an infinity gets the byte 255 and reads as NaN throughout.
+ *   block_table [batch, table_width] int32: row i of sequence b lies in page
+ *     block_table[b, i / page], row i % page.  An entry outside [0, n_pages) is a page that is
+ *     not there: its rows are not written, not read back and attended by no query row (so the pages
+ *     behind a sliding window can be given back).  Sequences may share pages, as far as no two calls or
+ *     sequences write one row at the same time.
+ * n_pages * n_kv_h * page is at most 2^31 - 65537; offsets are 64-bit.  Pages and scales are 16-byte
+ * aligned.
+ *
+ * New tokens come in one of two forms: T for each sequence (cu_q NULL), or ragged,
+ * `total` token rows of which sequence b has cu_q[b] .. cu_q[b + 1] - 1 (cu_q: [batch + 1] int32, not
+ * falling).  Rows outside [cu_q[0], cu_q[batch]) are no tokens and nothing is written for them.  An
+ * input's three strides, in elements, are those of the sequence (not used with cu_q), the token
+ * and the head: multiples of 8, not negative; hd elements lie next to each other.
+ *
+ * These calls take their arguments in one struct (see below); the fields have the order given there.  Like the
+ * other serving operators they are stream-ordered, allocate nothing and keep nothing between calls.
+ */
+
+/*
+ * fmha_paged_append -- K and V rows of new tokens into the cache: token t of sequence b to row
+ * start[b] + t (start: [batch] int32; negative rows, and rows behind the block table, are left out).
+ */
+struct fmha_paged_append_args {
+    const void *k, *v; /* bf16, n_kv_h heads */
+    void *k_pages, *v_pages;
+    void *k_scales, *v_scales; /* both NULL: bf16 pages */
+    const int *block_table, *start, *cu_q;
+    fmha_stream_t stream;
+    long long k_strides[3], v_strides[3]; /* sequence, token, head */
+    int batch, T, total, n_kv_h, hd, page, n_pages, table_width;
+};
+int fmha_paged_append(const struct fmha_paged_append_args* args);
+
+/*
+ * fmha_paged_gather -- rows of the cache back as contiguous bf16: k, v [batch, n_kv_h, rows, hd],
+ * row i of sequence b being cache row start[b] + i (start NULL: i).  Rows at or behind the sequence's
+ * length seq_lens[b], and those whose page is not there, are left as they are.
+ */
+struct fmha_paged_gather_args {
+    const void *k_pages, *v_pages, *k_scales, *v_scales;
+    const int *block_table, *seq_lens, *start;
+    void *k, *v;
+    fmha_stream_t stream;
+    int batch, rows, n_kv_h, hd, page, n_pages, table_width, reserved;
+};
+int fmha_paged_gather(const struct fmha_paged_gather_args* args);
+
+/*
+ * fmha_fwd_paged -- the forward for new tokens over the cache, their own rows already appended:
+ * O (bf16) and LSE (fp32), [batch, n_h, T, hd] and [batch, n_h, T], or with cu_q [total, n_h, hd]
+ * and [total, n_h].
+ *
+ * seq_lens: [batch] int32, the keys of each sequence, new tokens included (clamped to [0, s_k]); s_k bounds
+ *   them on the host and shapes the launch.  Rows of the pages from a sequence's length on reach no
+ *   result.
+ * T: with cu_q the most tokens that a sequence has, by which the kernel is chosen (a sequence with more
+ *   is computed all the same).
+ * Token t of a sequence with len keys and n new tokens sits at position p = len - n + t and attends
+ *   key j < len iff j's page is there, j <= p with causal, and with a window (j > p - window or
+ *   j < n_first).  A row that attends nothing gets O = 0 and LSE = -inf, or the sink's.
+ * sink: [n_h] fp32 logits or NULL (fmha_fwd_sink).
+ * K may hold anything at keys that a row does not attend, V at keys that no row of the sequence attends;
+ *   V has to be finite at the others.  A NaN score of an attended key makes O and LSE of its
+ *   row NaN, whatever the number of chunks.
+ * n_splits: chunks that a sequence's keys are divided into, 0 for the library's choice.
+ * workspace: fmha_fwd_paged_plan(same arguments) chunks > 1 need
+ *   fmha_workspace_bytes(1, n_h, rows, hd, chunks) bytes, rows being batch * T or total,
+ *   else unused; FMHA_ERR_WORKSPACE if it is smaller.  Two calls that may run at the same time need two.
+ */
+struct fmha_fwd_paged_args {
+    const void *q, *k_pages, *v_pages, *k_scales, *v_scales;
+    const int *block_table, *seq_lens, *cu_q;
+    void* o;
+    float* lse;
+    const float* sink;
+    void* workspace;
+    size_t workspace_bytes;
+    fmha_stream_t stream;
+    long long q_strides[3]; /* sequence, token, head */
+    float scale;
+    int batch, T, total, n_h, n_kv_h, hd, page, n_pages, table_width, s_k, window, n_first, causal, n_splits, reserved;
+};
+int fmha_fwd_paged(const struct fmha_fwd_paged_args* args);
+
+/* The number of chunks that fmha_fwd_paged uses (ragged: 1 with cu_q); a negative FMHA_ERR_* code for invalid arguments. */
+int fmha_fwd_paged_plan(int batch, int T, int total, int n_h, int n_kv_h, int hd, int page, int s_k, int window, int n_first,
+                        int causal, int ragged, int n_splits);
+
 /* ABI version: major * 10000 + minor * 100 + patch. */
 int fmha_version(void);
 
