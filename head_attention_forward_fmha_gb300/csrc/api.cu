@@ -204,6 +204,12 @@ int tc_min_rows(int hd) { return hd >= 256 ? 32 : 64; }
 // SS-form PV, 4 tensor-core kernels with one row tile per block
 std::atomic<int> g_path_override{0};
 
+}  // namespace
+
+int fmha::kernel_path() { return g_path_override.load(); }
+
+namespace {
+
 enum class Path { Decode, TensorCore, TensorCorePair, TensorCoreWide };
 
 struct KernelShape {

@@ -78,7 +78,8 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, int wanted) {
     PagedPlan p;
     const int hd = f->c.hd;
     const long long most = (long long)f->group * f->t.T;  // rows of a sequence under a KV head
-    p.tc = most >= tc_min_rows(hd);
+    const int path = kernel_path();
+    p.tc = path ? path >= 2 : most >= tc_min_rows(hd);
     p.rows = p.tc ? paged_tc_rows(hd) : paged_decode_rows(hd, most);
     const long long tokens = ragged ? f->t.total : (long long)f->t.batch * f->t.T;
     p.row_tiles = ragged ? std::min(tokens * f->group, (tokens * f->group + (long long)f->t.batch * (p.rows - 1)) / p.rows)
