@@ -61,14 +61,14 @@ bool tensor_map_encoder() {
     return g_encode != nullptr;
 }
 
-// Encodes a 3-D map with 128-byte swizzle.  The encoder is a driver call and needs a current
+// Encodes a map (3-D unless said otherwise) with 128-byte swizzle.  The encoder is a driver call and needs a current
 // context, which a host thread has from its first runtime call that makes one
 // current: if this is the thread's first use of CUDA, that is done here.
 CUresult encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
-                    const cuuint64_t* strides, const cuuint32_t* box) {
-    const cuuint32_t elem[3] = {1, 1, 1};
+                    const cuuint64_t* strides, const cuuint32_t* box, int rank = 3) {
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
     auto encode = [&] {
-        return g_encode(m, type, 3, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        return g_encode(m, type, rank, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
     CUresult r = encode();
@@ -79,9 +79,9 @@ CUresult encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, 
 
 }  // namespace
 
-CUresult fmha::encode_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
-                             const cuuint64_t* strides, const cuuint32_t* box) {
-    return tensor_map_encoder() ? encode_map(m, type, base, dims, strides, box) : CUDA_ERROR_NOT_SUPPORTED;
+CUresult fmha::encode_swizzled_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                                   const cuuint64_t* strides, const cuuint32_t* box, int rank) {
+    return tensor_map_encoder() ? encode_map(m, type, base, dims, strides, box, rank) : CUDA_ERROR_NOT_SUPPORTED;
 }
 
 namespace {

@@ -255,9 +255,9 @@ cudaError_t launch_paged_merge(const PagedFwd& a, cudaStream_t stream);
 // ---- shared by the API files (api.cu) --------------------------------------
 int sm_count();
 int kernel_path();  // what fmha_set_kernel_path has set
-// A 3-D tensor map with 128-byte swizzle (dims and box innermost first; strides in bytes of the outer two).
-CUresult encode_map_3d(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
-                       const cuuint64_t* strides, const cuuint32_t* box);
+// A tensor map with 128-byte swizzle (dims and box innermost first; strides in bytes of all but the innermost).
+CUresult encode_swizzled_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box, int rank);
 
 // ---- host-side errors (api.cu): set the calling thread's message, return code
 int fail(int code, const char* fmt, ...);

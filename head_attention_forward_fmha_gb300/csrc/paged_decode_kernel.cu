@@ -523,8 +523,8 @@ cudaError_t launch_t(const PagedFwd& f, cudaStream_t stream) {
     const cuuint32_t box[3] = {CODES ? 128u : 64u, (cuuint32_t)(box_keys / per_row), 1};
     const CUtensorMapDataType type = CODES ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap tmk = {}, tmv = {};  // without keys nothing is loaded
-    if (f.s_k > 0 && (encode_map_3d(&tmk, type, f.c.k_pages, dims, strides, box) != CUDA_SUCCESS ||
-        encode_map_3d(&tmv, type, f.c.v_pages, dims, strides, box) != CUDA_SUCCESS))
+    if (f.s_k > 0 && (encode_swizzled_map(&tmk, type, f.c.k_pages, dims, strides, box, 3) != CUDA_SUCCESS ||
+        encode_swizzled_map(&tmv, type, f.c.v_pages, dims, strides, box, 3) != CUDA_SUCCESS))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(f.row_tiles * f.c.n_kv_h), f.n_splits);

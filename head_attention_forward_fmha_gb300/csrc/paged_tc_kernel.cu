@@ -14,18 +14,25 @@
 // and PV(u) before QK(u + 2) in one slot is all the order that the slot needs, since MMAs
 // complete in order.  While the softmax of one slot runs, the tensor cores work on the other.
 //
-// Warp roles (13 warps): with two row tiles 0..3 and 4..7 softmax and epilogue of A and B (one row
-// per thread), 8 MMA issue and tensor memory, 9..12 loaders; with one 0..3, 4, and 5..12.  The
-// loaders look the pages up in the block table, two tiles ahead, and copy bf16 rows into the
-// swizzled operand layout (cp.async, 16 bytes each, zeros for keys that no row of the block attends, so that
-// nothing stale is multiplied), or load codes, expand them to bf16 (paged_common.cuh) and
-// store those.  Expanded columns 1 and 2 of each four change places: Q is stored the same way, and
-// O's columns are put right in the epilogue.
+// Warp roles: 4 warps per row tile softmax and epilogue (one row per thread), one warp MMA issue and
+// tensor memory, one producer, and for codes the converters.
+//   bf16 pages: the producer's lanes look a tile's pages up in the block table, one tile ahead, and load
+//     its boxes by TMA into the swizzled operand layout (a page that is not there is a box behind the
+//     pool: zeros).  Of a V tile at the end of the keys (or at the start of a window) it then clears the
+//     rows that no query row attends, so that nothing stale is multiplied.
+//   8-bit pages up to hd 256: bulk copies of 16 keys' codes each into a raw buffer, the scale
+//     bytes by cp.async, and the converters expand them to bf16 (paged_common.cuh) into the operand
+//     layout.  Expanded columns 1 and 2 of each four change places: Q is stored the same way, and O's
+//     columns are put right in the epilogue.
+//   8-bit pages at hd 512, where shared memory has no room for a raw buffer: eight warps load codes into
+//     registers, one tile ahead, and expand those.
 //
-// Softmax: scores against a reference, the maximum of the first tile in which the row attends a key.  P in
-// bf16 and its fp32 sum have the exponent range for what follows, so the reference moves (and O
-// is rescaled) only where a tile's sum passes 2^40: no maximum is taken otherwise.
+// Softmax: scores against a reference, the maximum of the first tile in which the row attends a key,
+// rounded up to a whole number.  P in bf16 and its fp32 sum have the exponent range for what follows, so
+// no further maximum is taken: only where 64 weights sum to over 2^40 does the reference move, by a
+// whole number, and the sum, O and the tile's weights so far are multiplied by the power of two.
 #include <atomic>
+#include <type_traits>
 #include "internal.h"
 #include "paged_common.cuh"
 #include "ptx.cuh"
@@ -33,20 +40,24 @@
 namespace fmha {
 namespace {
 
-template <int HD>
+template <int HD, bool CODES>
 struct PTCfg {
     static constexpr int BM = 128;
     static constexpr int NRT = HD <= 128 ? 2 : 1;         // row tiles
     static constexpr int BN = HD <= 128 ? 128 : 64;       // keys per tile
     static constexpr int HDV = HD == 512 ? 256 : HD;      // columns of O per block
     static constexpr int PARTS = HD / HDV;                // blocks per row tile
-    static constexpr int STG = HD == 512 ? 1 : 2;         // K and V stages
+    static constexpr bool RAW = CODES && HD <= 256;       // codes by way of a raw buffer
+    static constexpr int STG = HD == 512 ? 1 : HD == 64 ? 4 : 2;  // K and V stages
     static constexpr int NKC = HD == 512 ? 2 : 1;         // column chunks of a K tile, each with barriers of its own
     static constexpr int KCH = HD / NKC;
+    static constexpr int NB = KCH / 64;                   // 64-column blocks of a K chunk, and of V
     static constexpr int SW = 4 * NRT;                    // softmax warps
-    static constexpr int LW = 12 - SW;                    // loader warps
-    static constexpr int LT = 32 * LW;
-    static constexpr int THREADS = 13 * 32;
+    static constexpr int CW = !CODES ? 0 : NRT == 2 ? 4 : 8;  // converter warps
+    static constexpr int CT = 32 * CW;
+    static constexpr int WARPS = SW + 2 + CW;             // + MMA issuer (warp SW) and producer (SW + 1)
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int K_ARRIVALS = CODES ? CT : 1;     // on a full barrier of K or V
     static constexpr int Q_TILE = BM * HD * 2;
     static constexpr int Q_BYTES = NRT * Q_TILE;
     static constexpr int K_TILE = BN * HD * 2;
@@ -55,33 +66,55 @@ struct PTCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int OFF_K = Q_BYTES;
     static constexpr int OFF_V = OFF_K + STG * K_TILE;
-    static constexpr int OFF_BAR = OFF_V + STG * V_TILE;
-    static constexpr int N_BARS = 1 + 2 * STG * NKC + 2 * STG + 6 + 1;
+    static constexpr int OFF_RAW = OFF_V + STG * V_TILE;  // codes of K, of V
+    static constexpr int RAW_TILE = BN * HD;
+    static constexpr int OFF_SC = OFF_RAW + (RAW ? 2 * RAW_TILE : 0);  // scale bytes of K, of V
+    static constexpr int OFF_BAR = OFF_SC + (RAW ? 2 * BN : 0);
+    static constexpr int N_BARS = 1 + 2 * STG * NKC + 2 * STG + 6 + 1 + 4;
     static constexpr int NEED = 1024 + OFF_BAR + N_BARS * 8 + 16;
     static constexpr int SMEM = NEED < 120000 ? 120000 : NEED;  // one block per SM: each takes all of tensor memory
+    static_assert(NB == HDV / 64, "K chunks and V tiles have the same layout");
     static_assert(O_COL + NRT * HDV <= TMEM_COLS, "S and O fit in tensor memory");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Operand layout of a K chunk and of a V tile, NB blocks of 64 columns wide: groups of 8 keys, in each
+// the blocks one after another (1024 bytes: 8 rows of 128, 16-byte chunk c of row r at chunk c ^ (r % 8)).
+// So the rows of a page lie together, all blocks of them, and one TMA box brings them: a box costs ~50
+// clocks and ~2.4 for each 128 bytes (32 KB in boxes of 2 KB 1621 clocks, of 4 KB 1019, of 32 KB 669).
+template <int NB>
+__device__ __forceinline__ int operand_row(int key, int block) {
+    return (key >> 3) * (NB * 1024) + block * 1024 + (key & 7) * 128;
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// One arrival on the barrier when this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 32 packed words times a packed factor, in this thread's TMEM lane.
+__device__ __forceinline__ void tmem_scale_pairs(uint32_t taddr, uint32_t factor) {
+    float v[32];
+    tmem_ld32(taddr, v);
+    tmem_wait_ld();
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = mul_bf16x2(__float_as_uint(v[i]), factor);
+    tmem_st32u(taddr, w);
+}
+
+// 16 codes of a row as two 16-byte chunks of its bf16 operand row (128-byte swizzle).
+__device__ __forceinline__ void store_expanded(uint8_t* box_row, int c0, int key, const uint4& codes, const PagedFactor& f) {
+    uint32_t r[8];
+    paged_values4(codes.x, f, r[0], r[1]);
+    paged_values4(codes.y, f, r[2], r[3]);
+    paged_values4(codes.z, f, r[4], r[5]);
+    paged_values4(codes.w, f, r[6], r[7]);
+    *reinterpret_cast<uint4*>(box_row + ((c0 ^ (key & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(box_row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 // What a loader thread needs of one key tile: this lane's granule of 16 keys (lane < BN / 16) as a row of the
@@ -90,7 +123,7 @@ struct TileRows {
     int row, from, to;  // from, to: relative to the tile's first key
 };
 
-// One loader thread's share of a tile of codes: N pieces of 16 columns, PPR per key, going round the LT threads.
+// One converter thread's share of a tile of codes (hd 512): N pieces of 16 columns, PPR per key, going round the LT threads.
 template <int N, int PPR, int LT>
 struct Codes {
     uint4 codes[N];
@@ -110,36 +143,21 @@ struct Codes {
         }
     }
 
-    // As bf16 into a tile of 64-column boxes of `rows` 128-byte rows (16-byte chunk c of row r at chunk c ^ (r % 8)).
-    // A piece is two chunks; pieces 4 apart (their chunks lie in the same bank group) take theirs in the other order.
+    // As bf16 into an operand tile of `rows` keys.
     __device__ __forceinline__ void store(int tid, uint8_t* tile, int rows, unsigned* status) const {
 #pragma unroll
         for (int p = 0; p < N; ++p) {
-            const int idx = p * LT + tid, key = idx / PPR, i = idx % PPR;
-            const PagedFactor f = paged_factor(scales[p]);
-            uint32_t r[8];
-            paged_values4(codes[p].x, f, r[0], r[1]);
-            paged_values4(codes[p].y, f, r[2], r[3]);
-            paged_values4(codes[p].z, f, r[4], r[5]);
-            paged_values4(codes[p].w, f, r[6], r[7]);
-            const bool swap = PPR > 4 && (i & 4);
-            const uint4 a = make_uint4(r[0], r[1], r[2], r[3]), b = make_uint4(r[4], r[5], r[6], r[7]);
-            const int off = (i >> 2) * rows * 128 + key * 128, c0 = (i & 3) * 2 + (swap ? 1 : 0);
-            if (!FMHA_IN_BOUNDS(key < rows && off >= 0 && off + 128 <= rows * ((PPR + 3) / 4) * 128, kSitePagedKv, status)) continue;
-            uint4 x = a, y = b;
-            if (swap) {
-                x = b;
-                y = a;
-            }
-            *reinterpret_cast<uint4*>(tile + off + ((c0 ^ (key & 7)) << 4)) = x;
-            *reinterpret_cast<uint4*>(tile + off + (((c0 ^ 1) ^ (key & 7)) << 4)) = y;
+            const int idx = p * LT + tid, key = idx / PPR, i = idx % PPR, off = operand_row<PPR / 4>(key, i >> 2);
+            if (FMHA_IN_BOUNDS(key < rows && off >= 0 && off + 128 <= rows * (PPR / 4) * 128, kSitePagedKv, status))
+                store_expanded(tile + off, (i & 3) * 2, key, codes[p], paged_factor(scales[p]));
         }
     }
 };
 
 template <int HD, bool CODES, bool SINK>
-__global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const PagedFwd f) {
-    using C = PTCfg<HD>;
+__global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const PagedFwd f) {
+    using C = PTCfg<HD, CODES>;
     constexpr int BM = C::BM, BN = C::BN, STG = C::STG;
     launch_dependents();  // the merge grid may be scheduled now; it waits for this grid's results
     extern __shared__ uint8_t smem_raw[];
@@ -157,24 +175,28 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
     uint64_t* p_ready = s_full + 2;    // [2]
     uint64_t* o_done = p_ready + 2;    // [2]
     uint64_t* mma_drain = o_done + 2;  // every MMA the issuer launched has completed (exit drain)
+    uint64_t* raw_full = mma_drain + 1;   // [2] raw codes and scale bytes of K, of V (bf16: a V tile to be cleared in part)
+    uint64_t* raw_empty = raw_full + 2;   // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x % C::PARTS, kvh = blockIdx.x / C::PARTS % f.c.n_kv_h, split = blockIdx.y;
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 12 * 32);
+        mbar_init(q_full, (C::SW + C::CW) * 32);
         for (int s = 0; s < STG * C::NKC; ++s) {
-            mbar_init(&k_full[s], C::LT);
+            mbar_init(&k_full[s], C::K_ARRIVALS);
             mbar_init(&k_empty[s], 1);
         }
         for (int s = 0; s < STG; ++s) {
-            mbar_init(&v_full[s], C::LT);
+            mbar_init(&v_full[s], C::K_ARRIVALS);
             mbar_init(&v_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_ready[s], 128);
             mbar_init(&o_done[s], 1);
+            mbar_init(&raw_full[s], C::RAW ? 33 : 1);
+            mbar_init(&raw_empty[s], CODES ? C::CT : 1);
         }
         mbar_init(mma_drain, 1);
         mbar_fence_init();
@@ -182,7 +204,8 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
     grid_dependency_wait();  // every global access below follows the preceding kernel
     const PagedTile t = paged_tile(f, blockIdx.x / C::PARTS / f.c.n_kv_h, BM * C::NRT, f.status);
     if (t.n <= 0) return;
-    const PagedKeys k = paged_keys(f, t, split, BN, 16);
+    const int box_keys = CODES && !C::RAW ? 16 : min(f.c.page, BN);  // keys that are copied at once, from a multiple of that on
+    const PagedKeys k = paged_keys(f, t, split, BN, box_keys);
     if (k.n <= 0) {  // nothing to attend in this chunk: no tensor memory, no Q
         paged_write_empty(f, t, kvh, split, part * C::HDV, C::HDV);
         return;
@@ -196,27 +219,26 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n_rt = C::NRT == 2 && t.n > BM ? 2 : 1;
-    const int n_units = k.n * n_rt;
 
     // Q's rows as 64-column boxes of 128 swizzled rows per row tile, zeros behind the last row; of the
     // opposite sign for a negative scale (the softmax takes its magnitude), for codes with columns 1 and 2 of each
-    // four exchanged.  All but the MMA warp take part, w = 0 .. 11.
+    // four exchanged.  All but the MMA warp and the producer take part, w = 0 .. SW + CW - 1.
     auto load_q = [&](int w) {
-        constexpr int PPR = HD / 8, BATCH = 4;
+        constexpr int PPR = HD / 8, BATCH = HD <= 128 ? 4 : 8, QT = (C::SW + C::CW) * 32;
         const uint32_t sign = f.scale_log2 < 0.f ? 0x80008000u : 0u;
         const int total = n_rt * BM * PPR;
 #pragma unroll 1
-        for (int base = w * 32 + lane; base < total; base += 12 * 32 * BATCH) {
+        for (int base = w * 32 + lane; base < total; base += QT * BATCH) {
             uint4 u[BATCH];
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
-                const int i = base + y * 12 * 32, r = i / PPR;
+                const int i = base + y * QT, r = i / PPR;
                 u[y] = make_uint4(0u, 0u, 0u, 0u);
                 if (i < total && r < t.n) u[y] = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + i % PPR * 8));
             }
 #pragma unroll
             for (int y = 0; y < BATCH; ++y) {
-                const int i = base + y * 12 * 32, r = i / PPR, c = i % PPR;
+                const int i = base + y * QT, r = i / PPR, c = i % PPR;
                 uint4 v = u[y];
                 if constexpr (CODES)
                     v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
@@ -230,25 +252,213 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
         mbar_arrive(q_full);
     };
 
-    if (warp > C::SW) {
-        // ------------------------------------------------------------ loaders
+    // The page of this lane's granule of 16 keys (lane < BN / 16) of tile j, -1 where no key is needed.
+    auto page_of = [&](int j) {
+        if (j >= k.n || lane >= BN / 16) return -1;
+        const int key = k.key(j, BN) + 16 * lane;  // (the copy that it begins may reach into the keys)
+        return key < k.to(j) && (key | (box_keys - 1)) >= k.from(j) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
+    };
+    // all lanes of the warp go on or none: collectives follow
+    auto wait_all = [&](uint64_t* bar, unsigned parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, f.status)); };
+
+    if (warp == C::SW + 1) {
+        // ------------------------------------------------------------ producer
         // K_0, K_1, V_0, K_2, V_1, ...: the order in which the MMA warp takes them.
-        const int tid = threadIdx.x - (C::SW + 1) * 32;
-        // this lane's page of tile j, and with it the tile's rows
-        auto page_of = [&](int j) {
-            if (j >= k.n || lane >= BN / 16) return -1;
-            const int key = k.key(j, BN) + 16 * lane;
-            return key < k.to(j) && key + 16 > k.from(j) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
-        };
-        auto rows_of = [&](int j, int page) {
-            const int key0 = k.key(j, BN);
-            return TileRows{paged_row(f.c, page, kvh, key0 + 16 * lane), k.from(j) - key0, k.to(j) - key0};
-        };
+        if constexpr (!CODES) {
+            if (lane == 0) {
+                tma_prefetch_desc(&tmk);
+                tma_prefetch_desc(&tmv);
+            }
+            const int log_box = __ffs(box_keys) - 1, boxes = BN >> log_box;
+            // blocks block0 .. block0 + NB - 1 of K or V, all keys of tile j
+            auto load = [&](const CUtensorMap* map, int j, int page, int block0, uint8_t* tile, uint64_t* bar) {
+                const int key0 = k.key(j, BN);
+                if (lane == 0) mbar_arrive_expect_tx(bar, BN * C::NB * 128);
+                __syncwarp();
+                const int p = __shfl_sync(0xffffffffu, page, lane << (log_box - 4) & 31);
+                const int slab = p < 0 ? f.c.n_pages * f.c.n_kv_h : p * f.c.n_kv_h + kvh;  // behind the pool: zeros
+                const int row = (key0 + (lane << log_box)) & (f.c.page - 1);
+                if (lane < boxes && FMHA_IN_BOUNDS(row + box_keys <= f.c.page && ((lane + 1) << log_box) <= BN, kSitePagedKv, f.status))
+                    tma_load_5d(tile + (lane << log_box) * C::NB * 128, map, 0, 0, block0, row >> 3, slab, bar);
+            };
+            bool ok = true;
+            int k_issued = 0, v_issued = 0, cleared = 0, ahead = page_of(1), page_k = page_of(0), page_v = page_k;
+#pragma unroll 1
+            for (int j = 0; ok && j <= k.n; ++j) {
+                const int page = ahead;  // of tile j + 1
+                ahead = page_of(j + 2);
+                if (j < k.n) {
+                    const int s = j % STG;
+#pragma unroll 1
+                    for (int c = 0; ok && c < C::NKC; ++c) {
+                        ok = j < STG || wait_all(&k_empty[s * C::NKC + c], ((j / STG) - 1) & 1);
+                        if (ok) {
+                            load(&tmk, j, page_k, c * C::NB, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), &k_full[s * C::NKC + c]);
+                            ++k_issued;
+                        }
+                    }
+                }
+                if (ok && j > 0) {
+                    const int jv = j - 1, s = jv % STG;
+                    ok = jv < STG || wait_all(&v_empty[s], ((jv / STG) - 1) & 1);
+                    if (ok) {
+                        const int key0 = k.key(jv, BN), from = k.from(jv) - key0, to = k.to(jv) - key0;
+                        uint8_t* tile = sv + s * C::V_TILE;
+                        if (from <= 0 && to >= BN) {
+                            load(&tmv, jv, page_v, part * C::NB, tile, &v_full[s]);
+                        } else {
+                            load(&tmv, jv, page_v, part * C::NB, tile, &raw_full[0]);
+                            ok = wait_all(&raw_full[0], cleared++ & 1);
+                            const int lead = max(from, 0), rows = lead + BN - min(to, BN);  // those before `from`, those from `to` on
+                            for (int i = lane; ok && i < rows * (C::HDV / 8); i += 32) {
+                                const int r = i / (C::HDV / 8), c = i % (C::HDV / 8), row = r < lead ? r : r - lead + to;
+                                if (FMHA_IN_BOUNDS(row >= 0 && row < BN, kSitePagedKv, f.status))
+                                    *reinterpret_cast<uint4*>(tile + operand_row<C::NB>(row, c >> 3) + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (ok && lane == 0) mbar_arrive(&v_full[s]);
+                        }
+                        ++v_issued;
+                    }
+                }
+                page_v = page_k;
+                page_k = page;
+            }
+            // Exit drain: what was loaded has landed before the block exits, whatever the waits said.
+            drain_ring(k_full, STG * C::NKC, k_issued, f.status);
+            drain_ring(v_full, STG, v_issued, f.status);
+        } else if constexpr (C::RAW) {
+            // One raw buffer each for K and V, filled again as soon as the converters have read it: they go
+            // K_0 K_1 V_0 K_2 V_1 ..., so K_{j+2} can be on its way while they are at V_j.
+            const uint64_t pol = l2_policy_evict_first();
+            bool ok = true;
+            int issued[2] = {0, 0};
+            const int log_box = __ffs(box_keys) - 1;
+            auto load = [&](int x, int j, int page) {
+                ok = ok && (issued[x] == 0 || wait_all(&raw_empty[x], (issued[x] - 1) & 1));
+                if (!ok) return;
+                const int key0 = k.key(j, BN);
+                const uint8_t* const pool = static_cast<const uint8_t*>(x ? f.c.v_pages : f.c.k_pages);
+                const uint8_t* const sc = x ? f.c.v_scales : f.c.k_scales;
+                uint8_t* const raw = smem + C::OFF_RAW + x * C::RAW_TILE;
+                // box `lane` begins with granule lane * box_keys / 16
+                const int p = __shfl_sync(0xffffffffu, page, lane << (log_box - 4) & 31);
+                const int key = key0 + (lane << log_box), row = p < 0 ? -1 : ((p * f.c.n_kv_h + kvh) << f.c.log_page) + (key & (f.c.page - 1));
+                const bool there = (lane << log_box) < BN && row >= 0 &&
+                                   FMHA_IN_BOUNDS(paged_row_ok(f.c, row + box_keys - 1LL) && ((lane + 1) << log_box) <= BN, kSitePagedRow, f.status);
+                const unsigned boxes = __ballot_sync(0xffffffffu, there);
+                if (lane == 0) mbar_arrive_expect_tx(&raw_full[x], __popc(boxes) * box_keys * HD);
+                __syncwarp();
+                if (there) bulk_load_hint(smem_u32(raw + (lane << log_box) * HD), pool + (long long)row * HD, box_keys * HD, &raw_full[x], pol);
+                // scale bytes, four keys a lane
+                const int first = __shfl_sync(0xffffffffu, paged_row(f.c, page, kvh, key0 + 16 * lane), lane >> 2);
+                if (lane < BN / 4) {
+                    const bool live = first >= 0 && FMHA_IN_BOUNDS(paged_row_ok(f.c, first + 15LL), kSitePagedRow, f.status);
+                    cp_async4(smem + C::OFF_SC + x * BN + lane * 4, sc + (live ? first + (lane & 3) * 4 : 0), live);
+                }
+                cp_async_arrive(&raw_full[x]);
+                ++issued[x];
+            };
+            int page0 = page_of(0), page1 = page_of(1);
+            load(0, 0, page0);
+            load(1, 0, page0);
+            if (k.n > 1) load(0, 1, page1);
+#pragma unroll 1
+            for (int j = 2; ok && j <= k.n; ++j) {
+                const int page2 = page_of(j);
+                if (j < k.n) load(0, j, page2);
+                load(1, j - 1, page1);
+                page1 = page2;
+            }
+            // Exit drain: the last copies have landed (those before them had to, for the buffer to be free).
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (issued[x] > 0) mbar_wait(&raw_full[x], (issued[x] - 1) & 1, f.status);
+        }
+    } else if (warp > C::SW + 1) {
+        // ------------------------------------------------------------ converters
+        const int tid = threadIdx.x - (C::SW + 2) * 32;
         bool ok = true;
-        if constexpr (CODES) {
+        load_q(warp - 2);
+        if constexpr (C::RAW) {
+            // Pieces of 16 columns, PPR per key, going round the threads, four read before they are expanded.
+            auto convert = [&](int j, int x, uint8_t* tile) {
+                constexpr int PPR = HD / 16, N = BN * PPR / C::CT, STEP = C::CT / PPR;  // keys from one piece of a thread to the next
+                const int key0 = k.key(j, BN), from = k.from(j) - key0, to = k.to(j) - key0;
+                const uint8_t* const raw = smem + C::OFF_RAW + x * C::RAW_TILE;
+                const uint8_t* const sc = smem + C::OFF_SC + x * BN;
+                const int i = tid % PPR, first = tid / PPR;
+                // a piece is two neighbouring chunks; pieces 4 apart lie in the same banks: they store theirs in the other order
+                const int c0 = (i & 3) * 2 ^ (first & 7), flip = PPR > 4 ? (i >> 2) & 1 : 0;
+                static_assert(N % 4 == 0 && STEP % 8 == 0, "pieces in fours, at one place of the swizzle");
+#pragma unroll
+                for (int n0 = 0; n0 < N; n0 += 4) {
+                    uint4 u[4];
+                    uint32_t byte[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int key = first + (n0 + n) * STEP;
+                        u[n] = *reinterpret_cast<const uint4*>(raw + key * HD + i * 16);
+                        byte[n] = sc[key];
+                        if (key < from || key >= to) {  // nothing stale is multiplied
+                            u[n] = make_uint4(0u, 0u, 0u, 0u);
+                            byte[n] = 127u;
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int key = first + (n0 + n) * STEP;
+                        const PagedFactor fac = paged_factor(byte[n]);
+                        uint32_t r[8];
+                        paged_values4(u[n].x, fac, r[0], r[1]);
+                        paged_values4(u[n].y, fac, r[2], r[3]);
+                        paged_values4(u[n].z, fac, r[4], r[5]);
+                        paged_values4(u[n].w, fac, r[6], r[7]);
+                        if (!FMHA_IN_BOUNDS(key < BN && (i >> 2) < C::NB, kSitePagedKv, f.status)) continue;
+                        uint8_t* const row = tile + operand_row<C::NB>(key, i >> 2);
+                        uint4 a = make_uint4(r[0], r[1], r[2], r[3]), b = make_uint4(r[4], r[5], r[6], r[7]);
+                        if (flip) {
+                            const uint4 y = a;
+                            a = b;
+                            b = y;
+                        }
+                        *reinterpret_cast<uint4*>(row + ((c0 ^ flip) << 4)) = a;
+                        *reinterpret_cast<uint4*>(row + ((c0 ^ 1 ^ flip) << 4)) = b;
+                    }
+                }
+                fence_proxy_async_smem();
+            };
+            // K_0, K_1, V_0, K_2, V_1, ...
+#pragma unroll 1
+            for (int j = 0; ok && j <= k.n; ++j) {
+                if (j < k.n) {
+                    const int s = j % STG;
+                    ok = mbar_wait(&raw_full[0], j & 1, f.status) && (j < STG || mbar_wait(&k_empty[s], ((j / STG) - 1) & 1, f.status));
+                    if (ok) {
+                        convert(j, 0, sk + s * C::K_TILE);
+                        mbar_arrive(&raw_empty[0]);
+                        mbar_arrive(&k_full[s]);
+                    }
+                }
+                if (ok && j > 0) {
+                    const int jv = j - 1, s = jv % STG;
+                    ok = mbar_wait(&raw_full[1], jv & 1, f.status) && (jv < STG || mbar_wait(&v_empty[s], ((jv / STG) - 1) & 1, f.status));
+                    if (ok) {
+                        convert(jv, 1, sv + s * C::V_TILE);
+                        mbar_arrive(&raw_empty[1]);
+                        mbar_arrive(&v_full[s]);
+                    }
+                }
+            }
+        } else if constexpr (CODES) {
+            auto rows_of = [&](int j, int page) {
+                const int key0 = k.key(j, BN);
+                return TileRows{paged_row(f.c, page, kvh, key0 + 16 * lane), k.from(j) - key0, k.to(j) - key0};
+            };
             constexpr int KPPR = C::KCH / 16, VPPR = C::HDV / 16;
-            Codes<BN * KPPR / C::LT, KPPR, C::LT> kb[C::NKC];
-            Codes<BN * VPPR / C::LT, VPPR, C::LT> vb;
+            Codes<BN * KPPR / C::CT, KPPR, C::CT> kb[C::NKC];
+            Codes<BN * VPPR / C::CT, VPPR, C::CT> vb;
             const uint8_t* const kp = static_cast<const uint8_t*>(f.c.k_pages);
             const uint8_t* const vp = static_cast<const uint8_t*>(f.c.v_pages) + part * C::HDV;
             auto fetch_k = [&](const TileRows& r) {
@@ -259,7 +469,6 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
             TileRows r_v = rows_of(0, page_of(0));
             fetch_k(r_v);
             vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
-            load_q(warp - 1);
             // K_j and then V_{j - 1}, for j up to k.n (where there is no K_j)
 #pragma unroll 1
             for (int j = 0; ok && j <= k.n; ++j) {
@@ -271,150 +480,110 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
 #pragma unroll
                     for (int c = 0; c < C::NKC; ++c) {
                         const int q = s * C::NKC + c;
-                        ok = ok && (j < STG || mbar_wait(&k_empty[q], ((j / STG) - 1) & 1, f.status));
+                        ok = ok && (j < STG || wait_all(&k_empty[q], ((j / STG) - 1) & 1));
                         if (ok) {
                             kb[c].store(tid, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), BN, f.status);
                             fence_proxy_async_smem();
                             mbar_arrive(&k_full[q]);
                         }
                     }
-                    ok = __all_sync(0xffffffffu, ok);
                     if (ok && j + 1 < k.n) fetch_k(next);
                 }
                 if (ok && j > 0) {
                     const int jv = j - 1, s = jv % STG;
-                    ok = jv < STG || mbar_wait(&v_empty[s], ((jv / STG) - 1) & 1, f.status);
+                    ok = jv < STG || wait_all(&v_empty[s], ((jv / STG) - 1) & 1);
                     if (ok) {
                         vb.store(tid, sv + s * C::V_TILE, BN, f.status);
                         fence_proxy_async_smem();
                         mbar_arrive(&v_full[s]);
+                        if (j < k.n) vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
                     }
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (ok && j < k.n) vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
                 }
                 r_v = next;
             }
-        } else {
-            // A copy is announced when the next one has been issued, or when that one has to wait.
-            uint64_t* pending = nullptr;
-            auto announce = [&]() {
-                fence_proxy_async_smem();
-                mbar_arrive(pending);
-                pending = nullptr;
-            };
-            auto wait_empty = [&](uint64_t* bar, unsigned parity) {
-                if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-                if (pending) {
-                    cp_async_wait<0>();
-                    announce();
-                }
-                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, f.status));
-            };
-            auto copy = [&](const void* pages, const TileRows& r, int col0, int cols, uint8_t* tile, uint64_t* full) {
-                const __nv_bfloat16* const base = static_cast<const __nv_bfloat16*>(pages) + col0;
-                const uint32_t dst = smem_u32(tile);
-                const int ppr = cols / 8;  // a constant once inlined
-#pragma unroll 4
-                for (int idx = tid; idx < BN * ppr; idx += C::LT) {
-                    const int key = idx / ppr, i = idx % ppr;
-                    const int first = __shfl_sync(0xffffffffu, r.row, key >> 4), row = first + (key & 15);
-                    const bool live = first >= 0 && key >= r.from && key < r.to && FMHA_IN_BOUNDS(paged_row_ok(f.c, row), kSitePagedRow, f.status);
-                    const int off = (i >> 3) * BN * 128 + key * 128 + (((i & 7) ^ (key & 7)) << 4);
-                    if (FMHA_IN_BOUNDS(off >= 0 && off + 16 <= BN * cols * 2, kSitePagedKv, f.status))
-                        cp_async16(dst + off, base + (live ? (long long)row * HD + i * 8 : 0), live);
-                }
-                cp_async_commit();
-                if (pending) {
-                    cp_async_wait<1>();
-                    announce();
-                }
-                pending = full;
-            };
-            int ahead = page_of(1);
-            TileRows r_k = rows_of(0, page_of(0)), r_v = r_k;
-#pragma unroll 1
-            for (int j = 0; ok && j <= k.n; ++j) {
-                const int page = ahead;  // of tile j + 1
-                ahead = page_of(j + 2);
-                if (j < k.n) {
-                    const int s = j % STG;
-#pragma unroll
-                    for (int c = 0; c < C::NKC; ++c) {
-                        const int q = s * C::NKC + c;
-                        ok = ok && (j < STG || wait_empty(&k_empty[q], ((j / STG) - 1) & 1));
-                        if (ok) copy(f.c.k_pages, r_k, c * C::KCH, C::KCH, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), &k_full[q]);
-                    }
-                }
-                if (j == 0) load_q(warp - 1);
-                if (ok && j > 0) {
-                    const int jv = j - 1, s = jv % STG;
-                    ok = jv < STG || wait_empty(&v_empty[s], ((jv / STG) - 1) & 1);
-                    if (ok) copy(f.c.v_pages, r_v, part * C::HDV, C::HDV, sv + s * C::V_TILE, &v_full[s]);
-                }
-                r_v = r_k;
-                r_k = rows_of(j + 1, page);
-            }
-            cp_async_wait<0>();  // nothing is in flight when the block exits, whatever the waits said
-            if (pending) announce();
         }
     } else if (warp == C::SW) {
         // ------------------------------------------------------------ MMA issuer
-        // The whole warp walks the loop and one elected lane issues, so that the descriptors stay in
-        // uniform registers.
+        // The whole warp walks the loop, its waits agreed upon by all lanes, and one elected lane issues; the
+        // slot and the row tile of a unit are constants of the code: descriptors then stay in uniform registers.
         constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, 0);
         constexpr uint32_t idesc_o = idesc_bf16_f32(BM, C::HDV, 1);
         // A descriptor's low word holds the address in units of 16 bytes: the operands of a step
         // are a constant distance from the first.
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sq), 16, 1024);
-        const uint64_t k_desc = smem_desc_sw128(smem_u32(sk), 16, 1024);
-        const uint64_t v_desc = smem_desc_sw128(smem_u32(sv), BN * 128, 1024);
-        bool ok = mbar_wait(q_full, 0, f.status);
-        auto issue_qk = [&](int u) -> bool {
-            const int j = n_rt == 2 ? u >> 1 : u, rt = n_rt == 2 ? u & 1 : 0, s = j % STG;
-            const uint32_t d = tmem + (u & 1) * BN;
-            if (!FMHA_IN_BOUNDS(s >= 0 && C::OFF_K + (s + 1) * C::K_TILE <= C::OFF_V && (rt + 1) * C::Q_TILE <= C::OFF_K, kSitePagedDesc, f.status))
-                return false;
-            const uint64_t a0 = q_desc + rt * (C::Q_TILE / 16), b0 = k_desc + s * (C::K_TILE / 16);
-#pragma unroll 1
-            for (int c = 0; c < C::NKC; ++c) {
-                if (rt == 0 && !mbar_wait(&k_full[s * C::NKC + c], (j / STG) & 1, f.status)) return false;
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(sk), 16, C::NB * 1024);
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sv), 1024, C::NB * 1024);
+        bool ok = wait_all(q_full, 0);
+        auto chain = [&](auto rts) {
+            constexpr int NR = decltype(rts)::value;
+            // QK(u) of key tile j, for row tile RT, into slot SLOT
+            auto issue_qk = [&](int j, auto rt_, auto slot_) -> bool {
+                constexpr int RT = decltype(rt_)::value, SLOT = decltype(slot_)::value;
+                const int s = j % STG;
+                const uint32_t d = tmem + SLOT * BN;
+                if (!FMHA_IN_BOUNDS(s >= 0 && C::OFF_K + (s + 1) * C::K_TILE <= C::OFF_V && (RT + 1) * C::Q_TILE <= C::OFF_K, kSitePagedDesc, f.status))
+                    return false;
+                const uint64_t a0 = q_desc + RT * (C::Q_TILE / 16), b0 = k_desc + s * (C::K_TILE / 16);
+#pragma unroll
+                for (int c = 0; c < C::NKC; ++c) {
+                    if (RT == 0 && !wait_all(&k_full[s * C::NKC + c], (j / STG) & 1)) return false;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int y = 0; y < C::NB; ++y)  // blocks of 64 columns
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
+                                tc_mma_f16(d, a0 + (c * C::NB + y) * (BM * 128 / 16) + kk * 2, b0 + c * (C::K_TILE / C::NKC / 16) + y * 64 + kk * 2, idesc_s,
+                                           (c > 0 || y > 0 || kk > 0) ? 1u : 0u);
+                        if (RT == NR - 1) tc_commit(&k_empty[s * C::NKC + c]);
+                        if (c == C::NKC - 1) tc_commit(&s_full[SLOT]);
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            // PV(u) for slot SLOT, key tile j, row tile RT; phase: of the slot's barrier
+            auto issue_pv = [&](int j, unsigned phase, auto rt_, auto slot_) -> bool {
+                constexpr int RT = decltype(rt_)::value, SLOT = decltype(slot_)::value;
+                const int s = j % STG;
+                if (RT == 0 && !wait_all(&v_full[s], (j / STG) & 1)) return false;
+                if (!wait_all(&p_ready[SLOT], phase)) return false;
                 tc_fence_after();
+                const uint64_t b0 = v_desc + s * (C::V_TILE / 16);
+                if (!FMHA_IN_BOUNDS(s >= 0 && C::OFF_V + (s + 1) * C::V_TILE <= C::OFF_RAW && C::O_COL + (RT + 1) * C::HDV <= C::TMEM_COLS, kSitePagedDesc, f.status))
+                    return false;
                 if (elect_one()) {
 #pragma unroll
-                    for (int y = 0; y < C::KCH / 64; ++y) {  // 64-column boxes
-                        const int x = c * (C::KCH / 64) + y;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
-                            tc_mma_f16(d, a0 + x * (BM * 128 / 16) + kk * 2, b0 + x * (BN * 128 / 16) + kk * 2, idesc_s,
-                                       (c > 0 || y > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    if (rt == n_rt - 1) tc_commit(&k_empty[s * C::NKC + c]);
-                    if (c == C::NKC - 1) tc_commit(&s_full[u & 1]);
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        tc_mma_f16_ts(tmem + C::O_COL + RT * C::HDV, tmem + SLOT * BN + kk * 8, b0 + kk * (C::NB * 128), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&o_done[SLOT]);
+                    if (RT == NR - 1) tc_commit(&v_empty[s]);
                 }
                 __syncwarp();
+                return true;
+            };
+            constexpr std::integral_constant<int, 0> zero{};
+            constexpr std::integral_constant<int, 1> one{};
+            if constexpr (NR == 2) {
+                ok = ok && issue_qk(0, zero, zero) && issue_qk(0, one, one);
+#pragma unroll 1
+                for (int j = 0; ok && j < k.n; ++j) {
+                    ok = issue_pv(j, j & 1, zero, zero) && (j + 1 >= k.n || issue_qk(j + 1, zero, zero)) && issue_pv(j, j & 1, one, one) &&
+                         (j + 1 >= k.n || issue_qk(j + 1, one, one));
+                }
+            } else {
+                ok = ok && issue_qk(0, zero, zero) && (k.n < 2 || issue_qk(1, zero, one));
+#pragma unroll 1
+                for (int j = 0; ok && j < k.n; j += 2) {
+                    ok = issue_pv(j, (j >> 1) & 1, zero, zero) && (j + 2 >= k.n || issue_qk(j + 2, zero, zero)) &&
+                         (j + 1 >= k.n || issue_pv(j + 1, (j >> 1) & 1, zero, one)) && (j + 3 >= k.n || issue_qk(j + 3, zero, one));
+                }
             }
-            return true;
         };
-        for (int u = 0; ok && u < 2 && u < n_units; ++u) ok = issue_qk(u);
-        for (int u = 0; ok && u < n_units; ++u) {
-            const int j = n_rt == 2 ? u >> 1 : u, rt = n_rt == 2 ? u & 1 : 0, s = j % STG;
-            if (rt == 0 && !mbar_wait(&v_full[s], (j / STG) & 1, f.status)) break;
-            if (!mbar_wait(&p_ready[u & 1], (u >> 1) & 1, f.status)) break;
-            tc_fence_after();
-            const uint64_t b0 = v_desc + s * (C::V_TILE / 16);
-            const uint32_t p_col = tmem + (u & 1) * BN, o_col = tmem + C::O_COL + rt * C::HDV;
-            if (!FMHA_IN_BOUNDS(s >= 0 && C::OFF_V + (s + 1) * C::V_TILE <= C::OFF_BAR && o_col - tmem + C::HDV <= C::TMEM_COLS, kSitePagedDesc, f.status))
-                break;
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_f16_ts(o_col, p_col + kk * 8, b0 + kk * (16 * 128 / 16), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(&o_done[u & 1]);
-                if (rt == n_rt - 1) tc_commit(&v_empty[s]);
-            }
-            __syncwarp();
-            if (u + 2 < n_units && !issue_qk(u + 2)) break;
-        }
+        if (C::NRT == 2 && n_rt == 2)
+            chain(std::integral_constant<int, C::NRT>{});
+        else
+            chain(std::integral_constant<int, 1>{});
         // Exit drain: whatever the loop issued has completed before tensor memory and the operand
         // buffers are released, even if a wait gave up.
         if (elect_one()) tc_commit(mma_drain);
@@ -464,84 +633,103 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
                 const int lo = k.head(j) ? 0 : jlo, hi = k.head(j) ? fhi : jhi;
                 const bool full = pages == (1u << (BN / 16)) - 1u && key0 >= lo && key0 + BN - 1 <= hi;
                 // the row's scores from column `col` of the tile on, -inf where it attends no key
-                auto load_scores = [&](int col, float (&x)[32]) {
-                    tmem_ld32(s_addr + col, x);
+                auto load_scores = [&](int col, float (&x)[2][32]) {
+                    tmem_ld32(s_addr + col, x[0]);
+                    tmem_ld32(s_addr + col + 32, x[1]);
                     tmem_wait_ld();
                     if (!full) {
-                        const int first = key0 + col;
-                        const int k0 = max(0, lo - first), k1 = min(31, hi - first);
-                        uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
-                        const unsigned p = pages >> (col >> 4);
-                        in &= (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = (in >> i) & 1u ? x[i] : -INFINITY;
+                        for (int h = 0; h < 2; ++h) {
+                            const int first = key0 + col + h * 32;
+                            const int k0 = max(0, lo - first), k1 = min(31, hi - first);
+                            uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
+                            const unsigned p = pages >> ((col >> 4) + 2 * h);
+                            in &= (p & 1u ? 0xffffu : 0u) | (p & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[h][i] = (in >> i) & 1u ? x[h][i] : -INFINITY;
+                        }
                     }
                 };
-                float alpha = 1.f, sum;
-                uint32_t pk[BN / 2];
-                bool move = valid && m_ref == -INFINITY;
-#pragma unroll 1
-                for (int again = 0;; ++again) {
-                    if (__any_sync(0xffffffffu, move)) {
-                        float mx = -INFINITY;
-#pragma unroll 1
-                        for (int col = 0; col < BN; col += 32) {
-                            float x[32];
-                            load_scores(col, x);
+                auto top_of = [&](const float (&x)[2][32]) {
+                    float mx = -INFINITY;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
-                        }
-                        const float mt = mx * sl2;
-                        if (mt > m_ref) {
-                            if (m_ref != -INFINITY) alpha = ex2_approx(m_ref - mt);  // without a reference O is zero
-                            m_ref = mt;
-                            l *= alpha;
-                        }
-                    }
-                    const float mu = m_ref == -INFINITY ? 0.f : -m_ref;
-                    const uint64_t q2 = f32x2(sl2, sl2), mu2 = f32x2(mu, mu);
-                    uint64_t s2[2] = {0ull, 0ull};
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int col = 0; col < BN; col += 32) {
-                        float x[32];
+                        for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[h][i], x[h][i + 1]));
+                    return mx * sl2;
+                };
+                if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
+                    float mt = -INFINITY;
+#pragma unroll 1
+                    for (int col = 0; col < BN; col += 64) {
+                        float x[2][32];
                         load_scores(col, x);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float y0, y1;
-                            f32x2_split(fma_f32x2(f32x2(x[2 * i], x[2 * i + 1]), q2, mu2), y0, y1);
-                            y0 = ex2_approx(y0);
-                            y1 = ex2_approx(y1);
-                            pk[col / 2 + i] = pack_bf16x2(y0, y1);
-                            s2[i & 1] = add_f32x2(s2[i & 1], f32x2(y0, y1));
-                        }
+                        mt = fmaxf(mt, top_of(x));
                     }
-                    float a0, a1, b0, b1;
-                    f32x2_split(s2[0], a0, a1);
-                    f32x2_split(s2[1], b0, b1);
-                    sum = (a0 + a1) + (b0 + b1);
-                    move = sum > 1.0995116e12f;  // 2^40
-                    if (again > 0 || !__any_sync(0xffffffffu, move)) break;
+                    if (m_ref == -INFINITY) m_ref = ceilf(mt);  // O is zero without a reference
                 }
-                l += sum;
-                // O's rescale needs the unit before on this row tile: with two row tiles its PV completed before S did
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    if (n_rt == 1 && !__all_sync(0xffffffffu, mbar_wait(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1, f.status))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                // P over S: columns col / 2 on take the weights of the scores from col on, which have been read
 #pragma unroll 1
-                    for (int c = 0; c < C::HDV / 32; ++c) {
-                        float ov[32];
-                        tmem_ld32(o_addr(c), ov);
-                        tmem_wait_ld();
+                for (int col = 0; col < BN; col += 64) {
+                    uint32_t pk[32];
+                    float top;
+                    while (true) {
+                        float x[2][32];
+                        load_scores(col, x);
+                        const float mu = m_ref == -INFINITY ? 0.f : -m_ref;
+                        const uint64_t q2 = f32x2(sl2, sl2), mu2 = f32x2(mu, mu);
+                        uint64_t c2[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-                        tmem_st32(o_addr(c), ov);
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float y0, y1;
+                                f32x2_split(fma_f32x2(f32x2(x[h][2 * i], x[h][2 * i + 1]), q2, mu2), y0, y1);
+                                y0 = ex2_approx(y0);
+                                y1 = ex2_approx(y1);
+                                pk[h * 16 + i] = pack_bf16x2(y0, y1);
+                                c2[i & 1] = add_f32x2(c2[i & 1], f32x2(y0, y1));
+                            }
+                        float a0, a1, b0, b1;
+                        f32x2_split(c2[0], a0, a1);
+                        f32x2_split(c2[1], b0, b1);
+                        top = (a0 + a1) + (b0 + b1);
+                        const bool move = top > 1.0995116e12f;  // 2^40
+                        if (!__any_sync(0xffffffffu, move)) break;
+                        // the reference moves to the largest of these scores, for the rows that ask for it
+                        load_scores(col, x);
+                        const float d = move ? ceilf(top_of(x) - m_ref) : 0.f;
+                        const float alpha = d < 127.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;
+                        m_ref += d;
+                        l *= alpha;
+                        // O's rescale needs the unit before on this row tile: with two row tiles its PV completed before S did
+                        if (j > 0) {
+                            if (n_rt == 1 && !wait_all(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < C::HDV / 32; ++c) {
+                                float ov[32];
+                                tmem_ld32(o_addr(c), ov);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+                                tmem_st32(o_addr(c), ov);
+                            }
+                        }
+                        tmem_wait_st();
+                        const uint32_t a16 = __float_as_uint(alpha) >> 16;
+#pragma unroll 1
+                        for (int c = 0; c < col / 2; c += 32) tmem_scale_pairs(s_addr + c, a16 | (a16 << 16));
+                        tmem_wait_st();
                     }
+                    if (!ok) break;
+                    l += top;
+                    tmem_st32u(s_addr + col / 2, pk);
                 }
-#pragma unroll
-                for (int c = 0; c < BN / 64; ++c) tmem_st32u(s_addr + c * 32, pk + c * 32);
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&p_ready[slot]);
@@ -608,7 +796,7 @@ __global__ void __launch_bounds__(PTCfg<HD>::THREADS, 1) paged_tc_kernel(const P
 
 template <int HD, bool CODES, bool SINK>
 cudaError_t launch_t(const PagedFwd& f, cudaStream_t stream) {
-    using C = PTCfg<HD>;
+    using C = PTCfg<HD, CODES>;
     auto kern = paged_tc_kernel<HD, CODES, SINK>;
     static std::atomic<bool> attr_set[128];  // set once per device; any host thread may set it
     int dev = 0;
@@ -619,6 +807,17 @@ cudaError_t launch_t(const PagedFwd& f, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 128) attr_set[dev] = true;
     }
+    CUtensorMap tmk = {}, tmv = {};  // bf16 pages; without keys nothing is loaded
+    if (!CODES && f.s_k > 0) {
+        // [pool head][group of 8 rows][block][row of 8][64 columns], the order of the operand layout
+        const cuuint64_t row = (cuuint64_t)HD * 2;
+        const cuuint64_t dims[5] = {64, 8, HD / 64, (cuuint64_t)f.c.page / 8, (cuuint64_t)f.c.n_pages * f.c.n_kv_h};
+        const cuuint64_t strides[4] = {row, 128, row * 8, row * f.c.page};
+        const cuuint32_t box[5] = {64, 8, C::NB, (cuuint32_t)(f.c.page < C::BN ? f.c.page : C::BN) / 8, 1};
+        if (encode_swizzled_map(&tmk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.c.k_pages, dims, strides, box, 5) != CUDA_SUCCESS ||
+            encode_swizzled_map(&tmv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.c.v_pages, dims, strides, box, 5) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(f.row_tiles * C::PARTS * f.c.n_kv_h), f.n_splits);
     cfg.blockDim = dim3(C::THREADS);
@@ -627,7 +826,7 @@ cudaError_t launch_t(const PagedFwd& f, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {programmatic_launch_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, f);
+    return cudaLaunchKernelEx(&cfg, kern, tmk, tmv, f);
 }
 
 template <bool CODES, bool SINK>
@@ -643,7 +842,7 @@ cudaError_t launch_s(const PagedFwd& f, cudaStream_t stream) {
 
 }  // namespace
 
-int paged_tc_kv_tile(int hd) { return hd <= 128 ? PTCfg<128>::BN : PTCfg<256>::BN; }
+int paged_tc_kv_tile(int hd) { return hd <= 128 ? PTCfg<128, false>::BN : PTCfg<256, false>::BN; }
 int paged_tc_rows(int hd) { return hd <= 128 ? 256 : 128; }
 
 cudaError_t launch_paged_tc(const PagedFwd& f, cudaStream_t stream) {
