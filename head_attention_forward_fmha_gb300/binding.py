@@ -73,7 +73,7 @@ SIGNATURES = {
     "fmha_paged_append": ([ctypes.c_char_p], _i32),
     "fmha_paged_gather": ([ctypes.c_char_p], _i32),
     "fmha_fwd_paged": ([ctypes.c_char_p], _i32),
-    "fmha_fwd_paged_plan": ([_i32] * 13, _i32),
+    "fmha_fwd_paged_plan": ([_i32] * 14, _i32),
 }
 # Size of the fixed split-KV scratch fmha_fwd_noalloc uses (FMHA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -815,17 +815,17 @@ def fmha_paged_gather(k_pages, v_pages, k_scales, v_scales, block_table, seq_len
 _paged_plans = {}  # (chunks, workspace bytes) by shape and device
 
 
-def fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window=0, n_first=0, causal=False, total=None, n_splits=0):
+def fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window=0, n_first=0, causal=False, total=None, codes=False, n_splits=0):
     """The number of chunks that fmha_fwd_paged uses for sequences of up to s_k keys and T new tokens (total: the rows of a
-    ragged q; n_splits 0: its own choice)."""
+    ragged q; codes: 8-bit pages; n_splits 0: its own choice)."""
     n = (_lib or load()).fmha_fwd_paged_plan(batch, T, int(total or 0), n_h, n_kv_h, hd, page, s_k, int(window), int(n_first),
-                                             int(bool(causal)), int(total is not None), int(n_splits))
+                                             int(bool(causal)), int(total is not None), int(bool(codes)), int(n_splits))
     _check(n if n < 0 else 0, "fmha_fwd_paged_plan")
     return n
 
 
-def _paged_plan(batch, T, total, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, n_splits):
-    n = fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, total, n_splits)
+def _paged_plan(batch, T, total, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, codes, n_splits):
+    n = fmha_fwd_paged_plan(batch, T, n_h, n_kv_h, hd, page, s_k, window, n_first, causal, total, codes, n_splits)
     rows = batch * T if total is None else total
     return n, rows * n_h * n * (hd + 1) * 4 if n > 1 else 0
 
@@ -857,7 +857,7 @@ def fmha_fwd_paged(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_len
         o = _empty(shape, _BF16, dev, stream)
     if lse is None:
         lse = _empty(shape[:-1], _FP32, dev, stream)
-    key = (b, T, total, n_h, n_kv_h, hd, page, min(s_k, width * page), window, n_first, causal, n_splits, dev)
+    key = (b, T, total, n_h, n_kv_h, hd, page, min(s_k, width * page), window, n_first, causal, codes, n_splits, dev)
     plan = _paged_plans.get(key)
     if plan is None:
         plan = _remember(_paged_plans, key, _planned(dev, _paged_plan, *key[:-1]))

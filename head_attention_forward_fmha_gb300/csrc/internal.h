@@ -244,7 +244,7 @@ struct PagedFwd {
     int chunk_tiles, n_splits;  // key tiles per chunk (the last chunk takes what is left) and their number
     unsigned* status;
 };
-int paged_decode_kv_tile(int hd);                 // keys per tile
+int paged_decode_kv_tile(int hd, bool codes);     // keys per tile
 int paged_decode_rows(int hd, long long rows);    // query rows per thread block, given the rows per KV head of a sequence
 cudaError_t launch_paged_decode(const PagedFwd& a, int rows_per_cta, cudaStream_t stream);
 int paged_tc_kv_tile(int hd);

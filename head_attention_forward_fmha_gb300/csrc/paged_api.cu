@@ -64,6 +64,12 @@ int check_strides(const long long* s, const char* name) {
 // Rows per KV head from which on the tensor-core kernel is taken (decode kernel below).
 int tc_min_rows(int hd) { return hd >= 256 ? 24 : 40; }
 
+// Estimated time of a key tile in a block of the tensor-core kernel, `rows` being those of a sequence under a KV head.
+double tc_tile_us(int hd, bool codes, long long rows) {
+    if (hd <= 128) return (rows > 128 ? 2.0 : 1.4) * (codes ? 1.25 : 1.0);  // tiles of 128 keys
+    return hd == 256 ? (codes ? 2.0 : 0.95) : codes ? 3.7 : 1.55;          // of 64
+}
+
 // Kernel, row tiles and chunks of an attention call.  f->t.T is the number of new tokens of every
 // sequence, or with bounds the most that one has; wanted: the number of chunks asked for, 0 for the library's
 // choice.  Nothing is lost if a sequence has more tokens or keys than said here: row tiles are counted by
@@ -74,7 +80,7 @@ struct PagedPlan {
     long long row_tiles;
 };
 
-PagedPlan plan_paged(PagedFwd* f, bool ragged, int wanted) {
+PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
     PagedPlan p;
     const int hd = f->c.hd;
     const long long most = (long long)f->group * f->t.T;  // rows of a sequence under a KV head
@@ -85,17 +91,52 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, int wanted) {
     p.row_tiles = ragged ? std::min(tokens * f->group, (tokens * f->group + (long long)f->t.batch * (p.rows - 1)) / p.rows)
                          : f->t.batch * ((most + p.rows - 1) / p.rows);
     f->row_tiles = (int)std::min<long long>(p.row_tiles, INT_MAX);
-    const int tile = p.tc ? paged_tc_kv_tile(hd) : paged_decode_kv_tile(hd);
+    const int tile = p.tc ? paged_tc_kv_tile(hd) : paged_decode_kv_tile(hd, codes);
     long long span = f->s_k;
     if (f->window > 0) span = std::min<long long>(span, (long long)f->n_first + f->window + std::min<long long>(f->t.T, p.rows) + 2 * tile);
     const long long tiles = std::max(1LL, (span + tile - 1) / tile);
     long long n = wanted;
     if (n <= 0) {
-        // as many chunks as fill the GPU once (blocks of the decode kernel: two per SM), of 256 keys at least
-        const long long parts = p.tc && hd == 512 ? 2 : 1;
-        const long long slots = (long long)sm_count() * (p.tc || hd == 512 ? 1 : 2);
-        const long long units = std::max(1LL, p.row_tiles * f->c.n_kv_h * parts);
-        n = std::min(slots / units, std::max(1LL, tiles * tile / 256));
+        // The number of chunks with the least estimated time, over the lengths that a batch may have: sequences of
+        // s_k keys each, and (counted twice) lengths spread evenly up to it, where a sequence of n chunks
+        // fills (n + 1) / 2 blocks with n / 2 blocks' work on average.
+        const bool codes_ = codes;
+        const double sms = sm_count(), per_sm = p.tc || hd == 512 ? 1 : 2, slots = sms * per_sm;
+        const double units = (double)std::max(1LL, p.row_tiles) * f->c.n_kv_h * (p.tc && hd == 512 ? 2 : 1);
+        const double row_bytes = codes_ ? hd + 1.0 : 2.0 * hd;
+        const double parts_us = (double)f->rows * hd * 8.0 / 8e6;  // one chunk's partials, written and read
+        double best = 1e300;
+        const long long most_n = std::min<long long>(tiles, 64);
+        for (long long c = 1; c <= most_n; c += c < 8 ? 1 : c < 32 ? 2 : 8) {
+            const long long mine = (tiles + c - 1) / c;  // tiles of a block
+            double us[2];
+            for (int ragged_lens = 0; ragged_lens < 2; ++ragged_lens) {
+                const double blocks = units * (double)(ragged_lens ? c + 1 : 2 * c) / 2.0;
+                double fixed, body;
+                if (p.tc) {
+                    fixed = hd == 512 ? 12.0 : 7.0;
+                    body = (double)mine * tc_tile_us(hd, codes_, most);
+                } else {
+                    // a block takes in up to 38 KB a us (28 of codes), all of them 6.6 TB/s (5.2)
+                    const double rate = std::min(codes_ ? 28e3 : 38e3, (codes_ ? 5.2e6 : 6.6e6) / std::min(slots, blocks));
+                    fixed = 5.0;
+                    body = (double)mine * tile * 2.0 * row_bytes / rate;
+                }
+                const double ratio = blocks / slots;
+                if (ragged_lens) {
+                    const double work = units / slots * ((double)(c + 1) * fixed + (double)c * body) / 2.0;
+                    us[1] = std::max(fixed + body, work + (fixed + body) / 2.0);
+                } else {
+                    us[0] = std::max(1.0, ratio + 0.5 * (std::ceil(ratio) - ratio)) * (fixed + body);
+                }
+            }
+            double t = f->t.batch > 1 ? 0.35 * us[0] + 0.65 * us[1] : us[0];
+            if (c > 1) t += 3.0 + 0.05 * (double)c + 0.2 * (double)std::max(0LL, c - 16) + parts_us * (double)c;  // the merge
+            if (t < best * 0.98) {
+                best = t;
+                n = c;
+            }
+        }
     }
     n = std::max(1LL, std::min<long long>({n, tiles, 64}));
     // partials of at most 1 GiB
@@ -203,14 +244,15 @@ int fmha_paged_gather(const struct fmha_paged_gather_args* x) try {
 }
 
 int fmha_fwd_paged_plan(int batch, int T, int total, int n_h, int n_kv_h, int hd, int page, int s_k, int window, int n_first, int causal,
-                        int ragged, int n_splits) try {
-    if (ragged != 0 && ragged != 1) return fail(FMHA_ERR_SHAPE, "ragged must be 0 or 1 (got %d)", ragged);
+                        int ragged, int codes, int n_splits) try {
+    if ((ragged != 0 && ragged != 1) || (codes != 0 && codes != 1))
+        return fail(FMHA_ERR_SHAPE, "ragged and codes must be 0 or 1 (got %d and %d)", ragged, codes);
     PagedFwd f;
     const int width = page > 0 && s_k > 0 ? (int)(((long long)s_k + page - 1) / page) : 1;
     const int rc = check_fwd(batch, T, total, ragged != 0, n_h, n_kv_h, hd, page, 1, width, s_k, 1.f, window, n_first, causal, n_splits, &f);
     if (rc) return rc;
     if (f.rows == 0) return 1;
-    plan_paged(&f, ragged != 0, n_splits);
+    plan_paged(&f, ragged != 0, codes != 0, n_splits);
     return f.n_splits;
 } catch (...) {
     return fail(FMHA_ERR_LAUNCH, "unexpected host exception in fmha_fwd_paged_plan");
@@ -241,7 +283,7 @@ int fmha_fwd_paged(const struct fmha_fwd_paged_args* x) try {
     f.sink = x->sink;
     f.o = static_cast<__nv_bfloat16*>(x->o);
     f.lse = x->lse;
-    const PagedPlan p = plan_paged(&f, ragged, x->n_splits);
+    const PagedPlan p = plan_paged(&f, ragged, x->k_scales != nullptr, x->n_splits);
     if ((double)p.row_tiles * f.c.n_kv_h * 2 > INT_MAX) return fail(FMHA_ERR_SHAPE, "too many query rows");
     if (f.n_splits > 1) {
         const size_t need = (size_t)f.n_splits * f.rows * (f.c.hd + 1) * 4;

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppend a, 
             u[1][v] = __ldcs(reinterpret_cast<const uint4*>(a.v + va + (v * 8 << log_tpr)));
         }
         if (pos >= 0 && pos < (long long)c.width << c.log_page)
-            dst = paged_row(c, paged_entry(c, a.t.batch, b, (int)(pos >> c.log_page), a.status), h, (int)(pos & (c.page - 1)));
+            dst = paged_row(c, paged_page(c, paged_entry(c, a.t.batch, b, (int)(pos >> c.log_page), a.status)), h, (int)(pos & (c.page - 1)));
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) u[0][v] = u[1][v] = make_uint4(0u, 0u, 0u, 0u);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const PagedGather a, 
     if (!FMHA_IN_BOUNDS(b >= 0 && b < a.batch, kSitePagedSeq, a.status)) return;
     const long long pos = (a.start ? (long long)__ldg(a.start + b) : 0) + r;
     if (pos < 0 || pos >= __ldg(a.seq_lens + b) || pos >= (long long)c.width << c.log_page) return;
-    const int src = paged_row(c, paged_entry(c, a.batch, b, (int)(pos >> c.log_page), a.status), h, (int)(pos & (c.page - 1)));
+    const int src = paged_row(c, paged_page(c, paged_entry(c, a.batch, b, (int)(pos >> c.log_page), a.status)), h, (int)(pos & (c.page - 1)));
     if (src < 0 || !FMHA_IN_BOUNDS(paged_row_ok(c, src), kSitePagedRow, a.status)) return;
     const long long at = ((long long)src << log_tpr) + part;  // in 16-byte units
     const uint4 uk = __ldcs(static_cast<const uint4*>(c.k_pages) + at), uv = __ldcs(static_cast<const uint4*>(c.v_pages) + at);

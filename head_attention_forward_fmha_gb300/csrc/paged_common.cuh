@@ -12,13 +12,15 @@
 
 namespace fmha {
 
-// Entry `slot` of sequence b's block table; -1 where the page is not there.
+// Entry `slot` of sequence b's block table as it stands there, -1 outside it.  What is loaded is not
+// looked at here, so that nothing waits for it before paged_page does.
 __device__ __forceinline__ int paged_entry(const PagedCache& c, int batch, int b, int slot, unsigned* status) {
-    if (slot < 0 || slot >= c.width) return -1;
-    if (!FMHA_IN_BOUNDS(b >= 0 && b < batch, kSitePagedSeq, status)) return -1;
-    const int p = __ldg(c.table + (long long)b * c.width + slot);
-    return (unsigned)p < (unsigned)c.n_pages ? p : -1;
+    if (slot < 0 || slot >= c.width || !FMHA_IN_BOUNDS(b >= 0 && b < batch, kSitePagedSeq, status)) return -1;
+    return __ldg(c.table + (long long)b * c.width + slot);
 }
+
+// The page that an entry names, -1 for one that is not there.
+__device__ __forceinline__ int paged_page(const PagedCache& c, int entry) { return (unsigned)entry < (unsigned)c.n_pages ? entry : -1; }
 
 // Pool row of the first key of granule `key` (a multiple of 16) under `head`, given its page; -1 for no page.
 __device__ __forceinline__ int paged_row(const PagedCache& c, int page, int head, int key) {
@@ -57,8 +59,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-
-constexpr uint32_t kBf16x2Two120 = 0x7B807B80u;  // 2^120 twice
 
 // 2^(byte - 127) in fp32; NaN for 255.
 __device__ __forceinline__ float paged_scale(uint32_t byte) {

@@ -3,19 +3,21 @@
 // One thread block handles RT (8 or 16) query rows of one sequence that share a KV head, and
 // one chunk of that sequence's key tiles.  A producer warp streams the tiles from HBM through a ring
 // of TMA boxes (128-byte swizzle): its lanes look the tile's pages up in the block table, one
-// tile ahead, and each issues the boxes of its page (a page that is not there is a box
-// behind the pool, which the TMA fills with zeros).  Four consumer warps each take 16 keys
-// of a tile, which lie in one page:
+// tile ahead, and issue the boxes of the pages (a page that is not there is a box
+// behind the pool, which the TMA fills with zeros).  Four consumer warps, eight for codes, each take 16
+// keys of a tile, which lie in one page:
 //   S^T = K Q^T     mma.sync m16n8k16, keys as M, so that 8 query rows fill N = 8
 //   O^T += V^T P^T  keys as the reduction dimension; P transposed in registers (movmatrix)
 // with the online softmax between them, and merge their partial states at the end.
 //
-// 8-bit pages: the codes are expanded in registers to bf16 (paged_common.cuh, 7 integer and 2
-// multiply instructions for 4 codes), K's as fp32-exact multiples whose row scale goes to the scores,
-// V's to P, both in fp32.  Expansion takes bytes 0 and 2, then 1 and 3 of a word: for K the
-// order of the columns does not matter as long as Q has the same one (Q is stored so), for V the
-// pairs are two keys of one column.  V's operand is loaded by ldmatrix with transposition on pairs of
-// codes, so that rows g and g + 8 of the A operand are columns 2 g and 2 g + 1.
+// 8-bit pages: the codes become fp16 operands in registers, by the hardware's exact conversion (one
+// instruction for two codes; the step to bf16 took 4.5, and the kernel half its rate: 16 sequences of 16384
+// keys at hd 128 137 us).  Scales stay outside the MMAs: K's multiply the scores, V's the weights, in
+// fp32.  What fp16 asks for in range is kept apart as powers of two: Q's rows are scaled to a largest element in
+// [2^14, 2^15) (elements below 2^-29 of it lose bits), P carries a factor 2^12, and V's scales are taken
+// relative to the largest that the warp has met, O being kept in units of it (weights whose V lies
+// more than 2^26 below that lose bits).  V's operand is loaded by ldmatrix with
+// transposition on pairs of codes, so that rows g and g + 8 of the A operand are columns 2 g and 2 g + 1.
 #include <atomic>
 #include "internal.h"
 #include "paged_common.cuh"
@@ -27,11 +29,11 @@ namespace {
 template <int HD, int NB, bool CODES>
 struct PDCfg {
     static constexpr int RT = 8 * NB;                  // query rows per block
-    static constexpr int KW = HD <= 128 ? 4 : 2;       // key groups of 16 keys
-    static constexpr int DW = 4 / KW;                  // warps that share a key group's columns in P V
+    static constexpr int NCW = CODES ? 8 : 4;          // consumer warps
+    static constexpr int KW = HD <= 128 ? NCW : NCW / 2;  // key groups of 16 keys
+    static constexpr int DW = NCW / KW;                // warps that share a key group's columns in P V
     static constexpr int KT = 16 * KW;                 // keys per tile
     static constexpr int HDW = HD / DW;                // columns of O per warp
-    static constexpr int NCW = 4;
     static constexpr int THREADS = (NCW + 1) * 32;
     static constexpr int ROW = CODES ? HD : HD * 2;    // bytes of a stored row
     static constexpr int TILE_BYTES = KT * ROW;
@@ -46,9 +48,10 @@ struct PDCfg {
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
     static constexpr int OFF_LIVE = OFF_BAR + 2 * STAGES * 8;  // per stage: a bit for each 16 keys that are there
     static constexpr int OFF_SC = OFF_LIVE + (STAGES * 4 + 15) / 16 * 16;
-    static constexpr int OFF_ML = OFF_SC + STAGES * SC_BYTES;
-    static constexpr int SMEM = 1024 + OFF_ML + KW * RT * 8 + 16;
-    static_assert(KW * RT * HD * 4 <= STAGES * STAGE_BYTES, "the combine buffer reuses the ring");
+    static constexpr int OFF_QE = OFF_SC + STAGES * SC_BYTES;  // codes: power of two of each Q row
+    static constexpr int OFF_ML = OFF_QE + (CODES ? RT * 4 : 0);
+    static constexpr int SMEM = 1024 + OFF_ML + KW * RT * 12 + 16;
+    static_assert(KW <= 8 && KW * RT * HD * 4 <= STAGES * STAGE_BYTES, "the combine buffer reuses the ring");
 };
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool there) {
@@ -83,8 +86,10 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
     uint64_t* empty = full + C::STAGES;
     uint32_t* live = reinterpret_cast<uint32_t*>(smem + C::OFF_LIVE);
     uint8_t* scales = smem + C::OFF_SC;
+    int* q_exp = reinterpret_cast<int*>(smem + C::OFF_QE);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [KW][RT] (max, sum) per key group
-    int* abort_flag = reinterpret_cast<int*>(ml + C::KW * C::RT);
+    int* v_exp = reinterpret_cast<int*>(ml + C::KW * C::RT);   // [KW] codes: unit of a group's O
+    int* abort_flag = v_exp + C::KW * C::RT;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.x % f.c.n_kv_h, split = blockIdx.y;
@@ -110,59 +115,51 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
 
     // ------------------------------------------------------------ producer
     if (warp == C::NCW) {
-        // Lane = (K or V, page of the tile, 128-byte column box): at most 2 * 4 * 4 of them
-        // (hd 512 in bf16, 8 column boxes, takes two boxes a lane).
-        const int pages = C::KT / box_keys;
-        const int my_page = lane & 3, my_col = (lane >> 2) & 3, my_v = lane >> 4;
-        const bool mine = my_page < pages && my_col < C::NBOX;
+        const int log_pages = __ffs(C::KT / box_keys) - 1;                 // boxes along a tile's keys (and NBOX across)
         const int box_rows = CODES && HD == 64 ? box_keys / 2 : box_keys;  // rows of 128 bytes (two keys at 64 bytes each)
         if (lane == 0) {
             tma_prefetch_desc(&tmk);
             tma_prefetch_desc(&tmv);
         }
         const uint64_t pol = l2_policy_evict_first();
-        // the lanes' pages one tile ahead, by 16 keys: granule lane & 3
+        // the block table one tile ahead, by 16 keys: granule `lane`
         auto entry = [&](int it) {
-            if (it >= k.n) return -1;
-            const int key = k.key(it, C::KT) + 16 * (lane & 3);
-            return 16 * (lane & 3) < C::KT && key < k.to(it) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
+            if (it >= k.n || 16 * lane >= C::KT) return -1;
+            const int key = k.key(it, C::KT) + 16 * lane;
+            return key < k.to(it) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
         };
         int issued = 0, ahead = entry(0);
         for (int it = 0; it < k.n; ++it) {
-            const int s = it % C::STAGES, page = ahead, key = k.key(it, C::KT);
+            const int s = it % C::STAGES, page = paged_page(f.c, ahead), key = k.key(it, C::KT);
             ahead = entry(it + 1);
             // (all lanes go on or none: collectives follow)
             if (it >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) - 1) & 1, f.status))) break;
-            const unsigned there = __ballot_sync(0xffffffffu, lane < 4 && page >= 0);
-            // the box of page my_page starts at granule my_page * box_keys / 16
-            const int bp = __shfl_sync(0xffffffffu, page, my_page * (box_keys >> 4) & 3);
+            const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
             uint8_t* kst = stages + s * C::STAGE_BYTES;
             if (lane == 0) {
                 live[s] = there;
                 mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
             }
             __syncwarp();
-            if (mine) {
-                const int bkey = key + my_page * box_keys;
+            // box i: K's and then V's, of each first all pages of the first 128 bytes' columns
+            for (int i0 = 0; i0 < 2 * C::NBOX << log_pages; i0 += 32) {
+                const int i = i0 + lane, mine = i & ((1 << log_pages) - 1), col = (i >> log_pages) % C::NBOX, v = (i >> log_pages) / C::NBOX;
+                const int bp = __shfl_sync(0xffffffffu, page, mine * (box_keys >> 4) & 31);  // the box begins with that granule
                 const int slab = bp < 0 ? f.c.n_pages * f.c.n_kv_h : bp * f.c.n_kv_h + kvh;  // behind the pool: zeros
-                const int row = (bkey & (f.c.page - 1)) / (box_keys / box_rows);
-                uint8_t* dst = kst + my_v * C::TILE_BYTES + my_page * box_rows * 128;
-                for (int col = my_col; col < C::NBOX; col += 4)
-                    if (FMHA_IN_BOUNDS(s < C::STAGES && row >= 0 && row + box_rows <= f.c.page / (box_keys / box_rows) &&
-                                           my_v * C::TILE_BYTES + col * C::BOX_BYTES + (my_page + 1) * box_rows * 128 <= C::STAGE_BYTES,
-                                       kSitePagedKv, f.status))
-                        tma_load_3d_hint(dst + col * C::BOX_BYTES, my_v ? &tmv : &tmk, col * (CODES ? 128 : 64), row, slab, &full[s], pol);
+                const int row = ((key + mine * box_keys) & (f.c.page - 1)) / (box_keys / box_rows);
+                const int at = v * C::TILE_BYTES + col * C::BOX_BYTES + mine * box_rows * 128;
+                if (v < 2 && FMHA_IN_BOUNDS(s < C::STAGES && row >= 0 && row + box_rows <= f.c.page / (box_keys / box_rows) &&
+                                                at + box_rows * 128 <= C::STAGE_BYTES,
+                                            kSitePagedKv, f.status))
+                    tma_load_3d_hint(kst + at, v ? &tmv : &tmk, col * (CODES ? 128 : 64), row, slab, &full[s], pol);
             }
             if constexpr (CODES) {
-                // scale bytes, four keys a lane: lanes 0 .. KT / 4 - 1 K's, the next V's
-                constexpr int PER = C::KT / 4;
-                const int four = (lane % PER) * 4;
-                const int sp = __shfl_sync(0xffffffffu, page, four >> 4);
-                if (lane < 2 * PER) {
-                    const int row = paged_row(f.c, sp, kvh, key + (four & ~15)) + (four & 15);
-                    const bool ok = sp >= 0 && FMHA_IN_BOUNDS(paged_row_ok(f.c, row + 3), kSitePagedRow, f.status);
-                    const uint8_t* src = lane < PER ? f.c.k_scales : f.c.v_scales;
-                    cp_async4(scales + s * C::SC_BYTES + lane * 4, src + (ok ? row : 0), ok);
+                // scale bytes, four keys a lane
+                const int row = __shfl_sync(0xffffffffu, paged_row(f.c, page, kvh, key + 16 * lane), lane >> 2) + (lane & 3) * 4;
+                if (lane < C::KT / 4) {
+                    const bool ok = row >= (lane & 3) * 4 && FMHA_IN_BOUNDS(paged_row_ok(f.c, row + 3LL), kSitePagedRow, f.status);
+                    cp_async4(scales + s * C::SC_BYTES + lane * 4, f.c.k_scales + (ok ? row : 0), ok);
+                    cp_async4(scales + s * C::SC_BYTES + C::KT + lane * 4, f.c.v_scales + (ok ? row : 0), ok);
                 }
                 cp_async_arrive(&full[s]);
             }
@@ -176,16 +173,43 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
     // ------------------------------------------------------------ consumers
     const int kw = warp / C::DW, dw = warp - kw * C::DW;
 
-    // Q rows -> shared memory (zero rows past the end); for codes with columns 1 and 2 of each four exchanged
-    for (int i = threadIdx.x; i < C::RT * (HD / 8); i += C::NCW * 32) {
-        const int r = i / (HD / 8), c8 = i - r * (HD / 8);
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (r < t.n) val = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + c8 * 8));
-        if constexpr (CODES)
-            val = make_uint4(__byte_perm(val.x, val.y, 0x5410), __byte_perm(val.x, val.y, 0x7632), __byte_perm(val.z, val.w, 0x5410),
-                             __byte_perm(val.z, val.w, 0x7632));
-        if (FMHA_IN_BOUNDS(r * C::Q_STRIDE + c8 * 16 + 16 <= C::Q_BYTES, kSitePagedQ, f.status))
-            *reinterpret_cast<uint4*>(qs + r * C::Q_STRIDE + c8 * 16) = val;
+    // Q rows -> shared memory (zero rows past the end); for codes as fp16 times a power of two of the row
+    if constexpr (!CODES) {
+        for (int i = threadIdx.x; i < C::RT * (HD / 8); i += C::NCW * 32) {
+            const int r = i / (HD / 8), c8 = i - r * (HD / 8);
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (r < t.n) val = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + c8 * 8));
+            if (FMHA_IN_BOUNDS(r * C::Q_STRIDE + c8 * 16 + 16 <= C::Q_BYTES, kSitePagedQ, f.status))
+                *reinterpret_cast<uint4*>(qs + r * C::Q_STRIDE + c8 * 16) = val;
+        }
+    } else {
+        constexpr int LPR = HD >= 256 ? 32 : HD / 8, VEC = HD / 8 / LPR;  // lanes of a row, 16-byte pieces of a lane
+        for (int r0 = warp * (32 / LPR); r0 < C::RT; r0 += C::NCW * (32 / LPR)) {
+            const int r = r0 + lane / LPR, lc = lane % LPR;
+            uint4 u[VEC];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                u[v] = make_uint4(0, 0, 0, 0);
+                if (r < t.n) u[v] = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + (v * LPR + lc) * 8));
+                mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[v].x & 0x7FFF7FFFu, u[v].y & 0x7FFF7FFFu), __vmaxu2(u[v].z & 0x7FFF7FFFu, u[v].w & 0x7FFF7FFFu)));
+            }
+            mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+            for (int s = LPR / 2; s > 0; s >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            const int e = (int)(mx >> 7), up = e > 0 && e < 255 ? min(max(14 - (e - 127), -120), 120) : 0;
+            const float fac = __uint_as_float((uint32_t)(127 + up) << 23);
+            if (lc == 0 && FMHA_IN_BOUNDS(r < C::RT, kSitePagedQ, f.status)) q_exp[r] = up;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const uint32_t x[4] = {u[v].x, u[v].y, u[v].z, u[v].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) h[y] = pack_f16x2(bf16_lo(x[y]) * fac, bf16_hi(x[y]) * fac);
+                const int at = r * C::Q_STRIDE + (v * LPR + lc) * 16;
+                if (FMHA_IN_BOUNDS(r < C::RT && at + 16 <= C::Q_BYTES, kSitePagedQ, f.status)) *reinterpret_cast<uint4*>(qs + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
     }
 
     // Keys of each accumulator row of this thread (rows nb * 8 + 2 * (lane % 4) + i), and those that every row attends.
@@ -222,8 +246,14 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
     named_barrier_sync(1, C::NCW * 32);  // Q staged
 
     const float sl2 = f.scale_log2;
+    int row_exp[NB][2], v_unit = 0;  // codes: power of two of Q's rows; unit of O, as a scale byte
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) row_exp[nb][i] = CODES ? q_exp[nb * 8 + 2 * (lane & 3) + i] : 0;
     const uint32_t qs_addr = smem_u32(qs);
     const int g = lane >> 2, t4 = lane & 3;
+    constexpr float kBias = CODES ? 12.f : 0.f;  // log2 of the factor that P and its sum carry
     bool ok = true;
 
     for (int it = 0; it < k.n; ++it) {
@@ -274,43 +304,49 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
                     if (!FMHA_IN_BOUNDS(ka >= kst && ka + 8 <= kst + C::TILE_BYTES, kSitePagedLds, f.status)) ka = kst;
                     w[y] = lds64(ka);
                 }
-                uint32_t a[2][4];
-                a[0][0] = mul_bf16x2(e4m3x2_raw<true>(w[0].x), kBf16x2Two120);
-                a[0][1] = mul_bf16x2(e4m3x2_raw<true>(w[1].x), kBf16x2Two120);
-                a[0][2] = mul_bf16x2(e4m3x2_raw<false>(w[0].x), kBf16x2Two120);
-                a[0][3] = mul_bf16x2(e4m3x2_raw<false>(w[1].x), kBf16x2Two120);
-                a[1][0] = mul_bf16x2(e4m3x2_raw<true>(w[0].y), kBf16x2Two120);
-                a[1][1] = mul_bf16x2(e4m3x2_raw<true>(w[1].y), kBf16x2Two120);
-                a[1][2] = mul_bf16x2(e4m3x2_raw<false>(w[0].y), kBf16x2Two120);
-                a[1][3] = mul_bf16x2(e4m3x2_raw<false>(w[1].y), kBf16x2Two120);
+                uint32_t a[2][4];  // words 0 and 1 of keys g and g + 8
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    e4m3x4_to_f16(w[y].x, a[0][y], a[0][2 + y]);
+                    e4m3x4_to_f16(w[y].y, a[1][y], a[1][2 + y]);
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     uint32_t qa = qs_addr + (nb * 8 + g) * C::Q_STRIDE + (32 * kk + 8 * t4) * 2;
                     if (!FMHA_IN_BOUNDS(qa + 16 <= qs_addr + C::Q_BYTES, kSitePagedLds, f.status)) qa = qs_addr;
                     const uint4 q = lds128(qa);
-                    mma_bf16_16816(sc[nb], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
-                    mma_bf16_16816(sc[nb], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                    mma_f16_16816(sc[nb], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                    mma_f16_16816(sc[nb], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
                 }
             }
         }
 
         // scale, mask, online softmax (log2 domain)
-        float k0 = 1.f, k1 = 1.f, v0 = 1.f, v1 = 1.f;  // factors of keys g and g + 8
-        if constexpr (CODES) {
-            const uint8_t* ks = scales + s * C::SC_BYTES + 16 * kw + g;
-            k0 = paged_scale(ks[0]);
-            k1 = paged_scale(ks[8]);
-            v0 = paged_scale(ks[C::KT]);
-            v1 = paged_scale(ks[C::KT + 8]);
-        }
         const bool in_head = k.head(it);
         const int need_lo = in_head ? 0 : all_lo, need_hi = in_head ? all_f : all_hi;
         const bool edge = !there || kb < need_lo || kb + 15 > need_hi;
         const int j0 = kb + g, j1 = j0 + 8;
-        if (edge) {
-            // a key that no row attends has no factor, whatever memory holds there
-            if (!there || j0 < k.from(it) || j0 >= k.to(it)) v0 = 0.f;
-            if (!there || j1 < k.from(it) || j1 >= k.to(it)) v1 = 0.f;
+        uint32_t ke[2] = {127u, 127u};             // scale bytes of K's rows g and g + 8
+        float v0 = 1.f, v1 = 1.f, to_unit = 1.f;  // factors of their V rows in units of O, of O so far
+        if constexpr (CODES) {
+            const uint8_t* ks = scales + s * C::SC_BYTES + 16 * kw + g;
+            ke[0] = ks[0];
+            ke[1] = ks[8];
+            uint32_t b0 = ks[C::KT], b1 = ks[C::KT + 8];
+            if (edge) {
+                // a key that no row attends has no factor, whatever memory holds there
+                if (!there || j0 < k.from(it) || j0 >= k.to(it)) b0 = 0u;
+                if (!there || j1 < k.from(it) || j1 >= k.to(it)) b1 = 0u;
+            }
+            uint32_t top = max(b0 == 255u ? 0u : b0, b1 == 255u ? 0u : b1);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const int unit = max(v_unit, (int)top);
+            auto power = [](int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + e) << 23); };
+            to_unit = power(v_unit - unit);
+            v_unit = unit;
+            v0 = b0 == 255u ? NAN : power((int)b0 - unit);
+            v1 = b1 == 255u ? NAN : power((int)b1 - unit);
         }
         uint32_t pb[NB][2];
 #pragma unroll
@@ -318,7 +354,15 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
             float mx[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float x0 = sc[nb][i] * k0 * sl2, x1 = sc[nb][2 + i] * k1 * sl2;
+                float x0 = sc[nb][i] * sl2, x1 = sc[nb][2 + i] * sl2;
+                if constexpr (CODES) {
+                    // times K's scale, and the power of two that undoes Q's
+                    auto power = [&](uint32_t byte) {
+                        return byte == 255u ? NAN : __uint_as_float((uint32_t)min(max((int)byte - row_exp[nb][i], 1), 254) << 23);
+                    };
+                    x0 = sc[nb][i] * power(ke[0]) * sl2;
+                    x1 = sc[nb][2 + i] * power(ke[1]) * sl2;
+                }
                 if (edge) {
                     const int lo = in_head ? 0 : jlo[nb][i], hi = in_head ? fhi[nb][i] : jhi[nb][i];
                     x0 = (there && j0 >= lo && j0 <= hi) ? x0 : -INFINITY;
@@ -340,19 +384,20 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
                 const float mu = (mn == -INFINITY) ? 0.f : mn;
                 const float alpha = exp2f(m[nb][i] - mu);
                 m[nb][i] = mn;
-                const float p0 = exp2f(sc[nb][i] - mu);
-                const float p1 = exp2f(sc[nb][2 + i] - mu);
+                const float p0 = exp2f(sc[nb][i] - mu + kBias);
+                const float p1 = exp2f(sc[nb][2 + i] - mu + kBias);
                 l[nb][i] = l[nb][i] * alpha + p0 + p1;
-                sc[nb][i] = p0 * v0;
-                sc[nb][2 + i] = p1 * v1;
+                sc[nb][i] = CODES ? p0 * v0 : p0;
+                sc[nb][2 + i] = CODES ? p1 * v1 : p1;
+                const float fac = CODES ? alpha * to_unit : alpha;
 #pragma unroll
                 for (int db = 0; db < C::HDW / 16; ++db) {
-                    o[db][nb][i] *= alpha;
-                    o[db][nb][2 + i] *= alpha;
+                    o[db][nb][i] *= fac;
+                    o[db][nb][2 + i] *= fac;
                 }
             }
-            pb[nb][0] = movmatrix_t(pack_bf16x2(sc[nb][0], sc[nb][1]));
-            pb[nb][1] = movmatrix_t(pack_bf16x2(sc[nb][2], sc[nb][3]));
+            pb[nb][0] = movmatrix_t(CODES ? pack_f16x2(sc[nb][0], sc[nb][1]) : pack_bf16x2(sc[nb][0], sc[nb][1]));
+            pb[nb][1] = movmatrix_t(CODES ? pack_f16x2(sc[nb][2], sc[nb][3]) : pack_bf16x2(sc[nb][2], sc[nb][3]));
         }
 
         // O^T (columns x RT rows) += V^T P^T
@@ -397,13 +442,19 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
                 ldsm_x4_t(va, r[0], r[1], r[2], r[3]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    // (any E4M3 code is a finite number in this form: what P multiplies by zero stays zero)
-                    const uint32_t a0 = mul_bf16x2(e4m3x2_raw<true>(r[2 * y]), kBf16x2Two120);
-                    const uint32_t a1 = mul_bf16x2(e4m3x2_raw<false>(r[2 * y]), kBf16x2Two120);
-                    const uint32_t a2 = mul_bf16x2(e4m3x2_raw<true>(r[2 * y + 1]), kBf16x2Two120);
-                    const uint32_t a3 = mul_bf16x2(e4m3x2_raw<false>(r[2 * y + 1]), kBf16x2Two120);
+                    // two keys of column 2 g, then of column 2 g + 1.  (What memory holds at keys that no row
+                    // attends may be the codes' NaN: it counts as 0.)
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16(__byte_perm(r[2 * y], 0u, 0x3120), a0, a1);
+                    e4m3x4_to_f16(__byte_perm(r[2 * y + 1], 0u, 0x3120), a2, a3);
+                    if (edge) {
+                        a0 &= keep0;
+                        a1 &= keep0;
+                        a2 &= keep1;
+                        a3 &= keep1;
+                    }
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(o[2 * db + y][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+                    for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[2 * db + y][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
                 }
             }
         }
@@ -432,11 +483,19 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
                 const int mi = kw * C::RT + nb * 8 + 2 * lane + i;
                 if (FMHA_IN_BOUNDS(mi >= 0 && mi < C::KW * C::RT, kSitePagedComb, f.status)) ml[mi] = make_float2(m[nb][i], l[nb][i]);
             }
+        if (CODES && lane == 0) v_exp[kw] = v_unit;
     }
     named_barrier_sync(1, C::NCW * 32);
 
     // This warp's O, relative to the row's maximum over all key groups
     float* comb = reinterpret_cast<float*>(stages);  // [KW][RT][HD]
+    int common = 0;  // codes: the largest of the groups' units, in which the sum is formed
+    float to_common = 1.f;
+    if constexpr (CODES) {
+#pragma unroll
+        for (int w = 0; w < C::KW; ++w) common = max(common, v_exp[w]);
+        to_common = v_unit - common < -126 ? 0.f : __uint_as_float((uint32_t)(127 + v_unit - common) << 23);
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -445,7 +504,8 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < C::KW; ++w) M = fmaxf(M, ml[w * C::RT + r].x);
-            const float fac = exp2f(m[nb][i] - ((M == -INFINITY) ? 0.f : M));
+            float fac = exp2f(m[nb][i] - ((M == -INFINITY) ? 0.f : M));
+            if constexpr (CODES) fac *= to_common;
 #pragma unroll
             for (int db = 0; db < C::HDW / 16; ++db) {
                 // rows g and g + 8 of the operand: columns g and g + 8 of 16, for codes 2 g and 2 g + 1
@@ -472,7 +532,7 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
         int head;
         const long long row = paged_out_row(f, t, kvh, t.r0 + r, head);
         float inv, lse;
-        paged_finish(M, L, SINK ? sink_log2_of(f.sink, head, f.n_h, f.status) : -INFINITY, inv, lse);
+        paged_finish(M - kBias, L, SINK ? sink_log2_of(f.sink, head, f.n_h, f.status) : -INFINITY, inv, lse);
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -482,6 +542,12 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
             const float4 u0 = src[0], u1 = src[1];
             acc[0] += u0.x; acc[1] += u0.y; acc[2] += u0.z; acc[3] += u0.w;
             acc[4] += u1.x; acc[5] += u1.y; acc[6] += u1.z; acc[7] += u1.w;
+        }
+        if constexpr (CODES) {  // out of O's units; the divide first, within fp32's range
+            const float unit = paged_scale((uint32_t)common);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = acc[e] * inv * unit;
+            inv = 1.f;
         }
         if (!FMHA_IN_BOUNDS(row >= 0 && row < f.rows && split < f.n_splits, kSitePagedOut, f.status)) continue;
         if (f.n_splits == 1) {
@@ -550,7 +616,9 @@ cudaError_t launch_s(const PagedFwd& f, int rows, cudaStream_t stream) {
 
 }  // namespace
 
-int paged_decode_kv_tile(int hd) { return hd <= 128 ? 64 : 32; }
+int paged_decode_kv_tile(int hd, bool codes) {
+    return codes ? (hd <= 128 ? PDCfg<128, 1, true>::KT : PDCfg<256, 1, true>::KT) : hd <= 128 ? PDCfg<128, 1, false>::KT : PDCfg<256, 1, false>::KT;
+}
 int paged_decode_rows(int hd, long long rows) { return rows > 8 && hd <= 256 ? 16 : 8; }
 
 cudaError_t launch_paged_decode(const PagedFwd& f, int rows, cudaStream_t stream) {

@@ -53,10 +53,11 @@ struct PTCfg {
     static constexpr int KCH = HD / NKC;
     static constexpr int NB = KCH / 64;                   // 64-column blocks of a K chunk, and of V
     static constexpr int SW = 4 * NRT;                    // softmax warps
-    static constexpr int CW = !CODES ? 0 : NRT == 2 ? 4 : 8;  // converter warps
+    static constexpr int CW = CODES ? 8 : 0;              // converter warps
     static constexpr int CT = 32 * CW;
     static constexpr int WARPS = SW + 2 + CW;             // + MMA issuer (warp SW) and producer (SW + 1)
     static constexpr int THREADS = WARPS * 32;
+    static constexpr int CH = CODES && NRT == 2 ? 32 : 64;  // scores that a softmax thread holds (18 warps leave it 96 registers)
     static constexpr int K_ARRIVALS = CODES ? CT : 1;     // on a full barrier of K or V
     static constexpr int Q_TILE = BM * HD * 2;
     static constexpr int Q_BYTES = NRT * Q_TILE;
@@ -95,15 +96,25 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 32 packed words times a packed factor, in this thread's TMEM lane.
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// 16 packed words times a packed factor, in this thread's TMEM lane.  (32 columns are read, 16 written.)
 __device__ __forceinline__ void tmem_scale_pairs(uint32_t taddr, uint32_t factor) {
     float v[32];
     tmem_ld32(taddr, v);
     tmem_wait_ld();
-    uint32_t w[32];
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = mul_bf16x2(__float_as_uint(v[i]), factor);
-    tmem_st32u(taddr, w);
+    for (int i = 0; i < 16; ++i) w[i] = mul_bf16x2(__float_as_uint(v[i]), factor);
+    tmem_st16u(taddr, w);
 }
 
 // 16 codes of a row as two 16-byte chunks of its bf16 operand row (128-byte swizzle).
@@ -252,8 +263,8 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
         mbar_arrive(q_full);
     };
 
-    // The page of this lane's granule of 16 keys (lane < BN / 16) of tile j, -1 where no key is needed.
-    auto page_of = [&](int j) {
+    // The block table's entry for this lane's granule of 16 keys (lane < BN / 16) of tile j, -1 where no key is needed.
+    auto entry_of = [&](int j) {
         if (j >= k.n || lane >= BN / 16) return -1;
         const int key = k.key(j, BN) + 16 * lane;  // (the copy that it begins may reach into the keys)
         return key < k.to(j) && (key | (box_keys - 1)) >= k.from(j) ? paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) : -1;
@@ -282,11 +293,11 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                     tma_load_5d(tile + (lane << log_box) * C::NB * 128, map, 0, 0, block0, row >> 3, slab, bar);
             };
             bool ok = true;
-            int k_issued = 0, v_issued = 0, cleared = 0, ahead = page_of(1), page_k = page_of(0), page_v = page_k;
+            int k_issued = 0, v_issued = 0, cleared = 0, ahead = entry_of(1), page_k = paged_page(f.c, entry_of(0)), page_v = page_k;
 #pragma unroll 1
             for (int j = 0; ok && j <= k.n; ++j) {
-                const int page = ahead;  // of tile j + 1
-                ahead = page_of(j + 2);
+                const int page = paged_page(f.c, ahead);  // of tile j + 1
+                ahead = entry_of(j + 2);
                 if (j < k.n) {
                     const int s = j % STG;
 #pragma unroll 1
@@ -360,13 +371,16 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 cp_async_arrive(&raw_full[x]);
                 ++issued[x];
             };
-            int page0 = page_of(0), page1 = page_of(1);
+            int ahead = entry_of(2);
+            const int page0 = paged_page(f.c, entry_of(0));
+            int page1 = paged_page(f.c, entry_of(1));
             load(0, 0, page0);
             load(1, 0, page0);
             if (k.n > 1) load(0, 1, page1);
 #pragma unroll 1
             for (int j = 2; ok && j <= k.n; ++j) {
-                const int page2 = page_of(j);
+                const int page2 = paged_page(f.c, ahead);
+                ahead = entry_of(j + 1);
                 if (j < k.n) load(0, j, page2);
                 load(1, j - 1, page1);
                 page1 = page2;
@@ -391,13 +405,14 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 const int i = tid % PPR, first = tid / PPR;
                 // a piece is two neighbouring chunks; pieces 4 apart lie in the same banks: they store theirs in the other order
                 const int c0 = (i & 3) * 2 ^ (first & 7), flip = PPR > 4 ? (i >> 2) & 1 : 0;
-                static_assert(N % 4 == 0 && STEP % 8 == 0, "pieces in fours, at one place of the swizzle");
+                constexpr int U = N < 4 ? N : 4;
+                static_assert(N % U == 0 && STEP % 8 == 0, "pieces in fours, at one place of the swizzle");
 #pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 4) {
-                    uint4 u[4];
-                    uint32_t byte[4];
+                for (int n0 = 0; n0 < N; n0 += U) {
+                    uint4 u[U];
+                    uint32_t byte[U], most = 0u;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < U; ++n) {
                         const int key = first + (n0 + n) * STEP;
                         u[n] = *reinterpret_cast<const uint4*>(raw + key * HD + i * 16);
                         byte[n] = sc[key];
@@ -405,16 +420,26 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                             u[n] = make_uint4(0u, 0u, 0u, 0u);
                             byte[n] = 127u;
                         }
+                        most = max(most, byte[n]);
                     }
+                    const bool two = __any_sync(0xffffffffu, most > 134u);
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < U; ++n) {
                         const int key = first + (n0 + n) * STEP;
-                        const PagedFactor fac = paged_factor(byte[n]);
                         uint32_t r[8];
-                        paged_values4(u[n].x, fac, r[0], r[1]);
-                        paged_values4(u[n].y, fac, r[2], r[3]);
-                        paged_values4(u[n].z, fac, r[4], r[5]);
-                        paged_values4(u[n].w, fac, r[6], r[7]);
+                        const uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
+                        if (!two) {  // the factor in one step (paged_common.cuh)
+                            const uint32_t fac = (byte[n] + 120u) * 0x00800080u;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                r[2 * y] = mul_bf16x2(e4m3x2_raw<true>(w[y]), fac);
+                                r[2 * y + 1] = mul_bf16x2(e4m3x2_raw<false>(w[y]), fac);
+                            }
+                        } else {
+                            const PagedFactor fac = paged_factor(byte[n]);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) paged_values4(w[y], fac, r[2 * y], r[2 * y + 1]);
+                        }
                         if (!FMHA_IN_BOUNDS(key < BN && (i >> 2) < C::NB, kSitePagedKv, f.status)) continue;
                         uint8_t* const row = tile + operand_row<C::NB>(key, i >> 2);
                         uint4 a = make_uint4(r[0], r[1], r[2], r[3]), b = make_uint4(r[4], r[5], r[6], r[7]);
@@ -465,15 +490,15 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < C::NKC; ++c) kb[c].template load<HD>(tid, kp + c * C::KCH, f.c.k_scales, r, f.c, f.status);
             };
-            int ahead = page_of(1);
-            TileRows r_v = rows_of(0, page_of(0));
+            int ahead = entry_of(1);
+            TileRows r_v = rows_of(0, paged_page(f.c, entry_of(0)));
             fetch_k(r_v);
             vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
             // K_j and then V_{j - 1}, for j up to k.n (where there is no K_j)
 #pragma unroll 1
             for (int j = 0; ok && j <= k.n; ++j) {
-                const int page = ahead;  // of tile j + 1
-                ahead = page_of(j + 2);
+                const int page = paged_page(f.c, ahead);  // of tile j + 1
+                ahead = entry_of(j + 2);
                 const TileRows next = rows_of(j + 1, page);
                 if (j < k.n) {
                     const int s = j % STG;
@@ -606,18 +631,13 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             // |scale| log2(e), not 0: a masked -inf times 0 would be a NaN (2^-126 makes all weights equal as it should)
             const float sl2 = fmaxf(fabsf(f.scale_log2), 1.17549435e-38f);
             float m_ref = -INFINITY, l = 0.f;
-            // pages of a tile, by granule of 16 keys: looked up one tile ahead
-            auto page_there = [&](int j) {
-                if (j >= k.n || lane >= BN / 16) return false;
-                const int key = k.key(j, BN) + 16 * lane;
-                return key < k.to(j) && paged_entry(f.c, f.t.batch, t.b, key >> f.c.log_page, f.status) >= 0;
-            };
-            bool ahead = page_there(0), ok = true;
+            int ahead = entry_of(0);  // block-table entries of a tile, loaded one tile ahead
+            bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < k.n; ++j) {
                 const int u = j * n_rt + rt, slot = u & 1;
-                const unsigned pages = __ballot_sync(0xffffffffu, ahead);
-                ahead = page_there(j + 1);
+                const unsigned pages = __ballot_sync(0xffffffffu, paged_page(f.c, ahead) >= 0);
+                ahead = entry_of(j + 1);
                 if (!__all_sync(0xffffffffu, mbar_wait(&s_full[slot], (u >> 1) & 1, f.status))) {
                     ok = false;
                     break;
@@ -633,13 +653,13 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 const int lo = k.head(j) ? 0 : jlo, hi = k.head(j) ? fhi : jhi;
                 const bool full = pages == (1u << (BN / 16)) - 1u && key0 >= lo && key0 + BN - 1 <= hi;
                 // the row's scores from column `col` of the tile on, -inf where it attends no key
-                auto load_scores = [&](int col, float (&x)[2][32]) {
-                    tmem_ld32(s_addr + col, x[0]);
-                    tmem_ld32(s_addr + col + 32, x[1]);
+                auto load_scores = [&](int col, float (&x)[C::CH / 32][32]) {
+#pragma unroll
+                    for (int h = 0; h < C::CH / 32; ++h) tmem_ld32(s_addr + col + h * 32, x[h]);
                     tmem_wait_ld();
                     if (!full) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < C::CH / 32; ++h) {
                             const int first = key0 + col + h * 32;
                             const int k0 = max(0, lo - first), k1 = min(31, hi - first);
                             uint32_t in = k1 >= k0 ? (0xffffffffu >> (31 - k1)) & (0xffffffffu << k0) : 0u;
@@ -650,10 +670,10 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                         }
                     }
                 };
-                auto top_of = [&](const float (&x)[2][32]) {
+                auto top_of = [&](const float (&x)[C::CH / 32][32]) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < C::CH / 32; ++h)
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[h][i], x[h][i + 1]));
                     return mx * sl2;
@@ -661,8 +681,8 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
                     float mt = -INFINITY;
 #pragma unroll 1
-                    for (int col = 0; col < BN; col += 64) {
-                        float x[2][32];
+                    for (int col = 0; col < BN; col += C::CH) {
+                        float x[C::CH / 32][32];
                         load_scores(col, x);
                         mt = fmaxf(mt, top_of(x));
                     }
@@ -670,17 +690,18 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 }
                 // P over S: columns col / 2 on take the weights of the scores from col on, which have been read
 #pragma unroll 1
-                for (int col = 0; col < BN; col += 64) {
-                    uint32_t pk[32];
+                for (int col = 0; col < BN; col += C::CH) {
+                    uint32_t pk[C::CH / 2];
                     float top;
                     while (true) {
-                        float x[2][32];
+                        float x[C::CH / 32][32];
                         load_scores(col, x);
                         const float mu = m_ref == -INFINITY ? 0.f : -m_ref;
                         const uint64_t q2 = f32x2(sl2, sl2), mu2 = f32x2(mu, mu);
+                        const uint64_t one2 = f32x2(1.f, 1.f);  // (a packed add takes twice as long as a packed fma)
                         uint64_t c2[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < C::CH / 32; ++h)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 float y0, y1;
@@ -688,7 +709,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                                 y0 = ex2_approx(y0);
                                 y1 = ex2_approx(y1);
                                 pk[h * 16 + i] = pack_bf16x2(y0, y1);
-                                c2[i & 1] = add_f32x2(c2[i & 1], f32x2(y0, y1));
+                                c2[i & 1] = fma_f32x2(f32x2(y0, y1), one2, c2[i & 1]);
                             }
                         float a0, a1, b0, b1;
                         f32x2_split(c2[0], a0, a1);
@@ -722,12 +743,15 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                         tmem_wait_st();
                         const uint32_t a16 = __float_as_uint(alpha) >> 16;
 #pragma unroll 1
-                        for (int c = 0; c < col / 2; c += 32) tmem_scale_pairs(s_addr + c, a16 | (a16 << 16));
+                        for (int c = 0; c < col / 2; c += 16) tmem_scale_pairs(s_addr + c, a16 | (a16 << 16));
                         tmem_wait_st();
                     }
                     if (!ok) break;
                     l += top;
-                    tmem_st32u(s_addr + col / 2, pk);
+                    if constexpr (C::CH == 64)
+                        tmem_st32u(s_addr + col / 2, pk);
+                    else
+                        tmem_st16u(s_addr + col / 2, pk);
                 }
                 if (!ok) break;
                 tmem_wait_st();

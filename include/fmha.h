@@ -637,9 +637,9 @@ struct fmha_fwd_paged_args {
 };
 int fmha_fwd_paged(const struct fmha_fwd_paged_args* args);
 
-/* The number of chunks that fmha_fwd_paged uses (ragged: 1 with cu_q); a negative FMHA_ERR_* code for invalid arguments. */
+/* The number of chunks that fmha_fwd_paged uses (ragged: 1 with cu_q; codes: 1 for 8-bit pages); a negative FMHA_ERR_* code for invalid arguments. */
 int fmha_fwd_paged_plan(int batch, int T, int total, int n_h, int n_kv_h, int hd, int page, int s_k, int window, int n_first,
-                        int causal, int ragged, int n_splits);
+                        int causal, int ragged, int codes, int n_splits);
 
 /* ABI version: major * 10000 + minor * 100 + patch. */
 int fmha_version(void);
