@@ -27,10 +27,10 @@
 //   8-bit pages at hd 512, where shared memory has no room for a raw buffer: eight warps load codes into
 //     registers, one tile ahead, and expand those.
 //
-// Softmax: scores against a reference, the maximum of the first tile in which the row attends a key,
-// rounded up to a whole number.  P in bf16 and its fp32 sum have the exponent range for what follows, so
-// no further maximum is taken: only where 64 weights sum to over 2^40 does the reference move, by a
-// whole number, and the sum, O and the tile's weights so far are multiplied by the power of two.
+// Softmax: scores against a reference, the maximum of the first scores that the row attends (so that a row's
+// only key has P = 1, which bf16 holds).  P in bf16 and its fp32 sum have the exponent range for what
+// follows: only where a score passes the reference by 40 (log2 units) does that move, by a whole number, and the
+// sum, O and the tile's weights so far are multiplied by the power of two.
 #include <atomic>
 #include <type_traits>
 #include "internal.h"
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 const int u = j * n_rt + rt, slot = u & 1;
                 const unsigned pages = __ballot_sync(0xffffffffu, paged_page(f.c, ahead) >= 0);
                 ahead = entry_of(j + 1);
-                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[slot], (u >> 1) & 1, f.status))) {
+                if (!wait_all(&s_full[slot], (u >> 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -678,76 +678,73 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                         for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[h][i], x[h][i + 1]));
                     return mx * sl2;
                 };
-                if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
-                    float mt = -INFINITY;
+                // The weights of C::CH scores from column col on, as packed pairs; false if a wait gave up.
+                auto weights = [&](int col, uint32_t* pk) -> bool {
+                    float x[C::CH / 32][32];
+                    load_scores(col, x);
+                    const float mt = top_of(x);
+                    const bool move = mt > m_ref + 40.f;  // true without a reference
+                    if (__any_sync(0xffffffffu, move)) {
+                        float alpha = 1.f;
+                        if (move) {
+                            if (m_ref == -INFINITY) {  // O and l are zero
+                                m_ref = mt;
+                            } else {
+                                const float d = ceilf(mt - m_ref);
+                                alpha = d < 127.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;
+                                m_ref += d;
+                                l *= alpha;
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                            // O's rescale needs the PV before on this row tile; with two row tiles that completed before S did
+                            if (j > 0) {
+                                if (n_rt == 1 && !wait_all(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) return ok = false;
+                                tc_fence_after();
 #pragma unroll 1
-                    for (int col = 0; col < BN; col += C::CH) {
-                        float x[C::CH / 32][32];
-                        load_scores(col, x);
-                        mt = fmaxf(mt, top_of(x));
+                                for (int c = 0; c < C::HDV / 32; ++c) {
+                                    float ov[32];
+                                    tmem_ld32(o_addr(c), ov);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) ov[i] *= alpha;
+                                    tmem_st32(o_addr(c), ov);
+                                }
+                            }
+                            tmem_wait_st();
+                            const uint32_t a16 = __float_as_uint(alpha) >> 16;
+#pragma unroll 1
+                            for (int c = 0; c < col / 2; c += 16) tmem_scale_pairs(s_addr + c, a16 | (a16 << 16));
+                            tmem_wait_st();
+                            load_scores(col, x);  // so that they need not be kept meanwhile
+                        }
                     }
-                    if (m_ref == -INFINITY) m_ref = ceilf(mt);  // O is zero without a reference
-                }
+                    const float mu = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t q2 = f32x2(sl2, sl2), mu2 = f32x2(mu, mu);
+                    const uint64_t one2 = f32x2(1.f, 1.f);  // (a packed add takes twice as long as a packed fma)
+                    uint64_t c2[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int h = 0; h < C::CH / 32; ++h)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float y0, y1;
+                            f32x2_split(fma_f32x2(f32x2(x[h][2 * i], x[h][2 * i + 1]), q2, mu2), y0, y1);
+                            y0 = ex2_approx(y0);
+                            y1 = ex2_approx(y1);
+                            pk[h * 16 + i] = pack_bf16x2(y0, y1);
+                            c2[i & 1] = fma_f32x2(f32x2(y0, y1), one2, c2[i & 1]);
+                        }
+                    float a0, a1, b0, b1;
+                    f32x2_split(c2[0], a0, a1);
+                    f32x2_split(c2[1], b0, b1);
+                    l += (a0 + a1) + (b0 + b1);
+                    return true;
+                };
                 // P over S: columns col / 2 on take the weights of the scores from col on, which have been read
 #pragma unroll 1
                 for (int col = 0; col < BN; col += C::CH) {
                     uint32_t pk[C::CH / 2];
-                    float top;
-                    while (true) {
-                        float x[C::CH / 32][32];
-                        load_scores(col, x);
-                        const float mu = m_ref == -INFINITY ? 0.f : -m_ref;
-                        const uint64_t q2 = f32x2(sl2, sl2), mu2 = f32x2(mu, mu);
-                        const uint64_t one2 = f32x2(1.f, 1.f);  // (a packed add takes twice as long as a packed fma)
-                        uint64_t c2[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int h = 0; h < C::CH / 32; ++h)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float y0, y1;
-                                f32x2_split(fma_f32x2(f32x2(x[h][2 * i], x[h][2 * i + 1]), q2, mu2), y0, y1);
-                                y0 = ex2_approx(y0);
-                                y1 = ex2_approx(y1);
-                                pk[h * 16 + i] = pack_bf16x2(y0, y1);
-                                c2[i & 1] = fma_f32x2(f32x2(y0, y1), one2, c2[i & 1]);
-                            }
-                        float a0, a1, b0, b1;
-                        f32x2_split(c2[0], a0, a1);
-                        f32x2_split(c2[1], b0, b1);
-                        top = (a0 + a1) + (b0 + b1);
-                        const bool move = top > 1.0995116e12f;  // 2^40
-                        if (!__any_sync(0xffffffffu, move)) break;
-                        // the reference moves to the largest of these scores, for the rows that ask for it
-                        load_scores(col, x);
-                        const float d = move ? ceilf(top_of(x) - m_ref) : 0.f;
-                        const float alpha = d < 127.f ? __uint_as_float((uint32_t)(127 - (int)d) << 23) : 0.f;
-                        m_ref += d;
-                        l *= alpha;
-                        // O's rescale needs the unit before on this row tile: with two row tiles its PV completed before S did
-                        if (j > 0) {
-                            if (n_rt == 1 && !wait_all(&o_done[(u - 1) & 1], ((u - 1) >> 1) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < C::HDV / 32; ++c) {
-                                float ov[32];
-                                tmem_ld32(o_addr(c), ov);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) ov[i] *= alpha;
-                                tmem_st32(o_addr(c), ov);
-                            }
-                        }
-                        tmem_wait_st();
-                        const uint32_t a16 = __float_as_uint(alpha) >> 16;
-#pragma unroll 1
-                        for (int c = 0; c < col / 2; c += 16) tmem_scale_pairs(s_addr + c, a16 | (a16 << 16));
-                        tmem_wait_st();
-                    }
-                    if (!ok) break;
-                    l += top;
+                    if (!weights(col, pk)) break;
                     if constexpr (C::CH == 64)
                         tmem_st32u(s_addr + col / 2, pk);
                     else
