@@ -20,12 +20,13 @@
 //     its boxes by TMA into the swizzled operand layout (a page that is not there is a box behind the
 //     pool: zeros).  Of a V tile at the end of the keys (or at the start of a window) it then clears the
 //     rows that no query row attends, so that nothing stale is multiplied.
-//   8-bit pages up to hd 256: bulk copies of 16 keys' codes each into a raw buffer, the scale
-//     bytes by cp.async, and the converters expand them to bf16 (paged_common.cuh) into the operand
-//     layout.  Expanded columns 1 and 2 of each four change places: Q is stored the same way, and O's
-//     columns are put right in the epilogue.
-//   8-bit pages at hd 512, where shared memory has no room for a raw buffer: eight warps load codes into
-//     registers, one tile ahead, and expand those.
+//   8-bit pages: bulk copies of the pages' codes into a raw buffer, the scale bytes by cp.async, and the
+//     converters expand them to bf16 (paged_common.cuh) into the operand layout.  Expanded columns 1 and 2 of
+//     each four change places: Q is stored the same way, and O's columns are put right in the epilogue.
+//     (To fp16 by the hardware's conversion it takes half the instructions but, with the units that
+//     fp16's range asks for, not less time: 346 us for a chunk that takes 305.)
+// At hd 256 and 512 256 of Q's columns lie in tensor memory: QK takes its A operand from there, which at N = 64 is
+// faster (32 clocks an MMA, 48 with both operands from shared memory) and leaves room for stages and raw buffers.
 //
 // Softmax: scores against a reference, the maximum of the first scores that the row attends (so that a row's
 // only key has P = 1, which bf16 holds).  P in bf16 and its fp32 sum have the exponent range for what
@@ -47,35 +48,40 @@ struct PTCfg {
     static constexpr int BN = HD <= 128 ? 128 : 64;       // keys per tile
     static constexpr int HDV = HD == 512 ? 256 : HD;      // columns of O per block
     static constexpr int PARTS = HD / HDV;                // blocks per row tile
-    static constexpr bool RAW = CODES && HD <= 256;       // codes by way of a raw buffer
-    static constexpr int STG = HD == 512 ? 1 : HD == 64 ? 4 : 2;  // K and V stages
+    static constexpr int QT = HD >= 256 ? 256 : 0;        // columns of Q in tensor memory, the first ones
+    static constexpr int KST = HD == 64 ? 4 : HD == 128 ? 2 : HD == 256 ? 3 : CODES ? 1 : 2;  // K stages
+    static constexpr int VST = HD == 512 ? 1 : KST;       // V stages
     static constexpr int NKC = HD == 512 ? 2 : 1;         // column chunks of a K tile, each with barriers of its own
     static constexpr int KCH = HD / NKC;
     static constexpr int NB = KCH / 64;                   // 64-column blocks of a K chunk, and of V
     static constexpr int SW = 4 * NRT;                    // softmax warps
     static constexpr int CW = CODES ? 8 : 0;              // converter warps
     static constexpr int CT = 32 * CW;
-    static constexpr int WARPS = SW + 2 + CW;             // + MMA issuer (warp SW) and producer (SW + 1)
+    static constexpr int HW = HD == 512 && !CODES ? 4 : 0;  // warps that only help to load Q
+    static constexpr int QW = QT == HD ? SW : SW + CW + HW;  // warps that load Q
+    static constexpr int WARPS = SW + 2 + CW + HW;        // + MMA issuer (warp SW) and producer (SW + 1)
     static constexpr int THREADS = WARPS * 32;
     static constexpr int CH = CODES && NRT == 2 ? 32 : 64;  // scores that a softmax thread holds (18 warps leave it 96 registers)
     static constexpr int K_ARRIVALS = CODES ? CT : 1;     // on a full barrier of K or V
-    static constexpr int Q_TILE = BM * HD * 2;
+    static constexpr int Q_TILE = BM * (HD - QT) * 2;
     static constexpr int Q_BYTES = NRT * Q_TILE;
     static constexpr int K_TILE = BN * HD * 2;
     static constexpr int V_TILE = BN * HDV * 2;
-    static constexpr int O_COL = 2 * BN;                  // tensor memory: two S slots, then O of each row tile
+    static constexpr int O_COL = 2 * BN;                  // tensor memory: two S slots, then O of each row tile, then Q
+    static constexpr int Q_COL = O_COL + NRT * HDV;
     static constexpr int TMEM_COLS = 512;
     static constexpr int OFF_K = Q_BYTES;
-    static constexpr int OFF_V = OFF_K + STG * K_TILE;
-    static constexpr int OFF_RAW = OFF_V + STG * V_TILE;  // codes of K, of V
+    static constexpr int OFF_V = OFF_K + KST * K_TILE;
+    static constexpr int OFF_RAW = OFF_V + VST * V_TILE;  // codes of K, of V
     static constexpr int RAW_TILE = BN * HD;
-    static constexpr int OFF_SC = OFF_RAW + (RAW ? 2 * RAW_TILE : 0);  // scale bytes of K, of V
-    static constexpr int OFF_BAR = OFF_SC + (RAW ? 2 * BN : 0);
-    static constexpr int N_BARS = 1 + 2 * STG * NKC + 2 * STG + 6 + 1 + 4;
+    static constexpr int OFF_SC = OFF_RAW + (CODES ? 2 * RAW_TILE : 0);  // scale bytes of K, of V
+    static constexpr int OFF_BAR = OFF_SC + (CODES ? 2 * BN : 0);
+    static constexpr int N_BARS = 1 + 2 * KST * NKC + 2 * VST + 6 + 1 + 4;
     static constexpr int NEED = 1024 + OFF_BAR + N_BARS * 8 + 16;
     static constexpr int SMEM = NEED < 120000 ? 120000 : NEED;  // one block per SM: each takes all of tensor memory
     static_assert(NB == HDV / 64, "K chunks and V tiles have the same layout");
-    static_assert(O_COL + NRT * HDV <= TMEM_COLS, "S and O fit in tensor memory");
+    static_assert(Q_COL + QT / 2 <= TMEM_COLS, "S, O and Q fit in tensor memory");
+    static_assert(QT % KCH == 0 || QT == HD, "a K chunk meets Q in one place");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -117,59 +123,11 @@ __device__ __forceinline__ void tmem_scale_pairs(uint32_t taddr, uint32_t factor
     tmem_st16u(taddr, w);
 }
 
-// 16 codes of a row as two 16-byte chunks of its bf16 operand row (128-byte swizzle).
-__device__ __forceinline__ void store_expanded(uint8_t* box_row, int c0, int key, const uint4& codes, const PagedFactor& f) {
-    uint32_t r[8];
-    paged_values4(codes.x, f, r[0], r[1]);
-    paged_values4(codes.y, f, r[2], r[3]);
-    paged_values4(codes.z, f, r[4], r[5]);
-    paged_values4(codes.w, f, r[6], r[7]);
-    *reinterpret_cast<uint4*>(box_row + ((c0 ^ (key & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
-    *reinterpret_cast<uint4*>(box_row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
-// What a loader thread needs of one key tile: this lane's granule of 16 keys (lane < BN / 16) as a row of the
-// pool, -1 if no row attends a key of it or its page is not there; and the range of keys that count.
-struct TileRows {
-    int row, from, to;  // from, to: relative to the tile's first key
-};
-
-// One converter thread's share of a tile of codes (hd 512): N pieces of 16 columns, PPR per key, going round the LT threads.
-template <int N, int PPR, int LT>
-struct Codes {
-    uint4 codes[N];
-    uint32_t scales[N];
-
-    // base: the pool's first row from the tile's first column on; STRIDE bytes a row.
-    template <int STRIDE>
-    __device__ __forceinline__ void load(int tid, const uint8_t* base, const uint8_t* sc, const TileRows& t, const PagedCache& c,
-                                         unsigned* status) {
-#pragma unroll
-        for (int p = 0; p < N; ++p) {
-            const int idx = p * LT + tid, key = idx / PPR, i = idx % PPR;
-            const int first = __shfl_sync(0xffffffffu, t.row, key >> 4), row = first + (key & 15);
-            const bool live = first >= 0 && key >= t.from && key < t.to && FMHA_IN_BOUNDS(paged_row_ok(c, row), kSitePagedRow, status);
-            codes[p] = live ? __ldg(reinterpret_cast<const uint4*>(base + (long long)row * STRIDE + i * 16)) : make_uint4(0u, 0u, 0u, 0u);
-            scales[p] = live ? __ldg(sc + row) : 127u;
-        }
-    }
-
-    // As bf16 into an operand tile of `rows` keys.
-    __device__ __forceinline__ void store(int tid, uint8_t* tile, int rows, unsigned* status) const {
-#pragma unroll
-        for (int p = 0; p < N; ++p) {
-            const int idx = p * LT + tid, key = idx / PPR, i = idx % PPR, off = operand_row<PPR / 4>(key, i >> 2);
-            if (FMHA_IN_BOUNDS(key < rows && off >= 0 && off + 128 <= rows * (PPR / 4) * 128, kSitePagedKv, status))
-                store_expanded(tile + off, (i & 3) * 2, key, codes[p], paged_factor(scales[p]));
-        }
-    }
-};
-
 template <int HD, bool CODES, bool SINK>
 __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const PagedFwd f) {
     using C = PTCfg<HD, CODES>;
-    constexpr int BM = C::BM, BN = C::BN, STG = C::STG;
+    constexpr int BM = C::BM, BN = C::BN, KST = C::KST, VST = C::VST;
     launch_dependents();  // the merge grid may be scheduled now; it waits for this grid's results
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,10 +137,10 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* q_full = bars;
     uint64_t* k_full = bars + 1;
-    uint64_t* k_empty = k_full + STG * C::NKC;  // by stage and chunk
-    uint64_t* v_full = k_empty + STG * C::NKC;
-    uint64_t* v_empty = v_full + STG;
-    uint64_t* s_full = v_empty + STG;  // [2] by slot
+    uint64_t* k_empty = k_full + KST * C::NKC;  // by stage and chunk
+    uint64_t* v_full = k_empty + KST * C::NKC;
+    uint64_t* v_empty = v_full + VST;
+    uint64_t* s_full = v_empty + VST;  // [2] by slot
     uint64_t* p_ready = s_full + 2;    // [2]
     uint64_t* o_done = p_ready + 2;    // [2]
     uint64_t* mma_drain = o_done + 2;  // every MMA the issuer launched has completed (exit drain)
@@ -193,12 +151,12 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x % C::PARTS, kvh = blockIdx.x / C::PARTS % f.c.n_kv_h, split = blockIdx.y;
     if (threadIdx.x == 0) {
-        mbar_init(q_full, (C::SW + C::CW) * 32);
-        for (int s = 0; s < STG * C::NKC; ++s) {
+        mbar_init(q_full, C::QW * 32);
+        for (int s = 0; s < KST * C::NKC; ++s) {
             mbar_init(&k_full[s], C::K_ARRIVALS);
             mbar_init(&k_empty[s], 1);
         }
-        for (int s = 0; s < STG; ++s) {
+        for (int s = 0; s < VST; ++s) {
             mbar_init(&v_full[s], C::K_ARRIVALS);
             mbar_init(&v_empty[s], 1);
         }
@@ -206,7 +164,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             mbar_init(&s_full[s], 1);
             mbar_init(&p_ready[s], 128);
             mbar_init(&o_done[s], 1);
-            mbar_init(&raw_full[s], C::RAW ? 33 : 1);
+            mbar_init(&raw_full[s], CODES ? 33 : 1);
             mbar_init(&raw_empty[s], CODES ? C::CT : 1);
         }
         mbar_init(mma_drain, 1);
@@ -215,7 +173,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     grid_dependency_wait();  // every global access below follows the preceding kernel
     const PagedTile t = paged_tile(f, blockIdx.x / C::PARTS / f.c.n_kv_h, BM * C::NRT, f.status);
     if (t.n <= 0) return;
-    const int box_keys = CODES && !C::RAW ? 16 : min(f.c.page, BN);  // keys that are copied at once, from a multiple of that on
+    const int box_keys = min(f.c.page, BN);  // keys that are copied at once, from a multiple of that on
     const PagedKeys k = paged_keys(f, t, split, BN, box_keys);
     if (k.n <= 0) {  // nothing to attend in this chunk: no tensor memory, no Q
         paged_write_empty(f, t, kvh, split, part * C::HDV, C::HDV);
@@ -231,35 +189,37 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     const int n_rt = C::NRT == 2 && t.n > BM ? 2 : 1;
 
-    // Q's rows as 64-column boxes of 128 swizzled rows per row tile, zeros behind the last row; of the
-    // opposite sign for a negative scale (the softmax takes its magnitude), for codes with columns 1 and 2 of each
-    // four exchanged.  All but the MMA warp and the producer take part, w = 0 .. SW + CW - 1.
+    // Q of the opposite sign for a negative scale (the softmax takes its magnitude); for codes with columns 1 and 2 of each
+    // four exchanged; zeros behind the last row.
+    const uint32_t q_sign = f.scale_log2 < 0.f ? 0x80008000u : 0u;
+    auto as_operand = [&](uint4 v) {
+        if constexpr (CODES)
+            v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+        return make_uint4(v.x ^ q_sign, v.y ^ q_sign, v.z ^ q_sign, v.w ^ q_sign);
+    };
+    // Columns from QT on as 64-column boxes of 128 swizzled rows per row tile, by warps w = 0 .. QW - 1.
     auto load_q = [&](int w) {
-        constexpr int PPR = HD / 8, BATCH = HD <= 128 ? 4 : 8, QT = (C::SW + C::CW) * 32;
-        const uint32_t sign = f.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const int total = n_rt * BM * PPR;
+        if constexpr (C::QT < HD) {
+            constexpr int PPR = (HD - C::QT) / 8, BATCH = 8, QN = C::QW * 32;
+            const int total = n_rt * BM * PPR;
 #pragma unroll 1
-        for (int base = w * 32 + lane; base < total; base += QT * BATCH) {
-            uint4 u[BATCH];
+            for (int base = w * 32 + lane; base < total; base += QN * BATCH) {
+                uint4 u[BATCH];
 #pragma unroll
-            for (int y = 0; y < BATCH; ++y) {
-                const int i = base + y * QT, r = i / PPR;
-                u[y] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < total && r < t.n) u[y] = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + i % PPR * 8));
-            }
+                for (int y = 0; y < BATCH; ++y) {
+                    const int i = base + y * QN, r = i / PPR;
+                    u[y] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < total && r < t.n) u[y] = __ldg(reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + r) + C::QT + i % PPR * 8));
+                }
 #pragma unroll
-            for (int y = 0; y < BATCH; ++y) {
-                const int i = base + y * QT, r = i / PPR, c = i % PPR;
-                uint4 v = u[y];
-                if constexpr (CODES)
-                    v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                                   __byte_perm(v.z, v.w, 0x7632));
-                v = make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
-                const int at = (r / BM) * C::Q_TILE + (c >> 3) * BM * 128 + (r % BM) * 128 + (((c & 7) ^ (r & 7)) << 4);
-                if (i < total && FMHA_IN_BOUNDS(at >= 0 && at + 16 <= C::Q_BYTES, kSitePagedQ, f.status)) *reinterpret_cast<uint4*>(sq + at) = v;
+                for (int y = 0; y < BATCH; ++y) {
+                    const int i = base + y * QN, r = i / PPR, c = i % PPR;
+                    const int at = (r / BM) * C::Q_TILE + (c >> 3) * BM * 128 + (r % BM) * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    if (i < total && FMHA_IN_BOUNDS(at >= 0 && at + 16 <= C::Q_BYTES, kSitePagedQ, f.status)) *reinterpret_cast<uint4*>(sq + at) = as_operand(u[y]);
+                }
             }
+            fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         mbar_arrive(q_full);
     };
 
@@ -299,10 +259,10 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 const int page = paged_page(f.c, ahead);  // of tile j + 1
                 ahead = entry_of(j + 2);
                 if (j < k.n) {
-                    const int s = j % STG;
+                    const int s = j % KST;
 #pragma unroll 1
                     for (int c = 0; ok && c < C::NKC; ++c) {
-                        ok = j < STG || wait_all(&k_empty[s * C::NKC + c], ((j / STG) - 1) & 1);
+                        ok = j < KST || wait_all(&k_empty[s * C::NKC + c], ((j / KST) - 1) & 1);
                         if (ok) {
                             load(&tmk, j, page_k, c * C::NB, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), &k_full[s * C::NKC + c]);
                             ++k_issued;
@@ -310,8 +270,8 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                     }
                 }
                 if (ok && j > 0) {
-                    const int jv = j - 1, s = jv % STG;
-                    ok = jv < STG || wait_all(&v_empty[s], ((jv / STG) - 1) & 1);
+                    const int jv = j - 1, s = jv % VST;
+                    ok = jv < VST || wait_all(&v_empty[s], ((jv / VST) - 1) & 1);
                     if (ok) {
                         const int key0 = k.key(jv, BN), from = k.from(jv) - key0, to = k.to(jv) - key0;
                         uint8_t* tile = sv + s * C::V_TILE;
@@ -337,9 +297,9 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                 page_k = page;
             }
             // Exit drain: what was loaded has landed before the block exits, whatever the waits said.
-            drain_ring(k_full, STG * C::NKC, k_issued, f.status);
-            drain_ring(v_full, STG, v_issued, f.status);
-        } else if constexpr (C::RAW) {
+            drain_ring(k_full, KST * C::NKC, k_issued, f.status);
+            drain_ring(v_full, VST, v_issued, f.status);
+        } else {
             // One raw buffer each for K and V, filled again as soon as the converters have read it: they go
             // K_0 K_1 V_0 K_2 V_1 ..., so K_{j+2} can be on its way while they are at V_j.
             const uint64_t pol = l2_policy_evict_first();
@@ -390,15 +350,18 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             for (int x = 0; x < 2; ++x)
                 if (issued[x] > 0) mbar_wait(&raw_full[x], (issued[x] - 1) & 1, f.status);
         }
+    } else if (C::HW > 0 && warp > C::SW + 1) {
+        load_q(warp - 2);
     } else if (warp > C::SW + 1) {
         // ------------------------------------------------------------ converters
         const int tid = threadIdx.x - (C::SW + 2) * 32;
         bool ok = true;
-        load_q(warp - 2);
-        if constexpr (C::RAW) {
+        if constexpr (C::QT < HD) load_q(warp - 2);
+        if constexpr (CODES) {
             // Pieces of 16 columns, PPR per key, going round the threads, four read before they are expanded.
-            auto convert = [&](int j, int x, uint8_t* tile) {
-                constexpr int PPR = HD / 16, N = BN * PPR / C::CT, STEP = C::CT / PPR;  // keys from one piece of a thread to the next
+            // Columns from col0 on, as many as a K chunk or V tile has.
+            auto convert = [&](int j, int x, int col0, uint8_t* tile) {
+                constexpr int PPR = C::KCH / 16, N = BN * PPR / C::CT, STEP = C::CT / PPR;  // keys from one piece of a thread to the next
                 const int key0 = k.key(j, BN), from = k.from(j) - key0, to = k.to(j) - key0;
                 const uint8_t* const raw = smem + C::OFF_RAW + x * C::RAW_TILE;
                 const uint8_t* const sc = smem + C::OFF_SC + x * BN;
@@ -414,7 +377,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
 #pragma unroll
                     for (int n = 0; n < U; ++n) {
                         const int key = first + (n0 + n) * STEP;
-                        u[n] = *reinterpret_cast<const uint4*>(raw + key * HD + i * 16);
+                        u[n] = *reinterpret_cast<const uint4*>(raw + key * HD + col0 + i * 16);
                         byte[n] = sc[key];
                         if (key < from || key >= to) {  // nothing stale is multiplied
                             u[n] = make_uint4(0u, 0u, 0u, 0u);
@@ -458,73 +421,26 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
 #pragma unroll 1
             for (int j = 0; ok && j <= k.n; ++j) {
                 if (j < k.n) {
-                    const int s = j % STG;
-                    ok = mbar_wait(&raw_full[0], j & 1, f.status) && (j < STG || mbar_wait(&k_empty[s], ((j / STG) - 1) & 1, f.status));
-                    if (ok) {
-                        convert(j, 0, sk + s * C::K_TILE);
-                        mbar_arrive(&raw_empty[0]);
-                        mbar_arrive(&k_full[s]);
+                    const int s = j % KST;
+                    ok = wait_all(&raw_full[0], j & 1);
+#pragma unroll 1
+                    for (int c = 0; ok && c < C::NKC; ++c) {
+                        ok = j < KST || wait_all(&k_empty[s * C::NKC + c], ((j / KST) - 1) & 1);
+                        if (!ok) break;
+                        convert(j, 0, c * C::KCH, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC));
+                        if (c == C::NKC - 1) mbar_arrive(&raw_empty[0]);
+                        mbar_arrive(&k_full[s * C::NKC + c]);
                     }
                 }
                 if (ok && j > 0) {
-                    const int jv = j - 1, s = jv % STG;
-                    ok = mbar_wait(&raw_full[1], jv & 1, f.status) && (jv < STG || mbar_wait(&v_empty[s], ((jv / STG) - 1) & 1, f.status));
+                    const int jv = j - 1, s = jv % VST;
+                    ok = wait_all(&raw_full[1], jv & 1) && (jv < VST || wait_all(&v_empty[s], ((jv / VST) - 1) & 1));
                     if (ok) {
-                        convert(jv, 1, sv + s * C::V_TILE);
+                        convert(jv, 1, part * C::HDV, sv + s * C::V_TILE);
                         mbar_arrive(&raw_empty[1]);
                         mbar_arrive(&v_full[s]);
                     }
                 }
-            }
-        } else if constexpr (CODES) {
-            auto rows_of = [&](int j, int page) {
-                const int key0 = k.key(j, BN);
-                return TileRows{paged_row(f.c, page, kvh, key0 + 16 * lane), k.from(j) - key0, k.to(j) - key0};
-            };
-            constexpr int KPPR = C::KCH / 16, VPPR = C::HDV / 16;
-            Codes<BN * KPPR / C::CT, KPPR, C::CT> kb[C::NKC];
-            Codes<BN * VPPR / C::CT, VPPR, C::CT> vb;
-            const uint8_t* const kp = static_cast<const uint8_t*>(f.c.k_pages);
-            const uint8_t* const vp = static_cast<const uint8_t*>(f.c.v_pages) + part * C::HDV;
-            auto fetch_k = [&](const TileRows& r) {
-#pragma unroll
-                for (int c = 0; c < C::NKC; ++c) kb[c].template load<HD>(tid, kp + c * C::KCH, f.c.k_scales, r, f.c, f.status);
-            };
-            int ahead = entry_of(1);
-            TileRows r_v = rows_of(0, paged_page(f.c, entry_of(0)));
-            fetch_k(r_v);
-            vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
-            // K_j and then V_{j - 1}, for j up to k.n (where there is no K_j)
-#pragma unroll 1
-            for (int j = 0; ok && j <= k.n; ++j) {
-                const int page = paged_page(f.c, ahead);  // of tile j + 1
-                ahead = entry_of(j + 2);
-                const TileRows next = rows_of(j + 1, page);
-                if (j < k.n) {
-                    const int s = j % STG;
-#pragma unroll
-                    for (int c = 0; c < C::NKC; ++c) {
-                        const int q = s * C::NKC + c;
-                        ok = ok && (j < STG || wait_all(&k_empty[q], ((j / STG) - 1) & 1));
-                        if (ok) {
-                            kb[c].store(tid, sk + s * C::K_TILE + c * (C::K_TILE / C::NKC), BN, f.status);
-                            fence_proxy_async_smem();
-                            mbar_arrive(&k_full[q]);
-                        }
-                    }
-                    if (ok && j + 1 < k.n) fetch_k(next);
-                }
-                if (ok && j > 0) {
-                    const int jv = j - 1, s = jv % STG;
-                    ok = jv < STG || wait_all(&v_empty[s], ((jv / STG) - 1) & 1);
-                    if (ok) {
-                        vb.store(tid, sv + s * C::V_TILE, BN, f.status);
-                        fence_proxy_async_smem();
-                        mbar_arrive(&v_full[s]);
-                        if (j < k.n) vb.template load<HD>(tid, vp, f.c.v_scales, r_v, f.c, f.status);
-                    }
-                }
-                r_v = next;
             }
         }
     } else if (warp == C::SW) {
@@ -544,22 +460,28 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             // QK(u) of key tile j, for row tile RT, into slot SLOT
             auto issue_qk = [&](int j, auto rt_, auto slot_) -> bool {
                 constexpr int RT = decltype(rt_)::value, SLOT = decltype(slot_)::value;
-                const int s = j % STG;
+                const int s = j % KST;
                 const uint32_t d = tmem + SLOT * BN;
                 if (!FMHA_IN_BOUNDS(s >= 0 && C::OFF_K + (s + 1) * C::K_TILE <= C::OFF_V && (RT + 1) * C::Q_TILE <= C::OFF_K, kSitePagedDesc, f.status))
                     return false;
                 const uint64_t a0 = q_desc + RT * (C::Q_TILE / 16), b0 = k_desc + s * (C::K_TILE / 16);
 #pragma unroll
                 for (int c = 0; c < C::NKC; ++c) {
-                    if (RT == 0 && !wait_all(&k_full[s * C::NKC + c], (j / STG) & 1)) return false;
+                    if (RT == 0 && !wait_all(&k_full[s * C::NKC + c], (j / KST) & 1)) return false;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int y = 0; y < C::NB; ++y)  // blocks of 64 columns
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)  // 16 columns = 32 bytes into the swizzled row
-                                tc_mma_f16(d, a0 + (c * C::NB + y) * (BM * 128 / 16) + kk * 2, b0 + c * (C::K_TILE / C::NKC / 16) + y * 64 + kk * 2, idesc_s,
-                                           (c > 0 || y > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < 4; ++kk) {  // 16 columns = 32 bytes into the swizzled row
+                                const uint64_t b = b0 + c * (C::K_TILE / C::NKC / 16) + y * 64 + kk * 2;
+                                const int col = c * C::KCH + y * 64 + kk * 16;
+                                const uint32_t more = col > 0 ? 1u : 0u;
+                                if (col < C::QT)
+                                    tc_mma_f16_ts(d, tmem + C::Q_COL + col / 2, b, idesc_s, more);
+                                else
+                                    tc_mma_f16(d, a0 + (col - C::QT) / 64 * (BM * 128 / 16) + kk * 2, b, idesc_s, more);
+                            }
                         if (RT == NR - 1) tc_commit(&k_empty[s * C::NKC + c]);
                         if (c == C::NKC - 1) tc_commit(&s_full[SLOT]);
                     }
@@ -570,8 +492,8 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             // PV(u) for slot SLOT, key tile j, row tile RT; phase: of the slot's barrier
             auto issue_pv = [&](int j, unsigned phase, auto rt_, auto slot_) -> bool {
                 constexpr int RT = decltype(rt_)::value, SLOT = decltype(slot_)::value;
-                const int s = j % STG;
-                if (RT == 0 && !wait_all(&v_full[s], (j / STG) & 1)) return false;
+                const int s = j % VST;
+                if (RT == 0 && !wait_all(&v_full[s], (j / VST) & 1)) return false;
                 if (!wait_all(&p_ready[SLOT], phase)) return false;
                 tc_fence_after();
                 const uint64_t b0 = v_desc + s * (C::V_TILE / 16);
@@ -616,8 +538,30 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
         mbar_wait(mma_drain, 0, f.status);
     } else {
         // ------------------------------------------------------------ softmax and epilogue of row tile rt
-        load_q(warp);
         const int rt = warp >> 2, quarter = warp & 3;
+        if constexpr (C::QT > 0) {
+            // the first columns of this thread's row into tensor memory
+            const uint4* const src = reinterpret_cast<const uint4*>(f.q + paged_q_at(f, t, kvh, t.r0 + min(warp * 32 + lane, t.n - 1)));
+            const uint32_t t_q = tmem + ((uint32_t)(quarter * 32) << 16) + C::Q_COL;
+#pragma unroll 1
+            for (int c = 0; c < C::QT / 64; c += 2) {
+                uint32_t w[2][32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 v = as_operand(warp * 32 + lane < t.n ? __ldg(src + c * 8 + i) : make_uint4(0u, 0u, 0u, 0u));
+                    w[i / 8][i % 8 * 4] = v.x;
+                    w[i / 8][i % 8 * 4 + 1] = v.y;
+                    w[i / 8][i % 8 * 4 + 2] = v.z;
+                    w[i / 8][i % 8 * 4 + 3] = v.w;
+                }
+                const bool in = FMHA_IN_BOUNDS(C::Q_COL + c * 32 + 64 <= C::TMEM_COLS, kSitePagedTmem, f.status);
+                tmem_st32u(t_q + (in ? c * 32 : 0), w[0]);
+                tmem_st32u(t_q + (in ? c * 32 + 32 : 0), w[1]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+        }
+        load_q(warp);
         if (rt < n_rt) {
             const int row = rt * BM + quarter * 32 + lane;  // of the block's rows; its TMEM lane is row % 128
             const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -766,9 +710,9 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             paged_finish(m_ref, l, (SINK && valid) ? sink_log2_of(f.sink, head, f.n_h, f.status) : -INFINITY, inv, lse);
             const bool store = valid && ok && FMHA_IN_BOUNDS(orow >= 0 && orow < f.rows && split < f.n_splits, kSitePagedOut, f.status);
             const unsigned rows_live = __ballot_sync(0xffffffffu, store);
-            // through a 4 KB corner of the row tile's Q per warp (its MMAs are done), so that a
+            // through a 4 KB corner of the row tile's Q (or, with Q in tensor memory, of K) per warp, whose MMAs are done, so that a
             // store covers whole 64- or 128-byte pieces of rows
-            uint8_t* stage = sq + rt * C::Q_TILE + quarter * 4096;
+            uint8_t* stage = smem + (C::NRT == 2 ? rt * C::Q_TILE : 0) + quarter * 4096;
             if (ok) {
 #pragma unroll 1
                 for (int c = 0; c < C::HDV / 32; ++c) {
@@ -784,7 +728,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                         }
                     }
                     const int col = part * C::HDV + c * 32;
-                    if (!FMHA_IN_BOUNDS(col + 32 <= HD && quarter * 4096 + 4096 <= C::Q_TILE, kSitePagedComb, f.status)) continue;
+                    if (!FMHA_IN_BOUNDS(col + 32 <= HD && quarter * 4096 + 4096 <= (C::NRT == 2 ? C::Q_TILE : C::OFF_V), kSitePagedComb, f.status)) continue;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
