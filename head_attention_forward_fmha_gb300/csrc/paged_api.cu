@@ -61,13 +61,20 @@ int check_strides(const long long* s, const char* name) {
     return FMHA_OK;
 }
 
-// Rows per KV head from which on the tensor-core kernel is taken (decode kernel below).
-int tc_min_rows(int hd) { return hd >= 256 ? 24 : 40; }
+// Rows per KV head from which on the tensor-core kernel is taken, the decode kernel below.  Measured on
+// 8 ragged sequences of up to 8192 keys and 8 KV heads (us, decode kernel / tensor cores):
+//   bf16   hd  64   16 rows  21 / 30   24 rows  32 / 32     codes  16 rows   28 / 41   24 rows   48 /  41
+//   bf16   hd 128   16 rows  28 / 34   24 rows  43 / 34     codes  16 rows   32 / 47   24 rows   52 /  48
+//   bf16   hd 256    8 rows  43 / 50   16 rows  51 / 51     codes  16 rows   64 / 78   24 rows  105 /  81
+//   bf16   hd 512    8 rows  95 / 110  10 rows 151 / 111    codes  24 rows  157 / 174  32 rows  195 / 174
+// The decode kernel reads the keys once for every 16 rows (8 at hd 512).
+int tc_min_rows(int hd, bool codes) { return hd == 512 ? (codes ? 25 : 9) : hd == 256 && !codes ? 9 : 17; }
 
-// Estimated time of a key tile in a block of the tensor-core kernel, `rows` being those of a sequence under a KV head.
+// Estimated time of a key tile in a block of the tensor-core kernel, `rows` being those of a sequence under a KV head
+// (measured: blocks of one and of two row tiles at hd 64 and 128, chunks of 512 tokens and 64 rows at hd 256 and 512).
 double tc_tile_us(int hd, bool codes, long long rows) {
-    if (hd <= 128) return (rows > 128 ? 2.0 : 1.4) * (codes ? 1.25 : 1.0);  // tiles of 128 keys
-    return hd == 256 ? (codes ? 2.0 : 0.95) : codes ? 3.7 : 1.55;          // of 64
+    if (hd <= 128) return (rows > 128 ? (hd == 64 ? 1.6 : 1.75) : (hd == 64 ? 1.05 : 1.1)) * (codes ? 1.4 : 1.0);  // tiles of 128 keys
+    return hd == 256 ? (codes ? 1.7 : 0.75) : codes ? 2.4 : 1.25;                                                  // of 64
 }
 
 // Kernel, row tiles and chunks of an attention call.  f->t.T is the number of new tokens of every
@@ -85,7 +92,7 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
     const int hd = f->c.hd;
     const long long most = (long long)f->group * f->t.T;  // rows of a sequence under a KV head
     const int path = kernel_path();
-    p.tc = path ? path >= 2 : most >= tc_min_rows(hd);
+    p.tc = path ? path >= 2 : most >= tc_min_rows(hd, codes);
     p.rows = p.tc ? paged_tc_rows(hd) : paged_decode_rows(hd, most);
     const long long tokens = ragged ? f->t.total : (long long)f->t.batch * f->t.T;
     p.row_tiles = ragged ? std::min(tokens * f->group, (tokens * f->group + (long long)f->t.batch * (p.rows - 1)) / p.rows)
@@ -100,39 +107,36 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
         // The number of chunks with the least estimated time, over the lengths that a batch may have: sequences of
         // s_k keys each, and (counted twice) lengths spread evenly up to it, where a sequence of n chunks
         // fills (n + 1) / 2 blocks with n / 2 blocks' work on average.
-        const bool codes_ = codes;
-        const double sms = sm_count(), per_sm = p.tc || hd == 512 ? 1 : 2, slots = sms * per_sm;
+        const bool one = p.tc || hd == 512 || (codes && p.rows == 16);  // block per SM
+        const double slots = sm_count() * (one ? 1.0 : 2.0);
         const double units = (double)std::max(1LL, p.row_tiles) * f->c.n_kv_h * (p.tc && hd == 512 ? 2 : 1);
-        const double row_bytes = codes_ ? hd + 1.0 : 2.0 * hd;
+        const double row_bytes = codes ? hd + 1.0 : 2.0 * hd;
+        // what a decode block takes in at most, bytes a us, and what all of them do
+        const double rate1 = codes ? (hd == 64 ? 11e3 : 20e3) : hd == 64 ? 26e3 : 36e3, rates = codes ? 5.6e6 : 6.8e6;
         const double parts_us = (double)f->rows * hd * 8.0 / 8e6;  // one chunk's partials, written and read
         double best = 1e300;
         const long long most_n = std::min<long long>(tiles, 64);
         for (long long c = 1; c <= most_n; c += c < 8 ? 1 : c < 32 ? 2 : 8) {
             const long long mine = (tiles + c - 1) / c;  // tiles of a block
+            const double bytes = (double)mine * tile * 2.0 * row_bytes;
             double us[2];
             for (int ragged_lens = 0; ragged_lens < 2; ++ragged_lens) {
-                const double blocks = units * (double)(ragged_lens ? c + 1 : 2 * c) / 2.0;
-                double fixed, body;
-                if (p.tc) {
-                    fixed = hd == 512 ? 12.0 : 7.0;
-                    body = (double)mine * tc_tile_us(hd, codes_, most);
-                } else {
-                    // a block takes in up to 38 KB a us (28 of codes), all of them 6.6 TB/s (5.2)
-                    const double rate = std::min(codes_ ? 28e3 : 38e3, (codes_ ? 5.2e6 : 6.6e6) / std::min(slots, blocks));
-                    fixed = 5.0;
-                    body = (double)mine * tile * 2.0 * row_bytes / rate;
-                }
-                const double ratio = blocks / slots;
+                const double blocks = units * (double)(ragged_lens ? c + 1 : 2 * c) / 2.0, ratio = blocks / slots;
+                const double fixed = p.tc ? (hd == 512 ? 10.0 : 8.0) : 4.0;
+                double body = p.tc ? (double)mine * tc_tile_us(hd, codes, most) : bytes / rate1;
                 if (ragged_lens) {
-                    const double work = units / slots * ((double)(c + 1) * fixed + (double)c * body) / 2.0;
-                    us[1] = std::max(fixed + body, work + (fixed + body) / 2.0);
+                    const double waits = ratio > 1.0 ? (fixed + body) / 2.0 : 0.0;  // for the last block to end
+                    double work = ratio * fixed + units / slots * (double)c * body / 2.0;
+                    if (!p.tc) work = std::max(work, ratio * 2.0 + fixed + units * (double)c / 2.0 * bytes / rates);
+                    us[1] = std::max(fixed + body, work + waits);
                 } else {
+                    if (!p.tc) body = std::max(body, bytes * std::min(slots, blocks) / rates);
                     us[0] = std::max(1.0, ratio + 0.5 * (std::ceil(ratio) - ratio)) * (fixed + body);
                 }
             }
             double t = f->t.batch > 1 ? 0.35 * us[0] + 0.65 * us[1] : us[0];
             if (c > 1) t += 3.0 + 0.05 * (double)c + 0.2 * (double)std::max(0LL, c - 16) + parts_us * (double)c;  // the merge
-            if (t < best * 0.98) {
+            if (t < best * 0.99) {
                 best = t;
                 n = c;
             }
