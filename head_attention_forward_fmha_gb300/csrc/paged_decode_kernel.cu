@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
             mx = max(mx & 0xFFFFu, mx >> 16);
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            const int e = (int)(mx >> 7), up = e > 0 && e < 255 ? min(max(14 - (e - 127), -120), 120) : 0;
+            const int e = (int)(mx >> 7), up = e < 255 ? min(max(14 - (e - 127), -120), 120) : 0;
             const float fac = __uint_as_float((uint32_t)(127 + up) << 23);
             if (lc == 0 && FMHA_IN_BOUNDS(r < C::RT, kSitePagedQ, f.status)) q_exp[r] = up;
 #pragma unroll

@@ -553,6 +553,8 @@ int fmha_fwd_first_packed(const struct fmha_fwd_first_args* args);
  *     less; code = E4M3(x / scale), to nearest, ties to even (x / scale is exact, so each value is
  *     rounded once); the row stands for scale * code, which is a bf16 value again (below 2^-133 the
  *     nearest one).  A row with a NaN or an infinity gets the byte 255 and reads as NaN throughout.
+ *     The codes 0x7F and 0xFF (E4M3's NaN) are never written; in rows that a caller fills otherwise they
+ *     may not stand at keys that are attended.
  *   block_table [batch, table_width] int32: row i of sequence b lies in page
  *     block_table[b, i / page], row i % page.  An entry outside [0, n_pages) is a page that is
  *     not there: its rows are not written, not read back and attended by no query row (so the pages
@@ -574,6 +576,7 @@ int fmha_fwd_first_packed(const struct fmha_fwd_first_args* args);
 /*
  * fmha_paged_append -- K and V rows of new tokens into the cache: token t of sequence b to row
  * start[b] + t (start: [batch] int32; negative rows, and rows behind the block table, are left out).
+ * Where two tokens of a call go to one row of the pool, what it holds afterwards is undefined.
  */
 struct fmha_paged_append_args {
     const void *k, *v; /* bf16, n_kv_h heads */
@@ -617,6 +620,9 @@ int fmha_paged_gather(const struct fmha_paged_gather_args* args);
  * K may hold anything at keys that a row does not attend, V at keys that no row of the sequence attends;
  *   V has to be finite at the others.  A NaN score of an attended key makes O and LSE of its
  *   row NaN, whatever the number of chunks.
+ * Weights are rounded to bf16 before they meet V; scores, sums and O are fp32.  With 8-bit pages and few rows
+ *   the operands are fp16 times powers of two: elements of q more than 2^29 below their row's largest
+ *   are lost, and a weight times its V row's scale is kept to 2^-37 of the largest such scale.
  * n_splits: chunks that a sequence's keys are divided into, 0 for the library's choice.
  * workspace: fmha_fwd_paged_plan(same arguments) chunks > 1 need
  *   fmha_workspace_bytes(1, n_h, rows, hd, chunks) bytes, rows being batch * T or total,

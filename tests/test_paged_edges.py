@@ -12,6 +12,7 @@ from head_attention_forward_fmha_gb300 import binding, torch_op  # noqa: F401  (
 
 DEV = "cuda"
 FORMS = ops.FORMS
+kernel = ops.kernel  # fixture: both kernels of the attention
 
 
 @pytest.fixture(autouse=True)
@@ -69,6 +70,42 @@ def test_ops_eager_and_compiled_match(form):
     assert not torch.equal(one[0].view(torch.uint8), cache[0].view(torch.uint8))
     ends = [x + 3 for x in lens]
     ref.assert_attention(a[:2], ref.attend(q, one, table, ends, 16, [0, 3, 6, 9], causal=True))
+
+
+# ------------------------------------------------------------------ padded batches
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("hd", ops.HD)
+@pytest.mark.parametrize("T,window", [(9, 0), (9, 3), (40, 0), (300, 100)])
+def test_more_tokens_than_keys(hd, T, window, form, kernel):
+    """Sequences with fewer keys than new tokens: the first rows stand before the first key and attend nothing."""
+    ops.check(ops.gen(50), hd, 8, 2, T, [4, 0, T, 2 * T, 1, T + 1], 16, form, window=window, n_first=min(window, 2), causal=True)
+    ops.check(ops.gen(51), hd, 8, 2, T, [4, 0, T - 1, 200], 16, form, window=window, n_first=min(window, 2), sink=True, n_splits=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_subnormal_queries(form, kernel):
+    """Query rows whose largest magnitude is a subnormal bf16 over keys large enough for it to count."""
+    ops.check(ops.gen(52), 128, 8, 2, 1, [100, 37], 16, form, q_mult=2.0 ** -129, k_mult=2.0 ** 121)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_appended_tokens_that_share_a_row_leave_the_others_alone(form):
+    """Two sequences that write the same row of the pool: that row is undefined, every other one is as it was or as written."""
+    g = ops.gen(53)
+    cache = ops.blank(4, 2, 16, 64, form)
+    before = [None if t is None else t.clone() for t in cache]
+    table, k = ops.ints([[1], [1], [2]]), ops.normal(g, 3, 2, 1, 64)
+    binding.fmha_paged_append(k, k, *cache, table, ops.ints([5, 5, 3]))
+    one = ops.blank(4, 2, 16, 64, form)
+    binding.fmha_paged_append(k[2:], k[2:], *one, table[2:].contiguous(), ops.ints([3]))
+    for a, b, c in zip(cache, one, before):
+        if a is not None:
+            a, b, c = (x.view(torch.uint8) for x in (a, b, c))
+            b[1, :, 5] = a[1, :, 5]
+            assert torch.equal(a, b) and not torch.equal(b[2], c[2])
 
 
 # ------------------------------------------------------------------ streams
