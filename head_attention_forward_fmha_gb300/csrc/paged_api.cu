@@ -125,7 +125,7 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
                 const double fixed = p.tc ? (hd == 512 ? 10.0 : 8.0) : 4.0;
                 double body = p.tc ? (double)mine * tc_tile_us(hd, codes, most) : bytes / rate1;
                 if (ragged_lens) {
-                    const double waits = ratio > 1.0 ? (fixed + body) / 2.0 : 0.0;  // for the last block to end
+                    const double waits = ratio > 1.0 ? (fixed + body) * 0.2 : 0.0;  // for the last block to end, long ones first
                     double work = ratio * fixed + units / slots * (double)c * body / 2.0;
                     if (!p.tc) work = std::max(work, ratio * 2.0 + fixed + units * (double)c / 2.0 * bytes / rates);
                     us[1] = std::max(fixed + body, work + waits);

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
         mbar_fence_init();
     }
     grid_dependency_wait();  // every global access below follows the preceding kernel
-    const PagedTile t = paged_tile(f, blockIdx.x / f.c.n_kv_h, C::RT, f.status);
+    const PagedTile t = paged_tile_by_keys<C::RT>(f, blockIdx.x / f.c.n_kv_h, f.status);
     if (t.n <= 0) return;
     // A tile's boxes: of min(page, KT) keys each, from a multiple of that on.
     const int box_keys = min(f.c.page, C::KT);

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
         mbar_fence_init();
     }
     grid_dependency_wait();  // every global access below follows the preceding kernel
-    const PagedTile t = paged_tile(f, blockIdx.x / C::PARTS / f.c.n_kv_h, BM * C::NRT, f.status);
+    const PagedTile t = paged_tile_by_keys<BM * C::NRT>(f, blockIdx.x / C::PARTS / f.c.n_kv_h, f.status);
     if (t.n <= 0) return;
     const int box_keys = min(f.c.page, BN);  // keys that are copied at once, from a multiple of that on
     const PagedKeys k = paged_keys(f, t, split, BN, box_keys);
