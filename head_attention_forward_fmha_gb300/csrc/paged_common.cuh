@@ -12,6 +12,39 @@
 
 namespace fmha {
 
+// Site codes of the checked build (ptx.cuh), 0x9nn: the cache in pages.
+enum PagedCheckSite : unsigned {
+    kSitePagedSeq = 0x901,   // paged cache: index of a length, a bound, a start or a block-table entry
+    kSitePagedRow = 0x902,   // paged cache: row of a page (and its scale byte)
+    kSitePagedIo = 0x903,    // paged append and gather: row of new tokens or of the contiguous output
+    kSitePagedQ = 0x904,     // paged attention: query row and its place in shared memory
+    kSitePagedKv = 0x905,    // paged attention: shared-memory offset of a key row, or box coordinates
+    kSitePagedLds = 0x906,   // paged attention: shared-memory operand of an mma.sync
+    kSitePagedTmem = 0x907,  // paged attention: tensor-memory columns of S, P and O
+    kSitePagedDesc = 0x908,  // paged attention: K and V stages the MMAs read
+    kSitePagedComb = 0x909,  // paged attention: combine or staging buffer
+    kSitePagedOut = 0x90a,   // paged attention and merge: output or partial row, sink
+};
+
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Four E4M3 bytes -> two fp16 pairs (bytes 0 and 1, bytes 2 and 3); exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Entry `slot` of sequence b's block table as it stands there, -1 outside it.  What is loaded is not
 // looked at here, so that nothing waits for it before paged_page does.
 __device__ __forceinline__ int paged_entry(const PagedCache& c, int batch, int b, int slot, unsigned* status) {

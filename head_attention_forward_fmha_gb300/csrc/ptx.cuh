@@ -45,7 +45,7 @@ constexpr bool kCheckedBuild = false;
 // Site codes: 0x1nn row-tile kernel, 0x2nn hd-512 kernel, 0x3nn decode
 // kernel, 0x4nn merge, 0x5nn shared epilogue / softmax helpers, 0x7nn
 // two-row-tile kernel, 0x8nn norm-and-rotation, 4-bit cache append, 4-bit
-// cache attention, 0x9nn cache in pages.
+// cache attention.
 enum CheckSite : unsigned {
     kSiteTcQLoad = 0x101,   // Q box coordinates
     kSiteTcKLoad = 0x102,   // K tile: first key, stage offset
@@ -101,16 +101,6 @@ enum CheckSite : unsigned {
     kSiteKv4Range = 0x80a,   // 4-bit attention: range factor index of an fp16 partial
     kSiteNrRow = 0x80b,      // norm-and-rotation kernel: head row loaded or stored, index of a position or start
     kSiteNrTable = 0x80c,    // norm-and-rotation kernel: row of the cosines and sines
-    kSitePagedSeq = 0x901,   // paged cache: index of a length, a bound, a start or a block-table entry
-    kSitePagedRow = 0x902,   // paged cache: row of a page (and its scale byte)
-    kSitePagedIo = 0x903,    // paged append and gather: row of new tokens or of the contiguous output
-    kSitePagedQ = 0x904,     // paged attention: query row and its place in shared memory
-    kSitePagedKv = 0x905,    // paged attention: shared-memory offset of a key row, or box coordinates
-    kSitePagedLds = 0x906,   // paged attention: shared-memory operand of an mma.sync
-    kSitePagedTmem = 0x907,  // paged attention: tensor-memory columns of S, P and O
-    kSitePagedDesc = 0x908,  // paged attention: K and V stages the MMAs read
-    kSitePagedComb = 0x909,  // paged attention: combine or staging buffer
-    kSitePagedOut = 0x90a,   // paged attention and merge: output or partial row, sink
 };
 
 static __device__ __noinline__ bool bounds_failed(unsigned site, unsigned* status) {
@@ -215,15 +205,6 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const void* tma
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_5d(void* smem_dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -336,16 +317,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
         : "=r"(r)
         : "r"(w));
     return r;
-}
-
-// Four E4M3 bytes -> two fp16 pairs (bytes 0 and 1, bytes 2 and 3); exact.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {

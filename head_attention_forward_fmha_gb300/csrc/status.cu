@@ -4,6 +4,7 @@
 // fmha_check_device_status().
 #include <mutex>
 #include "internal.h"
+#include "paged_common.cuh"
 #include "ptx.cuh"
 
 namespace fmha {
