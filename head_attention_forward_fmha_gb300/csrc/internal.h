@@ -226,6 +226,10 @@ struct PagedGather {
 };
 cudaError_t launch_paged_gather(const PagedGather& a, cudaStream_t stream);
 
+// Batches of up to this many sequences are looked through by every block; in larger ones the search goes by
+// their bounds (1024 sequences of one token at hd 64: 327 us when looked through, 179 with the search).
+constexpr int kPagedScan = 64;  // the plan counts row tiles by the same rule
+
 struct PagedFwd {
     PagedCache c;
     PagedTokens t;

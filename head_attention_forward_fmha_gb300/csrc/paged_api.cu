@@ -95,8 +95,9 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
     p.tc = path ? path >= 2 : most >= tc_min_rows(hd, codes);
     p.rows = p.tc ? paged_tc_rows(hd) : paged_decode_rows(hd, most);
     const long long tokens = ragged ? f->t.total : (long long)f->t.batch * f->t.T;
-    p.row_tiles = ragged ? std::min(tokens * f->group, (tokens * f->group + (long long)f->t.batch * (p.rows - 1)) / p.rows)
-                         : f->t.batch * ((most + p.rows - 1) / p.rows);
+    p.row_tiles = !ragged ? f->t.batch * ((most + p.rows - 1) / p.rows)
+                  : f->t.batch > kPagedScan ? tokens * f->group / p.rows + f->t.batch  // slots of paged_tile
+                                            : std::min(tokens * f->group, (tokens * f->group + (long long)f->t.batch * (p.rows - 1)) / p.rows);
     f->row_tiles = (int)std::min<long long>(p.row_tiles, INT_MAX);
     const int tile = p.tc ? paged_tc_kv_tile(hd) : paged_decode_kv_tile(hd, codes);
     long long span = f->s_k;

@@ -61,14 +61,26 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppend a, 
         const int tok = (int)(row / (unsigned)c.n_kv_h);
         h = (int)(row - (unsigned)tok * (unsigned)c.n_kv_h);
         token = tok;
-        // the first sequence whose end lies behind the token: ends at or before it are counted
+        // the first sequence whose end lies behind the token: ends at or before it are counted, or searched in large batches
         b = 0;
-        for (int b0 = 0; b0 < a.t.batch; b0 += 32) {
-            int end = INT_MAX;
-            if (b0 + lane < a.t.batch) end = __ldg(a.t.cu + b0 + lane + 1);
-            for (int g = 0; g < 32; g += 1 << log_tpr) {
-                const unsigned before = __ballot_sync(0xffffffffu, end <= __shfl_sync(0xffffffffu, tok, g));
-                if ((lane >> log_tpr) == (g >> log_tpr)) b += __popc(before);
+        if (a.t.batch <= kPagedScan) {
+            for (int b0 = 0; b0 < a.t.batch; b0 += 32) {
+                int end = INT_MAX;
+                if (b0 + lane < a.t.batch) end = __ldg(a.t.cu + b0 + lane + 1);
+                for (int g = 0; g < 32; g += 1 << log_tpr) {
+                    const unsigned before = __ballot_sync(0xffffffffu, end <= __shfl_sync(0xffffffffu, tok, g));
+                    if ((lane >> log_tpr) == (g >> log_tpr)) b += __popc(before);
+                }
+            }
+        } else {
+            for (int n = a.t.batch; n > 0;) {  // ends b .. b + n - 1 may lie behind it
+                const int half = n >> 1;
+                if (__ldg(a.t.cu + b + half + 1) <= tok) {
+                    b += half + 1;
+                    n -= half + 1;
+                } else {
+                    n = half;
+                }
             }
         }
         t = -1;

@@ -136,7 +136,7 @@ struct PagedTile {
 };
 
 // Row tile `idx` of the launch (tiles of `rows` rows, sequences one after another, each
-// sequence's last tile first: under a causal mask it has the most keys).  Warp-collective; all lanes get
+// sequence's last tile first: under a causal mask it has the most keys; ragged ones with empty slots between).  Warp-collective; all lanes get
 // the result; n = 0: past the last tile.
 __device__ __forceinline__ PagedTile paged_tile(const PagedFwd& f, int idx, int rows, unsigned* status) {
     const int lane = threadIdx.x & 31;
@@ -149,31 +149,30 @@ __device__ __forceinline__ PagedTile paged_tile(const PagedFwd& f, int idx, int 
         if (t.b >= f.t.batch) return t;
         t.T = f.t.T;
     } else {
-        bool found = false;
-        for (int b0 = 0; b0 < f.t.batch && !found; b0 += 32) {
-            int first = 0, n = 0;
-            if (b0 + lane < f.t.batch) paged_tokens(f.t, b0 + lane, first, n, status);
-            const int mine = (int)(((long long)n * f.group + rows - 1) / rows);
-            int upto = mine;
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const int other = __shfl_up_sync(0xffffffffu, upto, s);
-                if (lane >= s) upto += other;
+        // Sequence b's tiles begin at slot first * group / rows + b: it has as many slots as tiles, or one more.
+        int lo = 0, hi = f.t.batch;  // the sequence is one of [lo, hi)
+        while (lo < hi) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            bool before = false;
+            if (at < hi) {
+                int first, n;
+                paged_tokens(f.t, at, first, n, status);
+                before = (int)((long long)first * f.group / rows) + at <= idx;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, upto > idx);
-            if (past) {
-                const int who = __ffs(past) - 1;
-                t.b = b0 + who;
-                t.first = __shfl_sync(0xffffffffu, first, who);
-                t.T = __shfl_sync(0xffffffffu, n, who);
-                tiles = __shfl_sync(0xffffffffu, mine, who);
-                idx -= __shfl_sync(0xffffffffu, upto, who) - tiles;
-                found = true;
-            } else {
-                idx -= __shfl_sync(0xffffffffu, upto, 31);
-            }
+            const int reached = __popc(__ballot_sync(0xffffffffu, before));
+            if (reached == 0) return t;  // (rows before the first sequence)
+            lo += (reached - 1) * step;
+            hi = min(hi, lo + step);
+            if (step == 1) break;
         }
-        if (!found) return t;
+        t.b = lo;
+        paged_tokens(f.t, lo, t.first, t.T, status);
+        tiles = (int)(((long long)t.T * f.group + rows - 1) / rows);
+        idx -= (int)((long long)t.first * f.group / rows) + lo;
+        if (idx >= tiles) {
+            t.T = 0;
+            return t;
+        }
     }
     const int most = min((long long)f.s_k, (long long)f.c.width << f.c.log_page);
     if (FMHA_IN_BOUNDS(t.b < f.t.batch, kSitePagedSeq, status)) t.len = min(max(__ldg(f.seq_lens + t.b), 0), most);
@@ -184,12 +183,13 @@ __device__ __forceinline__ PagedTile paged_tile(const PagedFwd& f, int idx, int 
 
 // The same for blocks whose time goes with their keys: tiles in falling order of the keys that they reach, as far as
 // eighths of the longest sequence tell them apart, so that no long block begins when the others end
-// (in the order of the sequences / so: 16 ragged chunks of up to 512 tokens at hd 128 in 8 bits 210 / 168 us, 4 chunks of 512 in
+// (with more sequences looking through them costs more than that: 128 at hd 64, one token each, 30 us, 24 without).
+// Gains (in the order of the sequences / so: 16 ragged chunks of up to 512 tokens at hd 128 in 8 bits 210 / 168 us, 4 chunks of 512 in
 // bf16 over 200 to 8000 keys 133 / 95, 32 decode steps of ragged sequences at hd 64 in two chunks 38 / 30).
 template <int ROWS>
 __device__ __forceinline__ PagedTile paged_tile_by_keys(const PagedFwd& f, int idx, unsigned* status) {
     static_assert((ROWS & (ROWS - 1)) == 0, "tiles of a power of two of rows");
-    if (f.t.batch == 1) return paged_tile(f, idx, ROWS, status);  // its last tile first
+    if (f.t.batch > kPagedScan || (f.t.batch == 1 && !f.t.cu)) return paged_tile(f, idx, ROWS, status);
     constexpr int K = 8;
     const int lane = threadIdx.x & 31;
     const int most = min((long long)f.s_k, (long long)f.c.width << f.c.log_page);

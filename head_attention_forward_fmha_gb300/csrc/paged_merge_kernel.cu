@@ -3,7 +3,9 @@
 // One warp per (row of o, slice of up to 128 columns), as in merge_kernel.cu; what differs:
 // rows behind the last sequence of a ragged batch are left as they are, of a chunk with
 // LSE = -inf (nothing attended, as most chunks of short sequences) O is neither written nor read,
-// and a chunk with LSE = NaN makes O and LSE of its row NaN.
+// and a chunk with LSE = NaN makes O and LSE of its row NaN.  Bound by the latency of two rounds of loads: about 3 us
+// behind a decode step; partials of many rows (4 x 512 tokens of 64 heads: 67 MB a chunk) by L2, which is why the
+// plan splits long chunks of tokens only where there are too few blocks.
 #include "internal.h"
 #include "paged_common.cuh"
 #include "ptx.cuh"

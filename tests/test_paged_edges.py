@@ -85,6 +85,18 @@ def test_more_tokens_than_keys(hd, T, window, form, kernel):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("b,pad", [(64, (0, 0)), (65, (3, 2)), (200, (0, 5)), (1100, (130, 1))])
+def test_batches_on_both_sides_of_the_search(b, pad, form, kernel):
+    """Ragged batches whose sequences a block looks through and such in which it searches, some of them empty."""
+    new = [(i * 7) % 11 if i % 5 else 0 for i in range(b)]
+    new[b // 2], new[-1] = 300, 0
+    ops.check(ops.gen(54), 64, 4, 1, None, [n + (i * 13) % 50 for i, n in enumerate(new)], 16, form, new=new, pad=pad, causal=True)
+    new = [1 + (i % 17 == 0) * 40 for i in range(b)]
+    ops.check(ops.gen(55), 128, 8, 2, None, [n + i % 70 for i, n in enumerate(new)], 16, form, new=new, pad=pad, causal=True, n_splits=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
 def test_subnormal_queries(form, kernel):
     """Query rows whose largest magnitude is a subnormal bf16 over keys large enough for it to count."""
     ops.check(ops.gen(52), 128, 8, 2, 1, [100, 37], 16, form, q_mult=2.0 ** -129, k_mult=2.0 ** 121)
