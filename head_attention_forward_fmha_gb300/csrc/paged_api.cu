@@ -106,7 +106,7 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
     long long n = wanted;
     if (n <= 0) {
         // The number of chunks with the least estimated time, over the lengths that a batch may have: sequences of
-        // s_k keys each, and (counted twice) lengths spread evenly up to it, where a sequence of n chunks
+        // s_k keys each, and (counted more without a window) lengths spread evenly up to it, where a sequence of n chunks
         // fills (n + 1) / 2 blocks with n / 2 blocks' work on average.
         const bool one = p.tc || hd == 512 || (codes && p.rows == 16);  // block per SM
         const double slots = sm_count() * (one ? 1.0 : 2.0);
@@ -135,7 +135,8 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
                     us[0] = std::max(1.0, ratio + 0.5 * (std::ceil(ratio) - ratio)) * (fixed + body);
                 }
             }
-            double t = f->t.batch > 1 ? 0.35 * us[0] + 0.65 * us[1] : us[0];
+            const double even = f->t.batch == 1 ? 1.0 : f->window > 0 ? 0.8 : 0.25;  // a window makes long sequences alike
+            double t = even * us[0] + (1.0 - even) * us[1];
             if (c > 1) t += 3.0 + 0.05 * (double)c + 0.2 * (double)std::max(0LL, c - 16) + parts_us * (double)c;  // the merge
             if (t < best * 0.99) {
                 best = t;
