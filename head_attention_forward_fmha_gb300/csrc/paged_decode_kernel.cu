@@ -19,7 +19,7 @@
 // more than 2^26 below that lose bits).  V's operand is loaded by ldmatrix with
 // transposition on pairs of codes, so that rows g and g + 8 of the A operand are columns 2 g and 2 g + 1.
 //
-// What bounds it: bf16 is memory (16 sequences of 16384 keys, 32 query heads on 8 of 128: 157 us, 6.8 TB/s; 99 % of a
+// What bounds it: bf16 is memory (16 sequences of 16384 keys, 32 query heads on 8 of 128: 157 us, 6.8 TB/s; 97 % of a
 // plain copy with a window of 4096 in 32 sequences); a block takes in 36 KB a us at most, so short
 // batches are split until there are two blocks for each SM.  In 8 bits (107 us, 5.1 TB/s) the ALUs' 46 % and the latencies of
 // ldmatrix, conversion and shuffles in turn: eight consumer warps instead of four brought 137 -> 107 us.
