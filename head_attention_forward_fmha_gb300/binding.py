@@ -865,8 +865,9 @@ def fmha_fwd_paged(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_len
     handle = at = _handle(stream, dev)
     if workspace is not None:
         need, at = workspace.numel(), None
-    elif need:  # the call's own, of its stream's memory
-        workspace = need
+    else:  # the call's own, of its stream's memory, for chunks of the keys that the block table holds
+        s_k = min(s_k, width * page)
+        workspace = need or None
     pool, scales = (n_pages, n_kv_h, page, hd), (n_pages, n_kv_h, page)
     _run(_PAGED_FWD[codes], dev, q, k_pages, pool, v_pages, pool, k_scales, scales, v_scales, scales, block_table, (b, width), seq_lens, (b,),
          cu_q, (b + 1,), o, tuple(shape), lse, tuple(shape[:-1]), sink, (n_h,), workspace, at, need, handle, *qs,

@@ -152,6 +152,13 @@ PagedPlan plan_paged(PagedFwd* f, bool ragged, bool codes, int wanted) {
     return p;
 }
 
+// At most s_k keys; a window that holds them all is none.
+void bound_keys(PagedFwd* f, int s_k, int window, int n_first) {
+    f->s_k = s_k;
+    f->window = window >= s_k ? 0 : window;
+    f->n_first = f->window > 0 ? std::min(n_first, s_k) : 0;
+}
+
 int check_fwd(int batch, int T, int total, bool ragged, int n_h, int n_kv_h, int hd, int page, int n_pages, int width, int s_k, float scale,
               int window, int n_first, int causal, int n_splits, PagedFwd* f) {
     *f = PagedFwd{};
@@ -170,10 +177,8 @@ int check_fwd(int batch, int T, int total, bool ragged, int n_h, int n_kv_h, int
     f->n_h = n_h;
     f->group = n_h / n_kv_h;
     f->rows = (ragged ? (long long)total : (long long)batch * T) * n_h;
-    // keys that there are at most; a window that holds them all is none
-    f->s_k = n_pages == 0 ? 0 : (int)std::min<long long>(s_k, (long long)width * page);
-    f->window = window >= f->s_k ? 0 : window;
-    f->n_first = f->window > 0 ? std::min(n_first, f->s_k) : 0;
+    // keys that there are at most
+    bound_keys(f, n_pages == 0 ? 0 : (int)std::min<long long>(s_k, (long long)width * page), window, n_first);
     f->causal = causal;
     return FMHA_OK;
 }
@@ -289,7 +294,16 @@ int fmha_fwd_paged(const struct fmha_fwd_paged_args* x) try {
     f.sink = x->sink;
     f.o = static_cast<__nv_bfloat16*>(x->o);
     f.lse = x->lse;
-    const PagedPlan p = plan_paged(&f, ragged, x->k_scales != nullptr, x->n_splits);
+    const bool codes = x->k_scales != nullptr;
+    PagedPlan p = plan_paged(&f, ragged, codes, x->n_splits);
+    if (f.n_splits > 1 && f.s_k < x->s_k) {
+        // The workspace has been sized by fmha_fwd_paged_plan, which does not know how many keys the block table holds:
+        // no more chunks than it says for s_k.
+        PagedFwd told = f;
+        bound_keys(&told, x->s_k, x->window, x->n_first);
+        plan_paged(&told, ragged, codes, x->n_splits);
+        if (f.n_splits > told.n_splits) p = plan_paged(&f, ragged, codes, told.n_splits);
+    }
     if ((double)p.row_tiles * f.c.n_kv_h * 2 > INT_MAX) return fail(FMHA_ERR_SHAPE, "too many query rows");
     if (f.n_splits > 1) {
         const size_t need = (size_t)f.n_splits * f.rows * (f.c.hd + 1) * 4;
