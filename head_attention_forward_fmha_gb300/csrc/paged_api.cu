@@ -49,7 +49,7 @@ int check_tokens(int batch, int T, int total, bool ragged, int heads, PagedToken
     const double tokens = ragged ? (double)total : (double)batch * T;
     if (tokens * heads > kMost) return fail(FMHA_ERR_SHAPE, "%.0f tokens of %d heads are too many rows", tokens, heads);
     t->batch = batch;
-    t->T = T;
+    t->T = ragged ? std::min(T, total) : T;  // a sequence has no more than there are
     t->total = ragged ? total : 0;
     return FMHA_OK;
 }

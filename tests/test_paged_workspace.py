@@ -88,3 +88,28 @@ def test_binding_takes_a_planned_workspace(s_k, window, kernel):
         for w in (ws, None):
             got = binding.fmha_fwd_paged(q, *cache, table, n, s_k=s_k, window=window, causal=True, n_splits=splits, workspace=w)
             ref.assert_attention(got, ref.attend(q, cache, table, lens, page, window=window, causal=True))
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("n_h,n_kv,hd", [(64, 8, 128), (8, 8, 64), (32, 4, 256), (128, 1, 512)])
+def test_no_sequence_counts_more_tokens_than_there_are(n_h, n_kv, hd, codes):
+    """max_q above the rows of q: the plan is that of the call, which cuts it to them."""
+    for total in (1, 2, 7, 40):
+        for window in (0, 1000):
+            want = binding.fmha_fwd_paged_plan(3, total, n_h, n_kv, hd, 16, 8192, window, 4, True, total, codes)
+            for T in (total + 1, 512, 1 << 20):
+                assert binding.fmha_fwd_paged_plan(3, T, n_h, n_kv, hd, 16, 8192, window, 4, True, total, codes) == want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_q", [2, 3, 512])
+def test_binding_takes_a_workspace_planned_for_max_q(max_q):
+    """Two sequences of one token: a workspace planned for max_q tokens of a sequence."""
+    g = ops.gen(4)
+    lens, page = [4000, 33], 16
+    cache, table = ops.pool(g, lens, 2, page, 128, ops.FORMS[0])
+    q, n, cu = ops.normal(g, 2, 8, 128), ops.ints(lens), [0, 1, 2]
+    chunks = binding.fmha_fwd_paged_plan(2, max_q, 8, 2, 128, page, 4000, causal=True, total=2)
+    ws = torch.empty(binding.load().fmha_workspace_bytes(1, 8, 2, 128, chunks), dtype=torch.uint8, device=ops.DEV)
+    got = binding.fmha_fwd_paged(q, *cache, table, n, cu_q=ops.ints(cu), max_q=max_q, s_k=4000, causal=True, workspace=ws)
+    ref.assert_attention(got, ref.attend(q, cache, table, lens, page, cu, causal=True))
