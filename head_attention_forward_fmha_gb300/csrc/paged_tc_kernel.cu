@@ -29,9 +29,12 @@
 // faster (32 clocks an MMA, 48 with both operands from shared memory) and leaves room for stages and raw buffers.
 //
 // Softmax: scores against a reference, the maximum of the first scores that the row attends (so that a row's
-// only key has P = 1, which bf16 holds).  P in bf16 and its fp32 sum have the exponent range for what
-// follows: only where a score passes the reference by 40 (log2 units) does that move, by a whole number, and the
-// sum, O and the tile's weights so far are multiplied by the power of two.  (The check comes before a chunk's
+// only key has P = 1, which bf16 holds).  Only where a score passes the reference by kPast = 8 (log2 units) does that
+// move, by a whole number, and the sum, O and the tile's weights so far are multiplied by the power of two.  So P is at
+// most 2^8 and O's fp32 sum holds values of V up to 2^120 over the number of keys.  (P and its own sum would bear 40, but not
+// P V: with V of 2^90 O was infinite.  For a chunk of 512 tokens over 4 x 8192 keys both bounds take the same time with scores of
+// unit variance; with a deviation of 8, where 40 is never passed, hd 128 takes 276 us and 220 with 40, hd 64 233 and 200, hd 256
+// 472 and 416, hd 512 and 8 bits the same.)  (The check comes before a chunk's
 // exponentials: found afterwards, with the chunk done again, it cost 254 us where it now takes 222.)
 //
 // What bounds it (GB300; chunks of 512 tokens over 4 x 8192 keys, 32 query heads on 4): at hd 128 in bf16 a tile of 256 rows
@@ -92,6 +95,8 @@ struct PTCfg {
     static_assert(QT % KCH == 0 || QT == HD, "a K chunk meets Q in one place");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
+
+constexpr float kPast = 8.f;  // by how much a score may pass its row's reference
 
 // Operand layout of a K chunk and of a V tile, NB blocks of 64 columns wide: groups of 8 keys, in each
 // the blocks one after another (1024 bytes: 8 rows of 128, 16-byte chunk c of row r at chunk c ^ (r % 8)).
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
                     float x[C::CH / 32][32];
                     load_scores(col, x);
                     const float mt = top_of(x);
-                    const bool move = mt > m_ref + 40.f;  // true without a reference
+                    const bool move = mt > m_ref + kPast;  // true without a reference
                     if (__any_sync(0xffffffffu, move)) {
                         float alpha = 1.f;
                         if (move) {

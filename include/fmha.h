@@ -618,7 +618,8 @@ int fmha_paged_gather(const struct fmha_paged_gather_args* args);
  *   j < n_first).  A row that attends nothing gets O = 0 and LSE = -inf, or the sink's.
  * sink: [n_h] fp32 logits or NULL (fmha_fwd_sink).
  * K may hold anything at keys that a row does not attend, V at keys that no row of the sequence attends;
- *   V has to be finite at the others.  A NaN score of an attended key makes O and LSE of its
+ *   V has to be finite at the others, and below 2^120 over the number of keys (O is summed in fp32 before it is
+ *   divided, under weights of up to 2^8).  A NaN score of an attended key makes O and LSE of its
  *   row NaN, whatever the number of chunks.
  * Weights are rounded to bf16 before they meet V; scores, sums and O are fp32.  With 8-bit pages and few rows
  *   the operands are fp16 times powers of two: elements of q more than 2^29 below their row's largest
