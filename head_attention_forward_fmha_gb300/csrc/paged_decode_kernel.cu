@@ -252,12 +252,14 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
     }
     named_barrier_sync(1, C::NCW * 32);  // Q staged
 
-    const float sl2 = f.scale_log2;
-    int row_exp[NB][2], v_unit = 0;  // codes: power of two of Q's rows; unit of O, as a scale byte
+    // Codes: the scale's power of two goes with those of the rows of Q and K, so that a score leaves fp32's range only if its value does.
+    int scale_exp = 0;
+    const float sl2 = CODES ? frexpf(f.scale_log2, &scale_exp) : f.scale_log2;
+    int row_exp[NB][2], v_unit = 0;  // codes: power of two of Q's rows over the scale's; unit of O, as a scale byte
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) row_exp[nb][i] = CODES ? q_exp[nb * 8 + 2 * (lane & 3) + i] : 0;
+        for (int i = 0; i < 2; ++i) row_exp[nb][i] = CODES ? q_exp[nb * 8 + 2 * (lane & 3) + i] - scale_exp : 0;
     const uint32_t qs_addr = smem_u32(qs);
     const int g = lane >> 2, t4 = lane & 3;
     constexpr float kBias = CODES ? 12.f : 0.f;  // log2 of the factor that P and its sum carry
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
             for (int i = 0; i < 2; ++i) {
                 float x0 = sc[nb][i] * sl2, x1 = sc[nb][2 + i] * sl2;
                 if constexpr (CODES) {
-                    // times K's scale, and the power of two that undoes Q's
+                    // times K's scale, the power of two that undoes Q's, and the attention's scale
                     auto power = [&](uint32_t byte) {
                         return byte == 255u ? NAN : __uint_as_float((uint32_t)min(max((int)byte - row_exp[nb][i], 1), 254) << 23);
                     };

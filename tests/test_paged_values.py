@@ -1,6 +1,6 @@
-"""Scores that rise above a row's first ones over large values: O is summed in fp32 before its division, and what |V| times the number
-of keys times 2^8 (the most by which a score may pass its row's reference before that moves) leaves below 2^128 comes out finite, on
-both kernels of the attention over a cache in pages.  64-bit references and bounds are those of tests/paged_ref.py."""
+"""The ends of the number range in the attention over a cache in pages: values as large as O's fp32 sum allows (|V| times the number of
+keys times 2^8, the most by which a weight may pass its row's reference, below 2^128), and scores of ordinary size from factors that are
+far from it, on both kernels.  64-bit references and bounds are those of tests/paged_ref.py."""
 import pytest
 import torch
 
@@ -31,3 +31,12 @@ def test_large_values_under_rising_scores(hd, T, rise, size, form, kernel):
         got = binding.fmha_fwd_paged(q, *cache, table, ops.ints([n]), scale=1.0, n_splits=n_splits)
         assert torch.isfinite(got[0]).all()
         ref.assert_attention(got, ref.attend(q, cache, table, [n], page, scale=1.0))
+
+
+@pytest.mark.parametrize("form", ops.FORMS)
+@pytest.mark.parametrize("hd", ops.HD)
+@pytest.mark.parametrize("q_mult,k_mult,scale", [(2.0 ** -100, 2.0 ** -12, 2.0 ** 111), (1.0, 2.0 ** 100, 2.0 ** -103), (2.0 ** -90, 2.0 ** 90, 0.2),
+                                                 (2.0 ** 90, 2.0 ** -90, -0.2)])
+def test_scores_between_far_factors(hd, q_mult, k_mult, scale, form, kernel):
+    """Scores of ordinary size from queries, keys and a scale that are far from it."""
+    ops.check(ops.gen(hd), hd, 8, 2, 2, [0, 7, 200], 16, form, q_mult=q_mult, k_mult=k_mult, scale=scale)
