@@ -585,8 +585,9 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
             int jlo, jhi, fhi;
             paged_row_keys(f, t, k, t.r0 + row, jlo, jhi, fhi);
             const bool valid = row < t.n, warp_live = __any_sync(0xffffffffu, valid);
-            // |scale| log2(e), not 0: a masked -inf times 0 would be a NaN (2^-126 makes all weights equal as it should)
-            const float sl2 = fmaxf(fabsf(f.scale_log2), 1.17549435e-38f);
+            // |scale| log2(e), not 0: a masked -inf times 0 would be a NaN (the smallest number, 2^-149, makes the weights of any
+            // finite scores equal as it should)
+            const float sl2 = fmaxf(fabsf(f.scale_log2), 1.40129846e-45f);
             float m_ref = -INFINITY, l = 0.f;
             int ahead = entry_of(0);  // block-table entries of a tile, loaded one tile ahead
             bool ok = true;

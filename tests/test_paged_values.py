@@ -40,3 +40,12 @@ def test_large_values_under_rising_scores(hd, T, rise, size, form, kernel):
 def test_scores_between_far_factors(hd, q_mult, k_mult, scale, form, kernel):
     """Scores of ordinary size from queries, keys and a scale that are far from it."""
     ops.check(ops.gen(hd), hd, 8, 2, 2, [0, 7, 200], 16, form, q_mult=q_mult, k_mult=k_mult, scale=scale)
+
+
+@pytest.mark.parametrize("form", ops.FORMS)
+@pytest.mark.parametrize("hd", ops.HD)
+@pytest.mark.parametrize("T,window", [(2, 0), (40, 0), (40, 90)])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -140, -(2.0 ** -126)])
+def test_small_scales_over_large_products(hd, scale, T, window, form, kernel):
+    """A scale of 0 gives every key the same weight, however large its product with the query is, and one below 2^-126 counts."""
+    ops.check(ops.gen(hd), hd, 8, 2, T, [0, 7, 200], 16, form, q_mult=2.0 ** 58, k_mult=2.0 ** 58, scale=scale, window=window, causal=True)
