@@ -135,6 +135,13 @@ struct PagedTile {
     int r0, n;             // rows
 };
 
+// A tile that one warp has left in shared memory, in every lane of the calling one.  (By shuffles: read as it stands there, a ragged
+// decode batch in 8 bits took 248 us in place of 198 and a chunk at hd 256 365 in place of 344.)
+__device__ __forceinline__ PagedTile paged_tile_from(const PagedTile* s) {
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    return PagedTile{same(s->b), same(s->first), same(s->T), same(s->len), same(s->r0), same(s->n)};
+}
+
 // Row tile `idx` of the launch (tiles of `rows` rows, sequences one after another, each
 // sequence's last tile first: under a causal mask it has the most keys; ragged ones with empty slots between).  Warp-collective; all lanes get
 // the result; n = 0: past the last tile.

@@ -57,7 +57,9 @@ struct PDCfg {
     static constexpr int OFF_SC = OFF_LIVE + (STAGES * 4 + 15) / 16 * 16;
     static constexpr int OFF_QE = OFF_SC + STAGES * SC_BYTES;  // codes: power of two of each Q row
     static constexpr int OFF_ML = OFF_QE + (CODES ? RT * 4 : 0);
-    static constexpr int SMEM = 1024 + OFF_ML + KW * RT * 12 + 16;
+    static constexpr int OFF_TILE = OFF_ML + KW * RT * 12 + 16;  // (the abort flag's 16 bytes before it)
+    static constexpr int SMEM = 1024 + OFF_TILE + 32;
+    static_assert(OFF_TILE % 4 == 0 && sizeof(PagedTile) <= 32, "the block's rows");
     static_assert(KW <= 8 && KW * RT * HD * 4 <= STAGES * STAGE_BYTES, "the combine buffer reuses the ring");
 };
 
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [KW][RT] (max, sum) per key group
     int* v_exp = reinterpret_cast<int*>(ml + C::KW * C::RT);   // [KW] codes: unit of a group's O
     int* abort_flag = v_exp + C::KW * C::RT;
+    PagedTile* tile = reinterpret_cast<PagedTile*>(smem + C::OFF_TILE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.x % f.c.n_kv_h, split = blockIdx.y;
@@ -109,7 +112,14 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
         mbar_fence_init();
     }
     grid_dependency_wait();  // every global access below follows the preceding kernel
-    const PagedTile t = paged_tile_by_keys<C::RT>(f, blockIdx.x / f.c.n_kv_h, f.status);
+    // One warp reads which rows and keys are the block's, for all: lengths or bounds that another stream changes meanwhile give
+    // results of any value, but no two warps that wait for each other at different barriers.
+    if (warp == C::NCW) {
+        const PagedTile mine = paged_tile_by_keys<C::RT>(f, blockIdx.x / f.c.n_kv_h, f.status);
+        if (lane == 0) *tile = mine;
+    }
+    __syncthreads();
+    const PagedTile t = paged_tile_from(tile);
     if (t.n <= 0) return;
     // A tile's boxes: of min(page, KT) keys each, from a multiple of that on.
     const int box_keys = min(f.c.page, C::KT);
@@ -118,7 +128,6 @@ __global__ void __launch_bounds__(PDCfg<HD, NB, CODES>::THREADS)
         paged_write_empty(f, t, kvh, split, 0, HD);
         return;
     }
-    __syncthreads();
 
     // ------------------------------------------------------------ producer
     if (warp == C::NCW) {

@@ -88,7 +88,9 @@ struct PTCfg {
     static constexpr int OFF_SC = OFF_RAW + (CODES ? 2 * RAW_TILE : 0);  // scale bytes of K, of V
     static constexpr int OFF_BAR = OFF_SC + (CODES ? 2 * BN : 0);
     static constexpr int N_BARS = 1 + 2 * KST * NKC + 2 * VST + 6 + 1 + 4;
-    static constexpr int NEED = 1024 + OFF_BAR + N_BARS * 8 + 16;
+    static constexpr int OFF_TILE = OFF_BAR + N_BARS * 8 + 16;  // (the tensor-memory address before it)
+    static constexpr int NEED = 1024 + OFF_TILE + 32;
+    static_assert(OFF_TILE % 4 == 0 && sizeof(PagedTile) <= 32, "the block's rows");
     static constexpr int SMEM = NEED < 120000 ? 120000 : NEED;  // one block per SM: each takes all of tensor memory
     static_assert(NB == HDV / 64, "K chunks and V tiles have the same layout");
     static_assert(Q_COL + QT / 2 <= TMEM_COLS, "S, O and Q fit in tensor memory");
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
     uint64_t* raw_full = mma_drain + 1;   // [2] raw codes and scale bytes of K, of V (bf16: a V tile to be cleared in part)
     uint64_t* raw_empty = raw_full + 2;   // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
+    PagedTile* tile = reinterpret_cast<PagedTile*>(smem + C::OFF_TILE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x % C::PARTS, kvh = blockIdx.x / C::PARTS % f.c.n_kv_h, split = blockIdx.y;
@@ -184,21 +187,27 @@ __global__ void __launch_bounds__(PTCfg<HD, CODES>::THREADS, 1)
         mbar_fence_init();
     }
     grid_dependency_wait();  // every global access below follows the preceding kernel
-    const PagedTile t = paged_tile_by_keys<BM * C::NRT>(f, blockIdx.x / C::PARTS / f.c.n_kv_h, f.status);
-    if (t.n <= 0) return;
+    // One warp reads which rows and keys are the block's, for all: lengths or bounds that another stream changes meanwhile give
+    // results of any value, but no warps that disagree on what they wait for.
     const int box_keys = min(f.c.page, BN);  // keys that are copied at once, from a multiple of that on
+    if (warp == C::SW) {
+        const PagedTile mine = paged_tile_by_keys<BM * C::NRT>(f, blockIdx.x / C::PARTS / f.c.n_kv_h, f.status);
+        if (lane == 0) *tile = mine;
+        if (mine.n > 0 && paged_keys(f, mine, split, BN, box_keys).n > 0) {
+            tmem_alloc(tmem_slot, C::TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const PagedTile t = paged_tile_from(tile);
+    if (t.n <= 0) return;
     const PagedKeys k = paged_keys(f, t, split, BN, box_keys);
     if (k.n <= 0) {  // nothing to attend in this chunk: no tensor memory, no Q
         paged_write_empty(f, t, kvh, split, part * C::HDV, C::HDV);
         return;
     }
-    if (warp == C::SW) {
-        tmem_alloc(tmem_slot, C::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n_rt = C::NRT == 2 && t.n > BM ? 2 : 1;
 
