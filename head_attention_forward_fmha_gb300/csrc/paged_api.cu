@@ -15,7 +15,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 constexpr int kMost = 1 << 30;  // sizes and positions: differences of two stay within 32 bits
 
-// The pool and its block table.  codes: 1 when scales are given.
+// The pool and its block table, whose pointers check_cache_pointers looks at.
 int check_cache(int batch, int n_kv_h, int hd, int page, int n_pages, int width, PagedCache* c) {
     if (hd != 64 && hd != 128 && hd != 256 && hd != 512)
         return fail(FMHA_ERR_HEADDIM, "hd=%d: supported head dims are 64, 128, 256, 512", hd);

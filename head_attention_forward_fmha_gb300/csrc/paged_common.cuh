@@ -98,10 +98,9 @@ __device__ __forceinline__ float paged_scale(uint32_t byte) {
     return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x00400000u : byte << 23);
 }
 
-// Eight bf16 bits (as four words) of rows read back from 16 codes' half: words of codes w0, w1
-// under the row's scale byte.  Exact: a code has 4 significant bits, and the product is a
-// bf16 (below 2^-133 it is rounded to one).  2^(120 + byte - 127) is a bf16 up to byte 134;
-// above, the factor is applied in two steps.
+// What brings e4m3x2_raw's values to those of a row under its scale byte: the factor 2^(120 + byte - 127), as a bf16 pair.
+// Exact: a code has 4 significant bits, and the product is a bf16 (below 2^-133 it is rounded to one).  The factor is a bf16 up
+// to byte 134; above, it is applied in two steps.
 struct PagedFactor {
     uint32_t first, second;  // bf16 pairs
     bool two;
@@ -114,7 +113,7 @@ __device__ __forceinline__ PagedFactor paged_factor(uint32_t byte) {
     f.second = b | (b << 16);
     return f;
 }
-// The codes of one word: bytes 0, 2 and bytes 1, 3.
+// The four codes of a word as two bf16 pairs: bytes 0 and 2, bytes 1 and 3.
 __device__ __forceinline__ void paged_values4(uint32_t w, const PagedFactor& f, uint32_t& even, uint32_t& odd) {
     even = mul_bf16x2(e4m3x2_raw<true>(w), f.first);
     odd = mul_bf16x2(e4m3x2_raw<false>(w), f.first);

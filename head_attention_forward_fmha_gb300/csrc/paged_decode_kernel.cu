@@ -14,14 +14,14 @@
 // instruction for two codes; the step to bf16 took 4.5, and the kernel half its rate: 16 sequences of 16384
 // keys at hd 128 137 us).  Scales stay outside the MMAs: K's multiply the scores, V's the weights, in
 // fp32.  What fp16 asks for in range is kept apart as powers of two: Q's rows are scaled to a largest element in
-// [2^14, 2^15) (elements below 2^-29 of it lose bits), P carries a factor 2^12, and V's scales are taken
+// [2^14, 2^15) (elements below 2^-28 of it lose bits), P carries a factor 2^12, and V's scales are taken
 // relative to the largest that the warp has met, O being kept in units of it (weights whose V lies
 // more than 2^26 below that lose bits).  V's operand is loaded by ldmatrix with
 // transposition on pairs of codes, so that rows g and g + 8 of the A operand are columns 2 g and 2 g + 1.
 //
-// What bounds it: bf16 is memory (16 sequences of 16384 keys, 32 query heads on 8 of 128: 157 us, 6.8 TB/s; 97 % of a
-// plain copy with a window of 4096 in 32 sequences); a block takes in 36 KB a us at most, so short
-// batches are split until there are two blocks for each SM.  In 8 bits (107 us, 5.1 TB/s) the ALUs' 46 % and the latencies of
+// What bounds it: bf16 is memory (16 sequences of 16384 keys, 32 query heads on 8 of 128: 161 us, 6.7 TB/s in pages of 16 and 154 in
+// pages of 64; a plain copy's rate with a window of 4096 in 32 sequences); a block takes in 36 KB a us at most, so short
+// batches are split until there are two blocks for each SM.  In 8 bits (111 us, 4.9 TB/s; pages of 64 103) the ALUs' 44 % and the latencies of
 // ldmatrix, conversion and shuffles in turn: eight consumer warps instead of four brought 137 -> 107 us.
 // 16 rows for 9 and more: twice the accumulators for the same keys read once (one block per SM for codes); at
 // hd 512 they would spill.

@@ -39,10 +39,13 @@
 //
 // What bounds it (GB300; chunks of 512 tokens over 4 x 8192 keys, 32 query heads on 4): at hd 128 in bf16 a tile of 256 rows
 // and 128 keys takes 1.75 us, of which the MMAs need 1.33, the exponentials as long on half of the
-// SM's four schedulers' time: 1392 TFLOP/s, 73 % of the measured peak, for 8 x 2048 tokens.  At hd 256 (411 us,
-// 1295 TFLOP/s) and 512 (1222 us, each half of O with all of S: a third of the MMAs are done twice) the MMAs.  In 8 bits the
-// converters: 2.4 us a tile at hd 128 (310 us), 1.7 for 64 keys at 256 (959 us), 2.4 at 512 (2364 us), with 2.5 integer
-// instructions a value; fewer than eight warps for it take longer (six 452, four 514 us where eight took 305).
+// SM's four schedulers' time: 222 us; 1390 TFLOP/s, 73 % of the measured peak, for 8 x 2048 tokens over 8192 keys.  At hd 64 (201 us)
+// the softmax, 1.6 us a tile for half the MMAs: stalls on its scores from tensor memory and on fixed latencies, 1.6 each per
+// issue, with the tensor pipe at 30 %.  At hd 256 (419 us, 1270 TFLOP/s; 1470 for the 8 x 2048 tokens) and 512 (1234 us, each half of
+// O with all of S: a third of the MMAs are done twice) the MMAs.  In 8 bits the converters: 2.4 us a tile at hd 128
+// (309 us), 1.7 for 64 keys at 256 (921 us), 2.4 at 512 (2335 us), with 2.5 integer instructions a value; fewer than eight
+// warps for it take longer (six 452, four 514 us where eight took 305).  At hd 512 both blocks of a row tile load and convert all of K,
+// and load all 512 columns of V's codes, of which each uses its own 256: a quarter of a block's traffic from the pages.
 #include <atomic>
 #include <type_traits>
 #include "internal.h"

@@ -106,7 +106,8 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_s
               block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: Optional[torch.Tensor], max_q: Optional[int], scale: float,
               window: int, n_first: int, causal: bool, sink: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The forward over a cache in pages: q [b, n_h, T, hd], or with cu_q [total, n_h, hd], where rows that belong to no
-    sequence give rows of any value."""
+    sequence give rows of any value.  The lengths are bounded by what the block table holds, which the chunks divide: where it is
+    much wider than the sequences, pass a copy of the columns in use."""
     return binding.fmha_fwd_paged(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q=cu_q, max_q=max_q, scale=scale,
                                   window=window, n_first=n_first, causal=causal, sink=sink)
 
