@@ -66,7 +66,7 @@ struct K4TCfg {
     static constexpr int OFF_V = OFF_K + STG * K_TILE;
     static constexpr int OFF_BAR = OFF_V + STG * V_TILE;
     static constexpr int N_BARS = 1 + 2 * STG * NKC + 2 * STG + 3 * NSB + 1;
-    static constexpr int OFF_QS = OFF_BAR + N_BARS * 8 + 16;   // per-row factor of Q
+    static constexpr int OFF_QS = OFF_BAR + N_BARS * 8 + 16;   // per-row factor of Q (before it: tensor-memory address, sequence, length)
     static constexpr int NEED = 1024 + OFF_QS + BM * 4;
     static constexpr int SMEM = NEED < 120000 ? 120000 : NEED;  // one block per SM: each takes all of tensor memory
     static_assert(P_COL + NSB * BN / 2 <= TMEM_COLS, "S, O and P fit in tensor memory");
@@ -216,22 +216,36 @@ __global__ void __launch_bounds__(K4TCfg<HD>::THREADS, 1) kv4_tc_kernel(const K4
 
     // Keys: the virtual axis of kv4_kernel.cu, with tiles of BN keys and a
     // window part that starts at its first key.
+    // One warp reads the lengths for all: such that another stream changes meanwhile give results of any value, but no
+    // warps that disagree on what the block does.
     int len = f.s_k;
-    if (f.seq_lens && f.n_splits == 1 && f.batch <= 32) {
-        // Blocks start in the order of their index: with the longest sequence first,
-        // the shortest fill the last gaps (chunks of 128 tokens over four ragged
-        // sequences 38.6 -> 33.6 us).  Slot b holds the sequence that b others exceed.
-        // Chunks are even without it (16 sequences in 8 chunks at hd 512: 33.0, sorted 36.6 us).
-        const int mine = lane < f.batch ? seq_len(f, lane) : -1;
-        int ahead = 0;
-        for (int i = 0; i < f.batch; ++i) {
-            const int other = __shfl_sync(0xffffffffu, mine, i);
-            ahead += other > mine || (other == mine && i < lane);
+    if (f.seq_lens) {
+        int* const seq = reinterpret_cast<int*>(tmem_slot + 1);
+        if (warp == 4) {
+            if (f.n_splits == 1 && f.batch <= 32) {
+                // Blocks start in the order of their index: with the longest sequence first,
+                // the shortest fill the last gaps (chunks of 128 tokens over four ragged
+                // sequences 38.6 -> 33.6 us).  Slot b holds the sequence that b others exceed.
+                // Chunks are even without it (16 sequences in 8 chunks at hd 512: 33.0, sorted 36.6 us).
+                const int mine = lane < f.batch ? seq_len(f, lane) : -1;
+                int ahead = 0;
+                for (int i = 0; i < f.batch; ++i) {
+                    const int other = __shfl_sync(0xffffffffu, mine, i);
+                    ahead += other > mine || (other == mine && i < lane);
+                }
+                b = __ffs(__ballot_sync(0xffffffffu, lane < f.batch && ahead == b)) - 1;
+                len = __shfl_sync(0xffffffffu, mine, b);
+            } else {
+                len = seq_len(f, b);
+            }
+            if (lane == 0) {
+                seq[0] = b;
+                seq[1] = len;
+            }
         }
-        b = __ffs(__ballot_sync(0xffffffffu, lane < f.batch && ahead == b)) - 1;
-        len = __shfl_sync(0xffffffffu, mine, b);
-    } else if (f.seq_lens) {
-        len = seq_len(f, b);
+        __syncthreads();
+        b = __shfl_sync(0xffffffffu, seq[0], 0);
+        len = __shfl_sync(0xffffffffu, seq[1], 0);
     }
     const int slab = b * f.n_kv_h + kvh;
     const long long row0 = ((long long)b * f.n_h + (long long)kvh * a.group) * f.T;  // slab's first query row
