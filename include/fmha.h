@@ -631,7 +631,7 @@ int fmha_paged_gather(const struct fmha_paged_gather_args* args);
  * n_splits: chunks that a sequence's keys are divided into, 0 for the library's choice.
  * workspace: fmha_fwd_paged_plan(same arguments) chunks > 1 need
  *   fmha_workspace_bytes(1, n_h, rows, hd, chunks) bytes, rows being batch * T or total,
- *   else unused; FMHA_ERR_WORKSPACE if it is smaller.  (The call takes fewer chunks than that where the block
+ *   else unused; FMHA_ERR_WORKSPACE if it is smaller.  (The call may take fewer chunks than that where the block
  *   table holds fewer than s_k keys, never more.)  Two calls that may run at the same time need two.
  */
 struct fmha_fwd_paged_args {
